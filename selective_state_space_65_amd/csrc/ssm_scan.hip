@@ -50,6 +50,7 @@
 
 #include "ssm_scan.h"
 #include "device_common.h"
+#include "host_common.h"
 #include "scan_chunked.h"
 
 namespace {
@@ -2713,30 +2714,6 @@ __global__ __launch_bounds__(kBlockThreads) void scan_complex_generic_kernel(Sca
 // Host side: validation, planning, dispatch
 // ----------------------------------------------------------------------------
 
-thread_local int g_last_hip_error = 0;
-
-ssm_status_t hip_fail(hipError_t e) {
-  g_last_hip_error = (int)e;
-  return SSM_ERR_HIP;
-}
-
-bool mul_ok(int64_t a, int64_t b, int64_t* out) { return !__builtin_mul_overflow(a, b, out); }
-
-size_t io_size(ssm_dtype_t io) { return io == SSM_BF16 ? 2 : 4; }
-
-bool aligned(const void* p, size_t k) { return (reinterpret_cast<uintptr_t>(p) % k) == 0; }
-
-struct Range {
-  uintptr_t lo, hi;  // [lo, hi)
-};
-
-Range span(const void* p, int64_t bytes) {
-  uintptr_t lo = reinterpret_cast<uintptr_t>(p);
-  return Range{lo, lo + (uintptr_t)bytes};
-}
-
-bool overlap(Range a, Range b) { return a.lo < b.hi && b.lo < a.hi; }
-
 // Sizes of one call in elements.
 struct Shape {
   int64_t bd, bdl, bnl, dn, bdn;
@@ -3257,6 +3234,10 @@ ssm_status_t run_scan(ScanArgs& a, const Shape& sh, ssm_dtype_t io, bool vec, bo
   return SSM_OK;
 }
 
+static thread_local int g_last_hip_error = 0;
+
+int& ssmi_last_hip_error() { return g_last_hip_error; }
+
 extern "C" {
 
 int ssm_abi_version(void) { return SSM_ABI_VERSION; }
@@ -3274,7 +3255,7 @@ const char* ssm_status_string(ssm_status_t s) {
     case SSM_ERR_ALIAS: return "an output buffer overlaps an input buffer";
     case SSM_ERR_HIP: return "a HIP runtime call failed (see ssm_last_hip_error)";
     case SSM_ERR_UNSUPPORTED: return "valid arguments outside what this entry point implements (see the header)";
-    case SSM_ERR_WORKSPACE: return "the call needs more scratch than the entry point's fixed device array holds";
+    case SSM_ERR_WORKSPACE: return "the call needs more scratch than its workspace or the entry point's fixed device array holds";
   }
   return "unknown status";
 }
