@@ -16,6 +16,11 @@
  * ssm_scan_fwd_complex and ssm_state_update_complex are the prefill scan and
  * the decode step with a complex diagonal A.
  *
+ * Beside the selective scan stand a gated linear recurrence with one state
+ * per channel (ssm_gated_scan_fwd, ssm_gated_scan_bwd and the decode step
+ * ssm_gated_state_update) and the norm in front of a block, with the residual
+ * add fused in front of it (ssm_norm_fwd, ssm_norm_bwd).
+ *
  * What is computed (for every batch row b and channel d independently):
  *
  *   Delta_l = softplus(delta[b,d,l] + bias[d])   (or delta + bias, flag off)
@@ -78,7 +83,7 @@
 extern "C" {
 #endif
 
-#define SSM_ABI_VERSION 13
+#define SSM_ABI_VERSION 14
 
 struct ihipStream_t; /* the same incomplete type as HIP's hipStream_t */
 
@@ -97,7 +102,7 @@ typedef enum {
   SSM_ERR_ALIAS = 6,                /* an output overlaps an input           */
   SSM_ERR_HIP = 7,                  /* a HIP runtime call failed             */
   SSM_ERR_UNSUPPORTED = 8,          /* valid, but outside what this entry point implements */
-  SSM_ERR_WORKSPACE = 9             /* needs more scratch than the fixed device array holds */
+  SSM_ERR_WORKSPACE = 9             /* needs more scratch than its workspace, or the fixed device array, holds */
 } ssm_status_t;
 
 /*
@@ -464,6 +469,108 @@ ssm_status_t ssm_scan_bwd_complex(int64_t batch, int64_t dim, int64_t dstate, in
                                   const float* h0, const void* dy, const float* dlast, void* du, void* ddelta,
                                   float* dA, float* dB, float* dC, float* dD, void* dz, float* ddelta_bias,
                                   float* dh0, struct ihipStream_t* stream);
+
+/*
+ * Gated linear recurrence: one state per channel and a gate per (batch,
+ * channel, token), where the selective scan has dstate states per channel and
+ * B and C shared by the channels.  The pages set the SSM beside gated
+ * recurrences (the Chinese explainer's section on Delta as a gate: a large
+ * step resets the state, a small one keeps it); this is that recurrence with
+ * the gate as an input of its own.
+ *
+ *   v_l = gate[b,d,l] + gate_bias[d]            s_l = sigmoid(v_l)
+ *   a_l = s_l, or exp(-rate[d] * s_l) when rate is not NULL
+ *   w_l = 1 (SSM_GATED_PLAIN), 1 - a_l (SSM_GATED_CONVEX),
+ *         sqrt(1 - a_l^2) (SSM_GATED_NORM)
+ *   h_l = a_l h_{l-1} + w_l x[b,d,l]            (w_l x[b,d,l] where reset[b,l] != 0)
+ *   y[b,d,l] = h_l * silu(z[b,d,l])             (h_l without z)
+ *
+ * A reset starts a packed sequence: the state before it is dropped, whatever
+ * its value (infinities and NaN too); w_l keeps the token's own gate.  A gate
+ * whose a_l is exactly 0 drops the state in the same way.  rate must not be
+ * negative (a_l <= 1).
+ *
+ * The state and all arithmetic are fp32.
+ */
+typedef enum {
+  SSM_GATED_PLAIN = 0,  /* w = 1           */
+  SSM_GATED_CONVEX = 1, /* w = 1 - a       */
+  SSM_GATED_NORM = 2    /* w = sqrt(1-a^2) */
+} ssm_gated_mode_t;
+
+/*
+ * ssm_gated_scan_fwd -- the recurrence over a whole sequence.
+ *
+ *   x, gate    [batch, dim, seqlen]     io
+ *   gate_bias  [dim]                    fp32   may be NULL (0)
+ *   rate       [dim]                    fp32   may be NULL (a = s)
+ *   z          [batch, dim, seqlen]     io     may be NULL (no output gate)
+ *   reset      [batch, seqlen]          bytes  may be NULL; nonzero where the state is dropped
+ *   h0         [batch, dim]             fp32   may be NULL (0); may be the same pointer as last_state
+ *   y          [batch, dim, seqlen]     io     written
+ *   last_state [batch, dim]             fp32   written when not NULL
+ *   ckpt       [batch, dim, ceil(seqlen/128)] fp32  written when not NULL: the state before tokens
+ *                                              0, 128, 256, ..., which ssm_gated_scan_bwd reads
+ *
+ * Any sizes >= 1 and any element-aligned pointers; rows of 2^30 tokens or
+ * more are SSM_ERR_UNSUPPORTED, as is a mode outside ssm_gated_mode_t.  No
+ * output may overlap an input or another output, except last_state == h0.
+ * Allocates nothing; deterministic.
+ */
+ssm_status_t ssm_gated_scan_fwd(int64_t batch, int64_t dim, int64_t seqlen, ssm_dtype_t io, ssm_gated_mode_t mode,
+                                const void* x, const void* gate, const float* gate_bias, const float* rate,
+                                const void* z, const uint8_t* reset, const float* h0, void* y, float* last_state,
+                                float* ckpt, struct ihipStream_t* stream);
+
+/*
+ * ssm_gated_scan_bwd -- every gradient of sum(dy * y) + sum(dlast * last_state)
+ * for ssm_gated_scan_fwd.  The states are recomputed in fp32 from the
+ * checkpoints the forward wrote (for the same x .. h0; h0 itself is not read).
+ *
+ *   lambda_l = dy_l silu(z_l) + a_{l+1} lambda_{l+1}   (0 after a token before a reset; + dlast at the end)
+ *   dx = lambda w;  dL/da = lambda (h_{l-1} + x dw/da)  (h_{l-1} = 0 at a reset)
+ *   dgate = dL/da da/dv;  dgate_bias[d] = sum_{b,l} dgate;  drate[d] = sum_{b,l} dL/da da/drate
+ *   dz = dy h silu'(z);   dh0 = a_0 lambda_0
+ *
+ *   x .. reset                          as ssm_gated_scan_fwd
+ *   ckpt       [batch, dim, ceil(seqlen/128)] fp32  read
+ *   dy         [batch, dim, seqlen]     io
+ *   dlast      [batch, dim]             fp32   may be NULL (0)
+ *   dx, dgate  [batch, dim, seqlen]     io     written
+ *   dgate_bias [dim]                    fp32   written when not NULL
+ *   drate      [dim]                    fp32   written when rate and drate are not NULL
+ *   dz         [batch, dim, seqlen]     io     written when z and dz are not NULL
+ *   dh0        [batch, dim]             fp32   written when not NULL (the gradient at h0 = 0 without one)
+ *   workspace                           device memory, 4-byte aligned, of ssm_gated_scan_bwd_workspace_bytes
+ *                                       bytes (may be NULL when that is 0); overwritten
+ *
+ * Errors as ssm_gated_scan_fwd; SSM_ERR_WORKSPACE when workspace_bytes is too
+ * small.  Allocates nothing.  dgate_bias and drate are fixed-order sums, so the
+ * result is deterministic.  Calls that overlap in time need workspaces of
+ * their own.
+ */
+ssm_status_t ssm_gated_scan_bwd(int64_t batch, int64_t dim, int64_t seqlen, ssm_dtype_t io, ssm_gated_mode_t mode,
+                                const void* x, const void* gate, const float* gate_bias, const float* rate,
+                                const void* z, const uint8_t* reset, const float* ckpt, const void* dy,
+                                const float* dlast, void* dx, void* dgate, float* dgate_bias, float* drate, void* dz,
+                                float* dh0, void* workspace, int64_t workspace_bytes, struct ihipStream_t* stream);
+
+/* Bytes of workspace ssm_gated_scan_bwd takes for these sizes; bytes may be NULL. */
+ssm_status_t ssm_gated_scan_bwd_workspace_bytes(int64_t batch, int64_t dim, int64_t seqlen, ssm_dtype_t io,
+                                                int64_t* bytes);
+
+/*
+ * ssm_gated_state_update -- one decode step of the gated recurrence: equals
+ * ssm_gated_scan_fwd with seqlen = 1 and h0 = last_state = state.
+ *
+ *   state      [batch, dim]  fp32  read, then overwritten
+ *   x, gate, z [batch, dim]  io    z may be NULL
+ *   gate_bias, rate [dim]    fp32  may be NULL
+ *   y          [batch, dim]  io    written; must not overlap any input or state
+ */
+ssm_status_t ssm_gated_state_update(int64_t batch, int64_t dim, ssm_dtype_t io, ssm_gated_mode_t mode, float* state,
+                                    const void* x, const void* gate, const float* gate_bias, const float* rate,
+                                    const void* z, void* y, struct ihipStream_t* stream);
 
 /* Kernel paths of ssm_scan_fwd (reported by ssm_scan_fwd_plan). */
 typedef enum {

@@ -8,6 +8,7 @@ include/ssm_scan.h.  There is no fallback: if the library is missing the
 import fails with an error that says how to build it.
 """
 import ctypes
+import functools
 import os
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -30,7 +31,13 @@ STATUS_NAMES = {
     6: "SSM_ERR_ALIAS",
     7: "SSM_ERR_HIP",
     8: "SSM_ERR_UNSUPPORTED",
+    9: "SSM_ERR_WORKSPACE",
 }
+
+# ssm_gated_mode_t: the input weight of the gated recurrence.
+GATED_MODES = {"plain": 0, "convex": 1, "norm": 2}
+# Tokens between the checkpoints of gated_scan_fwd_save.
+GATED_CKPT_STEP = 128
 
 # Every symbol the header declares, with its ctypes signature.
 _I64 = ctypes.c_int64
@@ -62,6 +69,11 @@ SIGNATURES = {
                               ctypes.POINTER(_I64), ctypes.POINTER(_I64)]),
     "ssm_scan_fwd_plan_ex": (_I, [_I64, _I64, _I64, _I64, _I, _I, _I64, ctypes.POINTER(_I), ctypes.POINTER(_I64),
                                  ctypes.POINTER(_I64), ctypes.POINTER(_I64)]),
+    "ssm_gated_scan_fwd": (_I, [_I64, _I64, _I64, _I, _I, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P]),
+    "ssm_gated_scan_bwd": (_I, [_I64, _I64, _I64, _I, _I, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P,
+                                _P, _I64, _P]),
+    "ssm_gated_scan_bwd_workspace_bytes": (_I, [_I64, _I64, _I64, _I, ctypes.POINTER(_I64)]),
+    "ssm_gated_state_update": (_I, [_I64, _I64, _I, _I, _P, _P, _P, _P, _P, _P, _P, _P]),
     "ssm_status_string": (ctypes.c_char_p, [_I]),
     "ssm_last_hip_error": (_I, []),
     "ssm_abi_version": (_I, []),
@@ -642,4 +654,178 @@ def _state_update(disc, state, u, delta, A, B, C, D, z, delta_bias, delta_softpl
         _check("ssm_state_update", lib.ssm_state_update(batch, dim, dstate, _io_code(io), *tail))
     else:
         _check("ssm_state_update_ex", lib.ssm_state_update_ex(batch, dim, dstate, _io_code(io), disc, *tail))
+    return out
+
+
+def _placed(fn):
+    """Runs fn with its first argument's device current, on the caller's stream.
+
+    Without a stream, that is the device's current stream.  With one, the
+    outputs and the workspace are allocated on it (so that freed memory is
+    handed on in its order), and the tensors passed in are recorded on it.
+    """
+    @functools.wraps(fn)
+    def call(first, *args, stream=None, **kw):
+        import torch
+        if not first.is_cuda:
+            raise ValueError("%s: tensors must be on a GPU, got %s" % (fn.__name__, first.device))
+        if stream is None and first.device.index == torch.cuda.current_device():
+            return fn(first, *args, **kw)
+        with torch.cuda.device(first.device):
+            if stream is None:
+                return fn(first, *args, **kw)
+            with torch.cuda.stream(stream):
+                for t in (first,) + args + tuple(kw.values()):
+                    if isinstance(t, torch.Tensor):
+                        t.record_stream(stream)
+                return fn(first, *args, **kw)
+    return call
+
+
+def _mode_code(mode):
+    if mode not in GATED_MODES:
+        raise ValueError("mode must be one of %s" % sorted(GATED_MODES))
+    return GATED_MODES[mode]
+
+
+def _gated_inputs(x, gate, gate_bias, rate, z, reset):
+    import torch
+    if x.dim() != 3:
+        raise ValueError("x must be (batch, dim, seqlen)")
+    shape, io, dev = x.shape, x.dtype, x.device
+    _need(x, "x", shape, io, dev)
+    _need(gate, "gate", shape, io, dev)
+    if gate_bias is not None:
+        _need(gate_bias, "gate_bias", shape[1:2], torch.float32, dev)
+    if rate is not None:
+        _need(rate, "rate", shape[1:2], torch.float32, dev)
+    if z is not None:
+        _need(z, "z", shape, io, dev)
+    if reset is not None:
+        _need(reset, "reset", (shape[0], shape[2]), torch.bool if reset.dtype == torch.bool else torch.uint8, dev)
+    return shape[0], shape[1], shape[2], io, dev
+
+
+def gated_ckpt_shape(batch, dim, seqlen):
+    """Shape of the float32 checkpoint tensor of gated_scan_fwd_save / gated_scan_bwd."""
+    return (batch, dim, (seqlen + GATED_CKPT_STEP - 1) // GATED_CKPT_STEP)
+
+
+@_placed
+def gated_scan_fwd(x, gate, gate_bias=None, rate=None, z=None, reset=None, h0=None, mode="plain", out=None,
+                   last_state=None, ckpt=None, return_last_state=True):
+    """Gated linear recurrence over the sequence (ssm_gated_scan_fwd); returns (y, last_state).
+
+    h_l = a_l h_{l-1} + w_l x_l with a = sigmoid(gate + gate_bias), or
+    exp(-rate * sigmoid(gate + gate_bias)) with a rate (>= 0), and w = 1
+    ("plain"), 1 - a ("convex") or sqrt(1 - a^2) ("norm"); y = h, or h * silu(z).
+
+    x, gate, z: (batch, dim, seqlen) in one io dtype (float32 or bfloat16);
+    gate_bias, rate: (dim,) float32; reset: (batch, seqlen) uint8 or bool,
+    nonzero where a sequence starts and the state before is dropped; h0:
+    (batch, dim) float32, which may be the same tensor as last_state.  y has
+    the io dtype; last_state is float32 (None when return_last_state is False).
+    ckpt, when given, receives the backward's checkpoints (gated_ckpt_shape).
+    stream (keyword): run on that torch.cuda.Stream instead of the current one.
+    """
+    import torch
+    batch, dim, seqlen, io, dev = _gated_inputs(x, gate, gate_bias, rate, z, reset)
+    code = _mode_code(mode)
+    if h0 is not None:
+        _need(h0, "h0", (batch, dim), torch.float32, dev)
+    if out is None:
+        out = torch.empty_like(x)
+    else:
+        _need(out, "out", x.shape, io, dev)
+    if last_state is not None:
+        _need(last_state, "last_state", (batch, dim), torch.float32, dev)
+    elif return_last_state:
+        last_state = torch.empty((batch, dim), dtype=torch.float32, device=dev)
+    if ckpt is not None:
+        _need(ckpt, "ckpt", gated_ckpt_shape(batch, dim, seqlen), torch.float32, dev)
+    st = load_library().ssm_gated_scan_fwd(batch, dim, seqlen, _io_code(io), code, _ptr(x), _ptr(gate),
+                                           _ptr(gate_bias), _ptr(rate), _ptr(z), _ptr(reset), _ptr(h0), _ptr(out),
+                                           _ptr(last_state), _ptr(ckpt), _stream(dev, None))
+    _check("ssm_gated_scan_fwd", st)
+    return out, last_state
+
+
+@_placed
+def gated_scan_fwd_save(x, gate, gate_bias=None, rate=None, z=None, reset=None, h0=None, mode="plain", out=None,
+                        last_state=None, ckpt=None):
+    """gated_scan_fwd that also writes the backward's checkpoints; returns (y, last_state, ckpt)."""
+    import torch
+    if ckpt is None:
+        if x.dim() != 3:
+            raise ValueError("x must be (batch, dim, seqlen)")
+        ckpt = torch.empty(gated_ckpt_shape(*x.shape), dtype=torch.float32, device=x.device)
+    out, last_state = gated_scan_fwd(x, gate, gate_bias, rate, z, reset, h0, mode, out, last_state, ckpt)
+    return out, last_state, ckpt
+
+
+@_placed
+def gated_scan_bwd(x, gate, dy, ckpt, gate_bias=None, rate=None, z=None, reset=None, dlast=None, mode="plain",
+                   need=("dgate_bias", "drate", "dz", "dh0")):
+    """Gradients of sum(dy * y) + sum(dlast * last_state) for gated_scan_fwd (ssm_gated_scan_bwd).
+
+    ckpt is what gated_scan_fwd_save wrote for the same x, gate, gate_bias,
+    rate, z, reset, h0 and mode.  Returns a dict: dx, dgate (io dtype) and, when
+    named in `need`, dgate_bias (dim,), drate (dim,, only with a rate) and dh0
+    (batch, dim) in float32 and dz (io dtype, only with z); None for the others.
+    """
+    import torch
+    batch, dim, seqlen, io, dev = _gated_inputs(x, gate, gate_bias, rate, z, reset)
+    code = _mode_code(mode)
+    f32 = torch.float32
+    _need(dy, "dy", x.shape, io, dev)
+    _need(ckpt, "ckpt", gated_ckpt_shape(batch, dim, seqlen), f32, dev)
+    if dlast is not None:
+        _need(dlast, "dlast", (batch, dim), f32, dev)
+    g = dict(dx=torch.empty_like(x), dgate=torch.empty_like(x),
+             dgate_bias=torch.empty(dim, dtype=f32, device=dev) if "dgate_bias" in need else None,
+             drate=torch.empty(dim, dtype=f32, device=dev) if ("drate" in need and rate is not None) else None,
+             dz=torch.empty_like(x) if ("dz" in need and z is not None) else None,
+             dh0=torch.empty((batch, dim), dtype=f32, device=dev) if "dh0" in need else None)
+    lib = load_library()
+    io_code = _io_code(io)
+    size = _I64(0)
+    _check("ssm_gated_scan_bwd_workspace_bytes",
+           lib.ssm_gated_scan_bwd_workspace_bytes(batch, dim, seqlen, io_code, ctypes.byref(size)))
+    work = torch.empty(size.value, dtype=torch.uint8, device=dev) if size.value else None
+    st = lib.ssm_gated_scan_bwd(batch, dim, seqlen, io_code, code, _ptr(x), _ptr(gate), _ptr(gate_bias), _ptr(rate),
+                                _ptr(z), _ptr(reset), _ptr(ckpt), _ptr(dy), _ptr(dlast), _ptr(g["dx"]),
+                                _ptr(g["dgate"]), _ptr(g["dgate_bias"]), _ptr(g["drate"]), _ptr(g["dz"]),
+                                _ptr(g["dh0"]), _ptr(work), size.value, _stream(dev, None))
+    _check("ssm_gated_scan_bwd", st)
+    return g
+
+
+@_placed
+def gated_state_update(state, x, gate, gate_bias=None, rate=None, z=None, mode="plain", out=None):
+    """One decode step (ssm_gated_state_update), updating state (batch, dim) float32 in place; returns y (batch, dim).
+
+    x, gate, z: (batch, dim) in one io dtype; gate_bias, rate, mode as gated_scan_fwd.
+    """
+    import torch
+    if state.dim() != 2:
+        raise ValueError("state must be (batch, dim)")
+    shape, io, dev = state.shape, x.dtype, state.device
+    code = _mode_code(mode)
+    _need(state, "state", shape, torch.float32, dev)
+    _need(x, "x", shape, io, dev)
+    _need(gate, "gate", shape, io, dev)
+    if gate_bias is not None:
+        _need(gate_bias, "gate_bias", shape[1:], torch.float32, dev)
+    if rate is not None:
+        _need(rate, "rate", shape[1:], torch.float32, dev)
+    if z is not None:
+        _need(z, "z", shape, io, dev)
+    if out is None:
+        out = torch.empty_like(x)
+    else:
+        _need(out, "out", shape, io, dev)
+    st = load_library().ssm_gated_state_update(shape[0], shape[1], _io_code(io), code, _ptr(state), _ptr(x),
+                                               _ptr(gate), _ptr(gate_bias), _ptr(rate), _ptr(z), _ptr(out),
+                                               _stream(dev, None))
+    _check("ssm_gated_state_update", st)
     return out

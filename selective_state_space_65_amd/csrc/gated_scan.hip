@@ -1,0 +1,888 @@
+// gated_scan.hip -- gated linear recurrence (one state per channel, a gate per
+// token): prefill, backward and decode step.  C ABI: include/ssm_scan.h.
+//
+//   h_l = a_l h_{l-1} + w_l x_l,   a from the gate, w from a (see the header)
+//
+// Each token is an affine map of the state, and maps compose:
+// (a2, b2) after (a1, b1) = (a1 a2, a2 b1 + b2).  A lane takes 8 consecutive
+// tokens of one channel (16 bytes of bf16, 32 of fp32) and reduces them to one
+// map; a group of G lanes covers a tile of 8 G tokens and scans its lanes'
+// maps by DPP; the state after the tile is the carry into the next.  From the
+// state before its chunk each lane then runs its 8 tokens again and stores y.
+// Every stream is read once and written once.
+//
+// The backward walks the tiles from the last to the first.  In a tile it
+// recomputes the states from the forward's checkpoint (one every 128 tokens)
+// and runs the adjoint lambda_l = q_l + a_{l+1} lambda_{l+1}, which is the same
+// kind of recurrence in the other direction: mu_l = a_l lambda_l is carried
+// from lane to lane by maps mu -> A mu + B and a suffix scan.
+//
+// A token with a = 0 (a reset, or a gate that underflows) drops the state
+// whatever its value, so 0 * Inf must not appear: a tile in which any lane of
+// the wave has such a token runs the selecting form of each step (kDrop), and
+// every other tile the plain one.  Products of many a's are kept at FLT_MIN or
+// above so that they cannot reach 0 by underflow and be taken for a drop.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cfloat>
+#include <cstdint>
+
+#include "device_common.h"
+#include "host_common.h"
+#include "rows.h"
+#include "ssm_scan.h"
+
+namespace {
+
+constexpr int kTok = 8;         // tokens per lane
+constexpr int kCkptStep = 128;  // tokens between checkpoints
+constexpr int kMaxWaves = 16;   // waves that share one channel
+
+struct GatedArgs {
+  const void* x;
+  const void* gate;
+  const float* gate_bias;  // may be null
+  const float* rate;       // read by the kRate kernels only
+  const void* z;           // may be null
+  const uint8_t* reset;    // may be null
+  const float* h0;         // may be null
+  void* y;
+  float* last;  // may be null
+  float* ckpt;  // may be null in the forward
+  // backward only
+  const void* dy;
+  const float* dlast;  // may be null
+  void* dx;
+  void* dgate;
+  void* dz;      // may be null
+  float* dbias;  // [batch][dim] sums per row, may be null
+  float* drate;  // [batch][dim], may be null
+  float* dh0;    // may be null
+  int64_t channels;  // batch * dim
+  int64_t dim;
+  int seqlen;
+  int ckpts;  // checkpoints per channel
+};
+
+// ---- affine maps h -> a h + b ------------------------------------------------
+
+struct Map {
+  float a, b;
+};
+
+template <bool kDrop>
+__device__ __forceinline__ float apply(Map m, float h) {
+  const float r = __builtin_fmaf(m.a, h, m.b);
+  if constexpr (kDrop) return m.a == 0.0f ? m.b : r;
+  return r;
+}
+
+// `late` after `early`.
+template <bool kDrop>
+__device__ __forceinline__ Map compose(Map late, Map early) {
+  Map r;
+  r.b = apply<kDrop>(late, early.b);
+  r.a = __builtin_fmaxf(late.a * early.a, FLT_MIN);
+  if constexpr (kDrop) r.a = (late.a == 0.0f || early.a == 0.0f) ? 0.0f : r.a;
+  return r;
+}
+
+// DPP move: lanes without a source lane, or in a row that row_mask leaves out, keep `keep`.
+template <int ctrl, int row_mask = 0xf>
+__device__ __forceinline__ float dpp(float keep, float src) {
+  return __int_as_float(
+      __builtin_amdgcn_update_dpp(__float_as_int(keep), __float_as_int(src), ctrl, row_mask, 0xf, false));
+}
+
+template <int ctrl, int row_mask = 0xf>
+__device__ __forceinline__ Map dpp(Map m) {
+  return Map{dpp<ctrl, row_mask>(1.0f, m.a), dpp<ctrl, row_mask>(0.0f, m.b)};
+}
+
+__device__ __forceinline__ float lane_of(float v, int l) {
+  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), l));
+}
+
+constexpr int kRowShl = 0x100, kRowShr = 0x110, kWaveShl1 = 0x130, kWaveShr1 = 0x138, kRowBcast15 = 0x142,
+              kRowBcast31 = 0x143, kRowNewBcast = 0x150;
+
+// One step of the in-row scan, for groups of G lanes: the map `s` lanes below
+// (up: above), the identity where that lane belongs to another group.
+template <int G, int s, bool kUp>
+__device__ __forceinline__ Map neighbour(Map m, int gl) {
+  Map e = dpp<(kUp ? kRowShl : kRowShr) + s>(m);
+  if constexpr (G < 16) {
+    const bool inside = kUp ? gl + s < G : gl >= s;
+    e.a = inside ? e.a : 1.0f;
+    e.b = inside ? e.b : 0.0f;
+  }
+  return e;
+}
+
+// Inclusive prefix over the group (tokens run with the lanes).
+template <int G, bool kDrop>
+__device__ __forceinline__ Map prefix(Map m, int gl) {
+  if constexpr (G >= 2) m = compose<kDrop>(m, neighbour<G, 1, false>(m, gl));
+  if constexpr (G >= 4) m = compose<kDrop>(m, neighbour<G, 2, false>(m, gl));
+  if constexpr (G >= 8) m = compose<kDrop>(m, neighbour<G, 4, false>(m, gl));
+  if constexpr (G >= 16) m = compose<kDrop>(m, neighbour<G, 8, false>(m, gl));
+  if constexpr (G == 64) {
+    m = compose<kDrop>(m, dpp<kRowBcast15, 0xa>(m));
+    m = compose<kDrop>(m, dpp<kRowBcast31, 0xc>(m));
+  }
+  return m;
+}
+
+// Inclusive suffix over the group (the adjoint runs against the lanes).  Rows
+// of 16 lanes by DPP; across the four rows of a wave the row totals (in each
+// row's first lane) are read into scalars.
+template <int G, bool kDrop>
+__device__ __forceinline__ Map suffix(Map m, int gl) {
+  if constexpr (G >= 2) m = compose<kDrop>(m, neighbour<G, 1, true>(m, gl));
+  if constexpr (G >= 4) m = compose<kDrop>(m, neighbour<G, 2, true>(m, gl));
+  if constexpr (G >= 8) m = compose<kDrop>(m, neighbour<G, 4, true>(m, gl));
+  if constexpr (G >= 16) m = compose<kDrop>(m, neighbour<G, 8, true>(m, gl));
+  if constexpr (G == 64) {
+    const Map r1{lane_of(m.a, 16), lane_of(m.b, 16)};
+    const Map r2{lane_of(m.a, 32), lane_of(m.b, 32)};
+    const Map r3{lane_of(m.a, 48), lane_of(m.b, 48)};
+    const Map r23 = compose<kDrop>(r2, r3);
+    const Map r123 = compose<kDrop>(r1, r23);
+    const int row = gl >> 4;
+    Map e;
+    e.a = row == 0 ? r123.a : row == 1 ? r23.a : row == 2 ? r3.a : 1.0f;
+    e.b = row == 0 ? r123.b : row == 1 ? r23.b : row == 2 ? r3.b : 0.0f;
+    m = compose<kDrop>(m, e);
+  }
+  return m;
+}
+
+// The value of the lane before (after) in the group; `edge` in its first (last) lane.
+template <int G>
+__device__ __forceinline__ float lane_before(float v, float edge, int gl) {
+  if constexpr (G == 1) return edge;
+  if constexpr (G == 64) return dpp<kWaveShr1>(edge, v);
+  const float r = dpp<kRowShr + 1>(edge, v);
+  return G < 16 && gl == 0 ? edge : r;
+}
+
+template <int G>
+__device__ __forceinline__ float lane_after(float v, float edge, int gl) {
+  if constexpr (G == 1) return edge;
+  if constexpr (G == 64) return dpp<kWaveShl1>(edge, v);
+  const float r = dpp<kRowShl + 1>(edge, v);
+  return G < 16 && gl == G - 1 ? edge : r;
+}
+
+// The value of the group's last (first) lane, in all its lanes.
+template <int G>
+__device__ __forceinline__ float last_lane(float v, int lane) {
+  if constexpr (G == 1) return v;
+  if constexpr (G == 64) return lane_of(v, 63);
+  if constexpr (G == 16) return dpp<kRowNewBcast + 15>(v, v);
+  return __shfl(v, lane | (G - 1));
+}
+
+template <int G>
+__device__ __forceinline__ float first_lane(float v, int lane) {
+  if constexpr (G == 1) return v;
+  if constexpr (G == 64) return lane_of(v, 0);
+  if constexpr (G == 16) return dpp<kRowNewBcast>(v, v);
+  return __shfl(v, lane & ~(G - 1));
+}
+
+// ---- the gate ----------------------------------------------------------------
+
+// Per-channel constants of the gate: -bias log2(e); with a rate, the rate and
+// -rate log2(e).
+struct GateParams {
+  float nb, rate, nr;
+};
+
+template <bool kRate>
+__device__ __forceinline__ GateParams gate_params(const float* gate_bias, const float* rate, int64_t d) {
+  GateParams p;
+  p.nb = gate_bias ? -gate_bias[d] * kLog2e : 0.0f;
+  p.rate = kRate ? rate[d] : 0.0f;
+  p.nr = -p.rate * kLog2e;
+  return p;
+}
+
+// 1 - e^-q.  Below 1/4 the difference would cancel; the series to q^6 is
+// within q^6/5040 < 5e-8 of it, relative to q.
+__device__ __forceinline__ float one_minus_exp(float q, float e) {
+  float p = __builtin_fmaf(q, -1.0f / 720.0f, 1.0f / 120.0f);
+  p = __builtin_fmaf(q, p, -1.0f / 24.0f);
+  p = __builtin_fmaf(q, p, 1.0f / 6.0f);
+  p = __builtin_fmaf(q, p, -0.5f);
+  p = __builtin_fmaf(q, p, 1.0f);
+  return __builtin_fabsf(q) < 0.25f ? q * p : 1.0f - e;
+}
+
+// s = sigmoid(v), t = 1 - s without cancellation, the decay a and om = 1 - a.
+// The select keeps e * s from being Inf * 0 where s underflows.
+struct Gate {
+  float s, t, a, om;
+};
+
+template <bool kRate>
+__device__ __forceinline__ Gate gate_of(float g, const GateParams& p) {
+  Gate r;
+  const float e = exp2_hw(__builtin_fmaf(g, -kLog2e, p.nb));
+  r.s = rcp_hw(1.0f + e);
+  r.t = r.s == 0.0f ? 1.0f : e * r.s;
+  if constexpr (kRate) {
+    r.a = exp2_hw(p.nr * r.s);
+    r.om = one_minus_exp(p.rate * r.s, r.a);
+  } else {
+    r.a = r.s;
+    r.om = r.t;
+  }
+  return r;
+}
+
+template <int kMode>
+__device__ __forceinline__ float input_weight(float a, float om) {
+  if constexpr (kMode == SSM_GATED_PLAIN) return 1.0f;
+  if constexpr (kMode == SSM_GATED_CONVEX) return om;
+  return __builtin_amdgcn_sqrtf(om * (1.0f + a));
+}
+
+__device__ __forceinline__ float sigmoid_f32(float z) { return rcp_hw(1.0f + exp2_hw(-z * kLog2e)); }
+
+// Bit j set where token t + j starts a sequence.
+__device__ __forceinline__ uint32_t reset_bits(const uint8_t* row, int t, int seqlen, bool full) {
+  uint32_t lo = 0, hi = 0;
+  if (full) {
+    load_bytes8(row + t, &lo, &hi);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (t + j < seqlen) lo |= (uint32_t)row[t + j] << (8 * j);
+      if (t + 4 + j < seqlen) hi |= (uint32_t)row[t + 4 + j] << (8 * j);
+    }
+  }
+  uint32_t bits = 0;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    bits |= ((lo >> (8 * j)) & 0xffu) ? 1u << j : 0u;
+    bits |= ((hi >> (8 * j)) & 0xffu) ? 16u << j : 0u;
+  }
+  return bits;
+}
+
+// Bits where the state is dropped: resets and gates that are exactly 0.
+__device__ __forceinline__ uint32_t drop_bits(const float a[kTok], uint32_t resets) {
+  float m = a[0];
+#pragma unroll
+  for (int j = 1; j < kTok; ++j) m = __builtin_fminf(m, a[j]);
+  if (__builtin_expect(__ballot(m == 0.0f) != 0, 0)) {
+#pragma unroll
+    for (int j = 0; j < kTok; ++j) resets |= a[j] == 0.0f ? 1u << j : 0u;
+  }
+  return resets;
+}
+
+// A lane's tokens as one map.
+template <bool kDrop>
+__device__ __forceinline__ Map chunk_map(const float a[kTok], const float b[kTok], uint32_t drop) {
+  Map m{a[0], b[0]};
+#pragma unroll
+  for (int j = 1; j < kTok; ++j) {
+    const float h = __builtin_fmaf(a[j], m.b, b[j]);
+    m.b = kDrop && (drop >> j & 1) ? b[j] : h;
+    m.a *= a[j];
+  }
+  m.a = __builtin_fmaxf(m.a, FLT_MIN);
+  if constexpr (kDrop) m.a = drop ? 0.0f : m.a;
+  return m;
+}
+
+template <bool kDrop>
+__device__ __forceinline__ float next_state(float a, float b, float h, uint32_t drop, int j) {
+  const float r = __builtin_fmaf(a, h, b);
+  return kDrop && (drop >> j & 1) ? b : r;
+}
+
+// ---- the forward -------------------------------------------------------------
+
+// The scan of one tile: chunk maps, the state before each lane's chunk, the
+// carry, and the checkpoints; on return h[j] holds the states of the lane's tokens.
+template <int G, bool kDrop>
+__device__ __forceinline__ void scan_tile(const float a[kTok], const float b[kTok], uint32_t drop, int lane, int gl,
+                                          int wave, int waves, Map* totals, float& carry, float h[kTok],
+                                          float& before) {
+  const Map m = prefix<G, kDrop>(chunk_map<kDrop>(a, b, drop), gl);
+  float in = carry;
+  if (G == 64 && waves > 1) {
+    // Each wave's total through LDS; every wave folds all of them, taking its
+    // own carry-in on the way.
+    if (lane == 63) totals[wave] = m;
+    lds_barrier();
+    float c = carry;
+    for (int w = 0; w < waves; ++w) {
+      if (w == wave) in = c;
+      c = apply<true>(totals[w], c);
+    }
+    carry = c;
+  } else {
+    carry = last_lane<G>(apply<kDrop>(m, in), lane);
+  }
+  before = lane_before<G>(apply<kDrop>(m, in), in, gl);
+  float s = before;
+#pragma unroll
+  for (int j = 0; j < kTok; ++j) {
+    s = next_state<kDrop>(a[j], b[j], s, drop, j);
+    h[j] = s;
+  }
+}
+
+// G lanes per channel.  G < 64: waves are independent, 64 / G channels each.
+// G = 64: a block owns one channel and its waves take consecutive tiles of 512
+// tokens, joined through LDS.
+template <typename IoT, int G, int kMode, bool kRate>
+__global__ __launch_bounds__(G == 64 ? 64 * kMaxWaves : 256) void gated_fwd_kernel(GatedArgs p) {
+  __shared__ Map totals[2][G == 64 ? kMaxWaves : 1];
+  const int lane = threadIdx.x & 63, gl = lane & (G - 1);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int waves = blockDim.x >> 6;
+  int64_t ch = G == 64 ? (int64_t)blockIdx.x : ((int64_t)blockIdx.x * waves + wave) * (64 / G) + lane / G;
+  const bool live = ch < p.channels;
+  ch = live ? ch : p.channels - 1;
+  const int64_t bt = ch / p.dim, d = ch - bt * p.dim;
+  const int L = p.seqlen;
+  const IoT* xr = static_cast<const IoT*>(p.x) + ch * L;
+  const IoT* gr = static_cast<const IoT*>(p.gate) + ch * L;
+  const IoT* zr = static_cast<const IoT*>(p.z) + (p.z ? ch * L : 0);
+  IoT* yr = static_cast<IoT*>(p.y) + ch * L;
+  const uint8_t* rr = p.reset + (p.reset ? bt * L : 0);
+  float* ck = p.ckpt + (p.ckpt ? ch * p.ckpts : 0);
+  const GateParams gp = gate_params<kRate>(p.gate_bias, p.rate, d);
+  float carry = p.h0 ? p.h0[ch] : 0.0f;
+  // last_state may be h0: every wave has its value before any wave can end.
+  if (G == 64 && waves > 1) __syncthreads();
+
+  constexpr int kTile = G * kTok;
+  const int step = G == 64 ? kTile * waves : kTile;
+  int parity = 0;
+  for (int base = 0; base < L; base += step, parity ^= 1) {
+    const int t0 = G == 64 ? base + wave * kTile : base;
+    const int t = t0 + gl * kTok;
+    const bool full = t0 + kTile <= L;  // uniform over the wave
+    float xv[kTok], gv[kTok], a[kTok], b[kTok], h[kTok];
+    load_row8(xr, t, L, full, xv);
+    load_row8(gr, t, L, full, gv);
+    uint32_t drop = p.reset ? reset_bits(rr, t, L, full) : 0;
+#pragma unroll
+    for (int j = 0; j < kTok; ++j) {
+      const Gate g = gate_of<kRate>(gv[j], gp);
+      a[j] = g.a;
+      b[j] = input_weight<kMode>(g.a, g.om) * xv[j];
+    }
+    if (!full) {  // tokens past the end leave the state as it is
+#pragma unroll
+      for (int j = 0; j < kTok; ++j) {
+        a[j] = t + j < L ? a[j] : 1.0f;
+        b[j] = t + j < L ? b[j] : 0.0f;
+      }
+    }
+    drop = drop_bits(a, drop);
+    float before;
+    if (__ballot(drop != 0))
+      scan_tile<G, true>(a, b, drop, lane, gl, wave, waves, totals[parity], carry, h, before);
+    else
+      scan_tile<G, false>(a, b, drop, lane, gl, wave, waves, totals[parity], carry, h, before);
+    if (p.ckpt && (t & (kCkptStep - 1)) == 0 && t < L && live) ck[t / kCkptStep] = before;
+    if (p.z) {
+      float zv[kTok];
+      load_row8(zr, t, L, full, zv);
+#pragma unroll
+      for (int j = 0; j < kTok; ++j) h[j] *= silu_f32(zv[j]);
+    }
+    if (live) store_row8(yr, t, L, full, h);
+  }
+  if (p.last && live && gl == 0 && wave == (G == 64 ? 0 : wave)) p.last[ch] = carry;
+}
+
+// ---- the backward ------------------------------------------------------------
+
+// One tile of the backward.  ds holds dy silu'(z) and becomes dz; with a rate,
+// dg comes back without its factor.
+template <int G, int kMode, bool kRate, bool kDrop>
+__device__ __forceinline__ void bwd_tile(const float x[kTok], const Gate g[kTok], const float q[kTok], float h_in,
+                                         uint32_t drop, int valid, int lane, int gl, int wave, int waves, Map* totals,
+                                         float& mu, float ds[kTok], float dx[kTok], float dg[kTok], float& sum_r) {
+  float a[kTok], b[kTok], w[kTok], hp[kTok];  // hp: the state before each token
+#pragma unroll
+  for (int j = 0; j < kTok; ++j) {
+    a[j] = g[j].a;
+    w[j] = input_weight<kMode>(g[j].a, g[j].om);
+    b[j] = w[j] * x[j];
+  }
+  // The states, from the state before the tile.
+  const Map f = prefix<G, kDrop>(chunk_map<kDrop>(a, b, drop), gl);
+  float s = lane_before<G>(apply<kDrop>(f, h_in), h_in, gl);
+#pragma unroll
+  for (int j = 0; j < kTok; ++j) {
+    hp[j] = s;
+    s = next_state<kDrop>(a[j], b[j], s, drop, j);
+    ds[j] *= s;
+  }
+  if (valid < kTok) {  // tokens past the end: no gradient, whatever the state
+#pragma unroll
+    for (int j = 0; j < kTok; ++j) hp[j] = j < valid ? hp[j] : 0.0f;
+  }
+  // The adjoint: mu_j = a_j lambda_j, lambda_j = q_j + mu_{j+1}, as the lane's
+  // map of the mu that enters from the right.
+  Map r{1.0f, 0.0f};
+#pragma unroll
+  for (int j = kTok - 1; j >= 0; --j) {
+    const float lam = r.b + q[j];
+    r.b = kDrop && (drop >> j & 1) ? 0.0f : a[j] * lam;
+    r.a *= a[j];
+  }
+  r.a = __builtin_fmaxf(r.a, FLT_MIN);
+  if constexpr (kDrop) r.a = drop ? 0.0f : r.a;
+  r = suffix<G, kDrop>(r, gl);
+  float in = mu;
+  if (G == 64 && waves > 1) {
+    if (lane == 0) totals[wave] = r;
+    lds_barrier();
+    float c = mu;
+    for (int v = waves - 1; v >= 0; --v) {
+      if (v == wave) in = c;
+      c = apply<true>(totals[v], c);
+    }
+    mu = c;
+  } else {
+    mu = first_lane<G>(apply<kDrop>(r, in), lane);
+  }
+  float m = lane_after<G>(apply<kDrop>(r, in), in, gl);
+  float tr = 0.0f;
+#pragma unroll
+  for (int j = kTok - 1; j >= 0; --j) {
+    const bool dropped = kDrop && (drop >> j & 1);
+    const float lam = q[j] + m;
+    dx[j] = lam * w[j];
+    float da = dropped ? 0.0f : hp[j];  // dL/da over lambda
+    if constexpr (kMode == SSM_GATED_CONVEX) da -= x[j];
+    if constexpr (kMode == SSM_GATED_NORM) {
+      // dw/da = -a / w; da/dv vanishes faster than w, so 0 where w underflows
+      const float slope = w[j] > 0.0f ? a[j] * rcp_hw(w[j]) : 0.0f;
+      da = __builtin_fmaf(-slope, x[j], da);
+    }
+    da *= lam;
+    const float st = g[j].s * g[j].t;
+    if constexpr (kRate) {
+      // da/dv = -rate a s t (the caller has the rate), da/drate = -a s
+      const float na = -da * a[j];
+      dg[j] = na * st;
+      tr = __builtin_fmaf(na, g[j].s, tr);
+    } else {
+      dg[j] = da * st;
+    }
+    m = dropped ? 0.0f : a[j] * lam;
+  }
+  sum_r += tr;
+}
+
+template <typename IoT, int G, int kMode, bool kRate>
+__global__ __launch_bounds__(G == 64 ? 512 : 256) void gated_bwd_kernel(GatedArgs p) {
+  __shared__ Map totals[2][G == 64 ? kMaxWaves : 1];
+  const int lane = threadIdx.x & 63, gl = lane & (G - 1);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int waves = blockDim.x >> 6;
+  int64_t ch = G == 64 ? (int64_t)blockIdx.x : ((int64_t)blockIdx.x * waves + wave) * (64 / G) + lane / G;
+  const bool live = ch < p.channels;
+  ch = live ? ch : p.channels - 1;
+  const int64_t bt = ch / p.dim, d = ch - bt * p.dim;
+  const int L = p.seqlen;
+  const IoT* xr = static_cast<const IoT*>(p.x) + ch * L;
+  const IoT* gr = static_cast<const IoT*>(p.gate) + ch * L;
+  const IoT* zr = static_cast<const IoT*>(p.z) + (p.z ? ch * L : 0);
+  const IoT* dyr = static_cast<const IoT*>(p.dy) + ch * L;
+  IoT* dxr = static_cast<IoT*>(p.dx) + ch * L;
+  IoT* dgr = static_cast<IoT*>(p.dgate) + ch * L;
+  IoT* dzr = static_cast<IoT*>(p.dz) + (p.dz ? ch * L : 0);
+  const uint8_t* rr = p.reset + (p.reset ? bt * L : 0);
+  const float* ck = p.ckpt + ch * p.ckpts;
+  const GateParams gp = gate_params<kRate>(p.gate_bias, p.rate, d);
+  float mu = p.dlast ? p.dlast[ch] : 0.0f;
+  float sum_b = 0.0f, sum_r = 0.0f;
+
+  constexpr int kTile = G * kTok;
+  const int step = G == 64 ? kTile * waves : kTile;
+  int parity = 0;
+  for (int base = (L - 1) / step * step; base >= 0; base -= step, parity ^= 1) {
+    const int t0 = G == 64 ? base + wave * kTile : base;
+    const int t = t0 + gl * kTok;
+    const bool full = t0 + kTile <= L;
+    const int valid = L - t;
+    float x[kTok], gv[kTok], q[kTok], ds[kTok], dx[kTok], dg[kTok];
+    Gate g[kTok];
+    load_row8(xr, t, L, full, x);
+    load_row8(gr, t, L, full, gv);
+    load_row8(dyr, t, L, full, q);
+    uint32_t drop = p.reset ? reset_bits(rr, t, L, full) : 0;
+    const float h_in = t0 < L ? ck[t0 / kCkptStep] : 0.0f;
+#pragma unroll
+    for (int j = 0; j < kTok; ++j) g[j] = gate_of<kRate>(gv[j], gp);
+    if (!full) {
+#pragma unroll
+      for (int j = 0; j < kTok; ++j) {
+        if (t + j >= L) g[j].a = 1.0f, g[j].om = 0.0f, g[j].t = 0.0f, g[j].s = 0.0f, x[j] = 0.0f, q[j] = 0.0f;
+      }
+    }
+    if (p.z) {
+      float zv[kTok];
+      load_row8(zr, t, L, full, zv);
+#pragma unroll
+      for (int j = 0; j < kTok; ++j) {
+        const float sg = sigmoid_f32(zv[j]);
+        const float sz = zv[j] * sg;
+        ds[j] = q[j] * __builtin_fmaf(sz, 1.0f - sg, sg);  // dy silu'(z)
+        q[j] *= sz;
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < kTok; ++j) ds[j] = 0.0f;
+    }
+    {
+      float a[kTok];
+#pragma unroll
+      for (int j = 0; j < kTok; ++j) a[j] = g[j].a;
+      drop = drop_bits(a, drop);
+    }
+    if (__ballot(drop != 0))
+      bwd_tile<G, kMode, kRate, true>(x, g, q, h_in, drop, valid, lane, gl, wave, waves, totals[parity], mu, ds, dx,
+                                      dg, sum_r);
+    else
+      bwd_tile<G, kMode, kRate, false>(x, g, q, h_in, drop, valid, lane, gl, wave, waves, totals[parity], mu, ds, dx,
+                                       dg, sum_r);
+    float tb = 0.0f;
+#pragma unroll
+    for (int j = 0; j < kTok; ++j) {
+      if constexpr (kRate) dg[j] *= gp.rate;
+      tb += dg[j];
+    }
+    sum_b += tb;
+    if (live) {
+      store_row8(dxr, t, L, full, dx);
+      store_row8(dgr, t, L, full, dg);
+      if (p.dz) store_row8(dzr, t, L, full, ds);
+    }
+  }
+  // Row sums: over the group's lanes, then over the block's waves.
+#pragma unroll
+  for (int s = 1; s < G; s <<= 1) {
+    sum_b += __shfl_xor(sum_b, s);
+    if constexpr (kRate) sum_r += __shfl_xor(sum_r, s);
+  }
+  if constexpr (G == 64) {
+    if (waves > 1) {
+      lds_barrier();  // the last tile's totals have been read
+      if (lane == 0) totals[0][wave] = Map{sum_b, sum_r};
+      lds_barrier();
+      sum_b = sum_r = 0.0f;
+      for (int w = 0; w < waves; ++w) {
+        sum_b += totals[0][w].a;
+        sum_r += totals[0][w].b;
+      }
+      if (wave != 0) return;
+    }
+  }
+  if (live && gl == 0) {
+    if (p.dh0) p.dh0[ch] = mu;
+    if (p.dbias) p.dbias[ch] = sum_b;
+    if (kRate && p.drate) p.drate[ch] = sum_r;
+  }
+}
+
+// out[d] = sum over the batch rows, in order.
+__global__ __launch_bounds__(256) void gated_bwd_reduce_kernel(const float* bias_part, const float* rate_part,
+                                                               float* dbias, float* drate, int64_t batch,
+                                                               int64_t dim) {
+  const int64_t d = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (d >= dim) return;
+  float sb = 0.0f, sr = 0.0f;
+  for (int64_t b = 0; b < batch; ++b) {
+    if (dbias) sb += bias_part[b * dim + d];
+    if (drate) sr += rate_part[b * dim + d];
+  }
+  if (dbias) dbias[d] = sb;
+  if (drate) drate[d] = sr;
+}
+
+// ---- the decode step ---------------------------------------------------------
+
+struct StepArgs {
+  float* state;
+  const void* x;
+  const void* gate;
+  const float* gate_bias;
+  const float* rate;
+  const void* z;
+  void* y;
+  int64_t dim;
+  int blocks_per_row;
+};
+
+// V channels per thread (4: dim a multiple of 4, so they are of one batch row
+// and whole; 1: any dim).
+template <typename IoT, int V, int kMode, bool kRate>
+__global__ __launch_bounds__(256) void gated_step_kernel(StepArgs p) {
+  const int row = blockIdx.x / p.blocks_per_row;
+  const int64_t d = ((int64_t)(blockIdx.x - row * p.blocks_per_row) * blockDim.x + threadIdx.x) * V;
+  if (d >= p.dim) return;
+  const int64_t i = row * p.dim + d;
+  float x[V], g[V], z[V], h[V], y[V];
+  load_n<V>(static_cast<const IoT*>(p.x) + i, x);
+  load_n<V>(static_cast<const IoT*>(p.gate) + i, g);
+  load_n<V>(p.state + i, h);
+  if (p.z) load_n<V>(static_cast<const IoT*>(p.z) + i, z);
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    const GateParams gp = gate_params<kRate>(p.gate_bias, p.rate, d + j);
+    const Gate gt = gate_of<kRate>(g[j], gp);
+    const float b = input_weight<kMode>(gt.a, gt.om) * x[j];
+    h[j] = gt.a == 0.0f ? b : __builtin_fmaf(gt.a, h[j], b);
+    y[j] = p.z ? h[j] * silu_f32(z[j]) : h[j];
+  }
+  store_n<V>(p.state + i, h);
+  store_n<V>(static_cast<IoT*>(p.y) + i, y);
+}
+
+// ---- host side ---------------------------------------------------------------
+
+constexpr int64_t kMaxSeqlen = (int64_t)1 << 30;  // token offsets in a row fit an int
+
+struct GatedShape {
+  int64_t bd, bdl, ckpts, row_bytes;
+};
+
+ssm_status_t gated_shape(int64_t batch, int64_t dim, int64_t seqlen, ssm_dtype_t io, GatedShape* s) {
+  if (io != SSM_F32 && io != SSM_BF16) return SSM_ERR_DTYPE;
+  if (batch < 1 || dim < 1 || seqlen < 1) return SSM_ERR_SHAPE;
+  int64_t bytes;
+  if (!mul_ok(batch, dim, &s->bd) || !mul_ok(s->bd, seqlen, &s->bdl) || !mul_ok(s->bdl, 8, &bytes) ||
+      !mul_ok(s->bd, 64, &bytes) || !mul_ok(batch, seqlen, &bytes))
+    return SSM_ERR_SHAPE;
+  if (seqlen >= kMaxSeqlen || s->bd >= ((int64_t)1 << 31)) return SSM_ERR_UNSUPPORTED;
+  s->ckpts = (seqlen + kCkptStep - 1) / kCkptStep;
+  s->row_bytes = s->bdl * (int64_t)io_size(io);
+  return SSM_OK;
+}
+
+bool gated_mode_ok(ssm_gated_mode_t mode) {
+  return mode == SSM_GATED_PLAIN || mode == SSM_GATED_CONVEX || mode == SSM_GATED_NORM;
+}
+
+
+struct GatedPlan {
+  int group;     // lanes per channel
+  int threads;   // per block
+  int64_t blocks;
+};
+
+// Lanes per channel.  Rows of at most 8 (64) tokens fit one lane (8 lanes).
+// Longer rows take 16 lanes, four channels to a wave, while those waves fill
+// the chip; with fewer channels a block of 64 * W lanes takes one channel.
+GatedPlan gated_plan(int64_t channels, int64_t seqlen, int max_waves) {
+  GatedPlan p;
+  if (seqlen <= kTok) {
+    p.group = 1;
+  } else if (seqlen <= 8 * kTok) {
+    p.group = 8;
+  } else if (seqlen <= 16 * kTok || channels >= 8192) {
+    p.group = 16;
+  } else {
+    p.group = 64;
+    int64_t waves = 1;
+    while (waves < max_waves && channels * waves < 8192 && waves * 64 * kTok < seqlen) waves *= 2;
+    p.threads = (int)(64 * waves);
+    p.blocks = channels;
+    return p;
+  }
+  p.threads = 256;
+  const int64_t per_block = 256 / p.group;
+  p.blocks = (channels + per_block - 1) / per_block;
+  return p;
+}
+
+template <typename IoT, int kMode, bool kRate, bool kBwd>
+hipError_t launch_gated(const GatedArgs& a, hipStream_t st) {
+  const GatedPlan p = gated_plan(a.channels, a.seqlen, kBwd ? 8 : kMaxWaves);
+  const dim3 grid((unsigned)p.blocks), block(p.threads);
+#define SSM_GATED_LAUNCH(G)                                                                          \
+  if constexpr (kBwd)                                                                                \
+    hipLaunchKernelGGL((gated_bwd_kernel<IoT, G, kMode, kRate>), grid, block, 0, st, a);             \
+  else                                                                                               \
+    hipLaunchKernelGGL((gated_fwd_kernel<IoT, G, kMode, kRate>), grid, block, 0, st, a);             \
+  break
+  switch (p.group) {
+    case 1: SSM_GATED_LAUNCH(1);
+    case 8: SSM_GATED_LAUNCH(8);
+    case 16: SSM_GATED_LAUNCH(16);
+    default: SSM_GATED_LAUNCH(64);
+  }
+#undef SSM_GATED_LAUNCH
+  return hipGetLastError();
+}
+
+template <typename IoT, bool kBwd>
+hipError_t launch_gated(const GatedArgs& a, ssm_gated_mode_t mode, hipStream_t st) {
+  switch (mode) {
+    case SSM_GATED_PLAIN:
+      return a.rate ? launch_gated<IoT, SSM_GATED_PLAIN, true, kBwd>(a, st)
+                    : launch_gated<IoT, SSM_GATED_PLAIN, false, kBwd>(a, st);
+    case SSM_GATED_CONVEX:
+      return a.rate ? launch_gated<IoT, SSM_GATED_CONVEX, true, kBwd>(a, st)
+                    : launch_gated<IoT, SSM_GATED_CONVEX, false, kBwd>(a, st);
+    default:
+      return a.rate ? launch_gated<IoT, SSM_GATED_NORM, true, kBwd>(a, st)
+                    : launch_gated<IoT, SSM_GATED_NORM, false, kBwd>(a, st);
+  }
+}
+
+template <typename IoT, int V>
+hipError_t launch_step(const StepArgs& a, ssm_gated_mode_t mode, unsigned blocks, int threads, hipStream_t st) {
+#define SSM_GATED_STEP(M)                                                                                  \
+  if (a.rate)                                                                                              \
+    hipLaunchKernelGGL((gated_step_kernel<IoT, V, M, true>), dim3(blocks), dim3(threads), 0, st, a);       \
+  else                                                                                                     \
+    hipLaunchKernelGGL((gated_step_kernel<IoT, V, M, false>), dim3(blocks), dim3(threads), 0, st, a);      \
+  break
+  switch (mode) {
+    case SSM_GATED_PLAIN: SSM_GATED_STEP(SSM_GATED_PLAIN);
+    case SSM_GATED_CONVEX: SSM_GATED_STEP(SSM_GATED_CONVEX);
+    default: SSM_GATED_STEP(SSM_GATED_NORM);
+  }
+#undef SSM_GATED_STEP
+  return hipGetLastError();
+}
+
+GatedArgs gated_args(const GatedShape& s, int64_t dim, int64_t seqlen, const void* x, const void* gate,
+                     const float* gate_bias, const float* rate, const void* z, const uint8_t* reset) {
+  GatedArgs a{};
+  a.x = x; a.gate = gate; a.gate_bias = gate_bias; a.rate = rate; a.z = z; a.reset = reset;
+  a.channels = s.bd; a.dim = dim; a.seqlen = (int)seqlen; a.ckpts = (int)s.ckpts;
+  return a;
+}
+
+// Workspace of the backward: dgate_bias and drate sums per batch row.  With
+// one batch row the kernel writes the sums themselves.
+int64_t bwd_workspace(const GatedShape& s, int64_t batch) { return batch > 1 ? 2 * s.bd * 4 : 0; }
+
+}  // namespace
+
+// ----------------------------------------------------------------------------
+// C ABI
+// ----------------------------------------------------------------------------
+
+extern "C" {
+
+ssm_status_t ssm_gated_scan_fwd(int64_t batch, int64_t dim, int64_t seqlen, ssm_dtype_t io, ssm_gated_mode_t mode,
+                                const void* x, const void* gate, const float* gate_bias, const float* rate,
+                                const void* z, const uint8_t* reset, const float* h0, void* y, float* last_state,
+                                float* ckpt, struct ihipStream_t* stream) {
+  GatedShape s;
+  ssm_status_t st = gated_shape(batch, dim, seqlen, io, &s);
+  if (st != SSM_OK) return st;
+  if (!gated_mode_ok(mode)) return SSM_ERR_UNSUPPORTED;
+  if (!x || !gate || !y) return SSM_ERR_NULL;
+  const size_t es = io_size(io);
+  const bool in_place = h0 && h0 == last_state;
+  const Buf ins[] = {{x, s.row_bytes, es}, {gate, s.row_bytes, es}, {z, s.row_bytes, es}, {gate_bias, dim * 4, 4},
+                     {rate, dim * 4, 4}, {reset, batch * seqlen, 1}, {in_place ? nullptr : h0, s.bd * 4, 4}};
+  const Buf outs[] = {{y, s.row_bytes, es}, {last_state, s.bd * 4, 4}, {ckpt, s.bd * s.ckpts * 4, 4}};
+  st = check_buffers(ins, 7, outs, 3);
+  if (st != SSM_OK) return st;
+  GatedArgs a = gated_args(s, dim, seqlen, x, gate, gate_bias, rate, z, reset);
+  a.h0 = h0; a.y = y; a.last = last_state; a.ckpt = ckpt;
+  hipStream_t hs = reinterpret_cast<hipStream_t>(stream);
+  hipError_t e = io == SSM_BF16 ? launch_gated<bf16_t, false>(a, mode, hs) : launch_gated<float, false>(a, mode, hs);
+  return e == hipSuccess ? SSM_OK : hip_fail(e);
+}
+
+ssm_status_t ssm_gated_scan_bwd_workspace_bytes(int64_t batch, int64_t dim, int64_t seqlen, ssm_dtype_t io,
+                                                int64_t* bytes) {
+  GatedShape s;
+  ssm_status_t st = gated_shape(batch, dim, seqlen, io, &s);
+  if (st == SSM_OK && bytes) *bytes = bwd_workspace(s, batch);
+  return st;
+}
+
+ssm_status_t ssm_gated_scan_bwd(int64_t batch, int64_t dim, int64_t seqlen, ssm_dtype_t io, ssm_gated_mode_t mode,
+                                const void* x, const void* gate, const float* gate_bias, const float* rate,
+                                const void* z, const uint8_t* reset, const float* ckpt, const void* dy,
+                                const float* dlast, void* dx, void* dgate, float* dgate_bias, float* drate, void* dz,
+                                float* dh0, void* workspace, int64_t workspace_bytes, struct ihipStream_t* stream) {
+  GatedShape s;
+  ssm_status_t st = gated_shape(batch, dim, seqlen, io, &s);
+  if (st != SSM_OK) return st;
+  if (!gated_mode_ok(mode)) return SSM_ERR_UNSUPPORTED;
+  if (!x || !gate || !ckpt || !dy || !dx || !dgate) return SSM_ERR_NULL;
+  if (!rate) drate = nullptr;
+  if (!z) dz = nullptr;
+  const int64_t need = bwd_workspace(s, batch);
+  if (workspace_bytes < need) return SSM_ERR_WORKSPACE;
+  if (need && !workspace) return SSM_ERR_NULL;
+  if (!need) workspace = nullptr;
+  const size_t es = io_size(io);
+  const Buf ins[] = {{x, s.row_bytes, es}, {gate, s.row_bytes, es}, {z, s.row_bytes, es}, {gate_bias, dim * 4, 4},
+                     {rate, dim * 4, 4}, {reset, batch * seqlen, 1}, {ckpt, s.bd * s.ckpts * 4, 4},
+                     {dy, s.row_bytes, es}, {dlast, s.bd * 4, 4}};
+  const Buf outs[] = {{dx, s.row_bytes, es}, {dgate, s.row_bytes, es}, {dz, s.row_bytes, es},
+                      {dgate_bias, dim * 4, 4}, {drate, dim * 4, 4}, {dh0, s.bd * 4, 4}, {workspace, need, 4}};
+  st = check_buffers(ins, 9, outs, 7);
+  if (st != SSM_OK) return st;
+  GatedArgs a = gated_args(s, dim, seqlen, x, gate, gate_bias, rate, z, reset);
+  a.ckpt = const_cast<float*>(ckpt);
+  a.dy = dy; a.dlast = dlast; a.dx = dx; a.dgate = dgate; a.dz = dz; a.dh0 = dh0;
+  float* part = static_cast<float*>(workspace);
+  a.dbias = dgate_bias ? (part ? part : dgate_bias) : nullptr;
+  a.drate = drate ? (part ? part + s.bd : drate) : nullptr;
+  hipStream_t hs = reinterpret_cast<hipStream_t>(stream);
+  hipError_t e = io == SSM_BF16 ? launch_gated<bf16_t, true>(a, mode, hs) : launch_gated<float, true>(a, mode, hs);
+  if (e == hipSuccess && part && (dgate_bias || drate)) {
+    hipLaunchKernelGGL(gated_bwd_reduce_kernel, dim3((unsigned)((dim + 255) / 256)), dim3(256), 0, hs, part,
+                       part + s.bd, dgate_bias, drate, batch, dim);
+    e = hipGetLastError();
+  }
+  return e == hipSuccess ? SSM_OK : hip_fail(e);
+}
+
+ssm_status_t ssm_gated_state_update(int64_t batch, int64_t dim, ssm_dtype_t io, ssm_gated_mode_t mode, float* state,
+                                    const void* x, const void* gate, const float* gate_bias, const float* rate,
+                                    const void* z, void* y, struct ihipStream_t* stream) {
+  GatedShape s;
+  ssm_status_t st = gated_shape(batch, dim, 1, io, &s);
+  if (st != SSM_OK) return st;
+  if (!gated_mode_ok(mode)) return SSM_ERR_UNSUPPORTED;
+  if (!state || !x || !gate || !y) return SSM_ERR_NULL;
+  const size_t es = io_size(io);
+  const Buf ins[] = {{x, s.row_bytes, es}, {gate, s.row_bytes, es}, {z, s.row_bytes, es}, {gate_bias, dim * 4, 4},
+                     {rate, dim * 4, 4}};
+  const Buf outs[] = {{y, s.row_bytes, es}, {state, s.bd * 4, 4}};
+  st = check_buffers(ins, 5, outs, 2);
+  if (st != SSM_OK) return st;
+  const int vec = dim % 4 == 0 ? 4 : 1;
+  const int64_t lanes = dim / vec;
+  const int threads = (int)std::min<int64_t>(256, (lanes + 63) / 64 * 64);
+  const int64_t per_row = (lanes + threads - 1) / threads;
+  if (batch * per_row >= ((int64_t)1 << 31)) return SSM_ERR_UNSUPPORTED;
+  StepArgs a;
+  a.state = state; a.x = x; a.gate = gate; a.gate_bias = gate_bias; a.rate = rate; a.z = z; a.y = y;
+  a.dim = dim; a.blocks_per_row = (int)per_row;
+  hipStream_t hs = reinterpret_cast<hipStream_t>(stream);
+  const unsigned blocks = (unsigned)(batch * per_row);
+  hipError_t e;
+  if (io == SSM_BF16)
+    e = vec == 4 ? launch_step<bf16_t, 4>(a, mode, blocks, threads, hs) : launch_step<bf16_t, 1>(a, mode, blocks, threads, hs);
+  else
+    e = vec == 4 ? launch_step<float, 4>(a, mode, blocks, threads, hs) : launch_step<float, 1>(a, mode, blocks, threads, hs);
+  return e == hipSuccess ? SSM_OK : hip_fail(e);
+}
+
+}  // extern "C"
