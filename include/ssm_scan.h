@@ -572,6 +572,78 @@ ssm_status_t ssm_gated_state_update(int64_t batch, int64_t dim, ssm_dtype_t io, 
                                     const void* x, const void* gate, const float* gate_bias, const float* rate,
                                     const void* z, void* y, struct ihipStream_t* stream);
 
+/*
+ * The norm in front of a block, with the residual add in front of the norm
+ * (the Chinese explainer's section on the Mamba block: norm and residual
+ * around the SSM).  For every row of dim numbers:
+ *
+ *   s    = x + residual                 (x without a residual), rounded to the residual's type
+ *   mean = sum(s) / dim                 (0 for SSM_NORM_RMS)
+ *   rstd = 1 / sqrt(sum((s - mean)^2) / dim + eps)
+ *   y    = (s - mean) * rstd * weight + bias
+ *
+ * The sums, mean and rstd are fp32; the variance is summed from s - mean.
+ */
+typedef enum {
+  SSM_NORM_LAYER = 0, /* mean subtracted */
+  SSM_NORM_RMS = 1    /* mean taken as 0 */
+} ssm_norm_t;
+
+/*
+ * ssm_norm_fwd
+ *
+ *   x          [rows, dim]  io
+ *   residual   [rows, dim]  res_io  may be NULL
+ *   weight     [dim]        fp32    may be NULL (1)
+ *   bias       [dim]        fp32    may be NULL (0)
+ *   y          [rows, dim]  io      written
+ *   s          [rows, dim]  res_io  written when not NULL; needs a residual, and may be the same
+ *                                   pointer as residual (the residual stream is then updated in place)
+ *   mean, rstd [rows]       fp32    written when not NULL (mean: SSM_NORM_LAYER only)
+ *
+ * res_io is io or SSM_F32 (SSM_ERR_DTYPE otherwise); without a residual it
+ * must be io.  dim up to 32768 (larger is SSM_ERR_UNSUPPORTED, as is a kind
+ * outside ssm_norm_t), any rows >= 1, any element-aligned pointers.  No output
+ * may overlap an input or another output, except s == residual.  Allocates
+ * nothing; deterministic.
+ */
+ssm_status_t ssm_norm_fwd(int64_t rows, int64_t dim, ssm_dtype_t io, ssm_dtype_t res_io, ssm_norm_t kind,
+                          const void* x, const void* residual, const float* weight, const float* bias, float eps,
+                          void* y, void* s, float* mean, float* rstd, struct ihipStream_t* stream);
+
+/*
+ * ssm_norm_bwd -- every gradient of sum(dy * y) + sum(ds_out * s) for
+ * ssm_norm_fwd: with g = dy * weight and n = (s - mean) * rstd,
+ *
+ *   ds = rstd (g - sum(g) / dim - n sum(g n) / dim) + ds_out    (sum(g) for SSM_NORM_LAYER only)
+ *   dweight = sum over rows of dy * n;   dbias = sum over rows of dy
+ *
+ * ds is the gradient of x and of the residual alike.
+ *
+ *   dy         [rows, dim]  io
+ *   s          [rows, dim]  res_io  what the forward normalised (its s, or x without a residual)
+ *   weight     [dim]        fp32    may be NULL (1)
+ *   mean, rstd [rows]       fp32    as the forward wrote them (mean: SSM_NORM_LAYER only)
+ *   ds_out     [rows, dim]  res_io  the gradient that reaches s past the norm, may be NULL (0)
+ *   dx         [rows, dim]  io      ds, written
+ *   dresidual  [rows, dim]  res_io  ds, written when not NULL (dx in another type)
+ *   dweight, dbias [dim]    fp32    written when not NULL
+ *   workspace                       device memory, 4-byte aligned, of ssm_norm_bwd_workspace_bytes bytes
+ *                                   (may be NULL when neither dweight nor dbias is asked for); overwritten
+ *
+ * Errors as ssm_norm_fwd; SSM_ERR_WORKSPACE when workspace_bytes is too small.
+ * Allocates nothing; dweight and dbias are fixed-order sums, so the result is
+ * deterministic.  Calls that overlap in time need workspaces of their own.
+ */
+ssm_status_t ssm_norm_bwd(int64_t rows, int64_t dim, ssm_dtype_t io, ssm_dtype_t res_io, ssm_norm_t kind,
+                          const void* dy, const void* s, const float* weight, const float* mean, const float* rstd,
+                          const void* ds_out, void* dx, void* dresidual, float* dweight, float* dbias,
+                          void* workspace, int64_t workspace_bytes, struct ihipStream_t* stream);
+
+/* Bytes of workspace ssm_norm_bwd takes for these sizes when it sums dweight or dbias; bytes may be NULL. */
+ssm_status_t ssm_norm_bwd_workspace_bytes(int64_t rows, int64_t dim, ssm_dtype_t io, ssm_dtype_t res_io,
+                                          int64_t* bytes);
+
 /* Kernel paths of ssm_scan_fwd (reported by ssm_scan_fwd_plan). */
 typedef enum {
   SSM_PATH_SPLIT = 0,     /* one pass; a block owns 64 channels, its waves split the states */

@@ -36,6 +36,8 @@ STATUS_NAMES = {
 
 # ssm_gated_mode_t: the input weight of the gated recurrence.
 GATED_MODES = {"plain": 0, "convex": 1, "norm": 2}
+# ssm_norm_t: layer norm, or RMS norm (no mean).
+NORM_KINDS = {"layer": 0, "rms": 1}
 # Tokens between the checkpoints of gated_scan_fwd_save.
 GATED_CKPT_STEP = 128
 
@@ -74,6 +76,9 @@ SIGNATURES = {
                                 _P, _I64, _P]),
     "ssm_gated_scan_bwd_workspace_bytes": (_I, [_I64, _I64, _I64, _I, ctypes.POINTER(_I64)]),
     "ssm_gated_state_update": (_I, [_I64, _I64, _I, _I, _P, _P, _P, _P, _P, _P, _P, _P]),
+    "ssm_norm_fwd": (_I, [_I64, _I64, _I, _I, _I, _P, _P, _P, _P, ctypes.c_float, _P, _P, _P, _P, _P]),
+    "ssm_norm_bwd": (_I, [_I64, _I64, _I, _I, _I, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _I64, _P]),
+    "ssm_norm_bwd_workspace_bytes": (_I, [_I64, _I64, _I, _I, ctypes.POINTER(_I64)]),
     "ssm_status_string": (ctypes.c_char_p, [_I]),
     "ssm_last_hip_error": (_I, []),
     "ssm_abi_version": (_I, []),
@@ -829,3 +834,119 @@ def gated_state_update(state, x, gate, gate_bias=None, rate=None, z=None, mode="
                                                _stream(dev, None))
     _check("ssm_gated_state_update", st)
     return out
+
+
+def _kind_code(kind):
+    if kind not in NORM_KINDS:
+        raise ValueError("kind must be one of %s" % sorted(NORM_KINDS))
+    return NORM_KINDS[kind]
+
+
+def _need_residual(t, name, shape, io, device):
+    """A tensor of the residual stream: the io dtype, or float32."""
+    import torch
+    _need(t, name, shape, io if t.dtype == io else torch.float32, device)
+
+
+@_placed
+def norm_fwd(x, weight=None, bias=None, residual=None, eps=1e-5, kind="layer", out=None, residual_out=None,
+             save_stats=True):
+    """Norm over the last dimension with the residual add in front (ssm_norm_fwd); returns (y, s, mean, rstd).
+
+    s = x + residual, rounded to the residual's dtype (s is x without a
+    residual); y = (s - mean) * rstd * weight + bias for kind "layer", and
+    with mean 0 for kind "rms".  x: (..., dim) in float32 or bfloat16;
+    residual: the same shape, in x's dtype or float32; weight, bias: (dim,)
+    float32.  residual_out may be the residual itself, which is then updated
+    in place.  mean and rstd are float32 (...,) for norm_bwd: None without
+    save_stats, and mean None for "rms".
+    stream (keyword): run on that torch.cuda.Stream instead of the current one.
+    """
+    import torch
+    if x.dim() < 1:
+        raise ValueError("x must be (..., dim)")
+    shape, io, dev = x.shape, x.dtype, x.device
+    dim = shape[-1]
+    rows = x.numel() // dim if dim else 0
+    code = _kind_code(kind)
+    f32 = torch.float32
+    _need(x, "x", shape, io, dev)
+    if weight is not None:
+        _need(weight, "weight", shape[-1:], f32, dev)
+    if bias is not None:
+        _need(bias, "bias", shape[-1:], f32, dev)
+    if out is None:
+        out = torch.empty_like(x)
+    else:
+        _need(out, "out", shape, io, dev)
+    res_code = io_code = _io_code(io)
+    s = x
+    if residual is not None:
+        _need_residual(residual, "residual", shape, io, dev)
+        res_code = _io_code(residual.dtype)
+        if residual_out is None:
+            residual_out = torch.empty_like(residual)
+        else:
+            _need(residual_out, "residual_out", shape, residual.dtype, dev)
+        s = residual_out
+    elif residual_out is not None:
+        raise ValueError("residual_out needs a residual")
+    mean = rstd = None
+    if save_stats:
+        rstd = torch.empty(shape[:-1], dtype=f32, device=dev)
+        if kind == "layer":
+            mean = torch.empty(shape[:-1], dtype=f32, device=dev)
+    st = load_library().ssm_norm_fwd(rows, dim, io_code, res_code, code, _ptr(x), _ptr(residual), _ptr(weight),
+                                     _ptr(bias), eps, _ptr(out), _ptr(residual_out), _ptr(mean), _ptr(rstd),
+                                     _stream(dev, None))
+    _check("ssm_norm_fwd", st)
+    return out, s, mean, rstd
+
+
+@_placed
+def norm_bwd(dy, s, rstd, mean=None, weight=None, dresidual_out=None, kind="layer", need=("dweight", "dbias")):
+    """Gradients of sum(dy * y) + sum(dresidual_out * s) for norm_fwd (ssm_norm_bwd).
+
+    s, mean and rstd are what norm_fwd returned (mean for kind "layer" only).
+    dy: (..., dim) in the io dtype; dresidual_out, the gradient that reaches s
+    past the norm, in s's dtype.  Returns a dict: dx (io dtype), the gradient
+    of x and of the residual alike; dresidual, the same in s's dtype where
+    that is another, else None; and, when named in `need`, dweight and dbias
+    (dim,) float32.
+    """
+    import torch
+    if dy.dim() < 1:
+        raise ValueError("dy must be (..., dim)")
+    shape, io, dev = dy.shape, dy.dtype, dy.device
+    dim = shape[-1]
+    rows = dy.numel() // dim if dim else 0
+    code = _kind_code(kind)
+    f32 = torch.float32
+    _need(dy, "dy", shape, io, dev)
+    _need_residual(s, "s", shape, io, dev)
+    _need(rstd, "rstd", shape[:-1], f32, dev)
+    if kind == "layer":
+        if mean is None:
+            raise ValueError("kind \"layer\" needs the mean")
+        _need(mean, "mean", shape[:-1], f32, dev)
+    else:
+        mean = None
+    if weight is not None:
+        _need(weight, "weight", shape[-1:], f32, dev)
+    if dresidual_out is not None:
+        _need(dresidual_out, "dresidual_out", shape, s.dtype, dev)
+    g = dict(dx=torch.empty_like(dy), dresidual=torch.empty_like(s) if s.dtype != io else None,
+             dweight=torch.empty(dim, dtype=f32, device=dev) if "dweight" in need else None,
+             dbias=torch.empty(dim, dtype=f32, device=dev) if "dbias" in need else None)
+    lib = load_library()
+    io_code, res_code = _io_code(io), _io_code(s.dtype)
+    size = _I64(0)
+    if g["dweight"] is not None or g["dbias"] is not None:
+        _check("ssm_norm_bwd_workspace_bytes",
+               lib.ssm_norm_bwd_workspace_bytes(rows, dim, io_code, res_code, ctypes.byref(size)))
+    work = torch.empty(size.value, dtype=torch.uint8, device=dev) if size.value else None
+    st = lib.ssm_norm_bwd(rows, dim, io_code, res_code, code, _ptr(dy), _ptr(s), _ptr(weight), _ptr(mean),
+                          _ptr(rstd), _ptr(dresidual_out), _ptr(g["dx"]), _ptr(g["dresidual"]), _ptr(g["dweight"]),
+                          _ptr(g["dbias"]), _ptr(work), size.value, _stream(dev, None))
+    _check("ssm_norm_bwd", st)
+    return g

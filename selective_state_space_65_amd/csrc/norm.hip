@@ -1,0 +1,541 @@
+// norm.hip -- layer and RMS norm with the residual add in front of it: forward
+// and backward.  C ABI: include/ssm_scan.h.
+//
+// A row is held in registers from its one read to its write: G lanes (8 to 64,
+// or W waves of 64) take a row, each lane K pieces of 8 consecutive numbers,
+// piece k of the row's lanes next to each other so that every access is
+// contiguous.  The mean, then the sum of squares about it, are reduced over
+// the lanes by DPP and over a row's waves through LDS: every number is read
+// once and written once.
+//
+// The backward gives each group of lanes many rows.  Besides the two sums of
+// a row (g and g n) each lane keeps its own columns' sums of dy n and dy in
+// registers over all its rows; at the end a block adds its groups' sums in
+// LDS and writes one partial row, and a second kernel adds the partial rows,
+// all in a fixed order.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+
+#include "device_common.h"
+#include "host_common.h"
+#include "rows.h"
+#include "ssm_scan.h"
+
+namespace {
+
+constexpr int kPiece = 8;           // numbers per lane and piece
+constexpr int kMaxDim = 32768;      // 16 waves x 64 lanes x 4 pieces x 8
+constexpr int kMaxRowWaves = 16;
+
+template <int ctrl, int row_mask = 0xf>
+__device__ __forceinline__ float dpp_add(float v) {
+  return v + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), ctrl, row_mask, 0xf, true));
+}
+
+// Sum over the G lanes of a group, in all of them.
+template <int G>
+__device__ __forceinline__ float group_sum(float v) {
+  v = dpp_add<0xb1>(v);  // quad_perm 1,0,3,2
+  v = dpp_add<0x4e>(v);  // quad_perm 2,3,0,1
+  v = dpp_add<0x141>(v);  // row_half_mirror: the other quad of 8
+  if constexpr (G >= 16) v = dpp_add<0x128>(v);  // row_ror 8: the other half of 16
+  if constexpr (G == 32) v += __shfl_xor(v, 16);
+  if constexpr (G == 64) {
+    const float a = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 0));
+    const float b = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 16));
+    const float c = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 32));
+    const float d = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 48));
+    v = (a + b) + (c + d);
+  }
+  return v;
+}
+
+// Sum over a row: its lanes, then its waves (slots: one LDS row per use, so
+// that one barrier separates the writes from the reads).
+template <int G>
+__device__ __forceinline__ float row_sum(float v, float* slots, int lane, int row_wave, int row_waves) {
+  v = group_sum<G>(v);
+  if (G == 64 && row_waves > 1) {
+    if (lane == 0) slots[row_wave] = v;
+    lds_barrier();
+    v = slots[0];
+    for (int w = 1; w < row_waves; ++w) v += slots[w];
+  }
+  return v;
+}
+
+// ---- the forward -------------------------------------------------------------
+
+struct NormFwdArgs {
+  const void* x;
+  const void* residual;
+  const float* weight;  // may be null
+  const float* bias;    // may be null
+  void* y;
+  void* s;      // may be null
+  float* mean;  // may be null
+  float* rstd;  // may be null
+  int64_t rows;
+  int dim;
+  int row_waves;
+  float eps;
+};
+
+// x + residual rounded to the residual's type, as it is stored.
+template <typename ResT>
+__device__ __forceinline__ float add_res(float x, float r) {
+  return round_io<ResT>(x + r);
+}
+
+// G lanes a row, K pieces a lane; kRes: a residual is added.
+template <typename IoT, typename ResT, int G, int K, bool kRms, bool kRes>
+__global__ __launch_bounds__(1024) void norm_fwd_kernel(NormFwdArgs p) {
+  __shared__ float slots[2][kMaxRowWaves];
+  const int lane = threadIdx.x & 63, gl = lane & (G - 1);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int waves = blockDim.x >> 6;
+  const int W = G == 64 ? p.row_waves : 1;  // 1 or all of the block's waves
+  const int row_wave = W > 1 ? wave : 0;
+  const int64_t row = W > 1 ? (int64_t)blockIdx.x : ((int64_t)blockIdx.x * waves + wave) * (64 / G) + lane / G;
+  const bool live = row < p.rows;
+  const int64_t base = (live ? row : p.rows - 1) * p.dim;
+  const IoT* xr = static_cast<const IoT*>(p.x) + base;
+  const ResT* rr = static_cast<const ResT*>(p.residual) + (kRes ? base : 0);
+  const int dim = p.dim;
+  const float count = (float)dim;  // sums are divided by it: a constant row has exactly its mean
+
+  float v[K][kPiece];
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    const int c = ((k * W + row_wave) * G + gl) * kPiece;
+    load_row8(xr, c, dim, c + kPiece <= dim, v[k]);
+    if constexpr (kRes) {
+      float r[kPiece];
+      load_row8(rr, c, dim, c + kPiece <= dim, r);
+#pragma unroll
+      for (int j = 0; j < kPiece; ++j) v[k][j] = add_res<ResT>(v[k][j], r[j]);
+    }
+  }
+  float mean = 0.0f;
+  if constexpr (!kRms) {
+    float t = 0.0f;
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+      for (int j = 0; j < kPiece; ++j) t += v[k][j];
+    mean = row_sum<G>(t, slots[0], lane, row_wave, W) / count;
+  }
+  float q = 0.0f;
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    const int c = ((k * W + row_wave) * G + gl) * kPiece;
+#pragma unroll
+    for (int j = 0; j < kPiece; ++j) {
+      const float d = c + j < dim ? v[k][j] - mean : 0.0f;
+      q = __builtin_fmaf(d, d, q);
+    }
+  }
+  const float var = row_sum<G>(q, slots[1], lane, row_wave, W) / count;
+  const float rstd = 1.0f / __builtin_sqrtf(var + p.eps);
+  if (!live) return;
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    const int c = ((k * W + row_wave) * G + gl) * kPiece;
+    const bool full = c + kPiece <= dim;
+    if constexpr (kRes) {
+      if (p.s) store_row8(static_cast<ResT*>(p.s) + base, c, dim, full, v[k]);
+    }
+    float w[kPiece], b[kPiece], o[kPiece];
+    if (p.weight) load_row8(p.weight, c, dim, full, w);
+    if (p.bias) load_row8(p.bias, c, dim, full, b);
+#pragma unroll
+    for (int j = 0; j < kPiece; ++j) {
+      o[j] = (v[k][j] - mean) * rstd;
+      if (p.weight) o[j] *= w[j];
+      if (p.bias) o[j] += b[j];
+    }
+    store_row8(static_cast<IoT*>(p.y) + base, c, dim, full, o);
+  }
+  if (gl == 0 && row_wave == 0) {
+    if (!kRms && p.mean) p.mean[row] = mean;
+    if (p.rstd) p.rstd[row] = rstd;
+  }
+}
+
+// ---- the backward ------------------------------------------------------------
+
+struct NormBwdArgs {
+  const void* dy;
+  const void* s;
+  const float* weight;  // may be null
+  const float* mean;    // layer only
+  const float* rstd;
+  const void* ds_out;  // may be null
+  void* dx;
+  void* dres;      // may be null
+  float* part;     // [blocks][2][dim], or null without dweight and dbias
+  int64_t rows;
+  int dim;
+  int row_waves;
+};
+
+constexpr int kBwdWaves = 8;  // per block
+
+// A block's waves form kBwdWaves / W row groups (times 64 / G for short rows);
+// every group takes the rows group, group + groups, ...
+template <typename IoT, typename ResT, int G, int K, bool kRms>
+__global__ __launch_bounds__(64 * kMaxRowWaves) void norm_bwd_kernel(NormBwdArgs p) {
+  __shared__ float slots[2][2][kMaxRowWaves];
+  extern __shared__ float cols[];  // [2][dim] sums of the block
+  const int lane = threadIdx.x & 63, gl = lane & (G - 1);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int waves = blockDim.x >> 6;
+  const int W = G == 64 ? p.row_waves : 1;
+  const int row_wave = wave % W, wave_group = wave / W, wave_groups = waves / W;
+  const int group = wave_group * (64 / G) + lane / G, groups = wave_groups * (64 / G);
+  const int dim = p.dim;
+  const float inv = 1.0f / (float)dim;
+  float w[K][kPiece], aw[K][kPiece], ab[K][kPiece];
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    const int c = ((k * W + row_wave) * G + gl) * kPiece;
+    if (p.weight) load_row8(p.weight, c, dim, c + kPiece <= dim, w[k]);
+#pragma unroll
+    for (int j = 0; j < kPiece; ++j) {
+      if (!p.weight) w[k][j] = 1.0f;
+      aw[k][j] = ab[k][j] = 0.0f;
+    }
+  }
+  const int64_t per_sweep = (int64_t)gridDim.x * groups;
+  const int64_t sweeps = (p.rows + per_sweep - 1) / per_sweep;
+  int parity = 0;
+  for (int64_t i = 0; i < sweeps; ++i, parity ^= 1) {
+    const int64_t row = i * per_sweep + (int64_t)blockIdx.x * groups + group;
+    const bool live = row < p.rows;
+    const int64_t at = live ? row : p.rows - 1, base = at * dim;
+    const float mean = kRms ? 0.0f : p.mean[at];
+    const float rstd = p.rstd[at];
+    float n[K][kPiece], dy[K][kPiece];
+    float c1 = 0.0f, c2 = 0.0f;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int c = ((k * W + row_wave) * G + gl) * kPiece;
+      const bool full = c + kPiece <= dim;
+      load_row8(static_cast<const ResT*>(p.s) + base, c, dim, full, n[k]);
+      load_row8(static_cast<const IoT*>(p.dy) + base, c, dim, full, dy[k]);
+    }
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+#pragma unroll
+      for (int j = 0; j < kPiece; ++j) {
+        n[k][j] = (n[k][j] - mean) * rstd;
+        const float g = dy[k][j] * w[k][j];  // 0 past the row, where dy is
+        if constexpr (!kRms) c1 += g;
+        c2 = __builtin_fmaf(g, n[k][j], c2);
+        if (live) {
+          aw[k][j] = __builtin_fmaf(dy[k][j], n[k][j], aw[k][j]);
+          ab[k][j] += dy[k][j];
+        }
+      }
+    }
+    c1 = group_sum<G>(c1);
+    c2 = group_sum<G>(c2);
+    if (G == 64 && W > 1) {
+      float* s1 = slots[parity][0];
+      float* s2 = slots[parity][1];
+      if (lane == 0) s1[wave] = c1, s2[wave] = c2;
+      lds_barrier();
+      c1 = c2 = 0.0f;
+      for (int v = 0; v < W; ++v) c1 += s1[wave_group * W + v], c2 += s2[wave_group * W + v];
+    }
+    c1 *= inv;
+    c2 *= inv;
+    if (live) {
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        const int c = ((k * W + row_wave) * G + gl) * kPiece;
+        const bool full = c + kPiece <= dim;
+        float o[kPiece];
+#pragma unroll
+        for (int j = 0; j < kPiece; ++j) {
+          float g = dy[k][j] * w[k][j];
+          if constexpr (!kRms) g -= c1;
+          o[j] = rstd * __builtin_fmaf(-n[k][j], c2, g);
+        }
+        if (p.ds_out) {
+          float r[kPiece];
+          load_row8(static_cast<const ResT*>(p.ds_out) + base, c, dim, full, r);
+#pragma unroll
+          for (int j = 0; j < kPiece; ++j) o[j] += r[j];
+        }
+        store_row8(static_cast<IoT*>(p.dx) + base, c, dim, full, o);
+        if (p.dres) store_row8(static_cast<ResT*>(p.dres) + base, c, dim, full, o);
+      }
+    }
+  }
+  if (!p.part) return;
+  float* part = p.part + (int64_t)blockIdx.x * 2 * dim;
+  if (wave_groups == 1) {  // the block is one row group: its sums as they are
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int c = ((k * W + row_wave) * G + gl) * kPiece;
+      const bool full = c + kPiece <= dim;
+      store_row8(part, c, dim, full, aw[k]);
+      store_row8(part + dim, c, dim, full, ab[k]);
+    }
+    return;
+  }
+  // Column sums of the block: the groups of a wave by shuffles, then the wave
+  // groups one after another in LDS.
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+#pragma unroll
+    for (int j = 0; j < kPiece; ++j) {
+#pragma unroll
+      for (int d = G; d < 64; d <<= 1) {
+        aw[k][j] += __shfl_xor(aw[k][j], d);
+        ab[k][j] += __shfl_xor(ab[k][j], d);
+      }
+    }
+  }
+  for (int g = 0; g < wave_groups; ++g) {
+    if (g == wave_group && lane < G) {
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        const int c = ((k * W + row_wave) * G + gl) * kPiece;
+#pragma unroll
+        for (int j = 0; j < kPiece; ++j) {
+          if (c + j < dim) {
+            cols[c + j] = g ? cols[c + j] + aw[k][j] : aw[k][j];
+            cols[dim + c + j] = g ? cols[dim + c + j] + ab[k][j] : ab[k][j];
+          }
+        }
+      }
+    }
+    lds_barrier();
+  }
+  for (int c = threadIdx.x; c < 2 * dim; c += blockDim.x) part[c] = cols[c];
+}
+
+// dweight and dbias: 64 columns a block, 16 slices of the partial rows, the
+// slices added in order.
+__global__ __launch_bounds__(1024) void norm_bwd_reduce_kernel(const float* part, float* dweight, float* dbias,
+                                                               int blocks, int dim) {
+  __shared__ float sums[16][64];
+  const int col = threadIdx.x & 63, slice = threadIdx.x >> 6;
+  const int c = blockIdx.x * 64 + col;
+  float t = 0.0f;
+  if (c < 2 * dim) {
+    for (int b = slice; b < blocks; b += 16) t += part[(int64_t)b * 2 * dim + c];
+  }
+  sums[slice][col] = t;
+  lds_barrier();
+  if (slice == 0 && c < 2 * dim) {
+    for (int i = 1; i < 16; ++i) t += sums[i][col];
+    float* out = c < dim ? dweight : dbias;
+    if (out) out[c < dim ? c : c - dim] = t;
+  }
+}
+
+// ---- host side ---------------------------------------------------------------
+
+struct NormPlan {
+  int group, pieces, row_waves, threads;
+  int64_t blocks;
+};
+
+// Lanes, pieces and waves of a row: the fewest lanes that hold it at one piece
+// each up to a wave, then up to `most` pieces, then more waves.
+NormPlan norm_plan(int64_t dim, int most) {
+  NormPlan p;
+  p.group = 8;
+  while (p.group < 64 && p.group * kPiece < dim) p.group *= 2;
+  p.pieces = 1;
+  while (p.pieces < most && p.group * kPiece * p.pieces < dim) p.pieces *= 2;
+  p.row_waves = 1;
+  while (p.group * kPiece * p.pieces * p.row_waves < dim) p.row_waves *= 2;
+  while (p.row_waves > kMaxRowWaves) {
+    p.row_waves /= 2;
+    p.pieces *= 2;
+  }
+  p.threads = 256;
+  p.blocks = 0;
+  return p;
+}
+
+NormPlan fwd_plan(int64_t rows, int64_t dim) {
+  NormPlan p = norm_plan(dim, 4);
+  if (p.row_waves > 1) {
+    p.threads = 64 * p.row_waves;
+    p.blocks = rows;
+  } else {
+    const int64_t per_block = 4 * (64 / p.group);
+    p.blocks = (rows + per_block - 1) / per_block;
+  }
+  return p;
+}
+
+constexpr int64_t kBwdBlocks = 512;
+
+NormPlan bwd_plan(int64_t rows, int64_t dim) {
+  NormPlan p = norm_plan(dim, 2);
+  const int waves = std::max(p.row_waves, kBwdWaves);
+  p.threads = 64 * waves;
+  const int64_t groups = (int64_t)(waves / p.row_waves) * (64 / p.group);
+  p.blocks = std::min<int64_t>(kBwdBlocks, (rows + groups - 1) / groups);
+  return p;
+}
+
+#define SSM_NORM_GEOMETRY(CALL)                  \
+  switch (p.group) {                             \
+    case 8: CALL(8, 1); break;                   \
+    case 16: CALL(16, 1); break;                 \
+    case 32: CALL(32, 1); break;                 \
+    default:                                     \
+      if (p.pieces == 1) { CALL(64, 1); }        \
+      else if (p.pieces == 2) { CALL(64, 2); }   \
+      else { CALL(64, 4); }                      \
+  }
+
+template <typename IoT, typename ResT, bool kRms, bool kRes>
+hipError_t launch_norm_fwd(const NormFwdArgs& a, const NormPlan& p, hipStream_t st) {
+#define SSM_NORM_CALL(G, K)                                                                                  \
+  hipLaunchKernelGGL((norm_fwd_kernel<IoT, ResT, G, K, kRms, kRes>), dim3((unsigned)p.blocks), dim3(p.threads), 0, st, a)
+  SSM_NORM_GEOMETRY(SSM_NORM_CALL)
+#undef SSM_NORM_CALL
+  return hipGetLastError();
+}
+
+template <typename IoT, typename ResT>
+hipError_t launch_norm_fwd(const NormFwdArgs& a, const NormPlan& p, bool rms, hipStream_t st) {
+  if (a.residual)
+    return rms ? launch_norm_fwd<IoT, ResT, true, true>(a, p, st) : launch_norm_fwd<IoT, ResT, false, true>(a, p, st);
+  if constexpr (sizeof(IoT) == sizeof(ResT))  // without a residual its type is the io type
+    return rms ? launch_norm_fwd<IoT, ResT, true, false>(a, p, st) : launch_norm_fwd<IoT, ResT, false, false>(a, p, st);
+  return hipErrorInvalidValue;
+}
+
+template <typename IoT, typename ResT, bool kRms>
+hipError_t launch_norm_bwd(const NormBwdArgs& a, const NormPlan& p, hipStream_t st) {
+  const bool join = a.part && p.threads > 64 * p.row_waves;  // dim <= 4096: at most 32 KB
+  const size_t lds = join ? (size_t)2 * a.dim * 4 : 0;
+#define SSM_NORM_CALL(G, K)                                                                                     \
+  hipLaunchKernelGGL((norm_bwd_kernel<IoT, ResT, G, K, kRms>), dim3((unsigned)p.blocks), dim3(p.threads), lds, st, a)
+  SSM_NORM_GEOMETRY(SSM_NORM_CALL)
+#undef SSM_NORM_CALL
+  return hipGetLastError();
+}
+
+template <typename IoT, typename ResT>
+hipError_t launch_norm_bwd(const NormBwdArgs& a, const NormPlan& p, bool rms, hipStream_t st) {
+  return rms ? launch_norm_bwd<IoT, ResT, true>(a, p, st) : launch_norm_bwd<IoT, ResT, false>(a, p, st);
+}
+
+ssm_status_t norm_shape(int64_t rows, int64_t dim, ssm_dtype_t io, ssm_dtype_t res_io, int64_t* n) {
+  if (io != SSM_F32 && io != SSM_BF16) return SSM_ERR_DTYPE;
+  if (res_io != io && res_io != SSM_F32) return SSM_ERR_DTYPE;
+  if (rows < 1 || dim < 1) return SSM_ERR_SHAPE;
+  int64_t bytes;
+  if (!mul_ok(rows, dim, n) || !mul_ok(*n, 8, &bytes)) return SSM_ERR_SHAPE;
+  if (dim > kMaxDim || rows >= ((int64_t)1 << 31)) return SSM_ERR_UNSUPPORTED;
+  return SSM_OK;
+}
+
+bool norm_kind_ok(ssm_norm_t kind) { return kind == SSM_NORM_LAYER || kind == SSM_NORM_RMS; }
+
+}  // namespace
+
+// ----------------------------------------------------------------------------
+// C ABI
+// ----------------------------------------------------------------------------
+
+extern "C" {
+
+ssm_status_t ssm_norm_fwd(int64_t rows, int64_t dim, ssm_dtype_t io, ssm_dtype_t res_io, ssm_norm_t kind,
+                          const void* x, const void* residual, const float* weight, const float* bias, float eps,
+                          void* y, void* s, float* mean, float* rstd, struct ihipStream_t* stream) {
+  int64_t n;
+  ssm_status_t st = norm_shape(rows, dim, io, res_io, &n);
+  if (st != SSM_OK) return st;
+  if (!norm_kind_ok(kind)) return SSM_ERR_UNSUPPORTED;
+  if (!residual && res_io != io) return SSM_ERR_DTYPE;
+  if (!x || !y || (s && !residual)) return SSM_ERR_NULL;
+  if (kind == SSM_NORM_RMS) mean = nullptr;
+  const size_t es = io_size(io), rs = io_size(res_io);
+  const bool in_place = residual && s == residual;
+  const Buf ins[] = {{x, n * (int64_t)es, es}, {in_place ? nullptr : residual, n * (int64_t)rs, rs},
+                     {weight, dim * 4, 4}, {bias, dim * 4, 4}};
+  const Buf outs[] = {{y, n * (int64_t)es, es}, {s, n * (int64_t)rs, rs}, {mean, rows * 4, 4}, {rstd, rows * 4, 4}};
+  st = check_buffers(ins, 4, outs, 4);
+  if (st != SSM_OK) return st;
+  const NormPlan p = fwd_plan(rows, dim);
+  NormFwdArgs a;
+  a.x = x; a.residual = residual; a.weight = weight; a.bias = bias; a.y = y; a.s = s; a.mean = mean; a.rstd = rstd;
+  a.rows = rows; a.dim = (int)dim; a.row_waves = p.row_waves; a.eps = eps;
+  hipStream_t hs = reinterpret_cast<hipStream_t>(stream);
+  const bool rms = kind == SSM_NORM_RMS;
+  hipError_t e;
+  if (io == SSM_F32)
+    e = launch_norm_fwd<float, float>(a, p, rms, hs);
+  else if (res_io == SSM_BF16)
+    e = launch_norm_fwd<bf16_t, bf16_t>(a, p, rms, hs);
+  else
+    e = launch_norm_fwd<bf16_t, float>(a, p, rms, hs);
+  return e == hipSuccess ? SSM_OK : hip_fail(e);
+}
+
+ssm_status_t ssm_norm_bwd_workspace_bytes(int64_t rows, int64_t dim, ssm_dtype_t io, ssm_dtype_t res_io,
+                                          int64_t* bytes) {
+  int64_t n;
+  ssm_status_t st = norm_shape(rows, dim, io, res_io, &n);
+  if (st == SSM_OK && bytes) *bytes = bwd_plan(rows, dim).blocks * 2 * dim * 4;
+  return st;
+}
+
+ssm_status_t ssm_norm_bwd(int64_t rows, int64_t dim, ssm_dtype_t io, ssm_dtype_t res_io, ssm_norm_t kind,
+                          const void* dy, const void* s, const float* weight, const float* mean, const float* rstd,
+                          const void* ds_out, void* dx, void* dresidual, float* dweight, float* dbias,
+                          void* workspace, int64_t workspace_bytes, struct ihipStream_t* stream) {
+  int64_t n;
+  ssm_status_t st = norm_shape(rows, dim, io, res_io, &n);
+  if (st != SSM_OK) return st;
+  if (!norm_kind_ok(kind)) return SSM_ERR_UNSUPPORTED;
+  if (!dy || !s || !rstd || !dx || (kind == SSM_NORM_LAYER && !mean)) return SSM_ERR_NULL;
+  if (kind == SSM_NORM_RMS) mean = nullptr;
+  const NormPlan p = bwd_plan(rows, dim);
+  const bool sums = dweight || dbias;
+  const int64_t need = sums ? p.blocks * 2 * dim * 4 : 0;
+  if (workspace_bytes < need) return SSM_ERR_WORKSPACE;
+  if (need && !workspace) return SSM_ERR_NULL;
+  if (!need) workspace = nullptr;
+  const size_t es = io_size(io), rs = io_size(res_io);
+  const Buf ins[] = {{dy, n * (int64_t)es, es}, {s, n * (int64_t)rs, rs}, {weight, dim * 4, 4}, {mean, rows * 4, 4},
+                     {rstd, rows * 4, 4}, {ds_out, n * (int64_t)rs, rs}};
+  const Buf outs[] = {{dx, n * (int64_t)es, es}, {dresidual, n * (int64_t)rs, rs}, {dweight, dim * 4, 4},
+                      {dbias, dim * 4, 4}, {workspace, need, 4}};
+  st = check_buffers(ins, 6, outs, 5);
+  if (st != SSM_OK) return st;
+  NormBwdArgs a;
+  a.dy = dy; a.s = s; a.weight = weight; a.mean = mean; a.rstd = rstd; a.ds_out = ds_out; a.dx = dx;
+  a.dres = dresidual; a.part = static_cast<float*>(workspace); a.rows = rows; a.dim = (int)dim;
+  a.row_waves = p.row_waves;
+  hipStream_t hs = reinterpret_cast<hipStream_t>(stream);
+  const bool rms = kind == SSM_NORM_RMS;
+  hipError_t e;
+  if (io == SSM_F32)
+    e = launch_norm_bwd<float, float>(a, p, rms, hs);
+  else if (res_io == SSM_BF16)
+    e = launch_norm_bwd<bf16_t, bf16_t>(a, p, rms, hs);
+  else
+    e = launch_norm_bwd<bf16_t, float>(a, p, rms, hs);
+  if (e == hipSuccess && sums) {
+    hipLaunchKernelGGL(norm_bwd_reduce_kernel, dim3((unsigned)((2 * dim + 63) / 64)), dim3(1024), 0, hs, a.part,
+                       dweight, dbias, (int)p.blocks, (int)dim);
+    e = hipGetLastError();
+  }
+  return e == hipSuccess ? SSM_OK : hip_fail(e);
+}
+
+}  // extern "C"
