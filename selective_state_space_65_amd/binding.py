@@ -11,6 +11,8 @@ import ctypes
 import functools
 import os
 
+import torch
+
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libssm_scan.so")
 
@@ -662,6 +664,24 @@ def _state_update(disc, state, u, delta, A, B, C, D, z, delta_bias, delta_softpl
     return out
 
 
+@functools.lru_cache(maxsize=None)
+def _queries():
+    """(current device index, raw handle of a device's current stream): torch's own bindings of
+    torch.cuda.current_device and current_stream, whose Python objects cost 2 us a call; the public
+    functions where they are missing."""
+    device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", lambda i: torch.cuda.current_stream(i).cuda_stream)
+    return device, raw
+
+
+@functools.lru_cache(maxsize=1024)
+def _workspace_bytes(fn, *sizes):
+    """Workspace of a call by its sizes (host arithmetic in the library)."""
+    size = _I64(0)
+    _check(fn, getattr(load_library(), fn)(*sizes, ctypes.byref(size)))
+    return size.value
+
+
 def _placed(fn):
     """Runs fn with its first argument's device current, on the caller's stream.
 
@@ -671,10 +691,9 @@ def _placed(fn):
     """
     @functools.wraps(fn)
     def call(first, *args, stream=None, **kw):
-        import torch
         if not first.is_cuda:
             raise ValueError("%s: tensors must be on a GPU, got %s" % (fn.__name__, first.device))
-        if stream is None and first.device.index == torch.cuda.current_device():
+        if stream is None and first.get_device() == _queries()[0]():
             return fn(first, *args, **kw)
         with torch.cuda.device(first.device):
             if stream is None:
@@ -694,7 +713,6 @@ def _mode_code(mode):
 
 
 def _gated_inputs(x, gate, gate_bias, rate, z, reset):
-    import torch
     if x.dim() != 3:
         raise ValueError("x must be (batch, dim, seqlen)")
     shape, io, dev = x.shape, x.dtype, x.device
@@ -733,7 +751,6 @@ def gated_scan_fwd(x, gate, gate_bias=None, rate=None, z=None, reset=None, h0=No
     ckpt, when given, receives the backward's checkpoints (gated_ckpt_shape).
     stream (keyword): run on that torch.cuda.Stream instead of the current one.
     """
-    import torch
     batch, dim, seqlen, io, dev = _gated_inputs(x, gate, gate_bias, rate, z, reset)
     code = _mode_code(mode)
     if h0 is not None:
@@ -750,7 +767,7 @@ def gated_scan_fwd(x, gate, gate_bias=None, rate=None, z=None, reset=None, h0=No
         _need(ckpt, "ckpt", gated_ckpt_shape(batch, dim, seqlen), torch.float32, dev)
     st = load_library().ssm_gated_scan_fwd(batch, dim, seqlen, _io_code(io), code, _ptr(x), _ptr(gate),
                                            _ptr(gate_bias), _ptr(rate), _ptr(z), _ptr(reset), _ptr(h0), _ptr(out),
-                                           _ptr(last_state), _ptr(ckpt), _stream(dev, None))
+                                           _ptr(last_state), _ptr(ckpt), _queries()[1](dev.index))
     _check("ssm_gated_scan_fwd", st)
     return out, last_state
 
@@ -759,12 +776,11 @@ def gated_scan_fwd(x, gate, gate_bias=None, rate=None, z=None, reset=None, h0=No
 def gated_scan_fwd_save(x, gate, gate_bias=None, rate=None, z=None, reset=None, h0=None, mode="plain", out=None,
                         last_state=None, ckpt=None):
     """gated_scan_fwd that also writes the backward's checkpoints; returns (y, last_state, ckpt)."""
-    import torch
     if ckpt is None:
         if x.dim() != 3:
             raise ValueError("x must be (batch, dim, seqlen)")
         ckpt = torch.empty(gated_ckpt_shape(*x.shape), dtype=torch.float32, device=x.device)
-    out, last_state = gated_scan_fwd(x, gate, gate_bias, rate, z, reset, h0, mode, out, last_state, ckpt)
+    out, last_state = gated_scan_fwd.__wrapped__(x, gate, gate_bias, rate, z, reset, h0, mode, out, last_state, ckpt)
     return out, last_state, ckpt
 
 
@@ -778,7 +794,6 @@ def gated_scan_bwd(x, gate, dy, ckpt, gate_bias=None, rate=None, z=None, reset=N
     named in `need`, dgate_bias (dim,), drate (dim,, only with a rate) and dh0
     (batch, dim) in float32 and dz (io dtype, only with z); None for the others.
     """
-    import torch
     batch, dim, seqlen, io, dev = _gated_inputs(x, gate, gate_bias, rate, z, reset)
     code = _mode_code(mode)
     f32 = torch.float32
@@ -793,14 +808,12 @@ def gated_scan_bwd(x, gate, dy, ckpt, gate_bias=None, rate=None, z=None, reset=N
              dh0=torch.empty((batch, dim), dtype=f32, device=dev) if "dh0" in need else None)
     lib = load_library()
     io_code = _io_code(io)
-    size = _I64(0)
-    _check("ssm_gated_scan_bwd_workspace_bytes",
-           lib.ssm_gated_scan_bwd_workspace_bytes(batch, dim, seqlen, io_code, ctypes.byref(size)))
-    work = torch.empty(size.value, dtype=torch.uint8, device=dev) if size.value else None
+    size = _workspace_bytes("ssm_gated_scan_bwd_workspace_bytes", batch, dim, seqlen, io_code)
+    work = torch.empty(size, dtype=torch.uint8, device=dev) if size else None
     st = lib.ssm_gated_scan_bwd(batch, dim, seqlen, io_code, code, _ptr(x), _ptr(gate), _ptr(gate_bias), _ptr(rate),
                                 _ptr(z), _ptr(reset), _ptr(ckpt), _ptr(dy), _ptr(dlast), _ptr(g["dx"]),
                                 _ptr(g["dgate"]), _ptr(g["dgate_bias"]), _ptr(g["drate"]), _ptr(g["dz"]),
-                                _ptr(g["dh0"]), _ptr(work), size.value, _stream(dev, None))
+                                _ptr(g["dh0"]), _ptr(work), size, _queries()[1](dev.index))
     _check("ssm_gated_scan_bwd", st)
     return g
 
@@ -811,7 +824,6 @@ def gated_state_update(state, x, gate, gate_bias=None, rate=None, z=None, mode="
 
     x, gate, z: (batch, dim) in one io dtype; gate_bias, rate, mode as gated_scan_fwd.
     """
-    import torch
     if state.dim() != 2:
         raise ValueError("state must be (batch, dim)")
     shape, io, dev = state.shape, x.dtype, state.device
@@ -831,7 +843,7 @@ def gated_state_update(state, x, gate, gate_bias=None, rate=None, z=None, mode="
         _need(out, "out", shape, io, dev)
     st = load_library().ssm_gated_state_update(shape[0], shape[1], _io_code(io), code, _ptr(state), _ptr(x),
                                                _ptr(gate), _ptr(gate_bias), _ptr(rate), _ptr(z), _ptr(out),
-                                               _stream(dev, None))
+                                               _queries()[1](dev.index))
     _check("ssm_gated_state_update", st)
     return out
 
@@ -844,7 +856,6 @@ def _kind_code(kind):
 
 def _need_residual(t, name, shape, io, device):
     """A tensor of the residual stream: the io dtype, or float32."""
-    import torch
     _need(t, name, shape, io if t.dtype == io else torch.float32, device)
 
 
@@ -862,7 +873,6 @@ def norm_fwd(x, weight=None, bias=None, residual=None, eps=1e-5, kind="layer", o
     save_stats, and mean None for "rms".
     stream (keyword): run on that torch.cuda.Stream instead of the current one.
     """
-    import torch
     if x.dim() < 1:
         raise ValueError("x must be (..., dim)")
     shape, io, dev = x.shape, x.dtype, x.device
@@ -898,7 +908,7 @@ def norm_fwd(x, weight=None, bias=None, residual=None, eps=1e-5, kind="layer", o
             mean = torch.empty(shape[:-1], dtype=f32, device=dev)
     st = load_library().ssm_norm_fwd(rows, dim, io_code, res_code, code, _ptr(x), _ptr(residual), _ptr(weight),
                                      _ptr(bias), eps, _ptr(out), _ptr(residual_out), _ptr(mean), _ptr(rstd),
-                                     _stream(dev, None))
+                                     _queries()[1](dev.index))
     _check("ssm_norm_fwd", st)
     return out, s, mean, rstd
 
@@ -914,7 +924,6 @@ def norm_bwd(dy, s, rstd, mean=None, weight=None, dresidual_out=None, kind="laye
     that is another, else None; and, when named in `need`, dweight and dbias
     (dim,) float32.
     """
-    import torch
     if dy.dim() < 1:
         raise ValueError("dy must be (..., dim)")
     shape, io, dev = dy.shape, dy.dtype, dy.device
@@ -940,13 +949,12 @@ def norm_bwd(dy, s, rstd, mean=None, weight=None, dresidual_out=None, kind="laye
              dbias=torch.empty(dim, dtype=f32, device=dev) if "dbias" in need else None)
     lib = load_library()
     io_code, res_code = _io_code(io), _io_code(s.dtype)
-    size = _I64(0)
+    size = 0
     if g["dweight"] is not None or g["dbias"] is not None:
-        _check("ssm_norm_bwd_workspace_bytes",
-               lib.ssm_norm_bwd_workspace_bytes(rows, dim, io_code, res_code, ctypes.byref(size)))
-    work = torch.empty(size.value, dtype=torch.uint8, device=dev) if size.value else None
+        size = _workspace_bytes("ssm_norm_bwd_workspace_bytes", rows, dim, io_code, res_code)
+    work = torch.empty(size, dtype=torch.uint8, device=dev) if size else None
     st = lib.ssm_norm_bwd(rows, dim, io_code, res_code, code, _ptr(dy), _ptr(s), _ptr(weight), _ptr(mean),
                           _ptr(rstd), _ptr(dresidual_out), _ptr(g["dx"]), _ptr(g["dresidual"]), _ptr(g["dweight"]),
-                          _ptr(g["dbias"]), _ptr(work), size.value, _stream(dev, None))
+                          _ptr(g["dbias"]), _ptr(work), size, _queries()[1](dev.index))
     _check("ssm_norm_bwd", st)
     return g

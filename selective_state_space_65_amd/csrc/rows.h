@@ -12,6 +12,7 @@ namespace {
 
 typedef uint32_t words2 __attribute__((ext_vector_type(2)));
 typedef uint32_t words4 __attribute__((ext_vector_type(4)));
+typedef words4 words4_any __attribute__((aligned(2), may_alias));
 
 // 8 bytes at any address.
 __device__ __forceinline__ void load_bytes8(const uint8_t* p, uint32_t* lo, uint32_t* hi) {
@@ -21,27 +22,74 @@ __device__ __forceinline__ void load_bytes8(const uint8_t* p, uint32_t* lo, uint
   *hi = w.y;
 }
 
-__device__ __forceinline__ void load8u(const float* p, float out[8]) {
-  words4 a, b;
-  __builtin_memcpy(&a, p, 16);
-  __builtin_memcpy(&b, p + 4, 16);
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    out[j] = __uint_as_float(a[j]);
-    out[4 + j] = __uint_as_float(b[j]);
-  }
+// One 16-byte access at any element address.  kStream: the line is read or
+// written once and not wanted again soon (non-temporal), so that it does not
+// push out what other waves still read.
+template <bool kStream>
+__device__ __forceinline__ words4 load16(const void* p) {
+  if constexpr (kStream) return __builtin_nontemporal_load(static_cast<const words4_any*>(p));
+  return *static_cast<const words4_any*>(p);
 }
 
-__device__ __forceinline__ void load8u(const bf16_t* p, float out[8]) {
-  words4 a;
-  __builtin_memcpy(&a, p, 16);
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    out[2 * j] = bf16_lo(a[j]);
-    out[2 * j + 1] = bf16_hi(a[j]);
-  }
+template <bool kStream>
+__device__ __forceinline__ void store16(void* p, words4 v) {
+  if constexpr (kStream)
+    __builtin_nontemporal_store(v, static_cast<words4_any*>(p));
+  else
+    *static_cast<words4_any*>(p) = v;
 }
 
+// 8 consecutive elements as they are in memory: loaded ahead of their use in
+// half the registers that 8 fp32 values take when the elements are bf16.
+template <typename T>
+struct Raw8;
+
+template <>
+struct Raw8<float> {
+  words4 lo, hi;
+  template <bool kStream>
+  __device__ __forceinline__ void load(const float* p) {
+    lo = load16<kStream>(p);
+    hi = load16<kStream>(p + 4);
+  }
+  __device__ __forceinline__ void load_part(const float* row, int t, int n) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) (j < 4 ? lo : hi)[j & 3] = t + j < n ? __float_as_uint(row[t + j]) : 0u;
+  }
+  __device__ __forceinline__ void get(float out[8]) const {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      out[j] = __uint_as_float(lo[j]);
+      out[4 + j] = __uint_as_float(hi[j]);
+    }
+  }
+};
+
+template <>
+struct Raw8<bf16_t> {
+  words4 w;
+  template <bool kStream>
+  __device__ __forceinline__ void load(const bf16_t* p) {
+    w = load16<kStream>(p);
+  }
+  __device__ __forceinline__ void load_part(const bf16_t* row, int t, int n) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t lo = t + 2 * j < n ? row[t + 2 * j] : 0u;
+      const uint32_t hi = t + 2 * j + 1 < n ? row[t + 2 * j + 1] : 0u;
+      w[j] = lo | hi << 16;
+    }
+  }
+  __device__ __forceinline__ void get(float out[8]) const {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      out[2 * j] = bf16_lo(w[j]);
+      out[2 * j + 1] = bf16_hi(w[j]);
+    }
+  }
+};
+
+template <bool kStream>
 __device__ __forceinline__ void store8u(float* p, const float v[8]) {
   words4 a, b;
 #pragma unroll
@@ -49,33 +97,39 @@ __device__ __forceinline__ void store8u(float* p, const float v[8]) {
     a[j] = __float_as_uint(v[j]);
     b[j] = __float_as_uint(v[4 + j]);
   }
-  __builtin_memcpy(p, &a, 16);
-  __builtin_memcpy(p + 4, &b, 16);
+  store16<kStream>(p, a);
+  store16<kStream>(p + 4, b);
 }
 
+template <bool kStream>
 __device__ __forceinline__ void store8u(bf16_t* p, const float v[8]) {
   words4 a;
 #pragma unroll
   for (int j = 0; j < 4; ++j) a[j] = Io<bf16_t>::pack2(v[2 * j], v[2 * j + 1]);
-  __builtin_memcpy(p, &a, 16);
+  store16<kStream>(p, a);
 }
 
-// Elements [t, t + 8) of a row of n; full: t + 8 <= n for the whole wave.
-// Elements past the row read as 0 and are not written.
+// Elements [t, t + 8) of a row of n; full: t + 8 <= n.  Elements past the row
+// read as 0 and are not written.
+template <bool kStream = false, typename T>
+__device__ __forceinline__ Raw8<T> load_raw8(const T* row, int t, int n, bool full) {
+  Raw8<T> r;
+  if (full)
+    r.template load<kStream>(row + t);
+  else
+    r.load_part(row, t, n);
+  return r;
+}
+
 template <typename T>
 __device__ __forceinline__ void load_row8(const T* row, int t, int n, bool full, float out[8]) {
-  if (full) {
-    load8u(row + t, out);
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) out[j] = t + j < n ? Io<T>::load1(row + t + j) : 0.0f;
-  }
+  load_raw8(row, t, n, full).get(out);
 }
 
-template <typename T>
+template <bool kStream = false, typename T>
 __device__ __forceinline__ void store_row8(T* row, int t, int n, bool full, const float v[8]) {
   if (full) {
-    store8u(row + t, v);
+    store8u<kStream>(row + t, v);
   } else {
 #pragma unroll
     for (int j = 0; j < 8; ++j)
