@@ -277,9 +277,9 @@ __device__ __forceinline__ float sigmoid_f32(float z) { return rcp_hw(1.0f + exp
 // Bit j set where token t + j starts a sequence.
 __device__ __forceinline__ uint32_t reset_bits(const uint8_t* row, int t, int seqlen, bool full) {
   uint32_t lo = 0, hi = 0;
-  if (full) {
+  if (full || t + 8 <= seqlen) {
     load_bytes8(row + t, &lo, &hi);
-  } else {
+  } else if (t < seqlen) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       if (t + j < seqlen) lo |= (uint32_t)row[t + j] << (8 * j);
@@ -652,13 +652,24 @@ __global__ __launch_bounds__(G == 64 ? 64 * kMaxBwdWaves : 256, 3) void gated_bw
 }
 
 // out[d] = sum over the batch rows, in order.
-__global__ __launch_bounds__(256) void gated_bwd_reduce_kernel(const float* bias_part, const float* rate_part,
+__global__ __launch_bounds__(64) void gated_bwd_reduce_kernel(const float* bias_part, const float* rate_part,
                                                                float* dbias, float* drate, int64_t batch,
                                                                int64_t dim) {
-  const int64_t d = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t d = (int64_t)blockIdx.x * 64 + threadIdx.x;
   if (d >= dim) return;
   float sb = 0.0f, sr = 0.0f;
-  for (int64_t b = 0; b < batch; ++b) {
+  int64_t b = 0;
+  for (; b + 8 <= batch; b += 8) {  // 8 rows requested at once, added in order
+    float vb[8], vr[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      vb[j] = dbias ? bias_part[(b + j) * dim + d] : 0.0f;
+      vr[j] = drate ? rate_part[(b + j) * dim + d] : 0.0f;
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sb += vb[j], sr += vr[j];
+  }
+  for (; b < batch; ++b) {
     if (dbias) sb += bias_part[b * dim + d];
     if (drate) sr += rate_part[b * dim + d];
   }
@@ -906,7 +917,7 @@ ssm_status_t ssm_gated_scan_bwd(int64_t batch, int64_t dim, int64_t seqlen, ssm_
   hipStream_t hs = reinterpret_cast<hipStream_t>(stream);
   hipError_t e = io == SSM_BF16 ? launch_gated<bf16_t, true>(a, mode, hs) : launch_gated<float, true>(a, mode, hs);
   if (e == hipSuccess && part && (dgate_bias || drate)) {
-    hipLaunchKernelGGL(gated_bwd_reduce_kernel, dim3((unsigned)((dim + 255) / 256)), dim3(256), 0, hs, part,
+    hipLaunchKernelGGL(gated_bwd_reduce_kernel, dim3((unsigned)((dim + 63) / 64)), dim3(64), 0, hs, part,
                        part + s.bd, dgate_bias, drate, batch, dim);
     e = hipGetLastError();
   }

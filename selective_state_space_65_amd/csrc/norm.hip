@@ -66,6 +66,12 @@ __device__ __forceinline__ float row_sum(float v, float* slots, int lane, int ro
   return v;
 }
 
+// Whether the piece at column c is whole in every lane of the group.
+template <int G>
+__device__ __forceinline__ bool whole(int c, int gl, int dim) {
+  return c - gl * kPiece + G * kPiece <= dim;
+}
+
 // ---- the forward -------------------------------------------------------------
 
 struct NormFwdArgs {
@@ -110,10 +116,10 @@ __global__ __launch_bounds__(1024) void norm_fwd_kernel(NormFwdArgs p) {
 #pragma unroll
   for (int k = 0; k < K; ++k) {
     const int c = ((k * W + row_wave) * G + gl) * kPiece;
-    load_row8(xr, c, dim, c + kPiece <= dim, v[k]);
+    load_row8(xr, c, dim, whole<G>(c, gl, dim), v[k]);
     if constexpr (kRes) {
       float r[kPiece];
-      load_row8(rr, c, dim, c + kPiece <= dim, r);
+      load_row8(rr, c, dim, whole<G>(c, gl, dim), r);
 #pragma unroll
       for (int j = 0; j < kPiece; ++j) v[k][j] = add_res<ResT>(v[k][j], r[j]);
     }
@@ -143,7 +149,7 @@ __global__ __launch_bounds__(1024) void norm_fwd_kernel(NormFwdArgs p) {
 #pragma unroll
   for (int k = 0; k < K; ++k) {
     const int c = ((k * W + row_wave) * G + gl) * kPiece;
-    const bool full = c + kPiece <= dim;
+    const bool full = whole<G>(c, gl, dim);
     if constexpr (kRes) {
       if (p.s) store_row8(static_cast<ResT*>(p.s) + base, c, dim, full, v[k]);
     }
@@ -185,10 +191,10 @@ constexpr int kBwdWaves = 8;  // per block
 
 // A block's waves form kBwdWaves / W row groups (times 64 / G for short rows);
 // every group takes the rows group, group + groups, ...
-template <typename IoT, typename ResT, int G, int K, bool kRms>
-__global__ __launch_bounds__(64 * kMaxRowWaves) void norm_bwd_kernel(NormBwdArgs p) {
+template <typename IoT, typename ResT, int G, int K, bool kRms, int kThreads>
+__global__ __launch_bounds__(kThreads) void norm_bwd_kernel(NormBwdArgs p) {
   __shared__ float slots[2][2][kMaxRowWaves];
-  extern __shared__ float cols[];  // [2][dim] sums of the block
+  extern __shared__ __align__(16) float cols[];  // [wave groups][2][width] column sums
   const int lane = threadIdx.x & 63, gl = lane & (G - 1);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int waves = blockDim.x >> 6;
@@ -201,7 +207,7 @@ __global__ __launch_bounds__(64 * kMaxRowWaves) void norm_bwd_kernel(NormBwdArgs
 #pragma unroll
   for (int k = 0; k < K; ++k) {
     const int c = ((k * W + row_wave) * G + gl) * kPiece;
-    if (p.weight) load_row8(p.weight, c, dim, c + kPiece <= dim, w[k]);
+    if (p.weight) load_row8(p.weight, c, dim, whole<G>(c, gl, dim), w[k]);
 #pragma unroll
     for (int j = 0; j < kPiece; ++j) {
       if (!p.weight) w[k][j] = 1.0f;
@@ -210,22 +216,46 @@ __global__ __launch_bounds__(64 * kMaxRowWaves) void norm_bwd_kernel(NormBwdArgs
   }
   const int64_t per_sweep = (int64_t)gridDim.x * groups;
   const int64_t sweeps = (p.rows + per_sweep - 1) / per_sweep;
-  int parity = 0;
-  for (int64_t i = 0; i < sweeps; ++i, parity ^= 1) {
-    const int64_t row = i * per_sweep + (int64_t)blockIdx.x * groups + group;
-    const bool live = row < p.rows;
-    const int64_t at = live ? row : p.rows - 1, base = at * dim;
-    const float mean = kRms ? 0.0f : p.mean[at];
-    const float rstd = p.rstd[at];
-    float n[K][kPiece], dy[K][kPiece];
-    float c1 = 0.0f, c2 = 0.0f;
+  const int64_t first = (int64_t)blockIdx.x * groups + group;
+  // A row's pieces, requested a row ahead where few waves share a compute unit
+  // and the registers allow (4096 x 8000 training step 134.6 -> 128.3 us; at one
+  // piece the other waves cover the wait, 183.0 us without and 185.8 with at
+  // 32768 x 1024).
+  constexpr bool kAhead = K == 2;
+  Raw8<ResT> next_s[K], next_past[K];
+  Raw8<IoT> next_dy[K];
+  float next_mean = 0.0f, next_rstd = 0.0f;
+  const auto request = [&](int64_t i) {
+    const int64_t at = min(first + i * per_sweep, p.rows - 1), base = at * dim;
+    if (!kRms) next_mean = p.mean[at];
+    next_rstd = p.rstd[at];
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       const int c = ((k * W + row_wave) * G + gl) * kPiece;
-      const bool full = c + kPiece <= dim;
-      load_row8(static_cast<const ResT*>(p.s) + base, c, dim, full, n[k]);
-      load_row8(static_cast<const IoT*>(p.dy) + base, c, dim, full, dy[k]);
+      const bool full = whole<G>(c, gl, dim);
+      next_s[k] = load_raw8(static_cast<const ResT*>(p.s) + base, c, dim, full);
+      next_dy[k] = load_raw8(static_cast<const IoT*>(p.dy) + base, c, dim, full);
+      if (p.ds_out) next_past[k] = load_raw8(static_cast<const ResT*>(p.ds_out) + base, c, dim, full);
     }
+  };
+  if (kAhead) request(0);
+  int parity = 0;
+  for (int64_t i = 0; i < sweeps; ++i, parity ^= 1) {
+    const int64_t row = first + i * per_sweep;
+    const bool live = row < p.rows;
+    const int64_t base = (live ? row : p.rows - 1) * dim;
+    if (!kAhead) request(i);
+    const float mean = next_mean, rstd = next_rstd;
+    float n[K][kPiece], dy[K][kPiece];
+    Raw8<ResT> past[K];
+    float c1 = 0.0f, c2 = 0.0f;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      next_s[k].get(n[k]);
+      next_dy[k].get(dy[k]);
+      past[k] = next_past[k];
+    }
+    if (kAhead && i + 1 < sweeps) request(i + 1);
 #pragma unroll
     for (int k = 0; k < K; ++k) {
 #pragma unroll
@@ -256,7 +286,7 @@ __global__ __launch_bounds__(64 * kMaxRowWaves) void norm_bwd_kernel(NormBwdArgs
 #pragma unroll
       for (int k = 0; k < K; ++k) {
         const int c = ((k * W + row_wave) * G + gl) * kPiece;
-        const bool full = c + kPiece <= dim;
+        const bool full = whole<G>(c, gl, dim);
         float o[kPiece];
 #pragma unroll
         for (int j = 0; j < kPiece; ++j) {
@@ -266,7 +296,7 @@ __global__ __launch_bounds__(64 * kMaxRowWaves) void norm_bwd_kernel(NormBwdArgs
         }
         if (p.ds_out) {
           float r[kPiece];
-          load_row8(static_cast<const ResT*>(p.ds_out) + base, c, dim, full, r);
+          past[k].get(r);
 #pragma unroll
           for (int j = 0; j < kPiece; ++j) o[j] += r[j];
         }
@@ -281,16 +311,19 @@ __global__ __launch_bounds__(64 * kMaxRowWaves) void norm_bwd_kernel(NormBwdArgs
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       const int c = ((k * W + row_wave) * G + gl) * kPiece;
-      const bool full = c + kPiece <= dim;
+      const bool full = whole<G>(c, gl, dim);
       store_row8(part, c, dim, full, aw[k]);
       store_row8(part + dim, c, dim, full, ab[k]);
     }
     return;
   }
   // Column sums of the block: the groups of a wave by shuffles, then the wave
-  // groups one after another in LDS.
+  // groups' rows side by side in LDS, added in order.
+  const int width = K * W * G * kPiece;
+  float* mine = cols + wave_group * 2 * width;
 #pragma unroll
   for (int k = 0; k < K; ++k) {
+    const int c = ((k * W + row_wave) * G + gl) * kPiece;
 #pragma unroll
     for (int j = 0; j < kPiece; ++j) {
 #pragma unroll
@@ -299,41 +332,49 @@ __global__ __launch_bounds__(64 * kMaxRowWaves) void norm_bwd_kernel(NormBwdArgs
         ab[k][j] += __shfl_xor(ab[k][j], d);
       }
     }
-  }
-  for (int g = 0; g < wave_groups; ++g) {
-    if (g == wave_group && lane < G) {
+    if (lane < G) {
 #pragma unroll
-      for (int k = 0; k < K; ++k) {
-        const int c = ((k * W + row_wave) * G + gl) * kPiece;
-#pragma unroll
-        for (int j = 0; j < kPiece; ++j) {
-          if (c + j < dim) {
-            cols[c + j] = g ? cols[c + j] + aw[k][j] : aw[k][j];
-            cols[dim + c + j] = g ? cols[dim + c + j] + ab[k][j] : ab[k][j];
-          }
-        }
+      for (int j = 0; j < kPiece; j += 4) {
+        *reinterpret_cast<float4*>(mine + c + j) = make_float4(aw[k][j], aw[k][j + 1], aw[k][j + 2], aw[k][j + 3]);
+        *reinterpret_cast<float4*>(mine + width + c + j) =
+            make_float4(ab[k][j], ab[k][j + 1], ab[k][j + 2], ab[k][j + 3]);
       }
     }
-    lds_barrier();
   }
-  for (int c = threadIdx.x; c < 2 * dim; c += blockDim.x) part[c] = cols[c];
+  lds_barrier();
+  for (int c = threadIdx.x; c < 2 * dim; c += blockDim.x) {
+    const float* at = cols + (c < dim ? c : width + c - dim);
+    float t = at[0];
+    for (int g = 1; g < wave_groups; ++g) t += at[g * 2 * width];
+    part[c] = t;
+  }
 }
 
-// dweight and dbias: 64 columns a block, 16 slices of the partial rows, the
-// slices added in order.
+// dweight and dbias: 32 columns a block, 32 slices of the partial rows; a slice
+// requests 8 of its rows at once, and rows and slices are added in order.
 __global__ __launch_bounds__(1024) void norm_bwd_reduce_kernel(const float* part, float* dweight, float* dbias,
                                                                int blocks, int dim) {
-  __shared__ float sums[16][64];
-  const int col = threadIdx.x & 63, slice = threadIdx.x >> 6;
-  const int c = blockIdx.x * 64 + col;
+  __shared__ float sums[32][33];
+  const int col = threadIdx.x & 31, slice = threadIdx.x >> 5;
+  const int c = blockIdx.x * 32 + col;
   float t = 0.0f;
   if (c < 2 * dim) {
-    for (int b = slice; b < blocks; b += 16) t += part[(int64_t)b * 2 * dim + c];
+    const float* at = part + c;
+    int b = slice;
+    for (; b + 7 * 32 < blocks; b += 8 * 32) {
+      float v[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = at[(int64_t)(b + j * 32) * 2 * dim];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) t += v[j];
+    }
+    for (; b < blocks; b += 32) t += at[(int64_t)b * 2 * dim];
   }
   sums[slice][col] = t;
   lds_barrier();
   if (slice == 0 && c < 2 * dim) {
-    for (int i = 1; i < 16; ++i) t += sums[i][col];
+#pragma unroll
+    for (int i = 1; i < 32; ++i) t += sums[i][col];
     float* out = c < dim ? dweight : dbias;
     if (out) out[c < dim ? c : c - dim] = t;
   }
@@ -346,27 +387,31 @@ struct NormPlan {
   int64_t blocks;
 };
 
-// Lanes, pieces and waves of a row: the fewest lanes that hold it at one piece
-// each up to a wave, then up to `most` pieces, then more waves.
-NormPlan norm_plan(int64_t dim, int most) {
+// Lanes, pieces and waves of a row.  The fewest lanes that hold it at one piece
+// each, up to 8 waves: many short waves keep more rows' loads in flight than
+// few long ones (forward, 16384 x 2048 bf16 with an fp32 residual, 4 / 2 / 1
+// pieces: 80.3 / 76.6 / 72.1 us; 8192 x 4096 85.7 / 81.8 / 74.8; with the
+// backward, 16384 x 2048 bf16, 2 / 1 pieces: 114.0 / 102.7).  Then two pieces
+// (4096 x 8000 forward: 57.8 us, 65.1 at one piece and 16 waves).  Then, forward,
+// 16 waves; backward, whose column sums take 16 registers a piece, four pieces
+// (2048 x 16384: 217 us, 229 at two pieces and 16 waves, which spill).
+NormPlan norm_plan(int64_t dim, bool backward) {
   NormPlan p;
   p.group = 8;
   while (p.group < 64 && p.group * kPiece < dim) p.group *= 2;
-  p.pieces = 1;
-  while (p.pieces < most && p.group * kPiece * p.pieces < dim) p.pieces *= 2;
-  p.row_waves = 1;
-  while (p.group * kPiece * p.pieces * p.row_waves < dim) p.row_waves *= 2;
-  while (p.row_waves > kMaxRowWaves) {
-    p.row_waves /= 2;
-    p.pieces *= 2;
-  }
+  p.pieces = p.row_waves = 1;
+  const auto holds = [&] { return (int64_t)p.group * kPiece * p.pieces * p.row_waves >= dim; };
+  while (!holds() && p.row_waves < 8) p.row_waves *= 2;
+  if (!holds()) p.pieces = 2;
+  if (!holds()) backward ? p.pieces = 4 : p.row_waves = 16;
+  if (!holds()) p.pieces = 4, p.row_waves = 16;
   p.threads = 256;
   p.blocks = 0;
   return p;
 }
 
 NormPlan fwd_plan(int64_t rows, int64_t dim) {
-  NormPlan p = norm_plan(dim, 4);
+  NormPlan p = norm_plan(dim, false);
   if (p.row_waves > 1) {
     p.threads = 64 * p.row_waves;
     p.blocks = rows;
@@ -377,14 +422,17 @@ NormPlan fwd_plan(int64_t rows, int64_t dim) {
   return p;
 }
 
-constexpr int64_t kBwdBlocks = 512;
-
+// Two blocks to a compute unit, each with a partial row of column sums; one
+// where a row takes the whole block and the partial rows are long (8192 x 4096
+// training step 190 us, 196 at 512 blocks; 2048 x 16384 217 against 232; but
+// 8191 x 1001, four rows to a block, 40 us at 512 and 45 at 128).
 NormPlan bwd_plan(int64_t rows, int64_t dim) {
-  NormPlan p = norm_plan(dim, 2);
+  NormPlan p = norm_plan(dim, true);
   const int waves = std::max(p.row_waves, kBwdWaves);
   p.threads = 64 * waves;
   const int64_t groups = (int64_t)(waves / p.row_waves) * (64 / p.group);
-  p.blocks = std::min<int64_t>(kBwdBlocks, (rows + groups - 1) / groups);
+  const int64_t most = p.row_waves < kBwdWaves ? 512 : 256;
+  p.blocks = std::min<int64_t>(most, (rows + groups - 1) / groups);
   return p;
 }
 
@@ -419,11 +467,18 @@ hipError_t launch_norm_fwd(const NormFwdArgs& a, const NormPlan& p, bool rms, hi
 
 template <typename IoT, typename ResT, bool kRms>
 hipError_t launch_norm_bwd(const NormBwdArgs& a, const NormPlan& p, hipStream_t st) {
-  const bool join = a.part && p.threads > 64 * p.row_waves;  // dim <= 4096: at most 32 KB
-  const size_t lds = join ? (size_t)2 * a.dim * 4 : 0;
+  // Blocks of several row groups join their column sums: kBwdWaves waves of
+  // 2 x pieces x lanes x 8 floats, at most 64 KB.
+  const bool join = a.part && p.threads > 64 * p.row_waves;
+  const size_t lds = join ? (size_t)(p.threads / 64) * 2 * p.pieces * p.group * kPiece * 4 : 0;
 #define SSM_NORM_CALL(G, K)                                                                                     \
-  hipLaunchKernelGGL((norm_bwd_kernel<IoT, ResT, G, K, kRms>), dim3((unsigned)p.blocks), dim3(p.threads), lds, st, a)
-  SSM_NORM_GEOMETRY(SSM_NORM_CALL)
+  hipLaunchKernelGGL((norm_bwd_kernel<IoT, ResT, G, K, kRms, 64 * kBwdWaves>), dim3((unsigned)p.blocks),        \
+                     dim3(p.threads), lds, st, a)
+  if (p.threads > 64 * kBwdWaves)
+    hipLaunchKernelGGL((norm_bwd_kernel<IoT, ResT, 64, 4, kRms, 64 * kMaxRowWaves>), dim3((unsigned)p.blocks),
+                       dim3(p.threads), lds, st, a);
+  else
+    SSM_NORM_GEOMETRY(SSM_NORM_CALL)
 #undef SSM_NORM_CALL
   return hipGetLastError();
 }
@@ -531,7 +586,7 @@ ssm_status_t ssm_norm_bwd(int64_t rows, int64_t dim, ssm_dtype_t io, ssm_dtype_t
   else
     e = launch_norm_bwd<bf16_t, float>(a, p, rms, hs);
   if (e == hipSuccess && sums) {
-    hipLaunchKernelGGL(norm_bwd_reduce_kernel, dim3((unsigned)((2 * dim + 63) / 64)), dim3(1024), 0, hs, a.part,
+    hipLaunchKernelGGL(norm_bwd_reduce_kernel, dim3((unsigned)((2 * dim + 31) / 32)), dim3(1024), 0, hs, a.part,
                        dweight, dbias, (int)p.blocks, (int)dim);
     e = hipGetLastError();
   }

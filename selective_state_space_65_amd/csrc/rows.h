@@ -1,8 +1,9 @@
 // rows.h -- loads and stores of consecutive elements of a row whose start need
 // only be element-aligned (rows of an odd length start anywhere).  The target
 // takes vector accesses at any element alignment, so a whole piece is one
-// 16-byte access (two for 8 fp32 values) whatever the row's length; a piece
-// that ends past the row is read and written element by element.  Internal:
+// 16-byte access (two for 8 fp32 values) whatever the row's length.  A piece
+// that ends past the row is read as the row's last 8 elements, shifted into
+// place, so that no lane reads past the row and none takes a loop of its own.  Internal:
 // not part of the C ABI.
 #pragma once
 
@@ -56,6 +57,26 @@ struct Raw8<float> {
 #pragma unroll
     for (int j = 0; j < 8; ++j) (j < 4 ? lo : hi)[j & 3] = t + j < n ? __float_as_uint(row[t + j]) : 0u;
   }
+  __device__ __forceinline__ void clear() { lo = hi = words4{0, 0, 0, 0}; }
+  // Elements s.. move to the front, zeros follow.
+  __device__ __forceinline__ void drop(int s) {
+    uint32_t v[8];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = lo[j], v[4 + j] = hi[j];
+    shift_words<4>(v, s & 4);
+    shift_words<2>(v, s & 2);
+    shift_words<1>(v, s & 1);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      lo[j] = s < 8 ? v[j] : 0u;
+      hi[j] = s < 8 ? v[4 + j] : 0u;
+    }
+  }
+  template <int n>
+  static __device__ __forceinline__ void shift_words(uint32_t v[8], int on) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = on ? (j + n < 8 ? v[j + n] : 0u) : v[j];
+  }
   __device__ __forceinline__ void get(float out[8]) const {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -79,6 +100,15 @@ struct Raw8<bf16_t> {
       const uint32_t hi = t + 2 * j + 1 < n ? row[t + 2 * j + 1] : 0u;
       w[j] = lo | hi << 16;
     }
+  }
+  __device__ __forceinline__ void clear() { w = words4{0, 0, 0, 0}; }
+  // Elements s.. move to the front, zeros follow.
+  __device__ __forceinline__ void drop(int s) {
+    uint32_t a = w[0], b = w[1], c = w[2], d = w[3];
+    if (s & 4) a = c, b = d, c = 0, d = 0;
+    if (s & 2) a = b, b = c, c = d, d = 0;
+    if (s & 1) a = a >> 16 | b << 16, b = b >> 16 | c << 16, c = c >> 16 | d << 16, d >>= 16;
+    w = s < 8 ? words4{a, b, c, d} : words4{0, 0, 0, 0};
   }
   __device__ __forceinline__ void get(float out[8]) const {
 #pragma unroll
@@ -109,15 +139,23 @@ __device__ __forceinline__ void store8u(bf16_t* p, const float v[8]) {
   store16<kStream>(p, a);
 }
 
-// Elements [t, t + 8) of a row of n; full: t + 8 <= n.  Elements past the row
-// read as 0 and are not written.
+// Elements [t, t + 8) of a row of n; full: t + 8 <= n in every lane of the
+// wave.  Elements past the row read as 0 and are not written.
 template <bool kStream = false, typename T>
 __device__ __forceinline__ Raw8<T> load_raw8(const T* row, int t, int n, bool full) {
   Raw8<T> r;
-  if (full)
+  if (full) {
     r.template load<kStream>(row + t);
-  else
+  } else if (n % 8 == 0) {  // pieces are whole or empty
+    r.clear();
+    if (t < n) r.template load<kStream>(row + t);
+  } else if (n > 8) {
+    const int at = t < n - 8 ? t : n - 8;
+    r.template load<kStream>(row + at);
+    r.drop(t - at);
+  } else {
     r.load_part(row, t, n);
+  }
   return r;
 }
 
@@ -128,9 +166,9 @@ __device__ __forceinline__ void load_row8(const T* row, int t, int n, bool full,
 
 template <bool kStream = false, typename T>
 __device__ __forceinline__ void store_row8(T* row, int t, int n, bool full, const float v[8]) {
-  if (full) {
+  if (full || t + 8 <= n) {
     store8u<kStream>(row + t, v);
-  } else {
+  } else if (t < n) {
 #pragma unroll
     for (int j = 0; j < 8; ++j)
       if (t + j < n) Io<T>::store1(row + t + j, v[j]);
