@@ -664,14 +664,13 @@ def _state_update(disc, state, u, delta, A, B, C, D, z, delta_bias, delta_softpl
     return out
 
 
-@functools.lru_cache(maxsize=None)
-def _queries():
-    """(current device index, raw handle of a device's current stream): torch's own bindings of
-    torch.cuda.current_device and current_stream, whose Python objects cost 2 us a call; the public
-    functions where they are missing."""
-    device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
-    raw = getattr(torch._C, "_cuda_getCurrentRawStream", lambda i: torch.cuda.current_stream(i).cuda_stream)
-    return device, raw
+# The entry points below cost as much host time as their smallest kernels run,
+# so their hot path is kept short: the current device and the raw handle of a
+# device's current stream come from torch's own bindings (0.1 us; the public
+# torch.cuda.current_stream builds an object, 2 us), with the public functions
+# where those are missing, and pointers are taken without a helper.
+_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda i: torch.cuda.current_stream(i).cuda_stream)
 
 
 @functools.lru_cache(maxsize=1024)
@@ -682,28 +681,24 @@ def _workspace_bytes(fn, *sizes):
     return size.value
 
 
-def _placed(fn):
-    """Runs fn with its first argument's device current, on the caller's stream.
+def _elsewhere(fn, stream, **args):
+    """Runs fn with its first argument's device current, on `stream` where one is given.
 
-    Without a stream, that is the device's current stream.  With one, the
-    outputs and the workspace are allocated on it (so that freed memory is
-    handed on in its order), and the tensors passed in are recorded on it.
+    The outputs and the workspace are then allocated on that stream (so that
+    freed memory is handed on in its order), and the tensors passed in are
+    recorded on it.
     """
-    @functools.wraps(fn)
-    def call(first, *args, stream=None, **kw):
-        if not first.is_cuda:
-            raise ValueError("%s: tensors must be on a GPU, got %s" % (fn.__name__, first.device))
-        if stream is None and first.get_device() == _queries()[0]():
-            return fn(first, *args, **kw)
-        with torch.cuda.device(first.device):
-            if stream is None:
-                return fn(first, *args, **kw)
-            with torch.cuda.stream(stream):
-                for t in (first,) + args + tuple(kw.values()):
-                    if isinstance(t, torch.Tensor):
-                        t.record_stream(stream)
-                return fn(first, *args, **kw)
-    return call
+    first = next(iter(args.values()))
+    if not first.is_cuda:
+        raise ValueError("%s: tensors must be on a GPU, got %s" % (fn.__name__, first.device))
+    with torch.cuda.device(first.device):
+        if stream is None:
+            return fn(**args)
+        with torch.cuda.stream(stream):
+            for t in args.values():
+                if isinstance(t, torch.Tensor):
+                    t.record_stream(stream)
+            return fn(**args)
 
 
 def _mode_code(mode):
@@ -734,9 +729,8 @@ def gated_ckpt_shape(batch, dim, seqlen):
     return (batch, dim, (seqlen + GATED_CKPT_STEP - 1) // GATED_CKPT_STEP)
 
 
-@_placed
 def gated_scan_fwd(x, gate, gate_bias=None, rate=None, z=None, reset=None, h0=None, mode="plain", out=None,
-                   last_state=None, ckpt=None, return_last_state=True):
+                   last_state=None, ckpt=None, return_last_state=True, stream=None):
     """Gated linear recurrence over the sequence (ssm_gated_scan_fwd); returns (y, last_state).
 
     h_l = a_l h_{l-1} + w_l x_l with a = sigmoid(gate + gate_bias), or
@@ -749,8 +743,10 @@ def gated_scan_fwd(x, gate, gate_bias=None, rate=None, z=None, reset=None, h0=No
     (batch, dim) float32, which may be the same tensor as last_state.  y has
     the io dtype; last_state is float32 (None when return_last_state is False).
     ckpt, when given, receives the backward's checkpoints (gated_ckpt_shape).
-    stream (keyword): run on that torch.cuda.Stream instead of the current one.
+    stream: run on that torch.cuda.Stream instead of the current one.
     """
+    if stream is not None or not x.is_cuda or x.get_device() != _device():
+        return _elsewhere(gated_scan_fwd, **locals())
     batch, dim, seqlen, io, dev = _gated_inputs(x, gate, gate_bias, rate, z, reset)
     code = _mode_code(mode)
     if h0 is not None:
@@ -765,28 +761,30 @@ def gated_scan_fwd(x, gate, gate_bias=None, rate=None, z=None, reset=None, h0=No
         last_state = torch.empty((batch, dim), dtype=torch.float32, device=dev)
     if ckpt is not None:
         _need(ckpt, "ckpt", gated_ckpt_shape(batch, dim, seqlen), torch.float32, dev)
-    st = load_library().ssm_gated_scan_fwd(batch, dim, seqlen, _io_code(io), code, _ptr(x), _ptr(gate),
-                                           _ptr(gate_bias), _ptr(rate), _ptr(z), _ptr(reset), _ptr(h0), _ptr(out),
-                                           _ptr(last_state), _ptr(ckpt), _queries()[1](dev.index))
-    _check("ssm_gated_scan_fwd", st)
+    lib = _lib or load_library()
+    st = lib.ssm_gated_scan_fwd(batch, dim, seqlen, _io_code(io), code, x.data_ptr(), gate.data_ptr(),
+                                _ptr(gate_bias), _ptr(rate), _ptr(z), _ptr(reset), _ptr(h0), out.data_ptr(),
+                                _ptr(last_state), _ptr(ckpt), _raw_stream(dev.index))
+    if st:
+        _check("ssm_gated_scan_fwd", st)
     return out, last_state
 
 
-@_placed
 def gated_scan_fwd_save(x, gate, gate_bias=None, rate=None, z=None, reset=None, h0=None, mode="plain", out=None,
-                        last_state=None, ckpt=None):
+                        last_state=None, ckpt=None, stream=None):
     """gated_scan_fwd that also writes the backward's checkpoints; returns (y, last_state, ckpt)."""
+    if stream is not None or not x.is_cuda or x.get_device() != _device():
+        return _elsewhere(gated_scan_fwd_save, **locals())
     if ckpt is None:
         if x.dim() != 3:
             raise ValueError("x must be (batch, dim, seqlen)")
         ckpt = torch.empty(gated_ckpt_shape(*x.shape), dtype=torch.float32, device=x.device)
-    out, last_state = gated_scan_fwd.__wrapped__(x, gate, gate_bias, rate, z, reset, h0, mode, out, last_state, ckpt)
+    out, last_state = gated_scan_fwd(x, gate, gate_bias, rate, z, reset, h0, mode, out, last_state, ckpt)
     return out, last_state, ckpt
 
 
-@_placed
 def gated_scan_bwd(x, gate, dy, ckpt, gate_bias=None, rate=None, z=None, reset=None, dlast=None, mode="plain",
-                   need=("dgate_bias", "drate", "dz", "dh0")):
+                   need=("dgate_bias", "drate", "dz", "dh0"), stream=None):
     """Gradients of sum(dy * y) + sum(dlast * last_state) for gated_scan_fwd (ssm_gated_scan_bwd).
 
     ckpt is what gated_scan_fwd_save wrote for the same x, gate, gate_bias,
@@ -794,6 +792,8 @@ def gated_scan_bwd(x, gate, dy, ckpt, gate_bias=None, rate=None, z=None, reset=N
     named in `need`, dgate_bias (dim,), drate (dim,, only with a rate) and dh0
     (batch, dim) in float32 and dz (io dtype, only with z); None for the others.
     """
+    if stream is not None or not x.is_cuda or x.get_device() != _device():
+        return _elsewhere(gated_scan_bwd, **locals())
     batch, dim, seqlen, io, dev = _gated_inputs(x, gate, gate_bias, rate, z, reset)
     code = _mode_code(mode)
     f32 = torch.float32
@@ -806,24 +806,26 @@ def gated_scan_bwd(x, gate, dy, ckpt, gate_bias=None, rate=None, z=None, reset=N
              drate=torch.empty(dim, dtype=f32, device=dev) if ("drate" in need and rate is not None) else None,
              dz=torch.empty_like(x) if ("dz" in need and z is not None) else None,
              dh0=torch.empty((batch, dim), dtype=f32, device=dev) if "dh0" in need else None)
-    lib = load_library()
+    lib = _lib or load_library()
     io_code = _io_code(io)
     size = _workspace_bytes("ssm_gated_scan_bwd_workspace_bytes", batch, dim, seqlen, io_code)
     work = torch.empty(size, dtype=torch.uint8, device=dev) if size else None
-    st = lib.ssm_gated_scan_bwd(batch, dim, seqlen, io_code, code, _ptr(x), _ptr(gate), _ptr(gate_bias), _ptr(rate),
-                                _ptr(z), _ptr(reset), _ptr(ckpt), _ptr(dy), _ptr(dlast), _ptr(g["dx"]),
-                                _ptr(g["dgate"]), _ptr(g["dgate_bias"]), _ptr(g["drate"]), _ptr(g["dz"]),
-                                _ptr(g["dh0"]), _ptr(work), size, _queries()[1](dev.index))
-    _check("ssm_gated_scan_bwd", st)
+    st = lib.ssm_gated_scan_bwd(batch, dim, seqlen, io_code, code, x.data_ptr(), gate.data_ptr(), _ptr(gate_bias),
+                                _ptr(rate), _ptr(z), _ptr(reset), _ptr(ckpt), dy.data_ptr(), _ptr(dlast),
+                                g["dx"].data_ptr(), g["dgate"].data_ptr(), _ptr(g["dgate_bias"]), _ptr(g["drate"]),
+                                _ptr(g["dz"]), _ptr(g["dh0"]), _ptr(work), size, _raw_stream(dev.index))
+    if st:
+        _check("ssm_gated_scan_bwd", st)
     return g
 
 
-@_placed
-def gated_state_update(state, x, gate, gate_bias=None, rate=None, z=None, mode="plain", out=None):
+def gated_state_update(state, x, gate, gate_bias=None, rate=None, z=None, mode="plain", out=None, stream=None):
     """One decode step (ssm_gated_state_update), updating state (batch, dim) float32 in place; returns y (batch, dim).
 
     x, gate, z: (batch, dim) in one io dtype; gate_bias, rate, mode as gated_scan_fwd.
     """
+    if stream is not None or not state.is_cuda or state.get_device() != _device():
+        return _elsewhere(gated_state_update, **locals())
     if state.dim() != 2:
         raise ValueError("state must be (batch, dim)")
     shape, io, dev = state.shape, x.dtype, state.device
@@ -841,10 +843,12 @@ def gated_state_update(state, x, gate, gate_bias=None, rate=None, z=None, mode="
         out = torch.empty_like(x)
     else:
         _need(out, "out", shape, io, dev)
-    st = load_library().ssm_gated_state_update(shape[0], shape[1], _io_code(io), code, _ptr(state), _ptr(x),
-                                               _ptr(gate), _ptr(gate_bias), _ptr(rate), _ptr(z), _ptr(out),
-                                               _queries()[1](dev.index))
-    _check("ssm_gated_state_update", st)
+    lib = _lib or load_library()
+    st = lib.ssm_gated_state_update(shape[0], shape[1], _io_code(io), code, state.data_ptr(), x.data_ptr(),
+                                    gate.data_ptr(), _ptr(gate_bias), _ptr(rate), _ptr(z), out.data_ptr(),
+                                    _raw_stream(dev.index))
+    if st:
+        _check("ssm_gated_state_update", st)
     return out
 
 
@@ -859,9 +863,8 @@ def _need_residual(t, name, shape, io, device):
     _need(t, name, shape, io if t.dtype == io else torch.float32, device)
 
 
-@_placed
 def norm_fwd(x, weight=None, bias=None, residual=None, eps=1e-5, kind="layer", out=None, residual_out=None,
-             save_stats=True):
+             save_stats=True, stream=None):
     """Norm over the last dimension with the residual add in front (ssm_norm_fwd); returns (y, s, mean, rstd).
 
     s = x + residual, rounded to the residual's dtype (s is x without a
@@ -871,8 +874,10 @@ def norm_fwd(x, weight=None, bias=None, residual=None, eps=1e-5, kind="layer", o
     float32.  residual_out may be the residual itself, which is then updated
     in place.  mean and rstd are float32 (...,) for norm_bwd: None without
     save_stats, and mean None for "rms".
-    stream (keyword): run on that torch.cuda.Stream instead of the current one.
+    stream: run on that torch.cuda.Stream instead of the current one.
     """
+    if stream is not None or not x.is_cuda or x.get_device() != _device():
+        return _elsewhere(norm_fwd, **locals())
     if x.dim() < 1:
         raise ValueError("x must be (..., dim)")
     shape, io, dev = x.shape, x.dtype, x.device
@@ -906,15 +911,15 @@ def norm_fwd(x, weight=None, bias=None, residual=None, eps=1e-5, kind="layer", o
         rstd = torch.empty(shape[:-1], dtype=f32, device=dev)
         if kind == "layer":
             mean = torch.empty(shape[:-1], dtype=f32, device=dev)
-    st = load_library().ssm_norm_fwd(rows, dim, io_code, res_code, code, _ptr(x), _ptr(residual), _ptr(weight),
-                                     _ptr(bias), eps, _ptr(out), _ptr(residual_out), _ptr(mean), _ptr(rstd),
-                                     _queries()[1](dev.index))
-    _check("ssm_norm_fwd", st)
+    lib = _lib or load_library()
+    st = lib.ssm_norm_fwd(rows, dim, io_code, res_code, code, x.data_ptr(), _ptr(residual), _ptr(weight), _ptr(bias),
+                          eps, out.data_ptr(), _ptr(residual_out), _ptr(mean), _ptr(rstd), _raw_stream(dev.index))
+    if st:
+        _check("ssm_norm_fwd", st)
     return out, s, mean, rstd
 
 
-@_placed
-def norm_bwd(dy, s, rstd, mean=None, weight=None, dresidual_out=None, kind="layer", need=("dweight", "dbias")):
+def norm_bwd(dy, s, rstd, mean=None, weight=None, dresidual_out=None, kind="layer", need=("dweight", "dbias"), stream=None):
     """Gradients of sum(dy * y) + sum(dresidual_out * s) for norm_fwd (ssm_norm_bwd).
 
     s, mean and rstd are what norm_fwd returned (mean for kind "layer" only).
@@ -924,6 +929,8 @@ def norm_bwd(dy, s, rstd, mean=None, weight=None, dresidual_out=None, kind="laye
     that is another, else None; and, when named in `need`, dweight and dbias
     (dim,) float32.
     """
+    if stream is not None or not dy.is_cuda or dy.get_device() != _device():
+        return _elsewhere(norm_bwd, **locals())
     if dy.dim() < 1:
         raise ValueError("dy must be (..., dim)")
     shape, io, dev = dy.shape, dy.dtype, dy.device
@@ -947,14 +954,15 @@ def norm_bwd(dy, s, rstd, mean=None, weight=None, dresidual_out=None, kind="laye
     g = dict(dx=torch.empty_like(dy), dresidual=torch.empty_like(s) if s.dtype != io else None,
              dweight=torch.empty(dim, dtype=f32, device=dev) if "dweight" in need else None,
              dbias=torch.empty(dim, dtype=f32, device=dev) if "dbias" in need else None)
-    lib = load_library()
+    lib = _lib or load_library()
     io_code, res_code = _io_code(io), _io_code(s.dtype)
     size = 0
     if g["dweight"] is not None or g["dbias"] is not None:
         size = _workspace_bytes("ssm_norm_bwd_workspace_bytes", rows, dim, io_code, res_code)
     work = torch.empty(size, dtype=torch.uint8, device=dev) if size else None
-    st = lib.ssm_norm_bwd(rows, dim, io_code, res_code, code, _ptr(dy), _ptr(s), _ptr(weight), _ptr(mean),
-                          _ptr(rstd), _ptr(dresidual_out), _ptr(g["dx"]), _ptr(g["dresidual"]), _ptr(g["dweight"]),
-                          _ptr(g["dbias"]), _ptr(work), size, _queries()[1](dev.index))
-    _check("ssm_norm_bwd", st)
+    st = lib.ssm_norm_bwd(rows, dim, io_code, res_code, code, dy.data_ptr(), s.data_ptr(), _ptr(weight), _ptr(mean),
+                          _ptr(rstd), _ptr(dresidual_out), g["dx"].data_ptr(), _ptr(g["dresidual"]),
+                          _ptr(g["dweight"]), _ptr(g["dbias"]), _ptr(work), size, _raw_stream(dev.index))
+    if st:
+        _check("ssm_norm_bwd", st)
     return g

@@ -64,13 +64,14 @@ struct GatedArgs {
   void* dx;
   void* dgate;
   void* dz;      // may be null
-  float* dbias;  // [batch][dim] sums per row, may be null
-  float* drate;  // [batch][dim], may be null
+  float* dbias;  // may be null: per-row sums [batch][dim], or [dim] where a block has every batch row
+  float* drate;  // likewise
   float* dh0;    // may be null
   int64_t channels;  // batch * dim
   int64_t dim;
   int seqlen;
   int ckpts;  // checkpoints per channel
+  int waves;  // waves of a row (64-lane groups only)
 };
 
 // ---- affine maps h -> a h + b ------------------------------------------------
@@ -527,9 +528,15 @@ template <typename IoT, int G, int kMode, bool kRate>
 __global__ __launch_bounds__(G == 64 ? 64 * kMaxBwdWaves : 256, 3) void gated_bwd_kernel(GatedArgs p) {
   __shared__ Map totals[2][G == 64 ? kMaxWaves : 1];
   const int lane = threadIdx.x & 63, gl = lane & (G - 1);
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int waves = blockDim.x >> 6;
+  const int block_wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int block_waves = blockDim.x >> 6;
+  // G = 64: the block's waves in rows of `waves`; several rows are the batch
+  // rows of one channel, whose sums the block then has whole.
+  const int waves = G == 64 ? p.waves : block_waves;
+  const int wave = G == 64 ? block_wave % waves : block_wave, first = block_wave - wave;
+  const bool joined = G == 64 && block_waves > waves;
   int64_t ch = G == 64 ? (int64_t)blockIdx.x : ((int64_t)blockIdx.x * waves + wave) * (64 / G) + lane / G;
+  if (joined) ch += block_wave / waves * p.dim;
   const bool live = ch < p.channels;
   ch = live ? ch : p.channels - 1;
   const int64_t bt = ch / p.dim, d = ch - bt * p.dim;
@@ -606,10 +613,10 @@ __global__ __launch_bounds__(G == 64 ? 64 * kMaxBwdWaves : 256, 3) void gated_bw
       drop = drop_bits(a, drop);
     }
     if (__ballot(drop != 0))
-      bwd_tile<G, kMode, kRate, true>(x, g, q, h_in, drop, valid, lane, gl, wave, waves, totals[parity], mu, ds, dx,
+      bwd_tile<G, kMode, kRate, true>(x, g, q, h_in, drop, valid, lane, gl, wave, waves, totals[parity] + first, mu, ds, dx,
                                       dg, sum_r);
     else
-      bwd_tile<G, kMode, kRate, false>(x, g, q, h_in, drop, valid, lane, gl, wave, waves, totals[parity], mu, ds, dx,
+      bwd_tile<G, kMode, kRate, false>(x, g, q, h_in, drop, valid, lane, gl, wave, waves, totals[parity] + first, mu, ds, dx,
                                        dg, sum_r);
     float tb = 0.0f;
 #pragma unroll
@@ -631,23 +638,23 @@ __global__ __launch_bounds__(G == 64 ? 64 * kMaxBwdWaves : 256, 3) void gated_bw
     sum_b += __shfl_xor(sum_b, s);
     if constexpr (kRate) sum_r += __shfl_xor(sum_r, s);
   }
-  if constexpr (G == 64) {
-    if (waves > 1) {
-      lds_barrier();  // the last tile's totals have been read
-      if (lane == 0) totals[0][wave] = Map{sum_b, sum_r};
-      lds_barrier();
-      sum_b = sum_r = 0.0f;
-      for (int w = 0; w < waves; ++w) {
-        sum_b += totals[0][w].a;
-        sum_r += totals[0][w].b;
-      }
-      if (wave != 0) return;
+  if (p.dh0 && live && gl == 0 && (G < 64 || wave == 0)) p.dh0[ch] = mu;
+  int64_t out = ch;
+  if (G == 64 && block_waves > 1) {
+    lds_barrier();  // the last tile's totals have been read
+    if (lane == 0) totals[0][block_wave] = Map{sum_b, sum_r};
+    lds_barrier();
+    if (block_wave != 0) return;
+    sum_b = sum_r = 0.0f;
+    for (int w = 0; w < block_waves; ++w) {
+      sum_b += totals[0][w].a;
+      sum_r += totals[0][w].b;
     }
+    if (joined) out = d;
   }
   if (live && gl == 0) {
-    if (p.dh0) p.dh0[ch] = mu;
-    if (p.dbias) p.dbias[ch] = sum_b;
-    if (kRate && p.drate) p.drate[ch] = sum_r;
+    if (p.dbias) p.dbias[out] = sum_b;
+    if (kRate && p.drate) p.drate[out] = sum_r;
   }
 }
 
@@ -744,24 +751,64 @@ bool gated_mode_ok(ssm_gated_mode_t mode) {
 
 struct GatedPlan {
   int group;  // lanes per channel
+  int waves;  // of a row, 64-lane groups
   int threads;
   int64_t blocks;
+  bool joined;  // backward: a block has every batch row of its channels
 };
 
-// Waves the launch aims at, by giving a channel's row to more waves of a
-// block: 32 (forward) and 16 (backward) for each of the 1024 SIMDs, so that
-// waves keep arriving as others end.  Measured, forward / 8192: 1 x 2560 x
-// 131072 fp32 750 / 785 us, 2 x 2048 x 8192 bf16 52.8 / 57.5 us; backward with
-// its forward, 16384 / 8192: 8 x 1536 x 2048 fp32 220.5 / 228.8 us.
-constexpr int64_t kFwdWaves = 32768;
-constexpr int64_t kBwdWaves = 16384;
+// Waves that share a row of `tiles` 512-token tiles.  More waves fill the chip
+// (from 12 on each of the 1024 SIMDs; past `enough` the launch only gets
+// longer), but the row is walked in steps of that many tiles, and a last step
+// that is mostly empty costs a whole one; 16 waves that walk it in a single
+// step have nothing to load ahead and one block to a compute unit.  1, 2, 3,
+// 4, 8 and 16 are the counts whose blocks fill a compute unit's registers.
+// Measured (us, bf16 unless said, waves in brackets): forward 3 x 1001 x 8001
+// 47.9 [8] 56.4 [16] 52.8 [6]; 4 x 1024 x 4160 30.3 [3] 33.9 [5] 41.9 [8]; 2 x
+// 5120 x 1500 29.5 [3] 35.6 [4] 36.1 [2]; fp32 1 x 2560 x 131072 750 [16] 774
+// [8] 798 [10], 8 x 1536 x 2048 72.7 [4] 78.9 [2], 1 x 2560 x 8192 65.1 [8]
+// 70.5 [16]; training step 4 x 1024 x 4160 86.8 [3] 102.5 [4] 124 [5]; 8 x 512
+// x 8200 160 [4] 188 [6] 207 [5]; 8 x 1536 x 2048 fp32 220.5 [2] 228.8 [1].
+constexpr int64_t kFewWaves = 12288;
+constexpr int64_t kEnoughFwd = 49152;
+constexpr int64_t kEnoughBwd = 24576;
+
+int64_t row_waves(int64_t channels, int64_t tiles, int64_t most, int64_t enough) {
+  if (channels * most < kFewWaves) {  // few rows: all the waves, balanced over the steps
+    const int64_t steps = (tiles + most - 1) / most;
+    return (tiles + steps - 1) / steps;
+  }
+  int64_t best = 1;
+  double least = 0.0;
+  for (int64_t w : {1, 2, 3, 4, 8, 16}) {
+    if (w > most || w > tiles || (w > 1 && channels * w > enough && channels * best >= kFewWaves)) break;
+    const int64_t steps = (tiles + w - 1) / w;
+    double cost = (double)(steps * w) / (double)tiles;
+    if (steps == 1 && w == 16) cost *= 1.1;
+    if (channels * w < kFewWaves) cost += (double)kFewWaves / (double)(channels * w);
+    if (w == 1 || cost <= least) best = w, least = cost;
+  }
+  return best;
+}
 
 // Rows of at most 256 tokens take the fewest lanes that hold them in one tile
 // (1, 8, 16 or 32), several channels to a wave.  Longer rows take whole waves:
 // groups of 16 lanes walking a long row lost to them even where they fill the
 // chip (4 x 4096 x 4096 bf16 forward 123.2 us at 16 lanes, 112.5 at 64).
-GatedPlan gated_plan(int64_t channels, int64_t seqlen, bool backward) {
+//
+// In the backward a block of whole rows takes all batch rows of its channel
+// where they fit 8 waves, so that their sums need no second launch: while the
+// launches are what the call waits for (3 x 1000 x 777 training step 35.4 ->
+// 31.0 us).  Larger rows of a batch lie far apart, often a power of two, and
+// read together they meet in the same memory channels (4 x 4096 x 4096 bf16
+// 296 -> 357 us).
+constexpr int64_t kJoinTokens = (int64_t)1 << 22;
+
+GatedPlan gated_plan(int64_t batch, int64_t dim, int64_t seqlen, bool backward) {
+  const int64_t channels = batch * dim;
   GatedPlan p;
+  p.waves = 1;
+  p.joined = batch == 1;
   if (seqlen <= 32 * kTok) {
     p.group = 1;
     while (p.group * kTok < seqlen) p.group = p.group == 1 ? 8 : 2 * p.group;
@@ -769,20 +816,21 @@ GatedPlan gated_plan(int64_t channels, int64_t seqlen, bool backward) {
     const int64_t per_block = 256 / p.group;
     p.blocks = (channels + per_block - 1) / per_block;
   } else {
-    const int most = backward ? kMaxBwdWaves : kMaxWaves;
-    const int64_t want = backward ? kBwdWaves : kFwdWaves;
-    int64_t waves = 1;
-    while (waves < most && channels * waves < want && waves * 64 * kTok < seqlen) waves *= 2;
+    const int64_t tiles = (seqlen + 64 * kTok - 1) / (64 * kTok);
+    const int64_t waves =
+        backward ? row_waves(channels, tiles, kMaxBwdWaves, kEnoughBwd) : row_waves(channels, tiles, kMaxWaves, kEnoughFwd);
     p.group = 64;
-    p.threads = (int)(64 * waves);
-    p.blocks = channels;
+    p.waves = (int)waves;
+    const int64_t rows = backward && batch * waves <= kMaxBwdWaves && channels * seqlen <= kJoinTokens ? batch : 1;
+    p.joined = rows == batch;
+    p.threads = (int)(64 * waves * rows);
+    p.blocks = channels / rows;
   }
   return p;
 }
 
 template <typename IoT, int kMode, bool kRate, bool kBwd>
-hipError_t launch_gated(const GatedArgs& a, hipStream_t st) {
-  const GatedPlan p = gated_plan(a.channels, a.seqlen, kBwd);
+hipError_t launch_gated(const GatedArgs& a, const GatedPlan& p, hipStream_t st) {
   const dim3 grid((unsigned)p.blocks), block(p.threads);
 #define SSM_GATED_LAUNCH(G)                                                                          \
   if constexpr (kBwd)                                                                                \
@@ -802,17 +850,17 @@ hipError_t launch_gated(const GatedArgs& a, hipStream_t st) {
 }
 
 template <typename IoT, bool kBwd>
-hipError_t launch_gated(const GatedArgs& a, ssm_gated_mode_t mode, hipStream_t st) {
+hipError_t launch_gated(const GatedArgs& a, const GatedPlan& p, ssm_gated_mode_t mode, hipStream_t st) {
   switch (mode) {
     case SSM_GATED_PLAIN:
-      return a.rate ? launch_gated<IoT, SSM_GATED_PLAIN, true, kBwd>(a, st)
-                    : launch_gated<IoT, SSM_GATED_PLAIN, false, kBwd>(a, st);
+      return a.rate ? launch_gated<IoT, SSM_GATED_PLAIN, true, kBwd>(a, p, st)
+                    : launch_gated<IoT, SSM_GATED_PLAIN, false, kBwd>(a, p, st);
     case SSM_GATED_CONVEX:
-      return a.rate ? launch_gated<IoT, SSM_GATED_CONVEX, true, kBwd>(a, st)
-                    : launch_gated<IoT, SSM_GATED_CONVEX, false, kBwd>(a, st);
+      return a.rate ? launch_gated<IoT, SSM_GATED_CONVEX, true, kBwd>(a, p, st)
+                    : launch_gated<IoT, SSM_GATED_CONVEX, false, kBwd>(a, p, st);
     default:
-      return a.rate ? launch_gated<IoT, SSM_GATED_NORM, true, kBwd>(a, st)
-                    : launch_gated<IoT, SSM_GATED_NORM, false, kBwd>(a, st);
+      return a.rate ? launch_gated<IoT, SSM_GATED_NORM, true, kBwd>(a, p, st)
+                    : launch_gated<IoT, SSM_GATED_NORM, false, kBwd>(a, p, st);
   }
 }
 
@@ -841,9 +889,9 @@ GatedArgs gated_args(const GatedShape& s, int64_t dim, int64_t seqlen, const voi
   return a;
 }
 
-// Workspace of the backward: dgate_bias and drate sums per batch row.  With
-// one batch row the kernel writes the sums themselves.
-int64_t bwd_workspace(const GatedShape& s, int64_t batch) { return batch > 1 ? 2 * s.bd * 4 : 0; }
+// Workspace of the backward: dgate_bias and drate sums per batch row, where no
+// block has them all.
+int64_t bwd_workspace(const GatedShape& s, const GatedPlan& p) { return p.joined ? 0 : 2 * s.bd * 4; }
 
 }  // namespace
 
@@ -872,7 +920,9 @@ ssm_status_t ssm_gated_scan_fwd(int64_t batch, int64_t dim, int64_t seqlen, ssm_
   GatedArgs a = gated_args(s, dim, seqlen, x, gate, gate_bias, rate, z, reset);
   a.h0 = h0; a.y = y; a.last = last_state; a.ckpt = ckpt;
   hipStream_t hs = reinterpret_cast<hipStream_t>(stream);
-  hipError_t e = io == SSM_BF16 ? launch_gated<bf16_t, false>(a, mode, hs) : launch_gated<float, false>(a, mode, hs);
+  const GatedPlan p = gated_plan(batch, dim, seqlen, false);
+  hipError_t e =
+      io == SSM_BF16 ? launch_gated<bf16_t, false>(a, p, mode, hs) : launch_gated<float, false>(a, p, mode, hs);
   return e == hipSuccess ? SSM_OK : hip_fail(e);
 }
 
@@ -880,7 +930,7 @@ ssm_status_t ssm_gated_scan_bwd_workspace_bytes(int64_t batch, int64_t dim, int6
                                                 int64_t* bytes) {
   GatedShape s;
   ssm_status_t st = gated_shape(batch, dim, seqlen, io, &s);
-  if (st == SSM_OK && bytes) *bytes = bwd_workspace(s, batch);
+  if (st == SSM_OK && bytes) *bytes = bwd_workspace(s, gated_plan(batch, dim, seqlen, true));
   return st;
 }
 
@@ -896,7 +946,8 @@ ssm_status_t ssm_gated_scan_bwd(int64_t batch, int64_t dim, int64_t seqlen, ssm_
   if (!x || !gate || !ckpt || !dy || !dx || !dgate) return SSM_ERR_NULL;
   if (!rate) drate = nullptr;
   if (!z) dz = nullptr;
-  const int64_t need = bwd_workspace(s, batch);
+  const GatedPlan p = gated_plan(batch, dim, seqlen, true);
+  const int64_t need = bwd_workspace(s, p);
   if (workspace_bytes < need) return SSM_ERR_WORKSPACE;
   if (need && !workspace) return SSM_ERR_NULL;
   if (!need) workspace = nullptr;
@@ -912,10 +963,11 @@ ssm_status_t ssm_gated_scan_bwd(int64_t batch, int64_t dim, int64_t seqlen, ssm_
   a.ckpt = const_cast<float*>(ckpt);
   a.dy = dy; a.dlast = dlast; a.dx = dx; a.dgate = dgate; a.dz = dz; a.dh0 = dh0;
   float* part = static_cast<float*>(workspace);
+  a.waves = p.waves;
   a.dbias = dgate_bias ? (part ? part : dgate_bias) : nullptr;
   a.drate = drate ? (part ? part + s.bd : drate) : nullptr;
   hipStream_t hs = reinterpret_cast<hipStream_t>(stream);
-  hipError_t e = io == SSM_BF16 ? launch_gated<bf16_t, true>(a, mode, hs) : launch_gated<float, true>(a, mode, hs);
+  hipError_t e = io == SSM_BF16 ? launch_gated<bf16_t, true>(a, p, mode, hs) : launch_gated<float, true>(a, p, mode, hs);
   if (e == hipSuccess && part && (dgate_bias || drate)) {
     hipLaunchKernelGGL(gated_bwd_reduce_kernel, dim3((unsigned)((dim + 63) / 64)), dim3(64), 0, hs, part,
                        part + s.bd, dgate_bias, drate, batch, dim);

@@ -394,15 +394,20 @@ struct NormPlan {
 // backward, 16384 x 2048 bf16, 2 / 1 pieces: 114.0 / 102.7).  Then two pieces
 // (4096 x 8000 forward: 57.8 us, 65.1 at one piece and 16 waves).  Then, forward,
 // 16 waves; backward, whose column sums take 16 registers a piece, four pieces
-// (2048 x 16384: 217 us, 229 at two pieces and 16 waves, which spill).
+// (2048 x 16384: 217 us, 229 at two pieces and 16 waves, which spill).  A
+// forward row of two waves that ends inside a piece takes one wave of two
+// pieces instead: the wave with the end would keep the other waiting (30000 x
+// 777 bf16 24.3 us, 28.5 on two; from three waves on it no longer pays, 16000 x
+// 2001 77.4 us, 83.5 at two pieces).
 NormPlan norm_plan(int64_t dim, bool backward) {
   NormPlan p;
   p.group = 8;
   while (p.group < 64 && p.group * kPiece < dim) p.group *= 2;
   p.pieces = p.row_waves = 1;
   const auto holds = [&] { return (int64_t)p.group * kPiece * p.pieces * p.row_waves >= dim; };
+  if (!backward && dim % kPiece && dim <= 2 * 64 * kPiece && !holds()) p.pieces = 2;
   while (!holds() && p.row_waves < 8) p.row_waves *= 2;
-  if (!holds()) p.pieces = 2;
+  if (!holds() && p.pieces < 2) p.pieces = 2;
   if (!holds()) backward ? p.pieces = 4 : p.row_waves = 16;
   if (!holds()) p.pieces = 4, p.row_waves = 16;
   p.threads = 256;

@@ -94,10 +94,12 @@ def run_all(d, io, mode, seed, what, dlast=True):
 
 # One token; inside and on the edges of a lane (8), of 8 lanes (64), of 16
 # lanes (128), of a wave (512) and of a block's waves; channel counts that leave
-# the last wave or block part empty; 8192 channels and more on 16 lanes each.
+# the last wave or block part empty; batch rows that fit one block of the
+# backward and that do not, at one wave a row and at several.
 SHAPES = [(1, 1, 1), (3, 70, 1), (2, 33, 5), (2, 65, 8), (1, 3, 9), (2, 37, 31), (5, 9, 64), (1, 17, 65), (2, 5, 100),
           (3, 7, 128), (1, 2, 129), (2, 3, 511), (1, 3, 512), (2, 2, 513), (1, 5, 1000), (2, 1, 1024), (1, 2, 1025),
-          (1, 2, 4099), (1, 1, 9001), (2, 4100, 131), (1, 8200, 160)]
+          (1, 2, 4099), (1, 1, 9001), (2, 4100, 131), (1, 8200, 160), (8, 3, 300), (9, 2, 300), (4, 5, 600), (5, 4, 1030),
+          (2, 2, 2100), (3, 2, 1500), (17, 1, 4000)]
 
 
 @pytest.mark.parametrize("io", ["f32", "bf16"])
