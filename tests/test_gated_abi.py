@@ -118,8 +118,9 @@ def test_workspace_bytes(lib):
     n = ctypes.c_int64(-1)
     assert lib.ssm_gated_scan_bwd_workspace_bytes(3, 100, 50, 0, ctypes.byref(n)) == 0 and n.value == 2 * 300 * 4
     assert lib.ssm_gated_scan_bwd_workspace_bytes(1, 100, 50, 1, ctypes.byref(n)) == 0 and n.value == 0
-    # long rows: none where one block takes every batch row of a channel
-    assert lib.ssm_gated_scan_bwd_workspace_bytes(4, 4096, 4096, 1, ctypes.byref(n)) == 0 and n.value == 0
+    # long rows: none where one block takes every batch row of a channel (small calls)
+    assert lib.ssm_gated_scan_bwd_workspace_bytes(3, 1000, 777, 1, ctypes.byref(n)) == 0 and n.value == 0
+    assert lib.ssm_gated_scan_bwd_workspace_bytes(4, 4096, 4096, 1, ctypes.byref(n)) == 0 and n.value == 8 * 4 * 4096
     assert lib.ssm_gated_scan_bwd_workspace_bytes(64, 100, 4096, 1, ctypes.byref(n)) == 0 and n.value == 2 * 6400 * 4
     assert lib.ssm_gated_scan_bwd_workspace_bytes(1, 100, 50, 0, None) == 0
     assert lib.ssm_gated_scan_bwd_workspace_bytes(0, 100, 50, 0, ctypes.byref(n)) == SHAPE
