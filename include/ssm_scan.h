@@ -513,7 +513,8 @@ typedef enum {
  *                                              0, 128, 256, ..., which ssm_gated_scan_bwd reads
  *
  * Any sizes >= 1 and any element-aligned pointers; rows of 2^30 tokens or
- * more are SSM_ERR_UNSUPPORTED, as is a mode outside ssm_gated_mode_t.  No
+ * more are SSM_ERR_UNSUPPORTED, as are launches of 2^32 lanes (2^26 channels
+ * of more than 256 tokens) and a mode outside ssm_gated_mode_t.  No
  * output may overlap an input or another output, except last_state == h0.
  * Allocates nothing; deterministic.
  */
@@ -602,8 +603,9 @@ typedef enum {
  *   mean, rstd [rows]       fp32    written when not NULL (mean: SSM_NORM_LAYER only)
  *
  * res_io is io or SSM_F32 (SSM_ERR_DTYPE otherwise); without a residual it
- * must be io.  dim up to 32768 (larger is SSM_ERR_UNSUPPORTED, as is a kind
- * outside ssm_norm_t), any rows >= 1, any element-aligned pointers.  No output
+ * must be io.  dim up to 32768 (larger is SSM_ERR_UNSUPPORTED, as are rows
+ * that take 2^32 lanes, one for every 8 numbers, and a kind outside
+ * ssm_norm_t), any rows >= 1, any element-aligned pointers.  No output
  * may overlap an input or another output, except s == residual.  Allocates
  * nothing; deterministic.
  */

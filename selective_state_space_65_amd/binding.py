@@ -743,7 +743,8 @@ def gated_scan_fwd(x, gate, gate_bias=None, rate=None, z=None, reset=None, h0=No
     (batch, dim) float32, which may be the same tensor as last_state.  y has
     the io dtype; last_state is float32 (None when return_last_state is False).
     ckpt, when given, receives the backward's checkpoints (gated_ckpt_shape).
-    stream: run on that torch.cuda.Stream instead of the current one.
+    stream: run on that torch.cuda.Stream instead of the current one; new
+    outputs then belong to it, as tensors made under torch.cuda.stream do.
     """
     if stream is not None or not x.is_cuda or x.get_device() != _device():
         return _elsewhere(gated_scan_fwd, **locals())
@@ -874,7 +875,8 @@ def norm_fwd(x, weight=None, bias=None, residual=None, eps=1e-5, kind="layer", o
     float32.  residual_out may be the residual itself, which is then updated
     in place.  mean and rstd are float32 (...,) for norm_bwd: None without
     save_stats, and mean None for "rms".
-    stream: run on that torch.cuda.Stream instead of the current one.
+    stream: run on that torch.cuda.Stream instead of the current one; new
+    outputs then belong to it, as tensors made under torch.cuda.stream do.
     """
     if stream is not None or not x.is_cuda or x.get_device() != _device():
         return _elsewhere(norm_fwd, **locals())

@@ -80,6 +80,12 @@ struct Map {
   float a, b;
 };
 
+// A product of a's kept off 0.  The factors are not negative, so their bits
+// order as unsigned integers and a NaN, above them all, stays.
+__device__ __forceinline__ float off_zero(float a) {
+  return __uint_as_float(max(__float_as_uint(a), __float_as_uint(FLT_MIN)));
+}
+
 template <bool kDrop>
 __device__ __forceinline__ float apply(Map m, float h) {
   const float r = __builtin_fmaf(m.a, h, m.b);
@@ -92,7 +98,7 @@ template <bool kDrop>
 __device__ __forceinline__ Map compose(Map late, Map early) {
   Map r;
   r.b = apply<kDrop>(late, early.b);
-  r.a = __builtin_fmaxf(late.a * early.a, FLT_MIN);
+  r.a = off_zero(late.a * early.a);
   if constexpr (kDrop) r.a = (late.a == 0.0f || early.a == 0.0f) ? 0.0f : r.a;
   return r;
 }
@@ -318,7 +324,7 @@ __device__ __forceinline__ Map chunk_map(const float a[kTok], const float b[kTok
     m.b = kDrop && (drop >> j & 1) ? b[j] : h;
     m.a *= a[j];
   }
-  m.a = __builtin_fmaxf(m.a, FLT_MIN);
+  m.a = off_zero(m.a);
   if constexpr (kDrop) m.a = drop ? 0.0f : m.a;
   return m;
 }
@@ -479,7 +485,7 @@ __device__ __forceinline__ void bwd_tile(const float x[kTok], const Gate g[kTok]
     r.b = kDrop && (drop >> j & 1) ? 0.0f : a[j] * lam;
     r.a *= a[j];
   }
-  r.a = __builtin_fmaxf(r.a, FLT_MIN);
+  r.a = off_zero(r.a);
   if constexpr (kDrop) r.a = drop ? 0.0f : r.a;
   r = suffix<G, kDrop>(r, gl);
   float in = mu;
@@ -908,7 +914,8 @@ ssm_status_t ssm_gated_scan_fwd(int64_t batch, int64_t dim, int64_t seqlen, ssm_
   GatedShape s;
   ssm_status_t st = gated_shape(batch, dim, seqlen, io, &s);
   if (st != SSM_OK) return st;
-  if (!gated_mode_ok(mode)) return SSM_ERR_UNSUPPORTED;
+  const GatedPlan p = gated_plan(batch, dim, seqlen, false);
+  if (!gated_mode_ok(mode) || !launch_ok(p.blocks, p.threads)) return SSM_ERR_UNSUPPORTED;
   if (!x || !gate || !y) return SSM_ERR_NULL;
   const size_t es = io_size(io);
   const bool in_place = h0 && h0 == last_state;
@@ -920,7 +927,6 @@ ssm_status_t ssm_gated_scan_fwd(int64_t batch, int64_t dim, int64_t seqlen, ssm_
   GatedArgs a = gated_args(s, dim, seqlen, x, gate, gate_bias, rate, z, reset);
   a.h0 = h0; a.y = y; a.last = last_state; a.ckpt = ckpt;
   hipStream_t hs = reinterpret_cast<hipStream_t>(stream);
-  const GatedPlan p = gated_plan(batch, dim, seqlen, false);
   hipError_t e =
       io == SSM_BF16 ? launch_gated<bf16_t, false>(a, p, mode, hs) : launch_gated<float, false>(a, p, mode, hs);
   return e == hipSuccess ? SSM_OK : hip_fail(e);
@@ -942,11 +948,11 @@ ssm_status_t ssm_gated_scan_bwd(int64_t batch, int64_t dim, int64_t seqlen, ssm_
   GatedShape s;
   ssm_status_t st = gated_shape(batch, dim, seqlen, io, &s);
   if (st != SSM_OK) return st;
-  if (!gated_mode_ok(mode)) return SSM_ERR_UNSUPPORTED;
+  const GatedPlan p = gated_plan(batch, dim, seqlen, true);
+  if (!gated_mode_ok(mode) || !launch_ok(p.blocks, p.threads)) return SSM_ERR_UNSUPPORTED;
   if (!x || !gate || !ckpt || !dy || !dx || !dgate) return SSM_ERR_NULL;
   if (!rate) drate = nullptr;
   if (!z) dz = nullptr;
-  const GatedPlan p = gated_plan(batch, dim, seqlen, true);
   const int64_t need = bwd_workspace(s, p);
   if (workspace_bytes < need) return SSM_ERR_WORKSPACE;
   if (need && !workspace) return SSM_ERR_NULL;
@@ -982,7 +988,11 @@ ssm_status_t ssm_gated_state_update(int64_t batch, int64_t dim, ssm_dtype_t io, 
   GatedShape s;
   ssm_status_t st = gated_shape(batch, dim, 1, io, &s);
   if (st != SSM_OK) return st;
-  if (!gated_mode_ok(mode)) return SSM_ERR_UNSUPPORTED;
+  const int vec = dim % 4 == 0 ? 4 : 1;
+  const int64_t lanes = dim / vec;
+  const int threads = (int)std::min<int64_t>(256, (lanes + 63) / 64 * 64);
+  const int64_t per_row = (lanes + threads - 1) / threads;
+  if (!gated_mode_ok(mode) || !launch_ok(batch * per_row, threads)) return SSM_ERR_UNSUPPORTED;
   if (!state || !x || !gate || !y) return SSM_ERR_NULL;
   const size_t es = io_size(io);
   const Buf ins[] = {{x, s.row_bytes, es}, {gate, s.row_bytes, es}, {z, s.row_bytes, es}, {gate_bias, dim * 4, 4},
@@ -990,11 +1000,6 @@ ssm_status_t ssm_gated_state_update(int64_t batch, int64_t dim, ssm_dtype_t io, 
   const Buf outs[] = {{y, s.row_bytes, es}, {state, s.bd * 4, 4}};
   st = check_buffers(ins, 5, outs, 2);
   if (st != SSM_OK) return st;
-  const int vec = dim % 4 == 0 ? 4 : 1;
-  const int64_t lanes = dim / vec;
-  const int threads = (int)std::min<int64_t>(256, (lanes + 63) / 64 * 64);
-  const int64_t per_row = (lanes + threads - 1) / threads;
-  if (batch * per_row >= ((int64_t)1 << 31)) return SSM_ERR_UNSUPPORTED;
   StepArgs a;
   a.state = state; a.x = x; a.gate = gate; a.gate_bias = gate_bias; a.rate = rate; a.z = z; a.y = y;
   a.dim = dim; a.blocks_per_row = (int)per_row;

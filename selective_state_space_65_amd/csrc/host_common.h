@@ -38,6 +38,9 @@ inline Range span(const void* p, int64_t bytes) {
 
 inline bool overlap(Range a, Range b) { return a.lo < b.hi && b.lo < a.hi; }
 
+// A launch's lanes are counted in 32 bits.
+inline bool launch_ok(int64_t blocks, int64_t threads) { return blocks < ((int64_t)1 << 32) / threads; }
+
 // One buffer of a call, for check_buffers; p may be null (not given).
 struct Buf {
   const void* p;

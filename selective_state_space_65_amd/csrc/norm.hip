@@ -519,7 +519,8 @@ ssm_status_t ssm_norm_fwd(int64_t rows, int64_t dim, ssm_dtype_t io, ssm_dtype_t
   int64_t n;
   ssm_status_t st = norm_shape(rows, dim, io, res_io, &n);
   if (st != SSM_OK) return st;
-  if (!norm_kind_ok(kind)) return SSM_ERR_UNSUPPORTED;
+  const NormPlan p = fwd_plan(rows, dim);
+  if (!norm_kind_ok(kind) || !launch_ok(p.blocks, p.threads)) return SSM_ERR_UNSUPPORTED;
   if (!residual && res_io != io) return SSM_ERR_DTYPE;
   if (!x || !y || (s && !residual)) return SSM_ERR_NULL;
   if (kind == SSM_NORM_RMS) mean = nullptr;
@@ -530,7 +531,6 @@ ssm_status_t ssm_norm_fwd(int64_t rows, int64_t dim, ssm_dtype_t io, ssm_dtype_t
   const Buf outs[] = {{y, n * (int64_t)es, es}, {s, n * (int64_t)rs, rs}, {mean, rows * 4, 4}, {rstd, rows * 4, 4}};
   st = check_buffers(ins, 4, outs, 4);
   if (st != SSM_OK) return st;
-  const NormPlan p = fwd_plan(rows, dim);
   NormFwdArgs a;
   a.x = x; a.residual = residual; a.weight = weight; a.bias = bias; a.y = y; a.s = s; a.mean = mean; a.rstd = rstd;
   a.rows = rows; a.dim = (int)dim; a.row_waves = p.row_waves; a.eps = eps;

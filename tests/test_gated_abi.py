@@ -66,6 +66,8 @@ def test_common_refusals(lib, call):
     assert call(lib, dim=-1) == SHAPE
     assert call(lib, batch=1 << 40, dim=1 << 30) == SHAPE
     assert call(lib, batch=1 << 16, dim=1 << 15) == UNSUPPORTED   # 2^31 channels
+    if call is not step:
+        assert call(lib, batch=1 << 13, dim=1 << 13, seqlen=300) == UNSUPPORTED   # 2^26 rows of 64 lanes
     assert call(lib, mode=3) == UNSUPPORTED
     assert call(lib, mode=-1) == UNSUPPORTED
     assert call(lib, x=addr(1) + 2) == ALIGN

@@ -182,6 +182,30 @@ def test_infinity_propagates(L):
     assert torch.isfinite(y[0, 1, :3]).all() and torch.isfinite(y[0, [0, 2, 3]]).all()
 
 
+@pytest.mark.parametrize("mode", MODES)
+@pytest.mark.parametrize("L", [6, 60, 120, 200, 1100, 4100])
+def test_nan_gate_propagates(mode, L):
+    """A NaN gate makes every later state of its channel NaN, wherever it stands in a lane's tokens, until a reset; in the
+    backward it reaches every earlier token."""
+    d = draw(1, 12, L, "f32", 650, z=False)
+    d["reset"].zero_()
+    at = [0, 1, 2, 3, 4, 5, L // 2, L // 2 + 1, L - 2, L - 1]
+    for c, t in enumerate(at):
+        d["gate"][0, c, t] = float("nan")
+    d["gate"][0, 10, 0] = float("nan")
+    y, last, ck = ssm.gated_scan_fwd_save(d["x"], d["gate"], d["gate_bias"], h0=d["h0"], mode=mode)
+    g = ssm.gated_scan_bwd(d["x"], d["gate"], d["x"], ck, d["gate_bias"], mode=mode)
+    torch.cuda.synchronize()
+    for c, t in enumerate(at):
+        assert torch.isfinite(y[0, c, :t]).all() and torch.isnan(y[0, c, t:]).all() and torch.isnan(last[0, c]), (c, t)
+        assert torch.isnan(g["dx"][0, c, :t]).all() and torch.isfinite(g["dx"][0, c, t + 1:]).all(), (c, t)
+        assert torch.isnan(g["dh0"][0, c])
+    assert torch.isfinite(y[0, 11]).all() and torch.isfinite(g["dx"][0, 11]).all()
+    d["reset"][0, L // 2] = 1
+    y = ssm.gated_scan_fwd(d["x"], d["gate"], d["gate_bias"], reset=d["reset"], h0=d["h0"], mode=mode)[0]
+    assert torch.isnan(y[0, 10, :L // 2]).all() and torch.isfinite(y[0, 10, L // 2:]).all()
+
+
 @pytest.mark.parametrize("rate", [False, True])
 @pytest.mark.parametrize("mode", MODES)
 @pytest.mark.parametrize("L", [4, 61, 127, 900])

@@ -79,6 +79,8 @@ def test_common_refusals(lib, call):
     assert call(lib, rows=1 << 50, dim=1 << 12) == SHAPE
     assert call(lib, dim=32769) == UNSUPPORTED
     assert call(lib, rows=1 << 31, dim=1) == UNSUPPORTED
+    if call is fwd:
+        assert call(lib, rows=1 << 26, dim=512) == UNSUPPORTED   # 2^32 lanes
     assert call(lib, kind=2) == UNSUPPORTED
     assert call(lib, weight=addr(3) + 2) == ALIGN
     assert call(lib, rstd=addr(8) + 1) == ALIGN
