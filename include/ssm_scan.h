@@ -72,6 +72,9 @@
  *    partial sums), freed on the same stream within the call.  The pool's
  *    release threshold is 0: freed blocks are reused by later calls on the
  *    stream and returned to the device at the next synchronisation.
+ *  - The gated recurrence and the norms (ssm_gated_*, ssm_norm_*) allocate
+ *    nothing; their backwards take a workspace of the caller's, whose size a
+ *    query gives.  Two calls that may overlap in time need two workspaces.
  *  - Calls on different streams are independent; the library is re-entrant.
  */
 #ifndef SSM_SCAN_H
@@ -473,10 +476,9 @@ ssm_status_t ssm_scan_bwd_complex(int64_t batch, int64_t dim, int64_t dstate, in
 /*
  * Gated linear recurrence: one state per channel and a gate per (batch,
  * channel, token), where the selective scan has dstate states per channel and
- * B and C shared by the channels.  The pages set the SSM beside gated
- * recurrences (the Chinese explainer's section on Delta as a gate: a large
- * step resets the state, a small one keeps it); this is that recurrence with
- * the gate as an input of its own.
+ * B and C shared by the channels.  The Chinese explainer reads Delta as a gate
+ * (a large step resets the state, a small one keeps it); this is a recurrence
+ * with that gate as an input of its own.
  *
  *   v_l = gate[b,d,l] + gate_bias[d]            s_l = sigmoid(v_l)
  *   a_l = s_l, or exp(-rate[d] * s_l) when rate is not NULL

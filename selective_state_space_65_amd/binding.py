@@ -701,6 +701,11 @@ def _elsewhere(fn, stream, **args):
             return fn(**args)
 
 
+def _vector(like, dim, device):
+    """A new (dim,) float32 tensor; the copy of a parameter's description is the cheaper call."""
+    return torch.empty(dim, dtype=torch.float32, device=device) if like is None else torch.empty_like(like)
+
+
 def _mode_code(mode):
     if mode not in GATED_MODES:
         raise ValueError("mode must be one of %s" % sorted(GATED_MODES))
@@ -803,8 +808,8 @@ def gated_scan_bwd(x, gate, dy, ckpt, gate_bias=None, rate=None, z=None, reset=N
     if dlast is not None:
         _need(dlast, "dlast", (batch, dim), f32, dev)
     g = dict(dx=torch.empty_like(x), dgate=torch.empty_like(x),
-             dgate_bias=torch.empty(dim, dtype=f32, device=dev) if "dgate_bias" in need else None,
-             drate=torch.empty(dim, dtype=f32, device=dev) if ("drate" in need and rate is not None) else None,
+             dgate_bias=_vector(gate_bias, dim, dev) if "dgate_bias" in need else None,
+             drate=_vector(rate, dim, dev) if ("drate" in need and rate is not None) else None,
              dz=torch.empty_like(x) if ("dz" in need and z is not None) else None,
              dh0=torch.empty((batch, dim), dtype=f32, device=dev) if "dh0" in need else None)
     lib = _lib or load_library()
@@ -912,7 +917,7 @@ def norm_fwd(x, weight=None, bias=None, residual=None, eps=1e-5, kind="layer", o
     if save_stats:
         rstd = torch.empty(shape[:-1], dtype=f32, device=dev)
         if kind == "layer":
-            mean = torch.empty(shape[:-1], dtype=f32, device=dev)
+            mean = torch.empty_like(rstd)
     lib = _lib or load_library()
     st = lib.ssm_norm_fwd(rows, dim, io_code, res_code, code, x.data_ptr(), _ptr(residual), _ptr(weight), _ptr(bias),
                           eps, out.data_ptr(), _ptr(residual_out), _ptr(mean), _ptr(rstd), _raw_stream(dev.index))
@@ -954,8 +959,8 @@ def norm_bwd(dy, s, rstd, mean=None, weight=None, dresidual_out=None, kind="laye
     if dresidual_out is not None:
         _need(dresidual_out, "dresidual_out", shape, s.dtype, dev)
     g = dict(dx=torch.empty_like(dy), dresidual=torch.empty_like(s) if s.dtype != io else None,
-             dweight=torch.empty(dim, dtype=f32, device=dev) if "dweight" in need else None,
-             dbias=torch.empty(dim, dtype=f32, device=dev) if "dbias" in need else None)
+             dweight=_vector(weight, dim, dev) if "dweight" in need else None,
+             dbias=_vector(weight, dim, dev) if "dbias" in need else None)
     lib = _lib or load_library()
     io_code, res_code = _io_code(io), _io_code(s.dtype)
     size = 0

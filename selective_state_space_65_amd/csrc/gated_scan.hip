@@ -245,7 +245,8 @@ struct Gate {
   float s, t, a, om;
 };
 
-template <bool kRate>
+// kSlow: the rate is below 1/4, so every token takes the series.
+template <bool kRate, bool kSlow = false>
 __device__ __forceinline__ Gate gate_of(float g, const GateParams& p) {
   Gate r;
   const float e = p.eb * exp2_hw(__builtin_fmaf(g, -kLog2e, p.nb));
@@ -261,15 +262,34 @@ __device__ __forceinline__ Gate gate_of(float g, const GateParams& p) {
     m = __builtin_fmaf(c, m, 1.0f / 6.0f);
     m = __builtin_fmaf(c, m, -0.5f);
     m = __builtin_fmaf(c, m, 1.0f);
-    const float big = exp2_hw(p.nr * r.s);
-    const bool near = c < 0.25f;
-    r.om = near ? c * m : 1.0f - big;
-    r.a = near ? __builtin_fmaf(-c, m, 1.0f) : big;
+    r.om = c * m;
+    r.a = __builtin_fmaf(-c, m, 1.0f);
+    if constexpr (!kSlow) {
+      const float e = exp2_hw(p.nr * r.s);
+      const bool near = c < 0.25f;
+      r.om = near ? r.om : 1.0f - e;
+      r.a = near ? r.a : e;
+    }
   } else {
     r.a = r.s;
     r.om = r.t;
   }
   return r;
+}
+
+// The gates of a lane's tokens.  slow: every lane's rate is below 1/4 (models
+// with a long memory keep it there), which saves the exponential of each token
+// (4 x 4096 x 4096 bf16, whose vector units were 95% busy: forward 121 -> 100
+// us, training step 311 -> 287).
+template <bool kRate>
+__device__ __forceinline__ void gates_of(const float g[kTok], const GateParams& p, bool slow, Gate out[kTok]) {
+  if (kRate && slow) {
+#pragma unroll
+    for (int j = 0; j < kTok; ++j) out[j] = gate_of<kRate, true>(g[j], p);
+  } else {
+#pragma unroll
+    for (int j = 0; j < kTok; ++j) out[j] = gate_of<kRate>(g[j], p);
+  }
 }
 
 template <int kMode>
@@ -389,6 +409,7 @@ __global__ __launch_bounds__(G == 64 ? 64 * kMaxWaves : 256) void gated_fwd_kern
   float* ck = p.ckpt + (p.ckpt ? ch * p.ckpts : 0);
   constexpr bool kStream = streamed<IoT>;
   const GateParams gp = gate_params<kRate>(p.gate_bias, p.rate, d);
+  const bool slow = kRate && __ballot(!(gp.rate < 0.25f)) == 0;
   float carry = p.h0 ? p.h0[ch] : 0.0f;
   // last_state may be h0: every wave has its value before any wave can end.
   if (G == 64 && waves > 1) __syncthreads();
@@ -416,11 +437,12 @@ __global__ __launch_bounds__(G == 64 ? 64 * kMaxWaves : 256) void gated_fwd_kern
     const Raw8<IoT> zc = nz;
     uint32_t drop = p.reset ? reset_bits(rr, t, L, full) : 0;
     if (G == 64 && base + step < L) request(base + step);
+    Gate g[kTok];
+    gates_of<kRate>(gv, gp, slow, g);
 #pragma unroll
     for (int j = 0; j < kTok; ++j) {
-      const Gate g = gate_of<kRate>(gv[j], gp);
-      a[j] = g.a;
-      b[j] = input_weight<kMode>(g.a, g.om) * xv[j];
+      a[j] = g[j].a;
+      b[j] = input_weight<kMode>(g[j].a, g[j].om) * xv[j];
     }
     if (!full) {  // tokens past the end leave the state as it is
 #pragma unroll
@@ -558,6 +580,7 @@ __global__ __launch_bounds__(G == 64 ? 64 * kMaxBwdWaves : 256, 3) void gated_bw
   const float* ck = p.ckpt + ch * p.ckpts;
   constexpr bool kStream = streamed<IoT>;
   const GateParams gp = gate_params<kRate>(p.gate_bias, p.rate, d);
+  const bool slow = kRate && __ballot(!(gp.rate < 0.25f)) == 0;
   float mu = p.dlast ? p.dlast[ch] : 0.0f;
   float sum_b = 0.0f, sum_r = 0.0f;
 
@@ -590,8 +613,7 @@ __global__ __launch_bounds__(G == 64 ? 64 * kMaxBwdWaves : 256, 3) void gated_bw
     const float h_in = nh;
     if (G == 64 && base >= step) request(base - step);
     uint32_t drop = p.reset ? reset_bits(rr, t, L, full) : 0;
-#pragma unroll
-    for (int j = 0; j < kTok; ++j) g[j] = gate_of<kRate>(gv[j], gp);
+    gates_of<kRate>(gv, gp, slow, g);
     if (!full) {
 #pragma unroll
       for (int j = 0; j < kTok; ++j) {

@@ -61,8 +61,9 @@ def check(got, want, err, io, what):
         what, bad.sum(), bad.size, np.nanmax(np.abs(got - want) / bound), np.argwhere(bad)[0])
 
 
-def run_all(d, io, mode, seed, what, dlast=True):
-    """Forward with checkpoints, backward; both against the reference."""
+def run_all(d, io, mode, seed, what, dlast=True, memory=1.0):
+    """Forward with checkpoints, backward; both against the reference.  memory: the longest memory over the 100 tokens
+    the reference's bounds assume, which they grow with."""
     batch, dim, L = d["x"].shape
     g = torch.Generator().manual_seed(seed + 1000)
     dy = torch.randn((batch, dim, L), generator=g).to(IO[io]).to(DEV)
@@ -74,11 +75,13 @@ def run_all(d, io, mode, seed, what, dlast=True):
     h = host(d)
     f = ref.forward(mode=mode, **h)
     b = ref.backward(dy=np64(dy), dlast=np64(dl), mode=mode, **h)
+    for r in (f, b):
+        r.update({k: v * memory for k, v in r.items() if k.endswith("_err")})
     check(y, f["y"], f["y_err"], io, what + " y")
     check(last, f["last"], f["last_err"], "f32", what + " last_state")
     for i in range(ck.shape[2]):
         want = (f["states"][..., 128 * i - 1] if i else (h["h0"] if h["h0"] is not None else np.zeros((batch, dim))))
-        check(ck[..., i], want, ref.K1 * (f["bars"][..., 128 * i - 1] if i else np.abs(want)), "f32", what + " ckpt")
+        check(ck[..., i], want, memory * ref.K1 * (f["bars"][..., 128 * i - 1] if i else np.abs(want)), "f32", what + " ckpt")
     for k in ("dx", "dgate", "dz"):
         if k in b:
             check(gr[k], b[k], b[k + "_err"], io, what + " " + k)
@@ -123,6 +126,23 @@ def test_modes_and_options(mode, rate, io, L):
     d = draw(2, 9, L, io, 301 + L, rate=rate, z=False, reset=False, h0=False)
     d["gate_bias"] = None
     run_all(d, io, mode, L, "all off", dlast=False)
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("mode", MODES)
+@pytest.mark.parametrize("L", [1, 7, 50, 120, 250, 700, 1500])
+def test_rates_around_a_quarter(L, mode, io):
+    """Rates below 1/4 (1 - a from its series alone), on it and above it, in every lane or side by side: v >= -4, so 1 - a is
+    at least 0.15 * 0.018 / 1.02 and a token's memory at most 380 tokens."""
+    for k in range(3):
+        d = draw(2, 13, L, io, 1700 + k, rate=True)
+        rate = torch.linspace(0.15, 0.249, 13)
+        if k:
+            rate[5], rate[9] = 0.25, 0.26
+        if k == 2:
+            rate[::2] = 3.0
+        d["rate"] = rate.to(DEV)
+        run_all(d, io, mode, L, "rates %d" % k, memory=3.8)
 
 
 @pytest.mark.parametrize("L", [5, 60, 128, 2000])
