@@ -72,6 +72,21 @@ __device__ __forceinline__ bool whole(int c, int gl, int dim) {
   return c - gl * kPiece + G * kPiece <= dim;
 }
 
+// request8 and finish8 for the group's piece of which the lane has column c.
+template <int G, typename T>
+__device__ __forceinline__ Raw8<T> request_piece(const T* row, int c, int gl, int dim) {
+  return request8<G == 8>(row, c - gl * kPiece, gl * kPiece, dim);
+}
+
+template <int G, typename T>
+__device__ __forceinline__ void finish_piece(Raw8<T>& r, int c, int gl, int dim) {
+  if (whole<G>(c, gl, dim)) return;
+  if (c - gl * kPiece >= dim)
+    r.clear();
+  else
+    finish8<G == 8>(r, c - gl * kPiece, gl * kPiece, dim);
+}
+
 // ---- the forward -------------------------------------------------------------
 
 struct NormFwdArgs {
@@ -113,13 +128,28 @@ __global__ __launch_bounds__(1024) void norm_fwd_kernel(NormFwdArgs p) {
   const float count = (float)dim;  // sums are divided by it: a constant row has exactly its mean
 
   float v[K][kPiece];
+  Raw8<IoT> px[K];
+  Raw8<ResT> pr[K];
+  Raw8<float> pw[K], pb[K];
 #pragma unroll
   for (int k = 0; k < K; ++k) {
     const int c = ((k * W + row_wave) * G + gl) * kPiece;
-    load_row8(xr, c, dim, whole<G>(c, gl, dim), v[k]);
+    px[k] = request_piece<G>(xr, c, gl, dim);
+    if constexpr (kRes) pr[k] = request_piece<G>(rr, c, gl, dim);
+  }
+  if constexpr (K == 1) {  // in flight during the sums, where the registers allow
+    if (p.weight) pw[0] = request_piece<G>(p.weight, (row_wave * G + gl) * kPiece, gl, dim);
+    if (p.bias) pb[0] = request_piece<G>(p.bias, (row_wave * G + gl) * kPiece, gl, dim);
+  }
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    const int c = ((k * W + row_wave) * G + gl) * kPiece;
+    finish_piece<G>(px[k], c, gl, dim);
+    if constexpr (kRes) finish_piece<G>(pr[k], c, gl, dim);
+    px[k].get(v[k]);
     if constexpr (kRes) {
       float r[kPiece];
-      load_row8(rr, c, dim, whole<G>(c, gl, dim), r);
+      pr[k].get(r);
 #pragma unroll
       for (int j = 0; j < kPiece; ++j) v[k][j] = add_res<ResT>(v[k][j], r[j]);
     }
@@ -154,8 +184,18 @@ __global__ __launch_bounds__(1024) void norm_fwd_kernel(NormFwdArgs p) {
       if (p.s) store_row8(static_cast<ResT*>(p.s) + base, c, dim, full, v[k]);
     }
     float w[kPiece], b[kPiece], o[kPiece];
-    if (p.weight) load_row8(p.weight, c, dim, full, w);
-    if (p.bias) load_row8(p.bias, c, dim, full, b);
+    if constexpr (K > 1) {
+      if (p.weight) pw[k] = request_piece<G>(p.weight, c, gl, dim);
+      if (p.bias) pb[k] = request_piece<G>(p.bias, c, gl, dim);
+    }
+    if (p.weight) {
+      finish_piece<G>(pw[k], c, gl, dim);
+      pw[k].get(w);
+    }
+    if (p.bias) {
+      finish_piece<G>(pb[k], c, gl, dim);
+      pb[k].get(b);
+    }
 #pragma unroll
     for (int j = 0; j < kPiece; ++j) {
       o[j] = (v[k][j] - mean) * rstd;
@@ -207,7 +247,11 @@ __global__ __launch_bounds__(kThreads) void norm_bwd_kernel(NormBwdArgs p) {
 #pragma unroll
   for (int k = 0; k < K; ++k) {
     const int c = ((k * W + row_wave) * G + gl) * kPiece;
-    if (p.weight) load_row8(p.weight, c, dim, whole<G>(c, gl, dim), w[k]);
+    if (p.weight) {
+      Raw8<float> r = request_piece<G>(p.weight, c, gl, dim);
+      finish_piece<G>(r, c, gl, dim);
+      r.get(w[k]);
+    }
 #pragma unroll
     for (int j = 0; j < kPiece; ++j) {
       if (!p.weight) w[k][j] = 1.0f;
@@ -232,10 +276,9 @@ __global__ __launch_bounds__(kThreads) void norm_bwd_kernel(NormBwdArgs p) {
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       const int c = ((k * W + row_wave) * G + gl) * kPiece;
-      const bool full = whole<G>(c, gl, dim);
-      next_s[k] = load_raw8(static_cast<const ResT*>(p.s) + base, c, dim, full);
-      next_dy[k] = load_raw8(static_cast<const IoT*>(p.dy) + base, c, dim, full);
-      if (p.ds_out) next_past[k] = load_raw8(static_cast<const ResT*>(p.ds_out) + base, c, dim, full);
+      next_s[k] = request_piece<G>(static_cast<const ResT*>(p.s) + base, c, gl, dim);
+      next_dy[k] = request_piece<G>(static_cast<const IoT*>(p.dy) + base, c, gl, dim);
+      if (p.ds_out) next_past[k] = request_piece<G>(static_cast<const ResT*>(p.ds_out) + base, c, gl, dim);
     }
   };
   if (kAhead) request(0);
@@ -251,6 +294,10 @@ __global__ __launch_bounds__(kThreads) void norm_bwd_kernel(NormBwdArgs p) {
     float c1 = 0.0f, c2 = 0.0f;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
+      const int c = ((k * W + row_wave) * G + gl) * kPiece;
+      finish_piece<G>(next_s[k], c, gl, dim);
+      finish_piece<G>(next_dy[k], c, gl, dim);
+      if (p.ds_out) finish_piece<G>(next_past[k], c, gl, dim);
       next_s[k].get(n[k]);
       next_dy[k].get(dy[k]);
       past[k] = next_past[k];
@@ -392,31 +439,32 @@ struct NormPlan {
 // few long ones (forward, 16384 x 2048 bf16 with an fp32 residual, 4 / 2 / 1
 // pieces: 80.3 / 76.6 / 72.1 us; 8192 x 4096 85.7 / 81.8 / 74.8; with the
 // backward, 16384 x 2048 bf16, 2 / 1 pieces: 114.0 / 102.7).  Then two pieces
-// (4096 x 8000 forward: 57.8 us, 65.1 at one piece and 16 waves).  Then, forward,
-// 16 waves; backward, whose column sums take 16 registers a piece, four pieces
-// (2048 x 16384: 217 us, 229 at two pieces and 16 waves, which spill).  A
-// forward row of two waves that ends inside a piece takes one wave of two
-// pieces instead: the wave with the end would keep the other waiting (30000 x
-// 777 bf16 24.3 us, 28.5 on two; from three waves on it no longer pays, 16000 x
-// 2001 77.4 us, 83.5 at two pieces).
-NormPlan norm_plan(int64_t dim, bool backward) {
+// (4096 x 8000 forward: 57.8 us, 65.1 at one piece and 16 waves), then four
+// (2048 x 16384 forward 59.4 us, 66.6 at two pieces and 16 waves; the training
+// step 217 and 229, the backward of 16 waves spilling), then 16 waves.
+//
+// one_wave: a row of two waves takes one of two pieces.  For forward bf16 rows
+// that end inside a piece, where the wave with the end keeps the other waiting
+// (30000 x 777 44.6 us, 48.8 on two waves; in fp32 the loads cover it, 8191 x
+// 1001 28.7 against 26.9 on two).
+NormPlan norm_plan(int64_t dim, bool one_wave) {
   NormPlan p;
   p.group = 8;
   while (p.group < 64 && p.group * kPiece < dim) p.group *= 2;
   p.pieces = p.row_waves = 1;
   const auto holds = [&] { return (int64_t)p.group * kPiece * p.pieces * p.row_waves >= dim; };
-  if (!backward && dim % kPiece && dim <= 2 * 64 * kPiece && !holds()) p.pieces = 2;
+  if (!holds() && one_wave && dim <= 2 * 64 * kPiece) p.pieces = 2;
   while (!holds() && p.row_waves < 8) p.row_waves *= 2;
-  if (!holds() && p.pieces < 2) p.pieces = 2;
-  if (!holds()) backward ? p.pieces = 4 : p.row_waves = 16;
-  if (!holds()) p.pieces = 4, p.row_waves = 16;
+  if (!holds()) p.pieces = 2;
+  if (!holds()) p.pieces = 4;
+  if (!holds()) p.row_waves = 16;
   p.threads = 256;
   p.blocks = 0;
   return p;
 }
 
-NormPlan fwd_plan(int64_t rows, int64_t dim) {
-  NormPlan p = norm_plan(dim, false);
+NormPlan fwd_plan(int64_t rows, int64_t dim, ssm_dtype_t io) {
+  NormPlan p = norm_plan(dim, io == SSM_BF16 && dim % kPiece != 0);
   if (p.row_waves > 1) {
     p.threads = 64 * p.row_waves;
     p.blocks = rows;
@@ -432,7 +480,7 @@ NormPlan fwd_plan(int64_t rows, int64_t dim) {
 // training step 190 us, 196 at 512 blocks; 2048 x 16384 217 against 232; but
 // 8191 x 1001, four rows to a block, 40 us at 512 and 45 at 128).
 NormPlan bwd_plan(int64_t rows, int64_t dim) {
-  NormPlan p = norm_plan(dim, true);
+  NormPlan p = norm_plan(dim, false);
   const int waves = std::max(p.row_waves, kBwdWaves);
   p.threads = 64 * waves;
   const int64_t groups = (int64_t)(waves / p.row_waves) * (64 / p.group);
@@ -519,7 +567,7 @@ ssm_status_t ssm_norm_fwd(int64_t rows, int64_t dim, ssm_dtype_t io, ssm_dtype_t
   int64_t n;
   ssm_status_t st = norm_shape(rows, dim, io, res_io, &n);
   if (st != SSM_OK) return st;
-  const NormPlan p = fwd_plan(rows, dim);
+  const NormPlan p = fwd_plan(rows, dim, io);
   if (!norm_kind_ok(kind) || !launch_ok(p.blocks, p.threads)) return SSM_ERR_UNSUPPORTED;
   if (!residual && res_io != io) return SSM_ERR_DTYPE;
   if (!x || !y || (s && !residual)) return SSM_ERR_NULL;

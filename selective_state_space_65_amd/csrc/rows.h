@@ -139,31 +139,50 @@ __device__ __forceinline__ void store8u(bf16_t* p, const float v[8]) {
   store16<kStream>(p, a);
 }
 
-// Elements [t, t + 8) of a row of n; full: t + 8 <= n in every lane of the
-// wave.  Elements past the row read as 0 and are not written.
-template <bool kStream = false, typename T>
-__device__ __forceinline__ Raw8<T> load_raw8(const T* row, int t, int n, bool full) {
+// Elements [t0 + l, t0 + l + 8) of a row of n, t0 the same in every lane of the
+// row and l >= 0, in two steps, so that several pieces can be in flight before
+// the first is touched: request8 loads the piece, or the row's last 8 elements
+// where the piece ends past the row; finish8, needed where some lane's piece
+// does, shifts those into place.  Elements past the row read as 0.  The loads
+// are unconditional: a branch here would have its loads waited for where the
+// branches join.  kShort: n may be below 8, and such a row is read element by
+// element.
+struct Place {
+  int base;      // of the lanes' row
+  uint32_t off;  // of the lane, so that a scalar base and a 32-bit offset address it
+};
+
+__device__ __forceinline__ Place place8(int t0, int l, int n) {
+  Place p;
+  p.base = min(t0, n - 8);
+  p.off = (uint32_t)min(l, n - 8 - p.base);
+  return p;
+}
+
+template <bool kShort, bool kStream = false, typename T>
+__device__ __forceinline__ Raw8<T> request8(const T* row, int t0, int l, int n) {
   Raw8<T> r;
-  if (full) {
-    r.template load<kStream>(row + t);
-  } else if (n % 8 == 0) {  // pieces are whole or empty
-    r.clear();
-    if (t < n) r.template load<kStream>(row + t);
-  } else if (n > 8) {
-    const int at = t < n - 8 ? t : n - 8;
-    r.template load<kStream>(row + at);
-    r.drop(t - at);
+  if (kShort && n < 8) {
+    r.load_part(row, t0 + l, n);
   } else {
-    r.load_part(row, t, n);
+    const Place p = place8(t0, l, n);
+    r.template load<kStream>(row + p.base + p.off);
   }
   return r;
 }
 
-template <typename T>
-__device__ __forceinline__ void load_row8(const T* row, int t, int n, bool full, float out[8]) {
-  load_raw8(row, t, n, full).get(out);
+template <bool kShort, typename T>
+__device__ __forceinline__ void finish8(Raw8<T>& r, int t0, int l, int n) {
+  if (kShort && n < 8) return;
+  const Place p = place8(t0, l, n);
+  const int s = t0 - p.base + l - (int)p.off;
+  if (n % 8)
+    r.drop(s);
+  else if (s)  // pieces are whole or empty
+    r.clear();
 }
 
+// Elements past the row are not written; full: no lane has any.
 template <bool kStream = false, typename T>
 __device__ __forceinline__ void store_row8(T* row, int t, int n, bool full, const float v[8]) {
   if (full || t + 8 <= n) {
