@@ -926,7 +926,8 @@ def norm_fwd(x, weight=None, bias=None, residual=None, eps=1e-5, kind="layer", o
     return out, s, mean, rstd
 
 
-def norm_bwd(dy, s, rstd, mean=None, weight=None, dresidual_out=None, kind="layer", need=("dweight", "dbias"), stream=None):
+def norm_bwd(dy, s, rstd, mean=None, weight=None, dresidual_out=None, kind="layer", need=("dweight", "dbias"),
+             stream=None):
     """Gradients of sum(dy * y) + sum(dresidual_out * s) for norm_fwd (ssm_norm_bwd).
 
     s, mean and rstd are what norm_fwd returned (mean for kind "layer" only).

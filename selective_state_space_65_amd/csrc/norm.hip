@@ -502,8 +502,9 @@ NormPlan bwd_plan(int64_t rows, int64_t dim) {
 
 template <typename IoT, typename ResT, bool kRms, bool kRes>
 hipError_t launch_norm_fwd(const NormFwdArgs& a, const NormPlan& p, hipStream_t st) {
-#define SSM_NORM_CALL(G, K)                                                                                  \
-  hipLaunchKernelGGL((norm_fwd_kernel<IoT, ResT, G, K, kRms, kRes>), dim3((unsigned)p.blocks), dim3(p.threads), 0, st, a)
+#define SSM_NORM_CALL(G, K)                                                                                 \
+  hipLaunchKernelGGL((norm_fwd_kernel<IoT, ResT, G, K, kRms, kRes>), dim3((unsigned)p.blocks),              \
+                     dim3(p.threads), 0, st, a)
   SSM_NORM_GEOMETRY(SSM_NORM_CALL)
 #undef SSM_NORM_CALL
   return hipGetLastError();

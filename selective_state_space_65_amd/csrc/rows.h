@@ -3,8 +3,8 @@
 // takes vector accesses at any element alignment, so a whole piece is one
 // 16-byte access (two for 8 fp32 values) whatever the row's length.  A piece
 // that ends past the row is read as the row's last 8 elements, shifted into
-// place, so that no lane reads past the row and none takes a loop of its own.  Internal:
-// not part of the C ABI.
+// place, so that no lane reads past the row and none takes a loop of its own.
+// Internal: not part of the C ABI.
 #pragma once
 
 #include "device_common.h"

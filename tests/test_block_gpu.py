@@ -199,3 +199,36 @@ def test_decode_graphs_share_states_and_memory():
         for h, e in zip(states, eager):
             assert torch.equal(h, e)
         _ = float(np.float64(out.float().abs().sum().item()))
+
+
+def test_two_streams_at_once():
+    """Norms and recurrences of different sizes on two streams at the same time give what they give alone."""
+    g = torch.Generator().manual_seed(11)
+    jobs = []
+    for batch, dim, L, io in ((3, 200, 700, torch.bfloat16), (5, 130, 90, torch.float32)):
+        x = [torch.randn((batch, dim, L), generator=g).to(DEV, io) for _ in range(4)]
+        r = torch.randn((batch * 40, dim), generator=g).to(DEV, io)
+        jobs.append((x, r))
+
+    def call(x, r):
+        y, last, ck = ssm.gated_scan_fwd_save(x[0], x[1], z=x[2], mode="norm")
+        gr = ssm.gated_scan_bwd(x[0], x[1], x[3], ck, z=x[2], mode="norm")
+        n, s, mean, rstd = ssm.norm_fwd(r)
+        gn = ssm.norm_bwd(n, s, rstd, mean=mean)
+        return [y, last, *(v for v in gr.values() if v is not None), n, *(v for v in gn.values() if v is not None)]
+
+    want = [call(*j) for j in jobs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    got = [[], []]
+    for _ in range(10):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append(call(*jobs[i]))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for run in got[i]:
+            for u, v in zip(run, want[i]):
+                assert torch.equal(u, v)

@@ -81,7 +81,8 @@ def run_all(d, io, mode, seed, what, dlast=True, memory=1.0):
     check(last, f["last"], f["last_err"], "f32", what + " last_state")
     for i in range(ck.shape[2]):
         want = (f["states"][..., 128 * i - 1] if i else (h["h0"] if h["h0"] is not None else np.zeros((batch, dim))))
-        check(ck[..., i], want, memory * ref.K1 * (f["bars"][..., 128 * i - 1] if i else np.abs(want)), "f32", what + " ckpt")
+        bar = f["bars"][..., 128 * i - 1] if i else np.abs(want)
+        check(ck[..., i], want, memory * ref.K1 * bar, "f32", what + " ckpt")
     for k in ("dx", "dgate", "dz"):
         if k in b:
             check(gr[k], b[k], b[k + "_err"], io, what + " " + k)
