@@ -72,6 +72,7 @@ struct GatedArgs {
   int seqlen;
   int ckpts;  // checkpoints per channel
   int waves;  // waves of a row (64-lane groups only)
+  int join;   // backward: batch rows of a channel that a block has, all of them, or 1
 };
 
 // ---- affine maps h -> a h + b ------------------------------------------------
@@ -560,21 +561,33 @@ __device__ __forceinline__ void bwd_tile(const float x[kTok], const Gate g[kTok]
 // Four waves on a SIMD in bf16 (128 registers; 4 x 4096 x 4096 training step 285
 // us, 296 at three); fp32 would spill there (4 x 4096 x 1024 145.2 us, 142.2 at
 // three).
+//
+// Where p.join is the batch, a block has every batch row of its channels and
+// writes their sums itself: with G < 64 in groups next to each other, with
+// G = 64 in rows of p.waves waves.
 template <typename IoT, int G, int kMode, bool kRate>
 __global__ __launch_bounds__(G == 64 ? 64 * kMaxBwdWaves : 256, sizeof(IoT) == 2 ? 4 : 3) void gated_bwd_kernel(
     GatedArgs p) {
+  constexpr int kSlots = G == 64 ? kMaxWaves : 256 / G;  // waves or groups of a block
   __shared__ Map totals[2][G == 64 ? kMaxWaves : 1];
+  __shared__ Map sums[kSlots];
   const int lane = threadIdx.x & 63, gl = lane & (G - 1);
   const int block_wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int block_waves = blockDim.x >> 6;
-  // G = 64: the block's waves in rows of `waves`; several rows are the batch
-  // rows of one channel, whose sums the block then has whole.
-  const int waves = G == 64 ? p.waves : block_waves;
+  const int waves = G == 64 ? p.waves : block_waves;  // of a row
   const int wave = G == 64 ? block_wave % waves : block_wave, first = block_wave - wave;
-  const bool joined = G == 64 && block_waves > waves;
-  int64_t ch = G == 64 ? (int64_t)blockIdx.x : ((int64_t)blockIdx.x * waves + wave) * (64 / G) + lane / G;
-  if (joined) ch += block_wave / waves * p.dim;
-  const bool live = ch < p.channels;
+  const int slot = G == 64 ? block_wave / waves : block_wave * (64 / G) + lane / G;
+  const int own = (G == 64 ? block_waves / waves : kSlots) / p.join;  // channels of the block
+  int64_t ch = (int64_t)blockIdx.x * own;
+  bool live = true;
+  if (p.join > 1) {
+    const int64_t c = ch + slot / p.join;
+    live = slot < own * p.join && c < p.dim;
+    ch = slot % p.join * p.dim + c;
+  } else {
+    ch += slot;
+    live = ch < p.channels;
+  }
   ch = live ? ch : p.channels - 1;
   const int64_t bt = ch / p.dim, d = ch - bt * p.dim;
   const int L = p.seqlen;
@@ -684,19 +697,24 @@ __global__ __launch_bounds__(G == 64 ? 64 * kMaxBwdWaves : 256, sizeof(IoT) == 2
   }
   if (p.dh0 && live && gl == 0 && (G < 64 || wave == 0)) p.dh0[ch] = mu;
   int64_t out = ch;
-  if (G == 64 && block_waves > 1) {
-    lds_barrier();  // the last tile's totals have been read
-    if (lane == 0) totals[0][block_wave] = Map{sum_b, sum_r};
+  bool writes = live && gl == 0;
+  const int parts = G == 64 ? block_waves : p.join;  // sums that make one output
+  if (parts > 1) {
+    if (gl == 0) sums[G == 64 ? block_wave : slot] = Map{sum_b, sum_r};
     lds_barrier();
-    if (block_wave != 0) return;
-    sum_b = sum_r = 0.0f;
-    for (int w = 0; w < block_waves; ++w) {
-      sum_b += totals[0][w].a;
-      sum_r += totals[0][w].b;
+    const int c = G == 64 ? 0 : threadIdx.x;  // of the block's channels
+    if (G < 64) out = (int64_t)blockIdx.x * own + c;
+    if (G == 64 && p.join > 1) out = d;
+    writes = G == 64 ? threadIdx.x == 0 : c < own && out < p.dim;
+    if (writes) {
+      sum_b = sum_r = 0.0f;
+      for (int i = c * parts; i < (c + 1) * parts; ++i) {
+        sum_b += sums[i].a;
+        sum_r += sums[i].b;
+      }
     }
-    if (joined) out = d;
   }
-  if (live && gl == 0) {
+  if (writes) {
     if (p.dbias) p.dbias[out] = sum_b;
     if (kRate && p.drate) p.drate[out] = sum_r;
   }
@@ -797,7 +815,7 @@ struct GatedPlan {
   int waves;  // of a row, 64-lane groups
   int threads;
   int64_t blocks;
-  bool joined;  // backward: a block has every batch row of its channels
+  int join;  // backward: batch rows of a channel in one block, all of them or 1
 };
 
 // Waves that share a row of `tiles` 512-token tiles.  More waves fill the chip
@@ -839,8 +857,8 @@ int64_t row_waves(int64_t channels, int64_t tiles, int64_t most, int64_t enough)
 // groups of 16 lanes walking a long row lost to them even where they fill the
 // chip (4 x 4096 x 4096 bf16 forward 123.2 us at 16 lanes, 112.5 at 64).
 //
-// In the backward a block of whole rows takes all batch rows of its channel
-// where they fit 8 waves, so that their sums need no second launch: while the
+// In the backward a block takes all batch rows of its channels where they fit
+// (8 waves, or 256 lanes), so that their sums need no second launch: while the
 // launches are what the call waits for (3 x 1000 x 777 training step 35.4 ->
 // 31.0 us).  Larger rows of a batch lie far apart, often a power of two, and
 // read together they meet in the same memory channels (4 x 4096 x 4096 bf16
@@ -850,24 +868,25 @@ constexpr int64_t kJoinTokens = (int64_t)1 << 22;
 GatedPlan gated_plan(int64_t batch, int64_t dim, int64_t seqlen, bool backward) {
   const int64_t channels = batch * dim;
   GatedPlan p;
-  p.waves = 1;
-  p.joined = batch == 1;
+  p.waves = p.join = 1;
+  const bool small = backward && channels * seqlen <= kJoinTokens;
   if (seqlen <= 32 * kTok) {
     p.group = 1;
     while (p.group * kTok < seqlen) p.group = p.group == 1 ? 8 : 2 * p.group;
     p.threads = 256;
-    const int64_t per_block = 256 / p.group;
-    p.blocks = (channels + per_block - 1) / per_block;
+    const int64_t slots = 256 / p.group;
+    if (small && batch <= slots) p.join = (int)batch;
+    const int64_t per_block = p.join > 1 ? slots / p.join : slots;
+    p.blocks = ((p.join > 1 ? dim : channels) + per_block - 1) / per_block;
   } else {
     const int64_t tiles = (seqlen + 64 * kTok - 1) / (64 * kTok);
     const int64_t waves = backward ? row_waves(channels, tiles, kMaxBwdWaves, kEnoughBwd)
                                    : row_waves(channels, tiles, kMaxWaves, kEnoughFwd);
     p.group = 64;
     p.waves = (int)waves;
-    const int64_t rows = backward && batch * waves <= kMaxBwdWaves && channels * seqlen <= kJoinTokens ? batch : 1;
-    p.joined = rows == batch;
-    p.threads = (int)(64 * waves * rows);
-    p.blocks = channels / rows;
+    if (small && batch * waves <= kMaxBwdWaves) p.join = (int)batch;
+    p.threads = (int)(64 * waves * p.join);
+    p.blocks = channels / p.join;
   }
   return p;
 }
@@ -934,7 +953,9 @@ GatedArgs gated_args(const GatedShape& s, int64_t dim, int64_t seqlen, const voi
 
 // Workspace of the backward: dgate_bias and drate sums per batch row, where no
 // block has them all.
-int64_t bwd_workspace(const GatedShape& s, const GatedPlan& p) { return p.joined ? 0 : 2 * s.bd * 4; }
+int64_t bwd_workspace(const GatedShape& s, const GatedPlan& p, int64_t batch) {
+  return p.join == batch ? 0 : 2 * s.bd * 4;
+}
 
 }  // namespace
 
@@ -973,7 +994,7 @@ ssm_status_t ssm_gated_scan_bwd_workspace_bytes(int64_t batch, int64_t dim, int6
                                                 int64_t* bytes) {
   GatedShape s;
   ssm_status_t st = gated_shape(batch, dim, seqlen, io, &s);
-  if (st == SSM_OK && bytes) *bytes = bwd_workspace(s, gated_plan(batch, dim, seqlen, true));
+  if (st == SSM_OK && bytes) *bytes = bwd_workspace(s, gated_plan(batch, dim, seqlen, true), batch);
   return st;
 }
 
@@ -990,7 +1011,7 @@ ssm_status_t ssm_gated_scan_bwd(int64_t batch, int64_t dim, int64_t seqlen, ssm_
   if (!x || !gate || !ckpt || !dy || !dx || !dgate) return SSM_ERR_NULL;
   if (!rate) drate = nullptr;
   if (!z) dz = nullptr;
-  const int64_t need = bwd_workspace(s, p);
+  const int64_t need = bwd_workspace(s, p, batch);
   if (workspace_bytes < need) return SSM_ERR_WORKSPACE;
   if (need && !workspace) return SSM_ERR_NULL;
   if (!need) workspace = nullptr;
@@ -1007,6 +1028,7 @@ ssm_status_t ssm_gated_scan_bwd(int64_t batch, int64_t dim, int64_t seqlen, ssm_
   a.dy = dy; a.dlast = dlast; a.dx = dx; a.dgate = dgate; a.dz = dz; a.dh0 = dh0;
   float* part = static_cast<float*>(workspace);
   a.waves = p.waves;
+  a.join = p.join;
   a.dbias = dgate_bias ? (part ? part : dgate_bias) : nullptr;
   a.drate = drate ? (part ? part + s.bd : drate) : nullptr;
   hipStream_t hs = reinterpret_cast<hipStream_t>(stream);

@@ -31,7 +31,7 @@ def fwd(lib, batch=2, dim=8, seqlen=300, io=0, mode=0, **over):
     return lib.ssm_gated_scan_fwd(batch, dim, seqlen, io, mode, *a.values(), None)
 
 
-def bwd(lib, batch=2, dim=8, seqlen=200, io=0, mode=0, nbytes=None, **over):
+def bwd(lib, batch=9, dim=8, seqlen=200, io=0, mode=0, nbytes=None, **over):
     a = dict(x=addr(1), gate=addr(2), gate_bias=addr(3), rate=addr(4), z=addr(5), reset=addr(6), ckpt=addr(7),
              dy=addr(8), dlast=addr(9), dx=addr(10), dgate=addr(11), dgate_bias=addr(12), drate=addr(13), dz=addr(14),
              dh0=addr(15), work=addr(16))
@@ -95,7 +95,7 @@ def test_bwd_refusals(lib):
     for field in ("x", "gate", "ckpt", "dy", "dx", "dgate"):
         assert bwd(lib, **{field: None}) == NULL
     assert bwd(lib, seqlen=0) == SHAPE
-    assert bwd(lib, nbytes=2 * 2 * 8 * 4 - 1) == WORKSPACE
+    assert bwd(lib, nbytes=2 * 9 * 8 * 4 - 1) == WORKSPACE
     assert bwd(lib, nbytes=0) == WORKSPACE
     assert bwd(lib, work=None) == NULL
     assert bwd(lib, work=addr(16) + 2) == ALIGN
@@ -118,9 +118,10 @@ def test_step_refusals(lib):
 
 def test_workspace_bytes(lib):
     n = ctypes.c_int64(-1)
-    assert lib.ssm_gated_scan_bwd_workspace_bytes(3, 100, 50, 0, ctypes.byref(n)) == 0 and n.value == 2 * 300 * 4
+    assert lib.ssm_gated_scan_bwd_workspace_bytes(40, 100, 50, 0, ctypes.byref(n)) == 0 and n.value == 2 * 4000 * 4
     assert lib.ssm_gated_scan_bwd_workspace_bytes(1, 100, 50, 1, ctypes.byref(n)) == 0 and n.value == 0
-    # long rows: none where one block takes every batch row of a channel (small calls)
+    # none where one block takes every batch row of a channel (small calls)
+    assert lib.ssm_gated_scan_bwd_workspace_bytes(32, 100, 50, 0, ctypes.byref(n)) == 0 and n.value == 0
     assert lib.ssm_gated_scan_bwd_workspace_bytes(3, 1000, 777, 1, ctypes.byref(n)) == 0 and n.value == 0
     assert lib.ssm_gated_scan_bwd_workspace_bytes(4, 4096, 4096, 1, ctypes.byref(n)) == 0 and n.value == 8 * 4 * 4096
     assert lib.ssm_gated_scan_bwd_workspace_bytes(64, 100, 4096, 1, ctypes.byref(n)) == 0 and n.value == 2 * 6400 * 4

@@ -103,7 +103,8 @@ def run_all(d, io, mode, seed, what, dlast=True, memory=1.0):
 SHAPES = [(1, 1, 1), (3, 70, 1), (2, 33, 5), (2, 65, 8), (1, 3, 9), (2, 37, 31), (5, 9, 64), (1, 17, 65), (2, 5, 100),
           (3, 7, 128), (1, 2, 129), (2, 3, 511), (1, 3, 512), (2, 2, 513), (1, 5, 1000), (2, 1, 1024), (1, 2, 1025),
           (1, 2, 4099), (1, 1, 9001), (2, 4100, 131), (1, 8200, 160), (8, 3, 300), (9, 2, 300), (4, 5, 600), (5, 4, 1030),
-          (2, 2, 2100), (3, 2, 1500), (17, 1, 4000)]
+          (2, 2, 2100), (3, 2, 1500), (17, 1, 4000), (8, 3, 200), (9, 3, 200), (7, 40, 250), (16, 5, 100), (17, 5, 100),
+          (32, 3, 50), (33, 2, 50), (5, 37, 60), (256, 2, 7), (257, 2, 7), (3, 200, 4), (4, 9000, 140)]
 
 
 @pytest.mark.parametrize("io", ["f32", "bf16"])
