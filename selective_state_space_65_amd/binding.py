@@ -716,7 +716,8 @@ def _gated_inputs(x, gate, gate_bias, rate, z, reset):
     if x.dim() != 3:
         raise ValueError("x must be (batch, dim, seqlen)")
     shape, io, dev = x.shape, x.dtype, x.device
-    _need(x, "x", shape, io, dev)
+    if not x.is_contiguous():
+        raise ValueError("x must be contiguous")
     _need(gate, "gate", shape, io, dev)
     if gate_bias is not None:
         _need(gate_bias, "gate_bias", shape[1:2], torch.float32, dev)
@@ -892,7 +893,8 @@ def norm_fwd(x, weight=None, bias=None, residual=None, eps=1e-5, kind="layer", o
     rows = x.numel() // dim if dim else 0
     code = _kind_code(kind)
     f32 = torch.float32
-    _need(x, "x", shape, io, dev)
+    if not x.is_contiguous():
+        raise ValueError("x must be contiguous")
     if weight is not None:
         _need(weight, "weight", shape[-1:], f32, dev)
     if bias is not None:
@@ -946,7 +948,8 @@ def norm_bwd(dy, s, rstd, mean=None, weight=None, dresidual_out=None, kind="laye
     rows = dy.numel() // dim if dim else 0
     code = _kind_code(kind)
     f32 = torch.float32
-    _need(dy, "dy", shape, io, dev)
+    if not dy.is_contiguous():
+        raise ValueError("dy must be contiguous")
     _need_residual(s, "s", shape, io, dev)
     _need(rstd, "rstd", shape[:-1], f32, dev)
     if kind == "layer":
