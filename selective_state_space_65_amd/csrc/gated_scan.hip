@@ -20,12 +20,12 @@
 // A token with a = 0 (a reset, or a gate that underflows) drops the state
 // whatever its value, so 0 * Inf must not appear: a tile in which any lane of
 // the wave has such a token runs the selecting form of each step (kDrop), and
-// every other tile the plain one.  Products of many a's are kept at FLT_MIN or
-// above so that they cannot reach 0 by underflow and be taken for a drop.
+// every other tile the plain one.  Products of many a's are kept at 2^-149, the
+// smallest float, or above so that they cannot reach 0 by underflow and be
+// taken for a drop.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
-#include <cfloat>
 #include <cstdint>
 
 #include "device_common.h"
@@ -81,11 +81,12 @@ struct Map {
   float a, b;
 };
 
-// A product of a's kept off 0.  The factors are not negative, so their bits
-// order as unsigned integers and a NaN, above them all, stays.
-__device__ __forceinline__ float off_zero(float a) {
-  return __uint_as_float(max(__float_as_uint(a), __float_as_uint(FLT_MIN)));
-}
+// A product of a's kept off 0, at the smallest subnormal: a state of size H then
+// shows at most H 2^-149 (5e-7 for the largest H) where its product with the
+// gates is gone, which is what rounding the product to a subnormal costs
+// anyway.  The factors are not negative, so their bits order as unsigned
+// integers and a NaN, above them all, stays.
+__device__ __forceinline__ float off_zero(float a) { return __uint_as_float(max(__float_as_uint(a), 1u)); }
 
 template <bool kDrop>
 __device__ __forceinline__ float apply(Map m, float h) {
