@@ -220,21 +220,28 @@ __device__ __forceinline__ float first_lane(float v, int lane) {
 // ---- the gate ----------------------------------------------------------------
 
 // Per-channel constants of the gate.  e^-(g + bias) is eb * 2^(nb - g log2 e)
-// with eb = e^-bias and nb = 0: rounding bias * log2 e instead would shift
-// every token of a channel the same way, which a long memory adds up.  A bias
-// beyond 20 goes into the exponent after all (eb = 1), where neither factor
-// can overflow against the other.
+// with nb the whole number next to -bias log2 e and eb = e^(-bias - nb ln 2), the
+// rest, from ln 2 in two parts (the reduction of Cody and Waite).  Rounding
+// bias * log2 e instead would shift every token of a channel the same way, which
+// a long memory adds up; the whole of e^-bias in eb would let the other factor
+// overflow, or vanish, before the product does.  A bias beyond 2^14 closes or
+// opens its gate, or meets a g whose own rounding is as large: it goes into the
+// exponent as it is, infinities too.
 struct GateParams {
   float eb, nb, rate, nr;
 };
+
+constexpr float kLn2Low = -1.9046542e-9f;  // ln 2 - kLn2
 
 template <bool kRate>
 __device__ __forceinline__ GateParams gate_params(const float* gate_bias, const float* rate, int64_t d) {
   GateParams p;
   const float bias = gate_bias ? gate_bias[d] : 0.0f;
-  const bool small = __builtin_fabsf(bias) <= 20.0f;
-  p.eb = small ? expf(-bias) : 1.0f;
-  p.nb = small ? 0.0f : -bias * kLog2e;
+  const bool split = __builtin_fabsf(bias) <= 16384.0f;
+  const float n = __builtin_rintf(-bias * kLog2e);
+  const float r = __builtin_fmaf(-n, kLn2Low, __builtin_fmaf(-n, kLn2, -bias));
+  p.eb = split ? expf(r) : 1.0f;
+  p.nb = split ? n : -bias * kLog2e;
   p.rate = kRate ? rate[d] : 0.0f;
   p.nr = -p.rate * kLog2e;
   return p;

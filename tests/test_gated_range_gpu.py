@@ -1,5 +1,6 @@
 """The gated recurrence at the ends of its ranges, through the C ABI against the
-token-by-token float64 form (needs an MI355X): states near the largest float.
+token-by-token float64 form (needs an MI355X): states near the largest float,
+gates far from their bias.
 
 Bounds as in test_gated_gpu.py; what a case adds to them stands at the case.
 """
@@ -9,7 +10,7 @@ import torch
 
 import gated_reference as ref
 import selective_state_space_65_amd as ssm
-from test_gated_gpu import DEV, IO, MODES, check, host, np64, say
+from test_gated_gpu import DEV, IO, MODES, check, host, np64, run_all, say
 
 pytestmark = pytest.mark.gpu
 
@@ -71,3 +72,57 @@ def test_a_large_gradient_ends_at_closed_gates(L, size):
     check(g["dx"], b["dx"], b["dx_err"] + lost, "f32", "dx")
     check(g["dgate"], b["dgate"], b["dgate_err"] + lost * hb * da, "f32", "dgate")
     check(g["dh0"], b["dh0"], b["dh0_err"] + lost, "f32", "dh0")
+
+
+@pytest.mark.parametrize("rate", [False, True])
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("mode", MODES)
+@pytest.mark.parametrize("L", [5, 40, 120, 600])
+def test_a_bias_that_the_gate_cancels(L, mode, io, rate):
+    """Biases up to 60 on either side and gates that bring their sum back to [-3, 3], so that memories stay within 100
+    tokens.  Beside the bounds' 16 u for the argument: log2 e as a float is off by 1.4e-8, 63 * 1.4e-8 < 15 u, which K1 =
+    300 u holds with 2 * 20 for the memory of sigmoid(3) (with a rate of 1.5 to 3, at least 0.07 off 1: 15 tokens)."""
+    say("gated bias %s %s rate=%s L=%d" % (mode, io, rate, L))
+    bias = torch.tensor([19.0, -19.5, 21.0, -20.5, 33.3, -27.7, 60.0, -59.0, 7.25])
+    d = dict(x=normal((2, 9, L), 80, io), z=normal((2, 9, L), 81, io), h0=normal((2, 9), 82), reset=None,
+             gate=(normal((2, 9, L), 83).clamp(-2.5, 2.5).cpu() - bias[:, None]).to(IO[io]).to(DEV),
+             gate_bias=bias.to(DEV), rate=torch.linspace(1.5, 3.0, 9).to(DEV) if rate else None)
+    run_all(d, io, mode, L, "bias")
+
+
+@pytest.mark.parametrize("mode", MODES)
+@pytest.mark.parametrize("L", [6, 40, 120, 250, 700])
+def test_a_gate_far_beyond_its_bias(L, mode):
+    """Gates of -92 and 95 under biases of 20 and -20: v = -72 and 75, where sigmoid(v) and its distance from 1 are still
+    normal floats, take a state of 1e31 to a number of the size of x and a token of 1e33 into it.  The argument of the
+    exponential, about 110, is rounded by 44 u, and log2 e adds 20 u: twice that and the memory of 20 stay within K1."""
+    say("gated far gate %s L=%d" % (mode, L))
+    bias = torch.tensor([20.0, -20.0, 19.0, -19.0, 20.0, -20.0, 0.0])
+    gate = normal((2, 7, L), 90).clamp(-2.5, 2.5).cpu() - bias[:, None]
+    x = normal((2, 7, L), 91).cpu()
+    for c in (0, 2, 4):  # the state goes through a nearly closed gate
+        x[:, c, c], gate[:, c, c + 1] = 1e31, -92.0
+    for c in (1, 3, 5):  # the token goes through its own, nearly open, gate
+        x[:, c, c], gate[:, c, c] = (1e33 if mode == "convex" else 1e16 if mode == "norm" else 1.0), 95.0
+    d = dict(x=x.to(DEV), gate=gate.to(DEV), gate_bias=bias.to(DEV), rate=None, z=None, reset=None, h0=normal((2, 7), 92))
+    run_all(d, "f32", mode, L, "far")
+    state = d["h0"].clone()
+    f = ref.forward(mode=mode, **host(d))
+    for t in range(6):
+        y = ssm.gated_state_update(state, d["x"][..., t].contiguous(), d["gate"][..., t].contiguous(), d["gate_bias"],
+                                   mode=mode)
+        check(y, f["y"][..., t], f["y_err"][..., t], "f32", "token %d" % t)
+
+
+def test_a_bias_that_is_not_finite():
+    """A bias of -Inf closes its channel (y = w x, the state dropped), one of Inf holds the state, NaN stays in its channel;
+    beyond 2^14 the same by size."""
+    bias = torch.tensor([-float("inf"), float("inf"), float("nan"), -1e5, 1e5, 3e38, -3e38, 0.0], device=DEV)
+    x, gate, h0 = normal((1, 8, 300), 95), normal((1, 8, 300), 96), normal((1, 8), 97)
+    y, last = ssm.gated_scan_fwd(x, gate, bias, h0=h0, mode="convex")
+    torch.cuda.synchronize()
+    for c in (0, 3, 6):
+        assert torch.equal(y[0, c], x[0, c])
+    for c in (1, 4, 5):
+        assert torch.equal(last[0, c], h0[0, c])
+    assert torch.isnan(y[0, 2]).all() and torch.isfinite(y[0, 7]).all()
