@@ -728,30 +728,45 @@ __global__ __launch_bounds__(G == 64 ? 64 * kMaxBwdWaves : 256, sizeof(IoT) == 2
   }
 }
 
-// out[d] = sum over the batch rows, in order.
-__global__ __launch_bounds__(64) void gated_bwd_reduce_kernel(const float* bias_part, const float* rate_part,
-                                                               float* dbias, float* drate, int64_t batch,
-                                                               int64_t dim) {
-  const int64_t d = (int64_t)blockIdx.x * 64 + threadIdx.x;
-  if (d >= dim) return;
-  float sb = 0.0f, sr = 0.0f;
-  int64_t b = 0;
-  for (; b + 8 <= batch; b += 8) {  // 8 rows requested at once, added in order
-    float vb[8], vr[8];
+// out[d] = the sum over the batch rows: 32 channels a block, blockDim / 32
+// slices of the rows.  A slice requests 8 of its rows at once; rows and slices
+// are added in order, in 64 bits, since a batch of many short rows is a long
+// sum (65536 rows of one token, one chain of 32 bits: off by 7e-4 of the sum).
+constexpr int kReduceSlices = 32;
+
+__global__ __launch_bounds__(32 * kReduceSlices) void gated_bwd_reduce_kernel(const float* bias_part,
+                                                                             const float* rate_part, float* dbias,
+                                                                             float* drate, int64_t batch,
+                                                                             int64_t dim) {
+  __shared__ double sums[2][kReduceSlices][33];
+  const int col = threadIdx.x & 31, slice = threadIdx.x >> 5, slices = blockDim.x >> 5;
+  const int64_t d = (int64_t)blockIdx.x * 32 + col;
+  double sb = 0.0, sr = 0.0;
+  if (d < dim) {
+    int64_t b = slice;
+    for (; b + 7 * slices < batch; b += 8 * slices) {
+      float vb[8], vr[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      vb[j] = dbias ? bias_part[(b + j) * dim + d] : 0.0f;
-      vr[j] = drate ? rate_part[(b + j) * dim + d] : 0.0f;
+      for (int j = 0; j < 8; ++j) {
+        vb[j] = dbias ? bias_part[(b + j * slices) * dim + d] : 0.0f;
+        vr[j] = drate ? rate_part[(b + j * slices) * dim + d] : 0.0f;
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) sb += vb[j], sr += vr[j];
     }
-#pragma unroll
-    for (int j = 0; j < 8; ++j) sb += vb[j], sr += vr[j];
+    for (; b < batch; b += slices) {
+      if (dbias) sb += bias_part[b * dim + d];
+      if (drate) sr += rate_part[b * dim + d];
+    }
   }
-  for (; b < batch; ++b) {
-    if (dbias) sb += bias_part[b * dim + d];
-    if (drate) sr += rate_part[b * dim + d];
+  sums[0][slice][col] = sb;
+  sums[1][slice][col] = sr;
+  lds_barrier();
+  if (slice == 0 && d < dim) {
+    for (int i = 1; i < slices; ++i) sb += sums[0][i][col], sr += sums[1][i][col];
+    if (dbias) dbias[d] = (float)sb;
+    if (drate) drate[d] = (float)sr;
   }
-  if (dbias) dbias[d] = sb;
-  if (drate) drate[d] = sr;
 }
 
 // ---- the decode step ---------------------------------------------------------
@@ -1043,7 +1058,9 @@ ssm_status_t ssm_gated_scan_bwd(int64_t batch, int64_t dim, int64_t seqlen, ssm_
   hipError_t e =
       io == SSM_BF16 ? launch_gated<bf16_t, true>(a, p, mode, hs) : launch_gated<float, true>(a, p, mode, hs);
   if (e == hipSuccess && part && (dgate_bias || drate)) {
-    hipLaunchKernelGGL(gated_bwd_reduce_kernel, dim3((unsigned)((dim + 63) / 64)), dim3(64), 0, hs, part,
+    int slices = 2;  // 8 rows each where the batch has them
+    while (slices < kReduceSlices && 8 * slices < batch) slices *= 2;
+    hipLaunchKernelGGL(gated_bwd_reduce_kernel, dim3((unsigned)((dim + 31) / 32)), dim3(32 * slices), 0, hs, part,
                        part + s.bd, dgate_bias, drate, batch, dim);
     e = hipGetLastError();
   }

@@ -1,6 +1,6 @@
 """The gated recurrence at the ends of its ranges, through the C ABI against the
 token-by-token float64 form (needs an MI355X): states near the largest float,
-gates far from their bias.
+gates far from their bias, batches of many short rows.
 
 Bounds as in test_gated_gpu.py; what a case adds to them stands at the case.
 """
@@ -126,3 +126,24 @@ def test_a_bias_that_is_not_finite():
     for c in (1, 4, 5):
         assert torch.equal(last[0, c], h0[0, c])
     assert torch.isnan(y[0, 2]).all() and torch.isfinite(y[0, 7]).all()
+
+
+@pytest.mark.parametrize("rate", [False, True])
+@pytest.mark.parametrize("shape", [(65536, 4, 1), (5000, 33, 7), (4096, 64, 64), (300, 65, 20), (9, 70, 700)])
+def test_sums_over_many_batch_rows(shape, rate):
+    """dgate_bias and drate over batches that no block holds whole, every row alike, so that each addition of a chain would
+    be rounded the same way: within the bound of a tree of additions, whatever the batch."""
+    say("gated batch sums %s rate=%s" % (shape, rate))
+    batch, dim, L = shape
+    d = dict(x=normal((1, dim, L), 100), gate=normal((1, dim, L), 101).clamp(-3, 3), h0=normal((1, dim), 102), z=None)
+    d = {k: v if v is None else v.expand(batch, *v.shape[1:]).contiguous() for k, v in d.items()}
+    d.update(gate_bias=torch.zeros(dim, device=DEV), reset=None,
+             rate=torch.linspace(1.2, 3.0, dim).to(DEV) if rate else None)
+    dy = normal((1, dim, L), 103).expand(shape).contiguous()
+    kw = {k: d[k] for k in ("gate_bias", "rate", "z", "reset")}
+    _, _, ck = ssm.gated_scan_fwd_save(d["x"], d["gate"], h0=d["h0"], **kw)
+    g = ssm.gated_scan_bwd(d["x"], d["gate"], dy, ck, **kw)
+    one = {k: v if v is None or k in ("gate_bias", "rate") else v[:1] for k, v in d.items()}
+    b = ref.backward(dy=np64(dy[:1]), mode="plain", **host(one))
+    for k in ("dgate_bias", "drate")[:1 + rate]:
+        check(g[k], batch * b[k], batch * b[k + "_err"], "f32", k)
