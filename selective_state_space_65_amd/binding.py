@@ -11,8 +11,6 @@ import ctypes
 import functools
 import os
 
-import torch
-
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libssm_scan.so")
 
@@ -668,9 +666,20 @@ def _state_update(disc, state, u, delta, A, B, C, D, z, delta_bias, delta_softpl
 # so their hot path is kept short: the current device and the raw handle of a
 # device's current stream come from torch's own bindings (0.1 us; the public
 # torch.cuda.current_stream builds an object, 2 us), with the public functions
-# where those are missing, and pointers are taken without a helper.
-_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda i: torch.cuda.current_stream(i).cuda_stream)
+# where those are missing, and pointers are taken without a helper.  torch is
+# bound by the first call, so that loading the library needs none (an import
+# statement in each function costs 0.1 us a call).
+torch = None
+_raw_stream = None
+
+
+def _device():
+    """The current device; the first call binds torch and puts torch's own function in this one's place."""
+    global torch, _device, _raw_stream
+    import torch
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda i: torch.cuda.current_stream(i).cuda_stream)
+    _device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+    return _device()
 
 
 @functools.lru_cache(maxsize=1024)
@@ -688,6 +697,7 @@ def _elsewhere(fn, stream, **args):
     freed memory is handed on in its order), and the tensors passed in are
     recorded on it.
     """
+    import torch
     first = next(iter(args.values()))
     if not first.is_cuda:
         raise ValueError("%s: tensors must be on a GPU, got %s" % (fn.__name__, first.device))
