@@ -701,6 +701,8 @@ def _elsewhere(fn, stream, **args):
     first = next(iter(args.values()))
     if not first.is_cuda:
         raise ValueError("%s: tensors must be on a GPU, got %s" % (fn.__name__, first.device))
+    if stream is not None and stream.device != first.device:
+        raise ValueError("%s: tensors are on %s, the stream on %s" % (fn.__name__, first.device, stream.device))
     with torch.cuda.device(first.device):
         if stream is None:
             return fn(**args)

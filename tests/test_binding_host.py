@@ -1,8 +1,14 @@
 """What the binding does before a GPU is touched: the library loads without
-torch."""
+torch, and a stream of another device than the tensors' is refused."""
 import os
 import subprocess
 import sys
+import types
+
+import pytest
+import torch
+
+import selective_state_space_65_amd as ssm
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
@@ -16,3 +22,16 @@ def test_library_loads_without_torch():
     r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=100)
     assert r.returncode == 0, r.stderr
     assert r.stdout.split(" ", 1)[1].strip() == "(1, 2, 2)"
+
+
+def test_stream_of_another_device_is_refused():
+    """Such a stream makes its own device current, so the call would run on the tensors' default stream instead, ordered with
+    nothing.  The tensor and the stream are stand-ins: two devices are not needed to say no."""
+    x = types.SimpleNamespace(is_cuda=True, device=torch.device("cuda", 0), get_device=lambda: 0)
+    side = types.SimpleNamespace(device=torch.device("cuda", 1))
+    for call in (lambda: ssm.gated_scan_fwd(x, x, stream=side), lambda: ssm.gated_scan_fwd_save(x, x, stream=side),
+                 lambda: ssm.gated_scan_bwd(x, x, x, x, stream=side),
+                 lambda: ssm.gated_state_update(x, x, x, stream=side), lambda: ssm.norm_fwd(x, stream=side),
+                 lambda: ssm.norm_bwd(x, x, x, stream=side)):
+        with pytest.raises(ValueError, match="stream"):
+            call()
