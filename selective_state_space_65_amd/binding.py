@@ -708,7 +708,7 @@ def _elsewhere(fn, stream, **args):
             return fn(**args)
         with torch.cuda.stream(stream):
             for t in args.values():
-                if isinstance(t, torch.Tensor):
+                if isinstance(t, torch.Tensor) and t.device == first.device:
                     t.record_stream(stream)
             return fn(**args)
 
