@@ -1,6 +1,7 @@
 """The gated recurrence at the ends of its ranges, through the C ABI against the
 token-by-token float64 form (needs an MI355X): states near the largest float,
-gates far from their bias, batches of many short rows.
+gates far from their bias, batches of many short rows, memories of thousands of
+tokens.
 
 Bounds as in test_gated_gpu.py; what a case adds to them stands at the case.
 """
@@ -147,3 +148,40 @@ def test_sums_over_many_batch_rows(shape, rate):
     b = ref.backward(dy=np64(dy[:1]), mode="plain", **host(one))
     for k in ("dgate_bias", "drate")[:1 + rate]:
         check(g[k], batch * b[k], batch * b[k + "_err"], "f32", k)
+
+
+def memory_of(d):
+    """What the reference's bounds grow by: they are (2 tau + 64) u, taken as 300 u for memories of tau <= 100 tokens; here tau
+    is the longest of the case's own gates, and no more than the tokens there are."""
+    a, _, _, _, _ = ref.gates(np64(d["gate"]), np64(d["gate_bias"]), np64(d["rate"]), "plain")
+    return (2 * min(1 / (1 - a).min(), a.shape[-1]) + 64) / 300
+
+
+@pytest.mark.parametrize("constant", [False, True])
+@pytest.mark.parametrize("mode", MODES)
+@pytest.mark.parametrize("gates", ["tau 1000", "tau 10000", "rates"])
+def test_long_memory(gates, mode, constant):
+    """Memories of thousands of tokens: a bias of a or of 1 - a that every token shares adds up over tau tokens, so the gates
+    of a row also run as one constant, whose rounding every token does share."""
+    L, dim = 6000, 7
+    say("gated long memory %s %s constant=%s" % (gates, mode, constant))
+    # x of one sign: the states are as large as the sums of magnitudes that the bounds are taken of
+    d = dict(x=normal((1, dim, L), 110).abs(), z=normal((1, dim, L), 111), h0=normal((1, dim), 112).abs(), reset=None, rate=None)
+    gate = normal((1, dim, 1), 113).expand(1, dim, L) if constant else normal((1, dim, L), 113)
+    d["gate"] = gate.clamp(-1, 1).contiguous()
+    if gates == "rates":
+        d.update(rate=torch.logspace(-2.7, -1, dim).to(DEV), gate_bias=normal((dim,), 114).clamp(-1, 1))
+    else:
+        tau = float(gates.split()[1])
+        d["gate_bias"] = torch.full((dim,), float(np.log(tau - 1)), device=DEV)
+    run_all(d, "f32", mode, 7, "long", memory=memory_of(d))
+    # the decode step, from the state in the middle of the row
+    f = ref.forward(mode=mode, **host(d))
+    state = torch.tensor(f["states"][..., 2999], dtype=torch.float32, device=DEV)
+    part = {k: d[k] if k in ("gate_bias", "rate") else None if d[k] is None else d[k][..., 3000:3200].contiguous()
+            for k in ("x", "gate", "z", "gate_bias", "rate")}
+    y = torch.stack([ssm.gated_state_update(state, *(part[k][..., t].contiguous() for k in ("x", "gate")),
+                                            d["gate_bias"], d["rate"], part["z"][..., t].contiguous(), mode=mode)
+                     for t in range(200)], -1)
+    # the state taken over is rounded once; 200 tokens add 200 roundings of 2 u to the gates' 64 u
+    check(y, f["y"][..., 3000:3200], f["y_err"][..., 3000:3200] * (2 * 200 + 65) / 300, "f32", "steps")
