@@ -489,8 +489,11 @@ ssm_status_t ssm_scan_bwd_complex(int64_t batch, int64_t dim, int64_t dstate, in
  *
  * A reset starts a packed sequence: the state before it is dropped, whatever
  * its value (infinities and NaN too); w_l keeps the token's own gate.  A gate
- * whose a_l is exactly 0 drops the state in the same way.  rate must not be
- * negative (a_l <= 1).
+ * whose a_l is exactly 0 drops the state in the same way; an a_l or 1 - a_l below
+ * the smallest normal float may count as 0.  A product of gates of several tokens
+ * does not: an infinite state stays infinite behind it, and a finite one of size
+ * H may show H 2^-149 where the product is smaller.  rate must not be negative
+ * (a_l <= 1).
  *
  * The state and all arithmetic are fp32.
  */
@@ -512,7 +515,8 @@ typedef enum {
  *   y          [batch, dim, seqlen]     io     written
  *   last_state [batch, dim]             fp32   written when not NULL
  *   ckpt       [batch, dim, ceil(seqlen/128)] fp32  written when not NULL: the state before tokens
- *                                              0, 128, 256, ..., which ssm_gated_scan_bwd reads
+ *                                              0, 128, 256, ..., for ssm_gated_scan_bwd (which reads
+ *                                              those that its tiles of 512 tokens start at)
  *
  * Any sizes >= 1 and any element-aligned pointers; rows of 2^30 tokens or
  * more are SSM_ERR_UNSUPPORTED, as are launches of 2^32 lanes (2^26 channels
@@ -548,8 +552,8 @@ ssm_status_t ssm_gated_scan_fwd(int64_t batch, int64_t dim, int64_t seqlen, ssm_
  *                                       bytes (may be NULL when that is 0); overwritten
  *
  * Errors as ssm_gated_scan_fwd; SSM_ERR_WORKSPACE when workspace_bytes is too
- * small.  Allocates nothing.  dgate_bias and drate are fixed-order sums, so the
- * result is deterministic.  Calls that overlap in time need workspaces of
+ * small.  Allocates nothing.  dgate_bias and drate are fixed-order sums (over a
+ * workspace's batch rows in 64 bits), so the result is deterministic.  Calls that overlap in time need workspaces of
  * their own.
  */
 ssm_status_t ssm_gated_scan_bwd(int64_t batch, int64_t dim, int64_t seqlen, ssm_dtype_t io, ssm_gated_mode_t mode,
@@ -585,7 +589,9 @@ ssm_status_t ssm_gated_state_update(int64_t batch, int64_t dim, ssm_dtype_t io, 
  *   rstd = 1 / sqrt(sum((s - mean)^2) / dim + eps)
  *   y    = (s - mean) * rstd * weight + bias
  *
- * The sums, mean and rstd are fp32; the variance is summed from s - mean.
+ * The sums, mean and rstd are fp32; the variance is summed from s - mean.  A row
+ * whose squares sum to more than the largest float (numbers of about 1e19 /
+ * sqrt(dim) and above) has rstd = 0.
  */
 typedef enum {
   SSM_NORM_LAYER = 0, /* mean subtracted */

@@ -12,8 +12,9 @@
 // Every stream is read once and written once.
 //
 // The backward walks the tiles from the last to the first.  In a tile it
-// recomputes the states from the forward's checkpoint (one every 128 tokens)
-// and runs the adjoint lambda_l = q_l + a_{l+1} lambda_{l+1}, which is the same
+// recomputes the states from the forward's checkpoint before it (the forward
+// writes one every 128 tokens, the tiles of 512 read every fourth) and runs the
+// adjoint lambda_l = q_l + a_{l+1} lambda_{l+1}, which is the same
 // kind of recurrence in the other direction: mu_l = a_l lambda_l is carried
 // from lane to lane by maps mu -> A mu + B and a suffix scan.
 //
@@ -36,14 +37,19 @@
 namespace {
 
 constexpr int kTok = 8;          // tokens per lane
-constexpr int kCkptStep = 128;   // tokens between checkpoints
+constexpr int kCkptStep = 128;   // tokens between checkpoints, as the header has it
 constexpr int kMaxWaves = 16;    // waves that share one channel
 constexpr int kMaxBwdWaves = 8;  // ... in the backward, which takes more registers
 
 // bf16 rows go past the caches: an access of a wave covers whole lines, each
 // touched once (forward at 4 x 4096 x 4096 116.8 -> 112.9 us, with its backward
 // 317.7 -> 303.2 us, interleaved).  An fp32 piece is two accesses to the same
-// line, and its second half would miss (8 x 1536 x 2048 219 -> 231 us).
+// line, and its second half would miss (8 x 1536 x 2048 219 -> 231 us).  With an
+// operator behind it that reads y, or every gradient, the difference stays
+// where the tensors are larger than the caches (4 x 4096 x 4096, forward and a
+// product 172 -> 163 us, training step and two products 422 -> 378) and turns
+// where they are not (1 x 4096 x 4096 training step and products 102 -> 106 us, 8
+// x 1024 x 1024 62 -> 65).
 template <typename IoT>
 constexpr bool streamed = sizeof(IoT) == 2;
 
@@ -842,17 +848,25 @@ struct GatedPlan {
 };
 
 // Waves that share a row of `tiles` 512-token tiles.  More waves fill the chip
-// (from 12 on each of the 1024 SIMDs; past `enough` the launch only gets
-// longer), but the row is walked in steps of that many tiles, and a last step
-// that is mostly empty costs a whole one; 16 waves that walk it in a single
-// step have nothing to load ahead and one block to a compute unit.  1, 2, 3,
-// 4, 8 and 16 are the counts whose blocks fill a compute unit's registers.
+// (up to 12 for each of the 1024 SIMDs, resident or queued; past `enough` a
+// row gets no more), but the row is walked in steps of that many tiles, and a
+// last step that is mostly empty costs a whole one; 16 waves that walk it in a
+// single step have nothing to load ahead and one block to a compute unit.  1, 2,
+// 3, 4, 8 and 16 are the counts whose blocks fill a compute unit's registers.
 // Measured (us, bf16 unless said, waves in brackets): forward 3 x 1001 x 8001
 // 47.9 [8] 56.4 [16] 52.8 [6]; 4 x 1024 x 4160 30.3 [3] 33.9 [5] 41.9 [8]; 2 x
 // 5120 x 1500 29.5 [3] 35.6 [4] 36.1 [2]; fp32 1 x 2560 x 131072 750 [16] 774
 // [8] 798 [10], 8 x 1536 x 2048 72.7 [4] 78.9 [2], 1 x 2560 x 8192 65.1 [8]
 // 70.5 [16]; training step 4 x 1024 x 4160 86.8 [3] 102.5 [4] 124 [5]; 8 x 512
 // x 8200 160 [4] 188 [6] 207 [5]; 8 x 1536 x 2048 fp32 220.5 [2] 228.8 [1].
+//
+// `enough` ends the larger counts above 12288 channels.  Measured past that edge,
+// the larger count is still the better one by up to 8% (4 x 3500 x 2048 fp32:
+// forward 87.5 [2, as planned] 80.8 [4], training step 256.9 [1, as planned] 242.1
+// [2] 238.4 [4]; 8 x 2560 x 4096: forward 117.4 [2, as planned] 111.2 [4], training
+// step 340.4 [1, as planned] 322.4 [4]); in bf16 at 2048 tokens 2 waves are the
+// best on both sides (8 x 1600 training step 107.7 [1, as planned] 104.2 [2] 108.4
+// [4]).  So the edge costs time above it and is no optimum.
 constexpr int64_t kFewWaves = 12288;
 constexpr int64_t kEnoughFwd = 49152;
 constexpr int64_t kEnoughBwd = 24576;
@@ -882,10 +896,14 @@ int64_t row_waves(int64_t channels, int64_t tiles, int64_t most, int64_t enough)
 //
 // In the backward a block takes all batch rows of its channels where they fit
 // (8 waves, or 256 lanes), so that their sums need no second launch: while the
-// launches are what the call waits for (3 x 1000 x 777 training step 35.4 ->
-// 31.0 us).  Larger rows of a batch lie far apart, often a power of two, and
-// read together they meet in the same memory channels (4 x 4096 x 4096 bf16
-// 296 -> 357 us).
+// launches are what the call waits for (bf16 training steps, two launches -> one:
+// 3 x 1000 x 777 35.6 -> 31.4 us, 4 x 1024 x 1024 35.3 -> 31.2, 8 x 1024 x 512
+// 35.4 -> 31.3, 4 x 4096 x 256 35.0 -> 31.1; in fp32 35.3 -> 33.8, 41.6 -> 44.5,
+// 42.7 -> 41.9, 39.9 -> 41.1).  Larger rows of a batch lie far apart, often a
+// power of two, and read together they meet in the same memory channels (bf16
+// 4 x 4096 x 1024 72 -> 76 us, 32 x 2400 x 60 36 -> 43, 4 x 4096 x 4096 296 -> 357;
+// fp32 4 x 2048 x 600 55 -> 63); small ones can lose to it too (32 x 2048 x 60
+// 35.0 -> 37.2, fp32 43.5 -> 51.0).
 constexpr int64_t kJoinTokens = (int64_t)1 << 22;
 
 GatedPlan gated_plan(int64_t batch, int64_t dim, int64_t seqlen, bool backward) {

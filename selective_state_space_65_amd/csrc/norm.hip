@@ -436,17 +436,24 @@ struct NormPlan {
 
 // Lanes, pieces and waves of a row.  The fewest lanes that hold it at one piece
 // each, up to 8 waves: many short waves keep more rows' loads in flight than
-// few long ones (forward, 16384 x 2048 bf16 with an fp32 residual, 4 / 2 / 1
-// pieces: 80.3 / 76.6 / 72.1 us; 8192 x 4096 85.7 / 81.8 / 74.8; with the
-// backward, 16384 x 2048 bf16, 2 / 1 pieces: 114.0 / 102.7).  Then two pieces
-// (4096 x 8000 forward: 57.8 us, 65.1 at one piece and 16 waves), then four
-// (2048 x 16384 forward 59.4 us, 66.6 at two pieces and 16 waves; the training
-// step 217 and 229, the backward of 16 waves spilling), then 16 waves.
+// few long ones.  Forward with a residual, 4 / 2 / 1 pieces, us for io-residual
+// bf16-bf16, bf16-fp32, fp32-fp32: 16384 x 2048 53.2 / 52.8 / 53.8, 80.8 / 79.9 /
+// 78.4, 107.4 / 105.3 / 103.3; 8192 x 4096 55.2 / 53.2 / 54.4, 83.4 / 78.2 / 75.9,
+// 109.2 / 101.5 / 97.8.  With the backward, 16384 x 2048 bf16-bf16, 2 / 1 pieces
+// 114.0 / 102.7.  Then two pieces (4096 x 8000, against one piece and 16 waves:
+// 53.7 / 61.2, 77.7 / 81.2, 102.7 / 105.6), then four (2048 x 16384, against two
+// and 16 waves: 59.6 / 66.8, 86.7 / 93.2, 114.3 / 121.8), then 16 waves, whose
+// backward spills (1024 x 32768 training step 332, 434, 478 us where its bytes take
+// 104, 182, 208 at a copy's rate; 2048 x 16384, which spills a few, 129, 216, 246).
 //
 // one_wave: a row of two waves takes one of two pieces.  For forward bf16 rows
-// that end inside a piece, where the wave with the end keeps the other waiting
-// (30000 x 777 44.6 us, 48.8 on two waves; in fp32 the loads cover it, 8191 x
-// 1001 28.7 against 26.9 on two).
+// that end inside a piece, where the wave with the end keeps the other waiting.
+// Two waves / one: with a bf16 residual 30000 x 777 48.6 / 44.0, 16384 x 1001 30.6
+// / 27.7, 65000 x 1023 128.9 / 115.3, 40000 x 515 50.7 / 49.3; with an fp32 residual
+// 62.2 / 61.2, 43.6 / 44.6, 175.1 / 176.5, 58.2 / 56.6.  Rows of whole pieces, and
+// fp32, where the loads cover it, gain or lose up to 9% by the width: bf16-bf16 30000 x
+// 776 39.0 / 39.9, 40000 x 600 45.0 / 43.2; fp32 16384 x 1001 56.6 / 57.5, 40000 x
+// 600 85.0 / 78.7.
 NormPlan norm_plan(int64_t dim, bool one_wave) {
   NormPlan p;
   p.group = 8;
@@ -476,9 +483,13 @@ NormPlan fwd_plan(int64_t rows, int64_t dim, ssm_dtype_t io) {
 }
 
 // Two blocks to a compute unit, each with a partial row of column sums; one
-// where a row takes the whole block and the partial rows are long (8192 x 4096
-// training step 190 us, 196 at 512 blocks; 2048 x 16384 217 against 232; but
-// 8191 x 1001, four rows to a block, 40 us at 512 and 45 at 128).
+// where a row takes the whole block and the partial rows are long.  Training
+// steps with a residual, 256 / 512 blocks, us for io-residual bf16-bf16, bf16-fp32,
+// fp32-fp32: 2048 x 16384 129 / 139, 216 / 233, 245 / 262; 4096 x 8000 102 / 113,
+// 189 / 195, 215 / 223; 8192 x 4096 119 / 105, 183 / 184, 206 / 211 (in bf16 alone the
+// second block's loads count for more); 8191 x 1001, four rows to a block, 44 / 38,
+// 60 / 56, 61 / 58; 16384 x 2048, two rows to a block, 113 / 99, 183 / 184, 209 /
+// 213.  128 blocks lose everywhere.
 NormPlan bwd_plan(int64_t rows, int64_t dim) {
   NormPlan p = norm_plan(dim, false);
   const int waves = std::max(p.row_waves, kBwdWaves);
@@ -522,7 +533,7 @@ hipError_t launch_norm_fwd(const NormFwdArgs& a, const NormPlan& p, bool rms, hi
 template <typename IoT, typename ResT, bool kRms>
 hipError_t launch_norm_bwd(const NormBwdArgs& a, const NormPlan& p, hipStream_t st) {
   // Blocks of several row groups join their column sums: kBwdWaves waves of
-  // 2 x pieces x lanes x 8 floats, at most 64 KB.
+  // 2 x lanes x 8 floats, at most 32 KB (such rows have one piece).
   const bool join = a.part && p.threads > 64 * p.row_waves;
   const size_t lds = join ? (size_t)(p.threads / 64) * 2 * p.pieces * p.group * kPiece * 4 : 0;
 #define SSM_NORM_CALL(G, K)                                                                                     \
