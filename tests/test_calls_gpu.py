@@ -1,6 +1,6 @@
 """Calls of the gated recurrence and the norms as programs make them (needs an
 MI355X): tensors in the wrong place beside a stream, and backwards that sum in
-a workspace on other streams.
+a workspace on other streams and in captured graphs.
 """
 import ctypes
 
@@ -97,3 +97,28 @@ def test_workspaces_on_two_streams_at_once():
     torch.cuda.synchronize()
     for j, g in got:
         assert same(g, want[j]), SUMMED[j]
+
+
+def test_workspaces_in_two_graphs():
+    """Two captured backwards of different sizes on one memory pool, replayed in turn with eager ones between: the gradients
+    of each replay are read before the next may write its own."""
+    calls = [training_call(s, 20 + i) for i, s in enumerate(SUMMED[:2])]
+    want = [c() for c in calls]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    torch.cuda.synchronize()
+    graphs, pool = [], None
+    for c in calls:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, pool=pool, stream=side):
+            held = c()
+        pool = g.pool()
+        graphs.append((g, held))
+    for k in range(6):
+        g, held = graphs[k % 2]
+        print("[gpu-case] workspace graph replay %d" % k, flush=True)
+        g.replay()
+        torch.cuda.synchronize()
+        assert same(held, want[k % 2])
+        assert same(calls[1 - k % 2](), want[1 - k % 2])
+        torch.cuda.synchronize()
