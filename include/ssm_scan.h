@@ -19,7 +19,9 @@
  * Beside the selective scan stand a gated linear recurrence with one state
  * per channel (ssm_gated_scan_fwd, ssm_gated_scan_bwd and the decode step
  * ssm_gated_state_update) and the norm in front of a block, with the residual
- * add fused in front of it (ssm_norm_fwd, ssm_norm_bwd).
+ * add fused in front of it (ssm_norm_fwd, ssm_norm_bwd).  Linear attention
+ * with a decay for each head (ssm_linear_attn_fwd, ssm_linear_attn_bwd and the
+ * decode step ssm_linear_attn_state_update) keeps a matrix of states per head.
  *
  * What is computed (for every batch row b and channel d independently):
  *
@@ -72,8 +74,9 @@
  *    partial sums), freed on the same stream within the call.  The pool's
  *    release threshold is 0: freed blocks are reused by later calls on the
  *    stream and returned to the device at the next synchronisation.
- *  - The gated recurrence and the norms (ssm_gated_*, ssm_norm_*) allocate
- *    nothing; their backwards take a workspace of the caller's, whose size a
+ *  - The gated recurrence, the norms and linear attention (ssm_gated_*,
+ *    ssm_norm_*, ssm_linear_attn_*) allocate nothing; their backwards, and the
+ *    linear-attention forward, take a workspace of the caller's, whose size a
  *    query gives.  Two calls that may overlap in time need two workspaces.
  *  - Calls on different streams are independent; the library is re-entrant.
  */
@@ -86,7 +89,7 @@
 extern "C" {
 #endif
 
-#define SSM_ABI_VERSION 14
+#define SSM_ABI_VERSION 15
 
 struct ihipStream_t; /* the same incomplete type as HIP's hipStream_t */
 
@@ -653,6 +656,113 @@ ssm_status_t ssm_norm_bwd(int64_t rows, int64_t dim, ssm_dtype_t io, ssm_dtype_t
 /* Bytes of workspace ssm_norm_bwd takes for these sizes when it sums dweight or dbias; bytes may be NULL. */
 ssm_status_t ssm_norm_bwd_workspace_bytes(int64_t rows, int64_t dim, ssm_dtype_t io, ssm_dtype_t res_io,
                                           int64_t* bytes);
+
+/*
+ * Linear attention with a decay for each head: the selective scan's recurrence
+ * with a dk x dv matrix of states per head in place of a channel's dstate
+ * states.  The Chinese explainer's S4-to-S6 sections let Delta, B and C depend on
+ * the token and keep A fixed; here k, q and step are those inputs, A = -rate is
+ * one number per head, and v takes the channels' place.
+ *
+ *   a_t = exp(-rate[h] step[b,t,h])                         (step 1 without one)
+ *   S_t = a_t S_{t-1} + k_t v_t^T                           (k_t v_t^T where reset[b,t] != 0)
+ *   y_t = scale S_t^T q_t
+ *
+ * Layouts (the last index fastest): q, k [batch, seqlen, groups, dk], v and y
+ * [batch, seqlen, heads, dv]; a group's q and k are shared by heads / groups
+ * heads in a row.  States are [batch, heads, dk, dv] fp32.  rate and step must
+ * not be negative.
+ *
+ * A reset drops the state before it, whatever its value (infinities and NaN
+ * too).  So does a decay that is 0, and a product of the decays of tokens of one
+ * chunk (64 in bf16, 32 in fp32, counted from a multiple of 512) that is below the
+ * smallest normal float.  A token's infinities and NaN reach no earlier token
+ * and none behind a reset.
+ *
+ * Decays and sums are fp32 or more.  In bf16, scores (q . k with their decay) and
+ * the state as q reads it are rounded to bf16 once for the product that follows;
+ * in the gradients of q and k, when those of rate or step are asked for, they
+ * keep 24 bits, as states do always.
+ *
+ * dk and dv up to 256, heads up to 16384 (larger is SSM_ERR_UNSUPPORTED, as are
+ * launches of 2^32 lanes); any seqlen >= 1, any element-aligned pointers;
+ * groups must divide heads (SSM_ERR_SHAPE).  No output may overlap an input or
+ * another output, except last_state == h0.  Allocates nothing; deterministic.
+ *
+ * ssm_linear_attn_fwd
+ *   q, k       [batch, seqlen, groups, dk]   io
+ *   v          [batch, seqlen, heads, dv]    io
+ *   rate       [heads]                       fp32
+ *   step       [batch, seqlen, heads]        io     may be NULL (1)
+ *   reset      [batch, seqlen]               bytes  may be NULL; nonzero where the state is dropped
+ *   h0         [batch, heads, dk, dv]        fp32   may be NULL (0); may be the same pointer as last_state
+ *   y          [batch, seqlen, heads, dv]    io     written
+ *   last_state [batch, heads, dk, dv]        fp32   written when not NULL
+ *   ckpt       [batch, heads, ceil(seqlen/512) + 1, dk, dv] fp32  written when not NULL: the state before
+ *                                            tokens 0, 512, 1024, ... and the last state, for ssm_linear_attn_bwd
+ *   workspace                                device memory, 8-byte aligned, of
+ *                                            ssm_linear_attn_fwd_workspace_bytes bytes (may be NULL when that is 0);
+ *                                            overwritten.  Too small is SSM_ERR_WORKSPACE.
+ */
+ssm_status_t ssm_linear_attn_fwd(int64_t batch, int64_t seqlen, int64_t heads, int64_t groups, int64_t dk, int64_t dv,
+                                 ssm_dtype_t io, const void* q, const void* k, const void* v, const float* rate,
+                                 const void* step, const uint8_t* reset, const float* h0, float scale, void* y,
+                                 float* last_state, float* ckpt, void* workspace, int64_t workspace_bytes,
+                                 struct ihipStream_t* stream);
+
+/* Bytes of workspace ssm_linear_attn_fwd takes for these sizes; bytes may be NULL. */
+ssm_status_t ssm_linear_attn_fwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t heads, int64_t groups,
+                                                 int64_t dk, int64_t dv, ssm_dtype_t io, int64_t* bytes);
+
+/*
+ * ssm_linear_attn_bwd -- every gradient of sum(dy * y) + sum(dlast * last_state)
+ * for ssm_linear_attn_fwd.  With R_t = dL/dS_t (what later tokens read of S_t
+ * included), g_t = -rate step_t and <., .> a sum over all elements:
+ *
+ *   R_t = scale q_t dy_t^T + a_{t+1} R_{t+1}     (no second part before a reset; + dlast at the end)
+ *   dq_t = scale S_t dy_t;   dk_t = R_t v_t;   dv_t = R_t^T k_t        (dq, dk summed over a group's heads)
+ *   dL/dg_t = a_t <S_{t-1}, R_t>                 (0 at a reset)
+ *   dstep = -rate dL/dg;  drate[h] = -sum_{b,t} step dL/dg;  dh0 = a_0 R_0
+ *
+ *   q .. reset, scale, rate              as ssm_linear_attn_fwd
+ *   ckpt                                 as the forward wrote it for the same q .. h0 (h0 is not read)
+ *   dy      [batch, seqlen, heads, dv]   io
+ *   dlast   [batch, heads, dk, dv]       fp32   may be NULL (0)
+ *   dq, dk  [batch, seqlen, groups, dk]  io     written
+ *   dv      [batch, seqlen, heads, dv]   io     written
+ *   drate   [heads]                      fp32   written when not NULL
+ *   dstep   [batch, seqlen, heads]       io     written when step and dstep are not NULL
+ *   dh0     [batch, heads, dk, dv]       fp32   written when not NULL (the gradient at h0 = 0 without one)
+ *   workspace                            device memory, 8-byte aligned, of ssm_linear_attn_bwd_workspace_bytes bytes
+ *                                        (may be NULL when that is 0); overwritten
+ */
+ssm_status_t ssm_linear_attn_bwd(int64_t batch, int64_t seqlen, int64_t heads, int64_t groups, int64_t dk, int64_t dv,
+                                 ssm_dtype_t io, const void* q, const void* k, const void* v, const float* rate,
+                                 const void* step, const uint8_t* reset, const float* ckpt, float scale,
+                                 const void* dy, const float* dlast, void* dq, void* dk_out, void* dv_out,
+                                 float* drate, void* dstep, float* dh0, void* workspace, int64_t workspace_bytes,
+                                 struct ihipStream_t* stream);
+
+/* Bytes of workspace ssm_linear_attn_bwd takes for these sizes; decays: nonzero when drate or dstep is asked for.
+ * bytes may be NULL. */
+ssm_status_t ssm_linear_attn_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t heads, int64_t groups,
+                                                 int64_t dk, int64_t dv, ssm_dtype_t io, int decays, int64_t* bytes);
+
+/*
+ * ssm_linear_attn_state_update -- one decode step: equals ssm_linear_attn_fwd
+ * with seqlen = 1 and h0 = last_state = state.
+ *
+ *   state   [batch, heads, dk, dv]  fp32  read, then overwritten
+ *   q, k    [batch, groups, dk]     io
+ *   v       [batch, heads, dv]      io
+ *   rate    [heads]                 fp32
+ *   step    [batch, heads]          io    may be NULL (1)
+ *   y       [batch, heads, dv]      io    written; must not overlap any input or state
+ */
+ssm_status_t ssm_linear_attn_state_update(int64_t batch, int64_t heads, int64_t groups, int64_t dk, int64_t dv,
+                                          ssm_dtype_t io, float* state, const void* q, const void* k, const void* v,
+                                          const float* rate, const void* step, float scale, void* y,
+                                          struct ihipStream_t* stream);
 
 /* Kernel paths of ssm_scan_fwd (reported by ssm_scan_fwd_plan). */
 typedef enum {

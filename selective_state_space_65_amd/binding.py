@@ -40,6 +40,8 @@ GATED_MODES = {"plain": 0, "convex": 1, "norm": 2}
 NORM_KINDS = {"layer": 0, "rms": 1}
 # Tokens between the checkpoints of gated_scan_fwd_save.
 GATED_CKPT_STEP = 128
+# Tokens between the states that linear_attn_fwd_save keeps.
+LINEAR_ATTN_CKPT_STEP = 512
 
 # Every symbol the header declares, with its ctypes signature.
 _I64 = ctypes.c_int64
@@ -79,6 +81,14 @@ SIGNATURES = {
     "ssm_norm_fwd": (_I, [_I64, _I64, _I, _I, _I, _P, _P, _P, _P, ctypes.c_float, _P, _P, _P, _P, _P]),
     "ssm_norm_bwd": (_I, [_I64, _I64, _I, _I, _I, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _I64, _P]),
     "ssm_norm_bwd_workspace_bytes": (_I, [_I64, _I64, _I, _I, ctypes.POINTER(_I64)]),
+    "ssm_linear_attn_fwd": (_I, [_I64, _I64, _I64, _I64, _I64, _I64, _I, _P, _P, _P, _P, _P, _P, _P, ctypes.c_float, _P,
+                                 _P, _P, _P, _I64, _P]),
+    "ssm_linear_attn_fwd_workspace_bytes": (_I, [_I64, _I64, _I64, _I64, _I64, _I64, _I, ctypes.POINTER(_I64)]),
+    "ssm_linear_attn_bwd": (_I, [_I64, _I64, _I64, _I64, _I64, _I64, _I, _P, _P, _P, _P, _P, _P, _P, ctypes.c_float, _P,
+                                 _P, _P, _P, _P, _P, _P, _P, _P, _I64, _P]),
+    "ssm_linear_attn_bwd_workspace_bytes": (_I, [_I64, _I64, _I64, _I64, _I64, _I64, _I, _I, ctypes.POINTER(_I64)]),
+    "ssm_linear_attn_state_update": (_I, [_I64, _I64, _I64, _I64, _I64, _I, _P, _P, _P, _P, _P, _P, ctypes.c_float, _P,
+                                          _P]),
     "ssm_status_string": (ctypes.c_char_p, [_I]),
     "ssm_last_hip_error": (_I, []),
     "ssm_abi_version": (_I, []),
@@ -989,3 +999,157 @@ def norm_bwd(dy, s, rstd, mean=None, weight=None, dresidual_out=None, kind="laye
     if st:
         _check("ssm_norm_bwd", st)
     return g
+
+
+def _linear_attn_inputs(q, k, v, rate, step, reset):
+    if q.dim() != 4 or v.dim() != 4:
+        raise ValueError("q must be (batch, seqlen, groups, dk), v (batch, seqlen, heads, dv)")
+    if not q.is_contiguous():
+        raise ValueError("q must be contiguous")
+    batch, seqlen, groups, dk = q.shape
+    heads, dv = v.shape[2:]
+    io, dev = q.dtype, q.device
+    _need(k, "k", q.shape, io, dev)
+    _need(v, "v", (batch, seqlen, heads, dv), io, dev)
+    _need(rate, "rate", (heads,), torch.float32, dev)
+    if step is not None:
+        _need(step, "step", (batch, seqlen, heads), io, dev)
+    if reset is not None:
+        _need(reset, "reset", (batch, seqlen), torch.bool if reset.dtype == torch.bool else torch.uint8, dev)
+    return batch, seqlen, heads, groups, dk, dv, io, dev
+
+
+def linear_attn_ckpt_shape(batch, seqlen, heads, dk, dv):
+    """Shape of the float32 checkpoint tensor of linear_attn_fwd_save / linear_attn_bwd."""
+    return (batch, heads, (seqlen + LINEAR_ATTN_CKPT_STEP - 1) // LINEAR_ATTN_CKPT_STEP + 1, dk, dv)
+
+
+def linear_attn_fwd(q, k, v, rate, step=None, reset=None, h0=None, scale=1.0, out=None, last_state=None, ckpt=None,
+                    return_last_state=True, stream=None):
+    """Linear attention with a decay for each head (ssm_linear_attn_fwd); returns (y, last_state).
+
+    S_t = a_t S_{t-1} + k_t v_t^T with a_t = exp(-rate * step_t), y_t = scale * S_t^T q_t.
+
+    q, k: (batch, seqlen, groups, dk), v: (batch, seqlen, heads, dv) in one io
+    dtype (float32 or bfloat16), each group's q and k shared by heads / groups
+    heads; rate: (heads,) float32, >= 0; step: (batch, seqlen, heads) in the io
+    dtype, >= 0 (1 without one); reset: (batch, seqlen) uint8 or bool, nonzero
+    where a sequence starts and the state before is dropped; h0: (batch, heads,
+    dk, dv) float32, which may be the same tensor as last_state.  y is like v;
+    last_state is float32 (None when return_last_state is False).  ckpt, when
+    given, receives the backward's checkpoints (linear_attn_ckpt_shape).
+    stream: run on that torch.cuda.Stream instead of the current one; new
+    outputs then belong to it, as tensors made under torch.cuda.stream do.
+    """
+    if stream is not None or not q.is_cuda or q.get_device() != _device():
+        return _elsewhere(linear_attn_fwd, **locals())
+    batch, seqlen, heads, groups, dk, dv, io, dev = _linear_attn_inputs(q, k, v, rate, step, reset)
+    f32 = torch.float32
+    state = (batch, heads, dk, dv)
+    if h0 is not None:
+        _need(h0, "h0", state, f32, dev)
+    if out is None:
+        out = torch.empty_like(v)
+    else:
+        _need(out, "out", v.shape, io, dev)
+    if last_state is not None:
+        _need(last_state, "last_state", state, f32, dev)
+    elif return_last_state:
+        last_state = torch.empty(state, dtype=f32, device=dev)
+    if ckpt is not None:
+        _need(ckpt, "ckpt", linear_attn_ckpt_shape(batch, seqlen, heads, dk, dv), f32, dev)
+    lib = _lib or load_library()
+    io_code = _io_code(io)
+    size = _workspace_bytes("ssm_linear_attn_fwd_workspace_bytes", batch, seqlen, heads, groups, dk, dv, io_code)
+    work = torch.empty(size, dtype=torch.uint8, device=dev) if size else None
+    st = lib.ssm_linear_attn_fwd(batch, seqlen, heads, groups, dk, dv, io_code, q.data_ptr(), k.data_ptr(),
+                                 v.data_ptr(), rate.data_ptr(), _ptr(step), _ptr(reset), _ptr(h0), scale,
+                                 out.data_ptr(), _ptr(last_state), _ptr(ckpt), _ptr(work), size,
+                                 _raw_stream(dev.index))
+    if st:
+        _check("ssm_linear_attn_fwd", st)
+    return out, last_state
+
+
+def linear_attn_fwd_save(q, k, v, rate, step=None, reset=None, h0=None, scale=1.0, out=None, last_state=None, ckpt=None,
+                         stream=None):
+    """linear_attn_fwd that also writes the backward's checkpoints; returns (y, last_state, ckpt)."""
+    if stream is not None or not q.is_cuda or q.get_device() != _device():
+        return _elsewhere(linear_attn_fwd_save, **locals())
+    if ckpt is None:
+        if q.dim() != 4 or v.dim() != 4:
+            raise ValueError("q must be (batch, seqlen, groups, dk), v (batch, seqlen, heads, dv)")
+        shape = linear_attn_ckpt_shape(q.shape[0], q.shape[1], v.shape[2], q.shape[3], v.shape[3])
+        ckpt = torch.empty(shape, dtype=torch.float32, device=q.device)
+    out, last_state = linear_attn_fwd(q, k, v, rate, step, reset, h0, scale, out, last_state, ckpt)
+    return out, last_state, ckpt
+
+
+def linear_attn_bwd(q, k, v, rate, dy, ckpt, step=None, reset=None, dlast=None, scale=1.0,
+                    need=("drate", "dstep", "dh0"), stream=None):
+    """Gradients of sum(dy * y) + sum(dlast * last_state) for linear_attn_fwd (ssm_linear_attn_bwd).
+
+    ckpt is what linear_attn_fwd_save wrote for the same q, k, v, rate, step,
+    reset, h0 and scale.  Returns a dict: dq, dk, dv (io dtype) and, when named
+    in `need`, drate (heads,) float32, dstep (io dtype, only with a step) and dh0
+    (batch, heads, dk, dv) float32; None for the others.
+    """
+    if stream is not None or not q.is_cuda or q.get_device() != _device():
+        return _elsewhere(linear_attn_bwd, **locals())
+    batch, seqlen, heads, groups, dk, dv, io, dev = _linear_attn_inputs(q, k, v, rate, step, reset)
+    f32 = torch.float32
+    state = (batch, heads, dk, dv)
+    _need(dy, "dy", v.shape, io, dev)
+    _need(ckpt, "ckpt", linear_attn_ckpt_shape(batch, seqlen, heads, dk, dv), f32, dev)
+    if dlast is not None:
+        _need(dlast, "dlast", state, f32, dev)
+    g = dict(dq=torch.empty_like(q), dk=torch.empty_like(k), dv=torch.empty_like(v),
+             drate=torch.empty_like(rate) if "drate" in need else None,
+             dstep=torch.empty_like(step) if ("dstep" in need and step is not None) else None,
+             dh0=torch.empty(state, dtype=f32, device=dev) if "dh0" in need else None)
+    lib = _lib or load_library()
+    io_code = _io_code(io)
+    decays = 1 if g["drate"] is not None or g["dstep"] is not None else 0
+    size = _workspace_bytes("ssm_linear_attn_bwd_workspace_bytes", batch, seqlen, heads, groups, dk, dv, io_code, decays)
+    work = torch.empty(size, dtype=torch.uint8, device=dev) if size else None
+    st = lib.ssm_linear_attn_bwd(batch, seqlen, heads, groups, dk, dv, io_code, q.data_ptr(), k.data_ptr(),
+                                 v.data_ptr(), rate.data_ptr(), _ptr(step), _ptr(reset), ckpt.data_ptr(), scale,
+                                 dy.data_ptr(), _ptr(dlast), g["dq"].data_ptr(), g["dk"].data_ptr(),
+                                 g["dv"].data_ptr(), _ptr(g["drate"]), _ptr(g["dstep"]), _ptr(g["dh0"]), _ptr(work),
+                                 size, _raw_stream(dev.index))
+    if st:
+        _check("ssm_linear_attn_bwd", st)
+    return g
+
+
+def linear_attn_state_update(state, q, k, v, rate, step=None, scale=1.0, out=None, stream=None):
+    """One decode step (ssm_linear_attn_state_update), updating state (batch, heads, dk, dv) float32 in place; returns
+    y (batch, heads, dv).
+
+    q, k: (batch, groups, dk), v: (batch, heads, dv), step: (batch, heads) in one io dtype; rate, scale as
+    linear_attn_fwd.
+    """
+    if stream is not None or not state.is_cuda or state.get_device() != _device():
+        return _elsewhere(linear_attn_state_update, **locals())
+    if state.dim() != 4 or q.dim() != 3:
+        raise ValueError("state must be (batch, heads, dk, dv), q (batch, groups, dk)")
+    batch, heads, dk, dv = state.shape
+    groups, io, dev = q.shape[1], q.dtype, state.device
+    _need(state, "state", state.shape, torch.float32, dev)
+    _need(q, "q", (batch, groups, dk), io, dev)
+    _need(k, "k", q.shape, io, dev)
+    _need(v, "v", (batch, heads, dv), io, dev)
+    _need(rate, "rate", (heads,), torch.float32, dev)
+    if step is not None:
+        _need(step, "step", (batch, heads), io, dev)
+    if out is None:
+        out = torch.empty_like(v)
+    else:
+        _need(out, "out", v.shape, io, dev)
+    lib = _lib or load_library()
+    st = lib.ssm_linear_attn_state_update(batch, heads, groups, dk, dv, _io_code(io), state.data_ptr(), q.data_ptr(),
+                                          k.data_ptr(), v.data_ptr(), rate.data_ptr(), _ptr(step), scale,
+                                          out.data_ptr(), _raw_stream(dev.index))
+    if st:
+        _check("ssm_linear_attn_state_update", st)
+    return out

@@ -3,8 +3,8 @@
 The library is the whole product path: C ABI + kernels in one shared object
 (csrc/ssm_scan.hip: the scan's ABI and most of its kernels;
 csrc/scan_chunked.hip: the chunked prefill scan; csrc/gated_scan.hip: the gated
-recurrence; csrc/norm.hip: the norms; header include/ssm_scan.h).  The translation units are
-compiled in parallel and linked.  Packed FP32 instructions are disabled for
+recurrence; csrc/norm.hip: the norms; csrc/linear_attn*.hip: linear attention; header
+include/ssm_scan.h).  The translation units are compiled in parallel and linked.  Packed FP32 instructions are disabled for
 every HIP compile (-packed-fp32-ops).
 """
 import os
@@ -13,7 +13,9 @@ import sys
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
-SRCS = [os.path.join(HERE, "csrc", name) for name in ("ssm_scan.hip", "scan_chunked.hip", "gated_scan.hip", "norm.hip")]
+SRCS = [os.path.join(HERE, "csrc", name) for name in ("ssm_scan.hip", "scan_chunked.hip", "gated_scan.hip", "norm.hip",
+                                                        "linear_attn.hip", "linear_attn_bf16.hip",
+                                                        "linear_attn_f32.hip")]
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libssm_scan.so")
 # Instruction-rate probes for the roofline (bench.py only; not the scan path).

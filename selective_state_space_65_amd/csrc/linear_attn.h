@@ -1,0 +1,66 @@
+// linear_attn.h -- arguments of the chunked linear-attention kernels, shared by
+// the translation units that build them (one per io type) and the one that
+// plans and launches the calls.  Internal: not part of the C ABI.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+namespace linattn {
+
+constexpr int kBlock = 512;  // tokens between saved states
+constexpr int kMaxDim = 256;
+
+// Rows of one operand, [batch, seqlen, heads, d]; head h of the call reads
+// head h / share of the operand.
+struct Side {
+  const void* p;
+  int heads, share, d;
+};
+
+// One pass  out_t = sU sI sum_s D(t, s) (q_t . k_s) v_s + sI D(t, border) q_t . state,
+// s <= t, or s >= t where reverse; the state is q.d = k.d rows by v.d columns.
+struct Role {
+  Side q, k, v;
+  void* out;             // [batch, seqlen, heads, v.d], io or fp32
+  int out_f32;
+  int reverse;
+  int transposed;        // states in memory are [v.d][k.d]
+  float s_in, s_up;      // sI, sU
+  const float* start;    // state a segment starts from (null: zero): slot segment * start_step
+  int64_t start_slots;   // of start_slots slots for each (batch, head)
+  int64_t start_step;
+  float* save;           // state at the border of every block of kBlock tokens, may be null
+  int64_t save_slots;    // (forward: before block c, and behind the last; reverse: behind block c)
+  float* last;           // state after the last (reverse: before the first) token, may be null
+  Side with;             // rows that the outputs are dotted with (p may be null)
+  float* dots;           // [v.d / 32 rounded up][batch, heads, seqlen]
+  float* part;           // state passes: a segment's own state, [batch, heads, segments][k.d][v.d]
+  float* total;          // and its decay, [batch, heads, segments]
+  int tiles;             // blocks side by side along v.d
+  int64_t first_block;   // of the launch that is this role's
+};
+
+struct Args {
+  Role role[3];
+  int roles;
+  int batch, heads;
+  int64_t seqlen;
+  const float* rate;
+  const void* step;      // may be null
+  const uint8_t* reset;  // may be null
+  int segments;
+  int64_t segment_len;   // a multiple of kBlock
+};
+
+// Columns of one block: 64, or 128 where v.d is above 64.
+inline int tile_width(int dv) { return dv > 64 ? 128 : 64; }
+
+// Launches the roles, whose contracted dimensions (k.d) have the same number
+// of 32-wide parts (rounded up to 1, 2, 4 or 8) and whose tile widths are the
+// same; exact: bf16 intermediates in three parts.
+hipError_t launch_bf16(const Args& a, int64_t blocks, bool state_only, bool exact, hipStream_t st);
+hipError_t launch_f32(const Args& a, int64_t blocks, bool state_only, bool exact, hipStream_t st);
+
+}  // namespace linattn

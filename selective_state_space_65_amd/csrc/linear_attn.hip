@@ -1,0 +1,608 @@
+// linear_attn.hip -- linear attention with a decay for each head: planning and
+// launching the chunked passes, the small kernels between them, and the decode
+// step.  C ABI: include/ssm_scan.h.
+//
+// With few (batch, head) pairs the tokens are cut into segments: a state pass
+// gives every segment's own state, a join turns them into the states the
+// segments start from, and the main pass runs all segments at once.
+//
+// The backward is the same pass three times over,
+//   dq = pass(dy, v, k), state S^T;   dv = reverse pass(k, q, dy), state R;
+//   dk = reverse pass(v, dy, q), state R^T,        R_t = dL/dS_t,
+// S from the forward's checkpoints.  The decays' gradient is
+//   dL/dg_t = <a_t S_{t-1}, R_t>
+//           = sum over u >= t in the block of (q_u . dq_u - k_u . dk_u) + <S, R> behind the block
+// since all that is written and read behind t cancels in the sum; blocks are
+// kBlock tokens, so that no longer sum loses what it cancels to.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+
+#include "device_common.h"
+#include "host_common.h"
+#include "linear_attn.h"
+#include "rows.h"
+#include "ssm_scan.h"
+
+namespace {
+
+using linattn::Args;
+using linattn::kBlock;
+using linattn::Role;
+using linattn::Side;
+
+// ---- between the passes ------------------------------------------------------
+
+// States of the segments' own tokens become the states the segments start from.
+// A thread has one element of the state and walks the segments, 8 requested at
+// once (in slots that it alone reads and writes).
+__global__ __launch_bounds__(256) void linear_attn_join_kernel(float* part, const float* total, const float* first,
+                                                               int64_t n, int segments, int reverse) {
+  const int64_t row = blockIdx.y;
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= n) return;
+  float* at = part + row * segments * n + i;
+  const float* decay = total + row * segments;
+  float s = first ? first[row * n + i] : 0.0f;
+  for (int j0 = 0; j0 < segments; j0 += 8) {
+    float x[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const int j = min(j0 + u, segments - 1);
+      x[u] = at[(reverse ? segments - 1 - j : j) * n];
+    }
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      if (j0 + u >= segments) break;
+      const int j = reverse ? segments - 1 - (j0 + u) : j0 + u;
+      at[j * n] = s;
+      const float d = decay[j];
+      s = (d == 0.0f ? 0.0f : s * d) + x[u];
+    }
+  }
+}
+
+// dq or dk of a group: its heads' parts, added in order.
+template <typename T>
+__global__ __launch_bounds__(256) void linear_attn_group_kernel(const float* part, T* out, int64_t n, int groups,
+                                                                int share, int d) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;  // [token][group][d]
+  if (i >= n) return;
+  const int64_t tg = i / d;
+  const float* at = part + tg * share * d + i % d;
+  float t = at[0];
+  for (int h = 1; h < share; ++h) t += at[(int64_t)h * d];
+  Io<T>::store1(out + i, t);
+}
+
+struct DecayArgs {
+  const float* states;   // ckpt: [rows][blocks + 1][n]
+  const float* dstates;  // [rows][blocks][n], behind each block
+  const float* dots_q;   // [parts_q][rows][seqlen]
+  const float* dots_k;   // [parts_k][rows][seqlen]
+  const float* rate;
+  const void* step;      // may be null
+  const uint8_t* reset;  // may be null
+  void* dstep;           // may be null
+  double* drate;         // [rows][blocks]
+  int64_t n, rows, seqlen;
+  int heads, blocks, parts_q, parts_k;
+};
+
+__device__ __forceinline__ double wave_sum(double v) {
+#pragma unroll
+  for (int m = 1; m < 64; m <<= 1) v += __shfl_xor(v, m);
+  return v;
+}
+
+// One block of kBlock tokens of one (batch, head); a thread has two tokens.
+template <typename T>
+__global__ __launch_bounds__(256) void linear_attn_decay_kernel(const DecayArgs p) {
+  __shared__ double slots[3][4];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int block = (int)(blockIdx.x % p.blocks);
+  const int64_t row = blockIdx.x / p.blocks;
+  const int head = (int)(row % p.heads);
+  const float* s = p.states + (row * (p.blocks + 1) + block + 1) * p.n;
+  const float* r = p.dstates + (row * p.blocks + block) * p.n;
+  double cross = 0.0;
+  for (int64_t i = tid; i < p.n; i += 256) cross += (double)s[i] * (double)r[i];
+  const int64_t t0 = (int64_t)block * kBlock;
+  double w[2] = {0.0, 0.0};
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const int64_t t = t0 + 2 * tid + j;
+    if (t >= p.seqlen) continue;
+    for (int i = 0; i < p.parts_q; ++i) w[j] += (double)p.dots_q[(i * p.rows + row) * p.seqlen + t];
+    for (int i = 0; i < p.parts_k; ++i) w[j] -= (double)p.dots_k[(i * p.rows + row) * p.seqlen + t];
+  }
+  cross = wave_sum(cross);
+  double behind = w[0] + w[1];  // of this lane and those behind it
+#pragma unroll
+  for (int m = 1; m < 64; m <<= 1) {
+    const double o = __shfl_down(behind, m);
+    if (lane + m < 64) behind += o;
+  }
+  if (lane == 0) slots[0][wave] = cross, slots[1][wave] = behind;
+  __syncthreads();
+  cross = slots[0][0] + slots[0][1] + slots[0][2] + slots[0][3];
+  for (int v = 3; v > wave; --v) behind += slots[1][v];
+  double sum = 0.0;
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const int64_t t = t0 + 2 * tid + j;
+    double g = cross + behind - (j ? w[0] : 0.0);
+    if (t >= p.seqlen) continue;
+    const int64_t at = row / p.heads * p.seqlen + t;
+    const double rate = (double)p.rate[head];
+    double step = 1.0;
+    if (p.step) step = (double)Io<T>::load1(static_cast<const T*>(p.step) + at * p.heads + head);
+    // Nothing is carried over a reset or a decay of 0 (e^-104 < 2^-149), whatever the sums' roundings say.
+    const bool dropped = (p.reset && p.reset[at]) || rate * step > 104.0;
+    if (dropped) g = 0.0;
+    if (!dropped) sum += g * step;
+    if (p.dstep) Io<T>::store1(static_cast<T*>(p.dstep) + at * p.heads + head, dropped ? 0.0f : (float)(-g * rate));
+  }
+  sum = wave_sum(sum);
+  if (lane == 0) slots[2][wave] = sum;
+  __syncthreads();
+  if (tid == 0) p.drate[row * p.blocks + block] = (slots[2][0] + slots[2][1]) + (slots[2][2] + slots[2][3]);
+}
+
+// drate[h] = -sum over the batch rows and blocks, in a fixed order.
+__global__ __launch_bounds__(256) void linear_attn_drate_kernel(const double* part, float* drate, int64_t batch,
+                                                                int heads, int blocks) {
+  __shared__ double slots[4];
+  const int head = blockIdx.x, tid = threadIdx.x;
+  double t = 0.0;
+  for (int64_t i = tid; i < batch * blocks; i += 256)
+    t += part[(i / blocks * heads + head) * blocks + i % blocks];
+  t = wave_sum(t);
+  if ((tid & 63) == 0) slots[tid >> 6] = t;
+  __syncthreads();
+  if (tid == 0) drate[head] = -(float)((slots[0] + slots[1]) + (slots[2] + slots[3]));
+}
+
+// ---- the decode step ---------------------------------------------------------
+
+struct StepArgs {
+  float* state;
+  const void* q;
+  const void* k;
+  const void* v;
+  const float* rate;
+  const void* step;  // may be null
+  void* y;
+  float scale;
+  int heads, groups, dk, dv, width;  // width: lanes along a row of the state
+};
+
+// A block has `width` x kVec columns of one (batch, head)'s state; its lanes take
+// every 256 / width-th row, kAhead of them in flight.
+template <typename T, int kVec>
+__global__ __launch_bounds__(256) void linear_attn_step_kernel(const StepArgs p) {
+  constexpr int kAhead = 8;
+  __shared__ float sums[256 * kVec];
+  __shared__ float keys[2][256];
+  const int tid = threadIdx.x, x = tid & (p.width - 1), rows = 256 / p.width, y0 = tid / p.width;
+  const int64_t row = blockIdx.x;
+  const int head = (int)(row % p.heads);
+  const int64_t batch = row / p.heads;
+  const int c = (blockIdx.y * p.width + x) * kVec;
+  const bool live = c < p.dv;
+  const int64_t side = (batch * p.groups + head / (p.heads / p.groups)) * p.dk;
+  const int cc = live ? c : 0;
+  float* state = p.state + row * p.dk * p.dv + cc;
+  float s[kAhead][kVec];
+  const auto request = [&](int k0) {
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) load_n<kVec>(state + (int64_t)min(k0 + u * rows, p.dk - 1) * p.dv, s[u]);
+  };
+  request(y0);
+  if (tid < p.dk) {
+    keys[0][tid] = Io<T>::load1(static_cast<const T*>(p.q) + side + tid);
+    keys[1][tid] = Io<T>::load1(static_cast<const T*>(p.k) + side + tid);
+  }
+  float v[kVec], out[kVec];
+  load_n<kVec>(static_cast<const T*>(p.v) + row * p.dv + cc, v);
+  float rate = p.rate[head];
+  if (p.step) rate *= Io<T>::load1(static_cast<const T*>(p.step) + row);
+  const float a = exp2_hw(-rate * kLog2e);
+#pragma unroll
+  for (int j = 0; j < kVec; ++j) out[j] = 0.0f;
+  lds_barrier();
+  for (int k0 = y0; k0 < p.dk; k0 += kAhead * rows) {
+    if (k0 != y0) request(k0);
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int k = k0 + u * rows;
+      if (k >= p.dk) break;
+      const float kk = keys[1][k], qq = keys[0][k];
+#pragma unroll
+      for (int j = 0; j < kVec; ++j) {
+        s[u][j] = __builtin_fmaf(kk, v[j], a == 0.0f ? 0.0f : s[u][j] * a);
+        out[j] = __builtin_fmaf(qq, s[u][j], out[j]);
+      }
+      if (live) store_n<kVec>(state + (int64_t)k * p.dv, s[u]);
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < kVec; ++j) sums[(y0 * p.width + x) * kVec + j] = out[j];
+  lds_barrier();
+  const int n = p.width * kVec, column = blockIdx.y * n + tid;
+  if (tid < n && column < p.dv) {
+    float t = sums[tid];
+    for (int i = 1; i < rows; ++i) t += sums[i * n + tid];
+    Io<T>::store1(static_cast<T*>(p.y) + row * p.dv + column, t * p.scale);
+  }
+}
+
+// ---- host side ---------------------------------------------------------------
+
+struct Sizes {
+  int64_t batch, seqlen, heads, groups, dk, dv;
+  int64_t rows() const { return batch * heads; }
+  int64_t state() const { return dk * dv; }
+  int64_t blocks() const { return (seqlen + kBlock - 1) / kBlock; }
+};
+
+ssm_status_t check_sizes(const Sizes& s, ssm_dtype_t io) {
+  if (io != SSM_F32 && io != SSM_BF16) return SSM_ERR_DTYPE;
+  if (s.batch < 1 || s.seqlen < 1 || s.heads < 1 || s.groups < 1 || s.dk < 1 || s.dv < 1) return SSM_ERR_SHAPE;
+  if (s.heads % s.groups) return SSM_ERR_SHAPE;
+  int64_t n, m;
+  if (!mul_ok(s.batch, s.seqlen, &n) || !mul_ok(n, s.heads, &n)) return SSM_ERR_SHAPE;
+  if (!mul_ok(n, s.dk, &m) || !mul_ok(m, 64, &m) || !mul_ok(n, s.dv, &m) || !mul_ok(m, 64, &m)) return SSM_ERR_SHAPE;
+  if (!mul_ok(s.batch, s.heads, &n) || !mul_ok(n, s.dk, &n) || !mul_ok(n, s.dv, &n) ||
+      !mul_ok(n, s.seqlen / kBlock + 3, &n) || !mul_ok(n, 16, &n))
+    return SSM_ERR_SHAPE;
+  if (s.dk > linattn::kMaxDim || s.dv > linattn::kMaxDim) return SSM_ERR_UNSUPPORTED;
+  if (s.heads > 16384 || s.batch > ((int64_t)1 << 30)) return SSM_ERR_UNSUPPORTED;
+  return SSM_OK;
+}
+
+int64_t tiles(int64_t dv) { return (dv + linattn::tile_width((int)dv) - 1) / linattn::tile_width((int)dv); }
+
+struct Split {
+  int64_t per, count;  // blocks of kBlock tokens in a segment, segments
+};
+
+Split split_tokens(const Sizes& s, int64_t blocks_each) {
+  Split p{s.blocks(), 1};
+  const int64_t wanted = blocks_each < 256 ? (512 + blocks_each - 1) / blocks_each : 1;
+  p.per = std::max<int64_t>(1, p.per / wanted);
+  p.count = (s.blocks() + p.per - 1) / p.per;
+  return p;
+}
+
+Split fwd_split(const Sizes& s) { return split_tokens(s, s.rows() * tiles(s.dv)); }
+Split bwd_split(const Sizes& s) { return split_tokens(s, s.rows() * (2 * tiles(s.dk) + tiles(s.dv))); }
+
+// Segments' states and decays.
+int64_t segment_bytes(const Sizes& s, const Split& p) { return p.count > 1 ? s.rows() * p.count * (s.state() + 1) * 4 : 0; }
+
+struct BwdSpace {
+  int64_t segments, dstates, dots_q, dots_k, drate, dq, dk, bytes;  // offsets
+};
+
+BwdSpace bwd_space(const Sizes& s, bool decays) {
+  BwdSpace w;
+  int64_t at = 0;
+  const auto take = [&](int64_t bytes) {
+    const int64_t here = at;
+    at += (bytes + 15) / 16 * 16;
+    return here;
+  };
+  w.drate = take(decays ? s.rows() * s.blocks() * 8 : 0);
+  w.segments = take(segment_bytes(s, bwd_split(s)));
+  w.dstates = take(decays ? s.rows() * s.blocks() * s.state() * 4 : 0);
+  w.dots_q = take(decays ? (s.dk + 31) / 32 * s.rows() * s.seqlen * 4 : 0);
+  w.dots_k = take(decays ? (s.dk + 31) / 32 * s.rows() * s.seqlen * 4 : 0);
+  const bool shared = s.groups != s.heads;
+  w.dq = take(shared ? s.rows() * s.seqlen * s.dk * 4 : 0);
+  w.dk = take(shared ? s.rows() * s.seqlen * s.dk * 4 : 0);
+  w.bytes = at;
+  return w;
+}
+
+hipError_t launch_pass(const Args& a, int64_t blocks, bool state_only, bool exact, ssm_dtype_t io, hipStream_t st) {
+  return io == SSM_BF16 ? linattn::launch_bf16(a, blocks, state_only, exact, st)
+                        : linattn::launch_f32(a, blocks, state_only, exact, st);
+}
+
+Args pass_args(const Sizes& s, const Split& p, const float* rate, const void* step, const uint8_t* reset) {
+  Args a = {};
+  a.batch = (int)s.batch;
+  a.heads = (int)s.heads;
+  a.seqlen = s.seqlen;
+  a.rate = rate;
+  a.step = step;
+  a.reset = reset;
+  a.segments = (int)p.count;
+  a.segment_len = p.per * kBlock;
+  return a;
+}
+
+// The states that the segments start from, into `space` (segment_bytes).
+hipError_t segment_states(Args a, Role role, const Sizes& s, const float* first, void* space, ssm_dtype_t io,
+                          hipStream_t st) {
+  role.part = static_cast<float*>(space);
+  role.total = role.part + s.rows() * a.segments * s.state();
+  role.tiles = (int)tiles(s.dv);
+  role.first_block = 0;
+  a.role[0] = role;
+  a.roles = 1;
+  const hipError_t e = launch_pass(a, s.rows() * a.segments * role.tiles, true, false, io, st);
+  if (e != hipSuccess) return e;
+  const int64_t n = s.state();
+  hipLaunchKernelGGL(linear_attn_join_kernel, dim3((unsigned)((n + 255) / 256), (unsigned)s.rows()), dim3(256), 0, st,
+                     role.part, role.total, first, n, a.segments, role.reverse);
+  return hipGetLastError();
+}
+
+bool passes_ok(const Sizes& s, const Split& p, int64_t blocks_each) {
+  return s.rows() < 65536 * (int64_t)16 && launch_ok(s.rows() * p.count * blocks_each, 256);
+}
+
+}  // namespace
+
+// ----------------------------------------------------------------------------
+// C ABI
+// ----------------------------------------------------------------------------
+
+extern "C" {
+
+ssm_status_t ssm_linear_attn_fwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t heads, int64_t groups,
+                                                 int64_t dk, int64_t dv, ssm_dtype_t io, int64_t* bytes) {
+  const Sizes s{batch, seqlen, heads, groups, dk, dv};
+  const ssm_status_t st = check_sizes(s, io);
+  if (st == SSM_OK && bytes) *bytes = segment_bytes(s, fwd_split(s));
+  return st;
+}
+
+ssm_status_t ssm_linear_attn_fwd(int64_t batch, int64_t seqlen, int64_t heads, int64_t groups, int64_t dk, int64_t dv,
+                                 ssm_dtype_t io, const void* q, const void* k, const void* v, const float* rate,
+                                 const void* step, const uint8_t* reset, const float* h0, float scale, void* y,
+                                 float* last_state, float* ckpt, void* workspace, int64_t workspace_bytes,
+                                 struct ihipStream_t* stream) {
+  const Sizes s{batch, seqlen, heads, groups, dk, dv};
+  ssm_status_t st = check_sizes(s, io);
+  if (st != SSM_OK) return st;
+  const Split p = fwd_split(s);
+  if (!passes_ok(s, p, tiles(dv))) return SSM_ERR_UNSUPPORTED;
+  if (!q || !k || !v || !rate || !y) return SSM_ERR_NULL;
+  const int64_t need = segment_bytes(s, p);
+  if (workspace_bytes < need) return SSM_ERR_WORKSPACE;
+  if (need && !workspace) return SSM_ERR_NULL;
+  if (!need) workspace = nullptr;
+  const size_t es = io_size(io);
+  const int64_t tokens = batch * seqlen, state = s.rows() * s.state() * 4;
+  const bool in_place = h0 && last_state == h0;
+  const Buf ins[] = {{q, tokens * groups * dk * (int64_t)es, es}, {k, tokens * groups * dk * (int64_t)es, es},
+                     {v, tokens * heads * dv * (int64_t)es, es}, {rate, heads * 4, 4},
+                     {step, tokens * heads * (int64_t)es, es}, {reset, tokens, 1}, {in_place ? nullptr : h0, state, 4}};
+  const Buf outs[] = {{y, tokens * heads * dv * (int64_t)es, es}, {last_state, state, 4},
+                      {ckpt, state * (s.blocks() + 1), 4}, {workspace, need, 8}};
+  st = check_buffers(ins, 7, outs, 4);
+  if (st != SSM_OK) return st;
+  if (in_place && !aligned(h0, 4)) return SSM_ERR_ALIGN;
+  hipStream_t hs = reinterpret_cast<hipStream_t>(stream);
+  Args a = pass_args(s, p, rate, step, reset);
+  const int share = (int)(heads / groups);
+  Role r = {};
+  r.q = Side{q, (int)groups, share, (int)dk};
+  r.k = Side{k, (int)groups, share, (int)dk};
+  r.v = Side{v, (int)heads, 1, (int)dv};
+  r.s_in = scale;
+  r.s_up = 1.0f;
+  r.start = h0;
+  r.start_slots = 1;
+  hipError_t e = hipSuccess;
+  if (p.count > 1) {
+    e = segment_states(a, r, s, h0, workspace, io, hs);
+    r.start = static_cast<const float*>(workspace);
+    r.start_slots = p.count;
+    r.start_step = 1;
+  }
+  if (e == hipSuccess) {
+    r.out = y;
+    r.save = ckpt;
+    r.save_slots = s.blocks() + 1;
+    r.last = last_state;
+    r.tiles = (int)tiles(dv);
+    a.role[0] = r;
+    a.roles = 1;
+    e = launch_pass(a, s.rows() * p.count * r.tiles, false, false, io, hs);
+  }
+  return e == hipSuccess ? SSM_OK : hip_fail(e);
+}
+
+ssm_status_t ssm_linear_attn_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t heads, int64_t groups,
+                                                 int64_t dk, int64_t dv, ssm_dtype_t io, int decays, int64_t* bytes) {
+  const Sizes s{batch, seqlen, heads, groups, dk, dv};
+  const ssm_status_t st = check_sizes(s, io);
+  if (st == SSM_OK && bytes) *bytes = bwd_space(s, decays != 0).bytes;
+  return st;
+}
+
+ssm_status_t ssm_linear_attn_bwd(int64_t batch, int64_t seqlen, int64_t heads, int64_t groups, int64_t dk, int64_t dv,
+                                 ssm_dtype_t io, const void* q, const void* k, const void* v, const float* rate,
+                                 const void* step, const uint8_t* reset, const float* ckpt, float scale,
+                                 const void* dy, const float* dlast, void* dq, void* dk_out, void* dv_out,
+                                 float* drate, void* dstep, float* dh0, void* workspace, int64_t workspace_bytes,
+                                 struct ihipStream_t* stream) {
+  const Sizes s{batch, seqlen, heads, groups, dk, dv};
+  ssm_status_t st = check_sizes(s, io);
+  if (st != SSM_OK) return st;
+  const Split p = bwd_split(s);
+  if (!passes_ok(s, p, 2 * tiles(dk) + tiles(dv))) return SSM_ERR_UNSUPPORTED;
+  if (!q || !k || !v || !rate || !ckpt || !dy || !dq || !dk_out || !dv_out) return SSM_ERR_NULL;
+  if (!step) dstep = nullptr;
+  const bool decays = drate || dstep;
+  const BwdSpace w = bwd_space(s, decays);
+  if (workspace_bytes < w.bytes) return SSM_ERR_WORKSPACE;
+  if (w.bytes && !workspace) return SSM_ERR_NULL;
+  if (!w.bytes) workspace = nullptr;
+  const size_t es = io_size(io);
+  const int64_t tokens = batch * seqlen, state = s.rows() * s.state() * 4;
+  const int64_t qk_bytes = tokens * groups * dk * (int64_t)es, v_bytes = tokens * heads * dv * (int64_t)es;
+  const int64_t step_bytes = tokens * heads * (int64_t)es;
+  const Buf ins[] = {{q, qk_bytes, es}, {k, qk_bytes, es}, {v, v_bytes, es}, {rate, heads * 4, 4},
+                     {step, step_bytes, es}, {reset, tokens, 1}, {ckpt, state * (s.blocks() + 1), 4},
+                     {dy, v_bytes, es}, {dlast, state, 4}};
+  const Buf outs[] = {{dq, qk_bytes, es}, {dk_out, qk_bytes, es}, {dv_out, v_bytes, es}, {drate, heads * 4, 4},
+                      {dstep, step_bytes, es}, {dh0, state, 4}, {workspace, w.bytes, 8}};
+  st = check_buffers(ins, 9, outs, 7);
+  if (st != SSM_OK) return st;
+  hipStream_t hs = reinterpret_cast<hipStream_t>(stream);
+  char* const space = static_cast<char*>(workspace);
+  const auto at = [&](int64_t offset) { return reinterpret_cast<float*>(space + offset); };
+  Args a = pass_args(s, p, rate, step, reset);
+  const int share = (int)(heads / groups);
+  const Side qs{q, (int)groups, share, (int)dk}, ks{k, (int)groups, share, (int)dk};
+  const Side vs{v, (int)heads, 1, (int)dv}, ys{dy, (int)heads, 1, (int)dv};
+  Role to_q = {}, to_k = {}, to_v = {};
+  to_v.q = ks; to_v.k = qs; to_v.v = ys;
+  to_v.reverse = 1;
+  to_v.s_in = 1.0f;
+  to_v.s_up = scale;
+  hipError_t e = hipSuccess;
+  if (p.count > 1) {
+    e = segment_states(a, to_v, s, dlast, at(w.segments), io, hs);
+    if (e != hipSuccess) return hip_fail(e);
+    to_v.start = at(w.segments);
+    to_v.start_slots = p.count;
+    to_v.start_step = 1;
+  } else {
+    to_v.start = dlast;
+    to_v.start_slots = 1;
+  }
+  to_v.out = dv_out;
+  to_v.last = dh0;
+  to_v.tiles = (int)tiles(dv);
+  if (decays) {
+    to_v.save = at(w.dstates);
+    to_v.save_slots = s.blocks();
+  }
+  to_k = to_v;
+  to_k.q = vs; to_k.k = ys; to_k.v = qs;
+  to_k.transposed = 1;
+  to_k.last = to_k.save = nullptr;
+  to_k.tiles = (int)tiles(dk);
+  to_q.q = ys; to_q.k = vs; to_q.v = ks;
+  to_q.transposed = 1;
+  to_q.s_in = scale;
+  to_q.s_up = 1.0f;
+  to_q.start = ckpt;
+  to_q.start_slots = s.blocks() + 1;
+  to_q.start_step = p.per;
+  to_q.tiles = to_k.tiles;
+  const bool shared = groups != heads;
+  to_q.out = shared ? at(w.dq) : dq;
+  to_k.out = shared ? at(w.dk) : dk_out;
+  to_q.out_f32 = to_k.out_f32 = shared;
+  if (decays) {
+    to_q.with = qs;
+    to_q.dots = at(w.dots_q);
+    to_k.with = ks;
+    to_k.dots = at(w.dots_k);
+  }
+  // dq's and dk's passes contract v's columns, dv's contracts q's.
+  const int64_t each = s.rows() * p.count;
+  a.role[0] = to_q;
+  a.role[1] = to_k;
+  a.role[1].first_block = each * to_q.tiles;
+  a.roles = 2;
+  e = launch_pass(a, each * (to_q.tiles + to_k.tiles), false, decays, io, hs);
+  if (e != hipSuccess) return hip_fail(e);
+  a.role[0] = to_v;
+  a.roles = 1;
+  e = launch_pass(a, each * to_v.tiles, false, false, io, hs);
+  if (e != hipSuccess) return hip_fail(e);
+  if (shared) {
+    const int64_t n = tokens * groups * dk;
+    const unsigned blocks = (unsigned)((n + 255) / 256);
+    for (int i = 0; i < 2; ++i) {
+      const float* part = at(i ? w.dk : w.dq);
+      if (io == SSM_BF16)
+        hipLaunchKernelGGL(linear_attn_group_kernel<bf16_t>, dim3(blocks), dim3(256), 0, hs, part,
+                           static_cast<bf16_t*>(i ? dk_out : dq), n, (int)groups, share, (int)dk);
+      else
+        hipLaunchKernelGGL(linear_attn_group_kernel<float>, dim3(blocks), dim3(256), 0, hs, part,
+                           static_cast<float*>(i ? dk_out : dq), n, (int)groups, share, (int)dk);
+    }
+    e = hipGetLastError();
+    if (e != hipSuccess) return hip_fail(e);
+  }
+  if (decays) {
+    DecayArgs d = {};
+    d.states = ckpt;
+    d.dstates = at(w.dstates);
+    d.dots_q = at(w.dots_q);
+    d.dots_k = at(w.dots_k);
+    d.rate = rate;
+    d.step = step;
+    d.reset = reset;
+    d.dstep = dstep;
+    d.drate = reinterpret_cast<double*>(space + w.drate);
+    d.n = s.state();
+    d.rows = s.rows();
+    d.seqlen = seqlen;
+    d.heads = (int)heads;
+    d.blocks = (int)s.blocks();
+    d.parts_q = d.parts_k = (int)((dk + 31) / 32);
+    const unsigned blocks = (unsigned)(s.rows() * s.blocks());
+    if (io == SSM_BF16)
+      hipLaunchKernelGGL(linear_attn_decay_kernel<bf16_t>, dim3(blocks), dim3(256), 0, hs, d);
+    else
+      hipLaunchKernelGGL(linear_attn_decay_kernel<float>, dim3(blocks), dim3(256), 0, hs, d);
+    if (drate)
+      hipLaunchKernelGGL(linear_attn_drate_kernel, dim3((unsigned)heads), dim3(256), 0, hs, d.drate, drate, batch,
+                         (int)heads, d.blocks);
+    e = hipGetLastError();
+  }
+  return e == hipSuccess ? SSM_OK : hip_fail(e);
+}
+
+ssm_status_t ssm_linear_attn_state_update(int64_t batch, int64_t heads, int64_t groups, int64_t dk, int64_t dv,
+                                          ssm_dtype_t io, float* state, const void* q, const void* k, const void* v,
+                                          const float* rate, const void* step, float scale, void* y,
+                                          struct ihipStream_t* stream) {
+  const Sizes s{batch, 1, heads, groups, dk, dv};
+  ssm_status_t st = check_sizes(s, io);
+  if (st != SSM_OK) return st;
+  if (!launch_ok(s.rows(), 256)) return SSM_ERR_UNSUPPORTED;
+  if (!state || !q || !k || !v || !rate || !y) return SSM_ERR_NULL;
+  const size_t es = io_size(io);
+  const int64_t rows = s.rows(), qk_bytes = batch * groups * dk * (int64_t)es;
+  const Buf ins[] = {{q, qk_bytes, es}, {k, qk_bytes, es}, {v, rows * dv * (int64_t)es, es}, {rate, heads * 4, 4},
+                     {step, rows * (int64_t)es, es}};
+  const Buf outs[] = {{state, rows * s.state() * 4, 4}, {y, rows * dv * (int64_t)es, es}};
+  st = check_buffers(ins, 5, outs, 2);
+  if (st != SSM_OK) return st;
+  StepArgs a;
+  a.state = state; a.q = q; a.k = k; a.v = v; a.rate = rate; a.step = step; a.y = y; a.scale = scale;
+  a.heads = (int)heads; a.groups = (int)groups; a.dk = (int)dk; a.dv = (int)dv;
+  hipStream_t hs = reinterpret_cast<hipStream_t>(stream);
+  const int vec = dv % 4 ? 1 : 4;
+  const int64_t units = (dv + vec - 1) / vec;
+  a.width = 64;
+  while (a.width > 8 && (a.width / 2 >= units || rows * ((units + a.width - 1) / a.width) < 512)) a.width /= 2;
+  const dim3 grid((unsigned)rows, (unsigned)((units + a.width - 1) / a.width));
+  if (io == SSM_BF16) {
+    if (vec == 4)
+      hipLaunchKernelGGL((linear_attn_step_kernel<bf16_t, 4>), grid, dim3(256), 0, hs, a);
+    else
+      hipLaunchKernelGGL((linear_attn_step_kernel<bf16_t, 1>), grid, dim3(256), 0, hs, a);
+  } else {
+    if (vec == 4)
+      hipLaunchKernelGGL((linear_attn_step_kernel<float, 4>), grid, dim3(256), 0, hs, a);
+    else
+      hipLaunchKernelGGL((linear_attn_step_kernel<float, 1>), grid, dim3(256), 0, hs, a);
+  }
+  const hipError_t e = hipGetLastError();
+  return e == hipSuccess ? SSM_OK : hip_fail(e);
+}
+
+}  // extern "C"

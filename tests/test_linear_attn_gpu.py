@@ -1,0 +1,393 @@
+"""Linear attention (forward, backward, decode step) through the C ABI against
+the float64 form (needs an MI355X).
+
+Two kinds of tests hold the values.  Inputs that are small whole numbers with a
+decay of 1 have sums that fp32, and bf16 where it rounds, hold exactly: every
+output has to be equal to the float64 form's, rounded once.  Other inputs are
+held to the bound of linear_attn_reference, value by value.
+"""
+import pytest
+import torch
+
+import linear_attn_reference as ref
+import selective_state_space_65_amd as ssm
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+F32, BF16 = torch.float32, torch.bfloat16
+NAMES = ("q", "k", "v", "rate", "step", "reset", "h0")
+
+
+def say(msg):
+    print("[gpu-case] " + msg, flush=True)
+
+
+def draw(batch, seqlen, heads, groups, dk, dv, io, seed, step=True, reset=0.0, h0=True, whole=False, rates=(0.002, 0.3)):
+    """Inputs on the CPU.  whole: numbers in {-1, 0, 1}, rate 0."""
+    g = torch.Generator().manual_seed(seed)
+
+    def values(*s, dtype=io):
+        return torch.randint(-1, 2, s, generator=g).to(dtype) if whole else torch.randn(s, generator=g).to(dtype)
+
+    d = dict(q=values(batch, seqlen, groups, dk), k=values(batch, seqlen, groups, dk), v=values(batch, seqlen, heads, dv))
+    low, high = rates
+    d["rate"] = torch.zeros(heads) if whole else low * (high / low) ** torch.rand(heads, generator=g)
+    if step:
+        d["step"] = torch.randint(0, 3, (batch, seqlen, heads), generator=g).to(io) if whole else \
+            (0.6 * torch.randn((batch, seqlen, heads), generator=g)).exp().to(io)
+    if reset:
+        d["reset"] = (torch.rand((batch, seqlen), generator=g) < reset).to(torch.uint8)
+    if h0:
+        d["h0"] = values(batch, heads, dk, dv, dtype=F32)
+    dy = values(batch, seqlen, heads, dv)
+    dlast = values(batch, heads, dk, dv, dtype=F32)
+    return d, dy, dlast
+
+
+def on_gpu(d):
+    return {k: v.to(DEV) for k, v in d.items()}
+
+
+def same(a, b):
+    return torch.allclose(a, b, rtol=0.0, atol=0.0, equal_nan=True)
+
+
+def run(d, dy=None, dlast=None, scale=1.0):
+    t = on_gpu(d)
+    y, last, ckpt = ssm.linear_attn_fwd_save(scale=scale, **t)
+    out = dict(y=y, last_state=last)
+    plain = ssm.linear_attn_fwd(scale=scale, **t)
+    assert same(plain[0], y) and same(plain[1], last)
+    if dy is not None:
+        h0 = t.pop("h0", None)
+        g = ssm.linear_attn_bwd(dy=dy.to(DEV), ckpt=ckpt, dlast=None if dlast is None else dlast.to(DEV), scale=scale, **t)
+        assert (g["dstep"] is None) == ("step" not in t)
+        out.update({k: v for k, v in g.items() if v is not None})
+        del h0
+    torch.cuda.synchronize()
+    return {k: v.cpu() for k, v in out.items()}, ckpt.cpu()
+
+
+def check(got, want, what):
+    for name, x in got.items():
+        value, bound = want[name]
+        assert x.shape == value.shape, (what, name)
+        off = (x.double() - value).abs()
+        bad = ~(off <= bound * (1 + 2.0 ** -7) + 1e-37)
+        assert not bad.any(), "%s %s: %d of %d off, worst %.3g of its bound, at %s" % (
+            what, name, bad.sum(), bad.numel(), (off / bound.clamp(min=1e-300)).max(), bad.nonzero()[0].tolist())
+
+
+def check_equal(got, want, what):
+    for name, x in got.items():
+        value = want[name][0].to(x.dtype)
+        assert torch.equal(x, value), "%s %s: %d of %d differ, first at %s" % (
+            what, name, (x != value).sum(), x.numel(), (x != value).nonzero()[0].tolist())
+
+
+# Widths on and around 32, 64, 128 and 256 and below 8; lengths on and around a
+# chunk (32, 64), a block of 512 and several of them; heads that share q and k.
+SHAPES = [(1, 1, 1, 1, 1, 1), (2, 3, 2, 1, 7, 9), (1, 31, 2, 2, 8, 8), (2, 64, 3, 3, 16, 64), (1, 65, 4, 2, 33, 65),
+          (3, 127, 5, 1, 64, 128), (1, 200, 2, 2, 128, 32), (2, 250, 2, 1, 100, 130), (1, 130, 3, 3, 129, 200),
+          (1, 256, 2, 2, 256, 256), (2, 90, 1, 1, 200, 5)]
+LONG = [(1, 513, 3, 1, 32, 40), (2, 1025, 2, 2, 20, 70), (1, 1600, 1, 1, 130, 64), (3, 2050, 2, 1, 8, 136)]
+
+
+@pytest.mark.parametrize("io", [F32, BF16])
+@pytest.mark.parametrize("shape", SHAPES)
+def test_exact(shape, io):
+    """Sums of at most 256 products of -1, 0 and 1: exact in bf16 as in fp32, but for the output's own rounding."""
+    i = SHAPES.index(shape)
+    say("linear attention exact %s %s" % (shape, io))
+    d, dy, dlast = draw(*shape, io, i, step=i % 2 == 0, reset=0.04 * (i % 3), h0=i % 4 != 1, whole=True)
+    if shape[4] > 128 or shape[5] > 128:  # scores up to 256 in bf16: keep q and dy sparse
+        d["q"][..., ::2] = 0
+        dy[..., ::2] = 0
+    got, _ = run(d, dy, dlast if i % 4 != 1 else None)
+    check_equal(got, ref.everything(d, dy, dlast if i % 4 != 1 else None, io=io), str(shape))
+
+
+@pytest.mark.parametrize("shape", LONG)
+def test_exact_long(shape):
+    """fp32, over several segments: sums below 2^24 are exact."""
+    i = LONG.index(shape)
+    say("linear attention exact long %s" % (shape,))
+    d, dy, dlast = draw(*shape, F32, 50 + i, step=True, reset=0.003 * (i % 2), whole=True)
+    got, _ = run(d, dy, dlast)
+    check_equal(got, ref.everything(d, dy, dlast), str(shape))
+
+
+@pytest.mark.parametrize("io", [F32, BF16])
+@pytest.mark.parametrize("shape", SHAPES + LONG)
+def test_values(shape, io):
+    i = (SHAPES + LONG).index(shape)
+    say("linear attention %s %s" % (shape, io))
+    d, dy, dlast = draw(*shape, io, 100 + i, step=i % 3 != 0, reset=0.01 * (i % 2), h0=i % 4 != 1)
+    dlast = dlast if i % 4 != 1 else None
+    got, _ = run(d, dy, dlast, scale=0.25)
+    check(got, ref.everything(d, dy, dlast, scale=0.25, io=io), str(shape))
+
+
+@pytest.mark.parametrize("io", [F32, BF16])
+def test_checkpoints(io):
+    d, _, _ = draw(2, 1100, 2, 2, 24, 40, io, 7)
+    got, ckpt = run(d)
+    _, _, states = ref.forward(**d)
+    size = ref.forward(**dict(d, q=d["q"].abs(), k=d["k"].abs(), v=d["v"].abs(), h0=d["h0"].abs()))[2]
+    n = 2 * (1100 + 64) + 160
+    assert torch.equal(ckpt[:, :, 0], d["h0"]) and torch.equal(ckpt[:, :, -1], got["last_state"])
+    for slot, token in ((1, 512), (2, 1024)):
+        assert ((ckpt[:, :, slot].double() - states[token - 1]).abs() <= n * ref.U * size[token - 1]).all()
+
+
+@pytest.mark.parametrize("io", [F32, BF16])
+def test_decays_of_every_size(io):
+    """A decay of 1 (step 0), one that is 0 (it drops the state), and small steps behind a large one."""
+    d, dy, dlast = draw(2, 300, 3, 3, 40, 24, io, 11)
+    d["step"][:, 50:60] = 0
+    d["step"][0, 100] = 60000.0
+    d["step"][:, 101:140] = 2.0 ** -10
+    d["step"][1, 200:210] = 7.0
+    d["step"][1, 210, 1] = float("inf")
+    d["rate"] = torch.tensor([0.0005, 0.2, 3.0])
+    finite = dict(d, step=d["step"].clamp(max=1e9))  # rate x 1e9: a decay of 0 all the same
+    got, _ = run(d, dy, dlast)
+    want = ref.everything(finite, dy, dlast, io=io)
+    for name in ("dstep", "drate"):  # the gradient at an infinite step: 0, as the decay is
+        assert not got[name].isnan().any()
+    check(got, want, "decays")
+
+
+@pytest.mark.parametrize("io", [F32, BF16])
+@pytest.mark.parametrize("field", ["q", "k", "v", "step"])
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+def test_not_a_number_stays_behind(io, field, value):
+    """A token's NaN or infinity reaches no earlier token, no other head or batch row, and none behind a reset."""
+    d, dy, _ = draw(2, 200, 2, 2, 40, 70, io, 13, rates=(0.01, 0.05))
+    d["reset"] = torch.zeros(2, 200, dtype=torch.uint8)
+    d["reset"][0, 90] = 1
+    clean = {k: v.clone() for k, v in d.items()}
+    if field == "step":
+        if value == float("inf"):
+            return  # a decay of 0: test_decays_of_every_size
+        d["step"][0, 77, 1] = value
+    else:
+        d[field][0, 77, 1, 3] = value
+    got, _ = run(d, dy)
+    want, bad = ref.everything(clean, dy, io=io), ref.everything(d, dy, io=io)
+    touched = torch.zeros(2, 200, 2, dtype=torch.bool)  # tokens of the reset's packed sequence, of that head
+    touched[0, :90, 1] = True
+    for name in ("y", "dq", "dk", "dv"):
+        x, (value_, bound) = got[name].double(), want[name]
+        keep = ~touched
+        assert ((x - value_).abs() <= bound * (1 + 2.0 ** -7) + 1e-37)[keep].all(), name
+        if name in ("y", "dq"):  # causal outputs: nothing before the token
+            assert ((x - value_).abs() <= bound * (1 + 2.0 ** -7) + 1e-37)[0, :77].all(), name
+        fine = bad[name][0].isfinite()  # what the recurrence keeps finite stays so
+        assert (x.isfinite() == fine).all(), name
+    assert ((got["last_state"].double() - want["last_state"][0]).abs() <= want["last_state"][1] + 1e-37).all()
+
+
+def test_state_that_is_not_finite_is_dropped():
+    d, dy, _ = draw(1, 150, 2, 1, 20, 30, BF16, 17)
+    d["h0"][0, 0, 3] = float("inf")
+    d["h0"][0, 1, :, 5] = float("nan")
+    d["reset"] = torch.zeros(1, 150, dtype=torch.uint8)
+    d["reset"][0, 70] = 1
+    got, _ = run(d)
+    fine = ref.everything(dict(d, h0=torch.zeros_like(d["h0"])), io=BF16)
+    assert ((got["y"].double() - fine["y"][0]).abs() <= fine["y"][1] * 1.01 + 1e-37)[:, 70:].all()
+    assert ((got["last_state"].double() - fine["last_state"][0]).abs() <= fine["last_state"][1] + 1e-37).all()
+    assert not got["y"][0, :70, 0].isfinite().any()
+    assert got["y"][0, :70, 1, 5].isnan().all() and got["y"][0, :70, 1, :5].isfinite().all()
+
+
+@pytest.mark.parametrize("io", [F32, BF16])
+def test_prompt_in_parts_then_tokens(io):
+    """The state carried from call to call in place; single tokens equal a prompt of one."""
+    d, _, _ = draw(2, 150, 4, 2, 48, 36, io, 19)
+    want = ref.everything(d, scale=0.5, io=io)
+    t = on_gpu(d)
+    state = t["h0"].clone()
+    ys = []
+    for a, b in ((0, 70), (70, 71), (71, 140)):
+        part = {k: t[k][:, a:b].contiguous() for k in ("q", "k", "v", "step")}
+        y, last = ssm.linear_attn_fwd(rate=t["rate"], h0=state, last_state=state, scale=0.5, **part)
+        assert last is state
+        ys.append(y)
+    one = {k: t[k][:, 140].contiguous() for k in ("q", "k", "v", "step")}
+    y1, last1 = ssm.linear_attn_fwd(rate=t["rate"], h0=state, scale=0.5, **{k: v[:, None].contiguous() for k, v in one.items()})
+    for i in range(140, 150):
+        now = {k: t[k][:, i].contiguous() for k in ("q", "k", "v", "step")}
+        y = ssm.linear_attn_state_update(state, now["q"], now["k"], now["v"], t["rate"], step=now["step"], scale=0.5)
+        if i == 140:
+            assert (state - last1).abs().max() <= 4 * ref.U * last1.abs().max()
+        ys.append(y[:, None])
+    check(dict(y=torch.cat(ys, 1).cpu(), last_state=state.cpu()), want, "parts")
+    del y1
+
+
+STEPS = [(1, 1, 1, 1, 1), (3, 4, 2, 5, 6), (2, 20, 4, 64, 128), (5, 3, 3, 256, 256), (70, 16, 16, 32, 64), (2, 2, 1, 100, 130),
+         (1, 3, 3, 255, 36), (40, 40, 8, 16, 20)]
+
+
+@pytest.mark.parametrize("io", [F32, BF16])
+@pytest.mark.parametrize("shape", STEPS)
+def test_state_update(shape, io):
+    batch, heads, groups, dk, dv = shape
+    i = STEPS.index(shape)
+    say("linear attention step %s %s" % (shape, io))
+    d, _, _ = draw(batch, 1, heads, groups, dk, dv, io, 200 + i, step=i % 2 == 0)
+    want = ref.everything(d, scale=0.3, io=io)
+    t = on_gpu(d)
+    state = t["h0"]
+    out = torch.empty(batch, heads, dv, dtype=io, device=DEV)
+    y = ssm.linear_attn_state_update(state, t["q"][:, 0], t["k"][:, 0], t["v"][:, 0], t["rate"],
+                                     step=t["step"][:, 0] if "step" in t else None, scale=0.3, out=out)
+    assert y is out
+    value, bound = want["y"]
+    check(dict(y=y.cpu()[:, None], last_state=state.cpu()), want, "step %s" % (shape,))
+
+
+def test_needless_outputs_are_left_out():
+    d, dy, dlast = draw(2, 700, 2, 1, 16, 24, F32, 23)
+    t = on_gpu(d)
+    h0 = t.pop("h0")
+    _, last, ckpt = ssm.linear_attn_fwd_save(h0=h0, **t)
+    full = ssm.linear_attn_bwd(dy=dy.to(DEV), ckpt=ckpt, dlast=dlast.to(DEV), **t)
+    for need in ((), ("drate",), ("dstep",), ("dh0",)):
+        g = ssm.linear_attn_bwd(dy=dy.to(DEV), ckpt=ckpt, dlast=dlast.to(DEV), need=need, **t)
+        for k, v in g.items():
+            if k in ("drate", "dstep", "dh0") and k not in need:
+                assert v is None
+            else:
+                assert torch.equal(v, full[k]), k
+    assert ssm.linear_attn_fwd(h0=h0, return_last_state=False, **t)[1] is None
+
+
+def test_bool_resets_and_given_outputs():
+    d, _, _ = draw(2, 100, 2, 2, 16, 24, BF16, 29, reset=0.1)
+    t = on_gpu(d)
+    y, last = ssm.linear_attn_fwd(**t)
+    out, state = torch.empty_like(y), torch.empty_like(last)
+    y2, last2 = ssm.linear_attn_fwd(out=out, last_state=state, **dict(t, reset=t["reset"].bool()))
+    assert y2 is out and last2 is state and torch.equal(y, y2) and torch.equal(last, last2)
+
+
+def test_repeats_are_equal():
+    d, dy, dlast = draw(1, 3000, 5, 1, 64, 96, BF16, 31, reset=0.002)
+    first, _ = run(d, dy, dlast)
+    for _ in range(3):
+        again, _ = run(d, dy, dlast)
+        assert all(torch.equal(first[k], again[k]) for k in first)
+
+
+def test_streams():
+    """On a side stream, and on two at once: each has a workspace of its own."""
+    jobs = [draw(1, 2100, 2, 2, 40, 72, BF16, 37 + i) for i in range(2)]
+    want = [run(*j) for j in jobs]
+    streams = [torch.cuda.Stream() for _ in jobs]
+    gpu = [(on_gpu(d), dy.to(DEV), dlast.to(DEV)) for d, dy, dlast in jobs]
+    torch.cuda.synchronize()
+    got = []
+    for (t, dy, dlast), s in zip(gpu, streams):
+        t = dict(t)
+        h0 = t.pop("h0")
+        y, last, ckpt = ssm.linear_attn_fwd_save(h0=h0, stream=s, **t)
+        got.append((y, last, ssm.linear_attn_bwd(dy=dy, ckpt=ckpt, dlast=dlast, stream=s, **t)))
+    torch.cuda.synchronize()
+    for (y, last, g), (w, _) in zip(got, want):
+        assert torch.equal(y.cpu(), w["y"]) and torch.equal(last.cpu(), w["last_state"])
+        assert all(torch.equal(g[k].cpu(), w[k]) for k in g)
+
+
+def test_graphs():
+    """Two captured training steps on one memory pool, replayed in turn with eager calls between, and a captured decode step."""
+    jobs = [draw(1, 1300, 2, 1, 40, 72, BF16, 41 + i) for i in range(2)]
+    gpu = [(on_gpu(d), dy.to(DEV), dlast.to(DEV)) for d, dy, dlast in jobs]
+
+    def step(t, dy, dlast):
+        t = dict(t)
+        h0 = t.pop("h0")
+        y, last, ckpt = ssm.linear_attn_fwd_save(h0=h0, **t)
+        return dict(y=y, last=last, **ssm.linear_attn_bwd(dy=dy, ckpt=ckpt, dlast=dlast, **t))
+
+    eager = [{k: v.clone() for k, v in step(*j).items()} for j in gpu]
+    torch.cuda.synchronize()
+    graphs, outs, pool = [], [], None
+    for j in gpu:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, pool=pool):
+            outs.append(step(*j))
+        pool = g.pool()
+        graphs.append(g)
+    for turn in range(3):
+        for g, out, want in zip(graphs, outs, eager):
+            g.replay()
+            torch.cuda.synchronize()
+            assert all(torch.equal(out[k], want[k]) for k in want), turn
+            step(*gpu[turn % 2])
+    t = gpu[0][0]
+    state, now = t["h0"].clone(), {k: t[k][:, 5].contiguous() for k in ("q", "k", "v", "step")}
+    want = state.clone()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        y = ssm.linear_attn_state_update(state, now["q"], now["k"], now["v"], t["rate"], step=now["step"])
+    for _ in range(3):
+        g.replay()
+        w = ssm.linear_attn_state_update(want, now["q"], now["k"], now["v"], t["rate"], step=now["step"])
+        torch.cuda.synchronize()
+        assert torch.equal(y, w) and torch.equal(state, want)
+
+
+def test_offsets_past_32_bits():
+    """v and y of more than 2^31 elements: the last tokens, behind a reset, equal a short call's."""
+    heads, dv, seqlen, tail = 16, 256, 540_000, 300
+    say("linear attention, %d elements" % (heads * dv * seqlen))
+    g = torch.Generator(device=DEV).manual_seed(5)
+    q, k = (torch.randn((1, seqlen, 1, 16), generator=g, device=DEV).to(BF16) for _ in range(2))
+    v = torch.randn((1, seqlen, heads, dv), generator=g, device=DEV, dtype=BF16)
+    rate = torch.full((heads,), 0.01, device=DEV)
+    reset = torch.zeros((1, seqlen), dtype=torch.uint8, device=DEV)
+    cut = seqlen - tail
+    cut -= cut % 512
+    reset[0, cut] = 1
+    y, last = ssm.linear_attn_fwd(q, k, v, rate, reset=reset)
+    ys, lasts = ssm.linear_attn_fwd(q[:, cut:].contiguous(), k[:, cut:].contiguous(), v[:, cut:].contiguous(), rate)
+    torch.cuda.synchronize()
+    assert torch.equal(y[:, cut:], ys) and torch.equal(last, lasts)
+
+
+def test_refusals():
+    q, v = torch.zeros(1, 8, 2, 16, device=DEV), torch.zeros(1, 8, 4, 24, device=DEV)
+    r, s = torch.ones(4, device=DEV), torch.zeros(1, 4, 16, 24, device=DEV)
+    with pytest.raises(ValueError, match="k: expected shape"):
+        ssm.linear_attn_fwd(q, q[:, :4].contiguous(), v, r)
+    with pytest.raises(TypeError, match="v: expected"):
+        ssm.linear_attn_fwd(q, q, v.bfloat16(), r)
+    with pytest.raises(ValueError, match="contiguous"):
+        ssm.linear_attn_fwd(q.transpose(1, 2).contiguous().transpose(1, 2), q, v, r)
+    with pytest.raises(ValueError, match="v must be contiguous"):
+        ssm.linear_attn_fwd(q, q, torch.zeros(1, 8, 4, 48, device=DEV)[..., ::2], r)
+    with pytest.raises(TypeError, match="rate"):
+        ssm.linear_attn_fwd(q, q, v, r.double())
+    with pytest.raises(ValueError, match="step"):
+        ssm.linear_attn_fwd(q, q, v, r, step=torch.ones(1, 8, 3, device=DEV))
+    with pytest.raises(TypeError, match="reset"):
+        ssm.linear_attn_fwd(q, q, v, r, reset=torch.zeros(1, 8, device=DEV))
+    with pytest.raises(ValueError, match="h0"):
+        ssm.linear_attn_fwd(q, q, v, r, h0=s[0])
+    with pytest.raises(TypeError, match="io tensors"):
+        ssm.linear_attn_fwd(q.half(), q.half(), v.half(), r)
+    with pytest.raises(ssm.SsmError, match="SSM_ERR_UNSUPPORTED"):
+        ssm.linear_attn_fwd(torch.zeros(1, 8, 2, 300, device=DEV), torch.zeros(1, 8, 2, 300, device=DEV), v, r)
+    with pytest.raises(ssm.SsmError, match="SSM_ERR_SHAPE"):
+        ssm.linear_attn_fwd(torch.zeros(1, 8, 3, 16, device=DEV), torch.zeros(1, 8, 3, 16, device=DEV), v, r)
+    with pytest.raises(ssm.SsmError, match="SSM_ERR_SHAPE"):
+        ssm.linear_attn_fwd(q[:, :0], q[:, :0], v[:, :0], r)
+    with pytest.raises(ssm.SsmError, match="SSM_ERR_ALIAS"):
+        ssm.linear_attn_fwd(q, q, v, r, out=v)
+    with pytest.raises(ValueError, match="ckpt"):
+        ssm.linear_attn_bwd(q, q, v, r, v, s)
+    with pytest.raises(ValueError, match="state"):
+        ssm.linear_attn_state_update(s[0], q[:, 0], q[:, 0], v[:, 0], r)
