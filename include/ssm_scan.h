@@ -21,7 +21,8 @@
  * ssm_gated_state_update) and the norm in front of a block, with the residual
  * add fused in front of it (ssm_norm_fwd, ssm_norm_bwd).  Linear attention
  * with a decay for each head (ssm_linear_attn_fwd, ssm_linear_attn_bwd and the
- * decode step ssm_linear_attn_state_update) keeps a matrix of states per head.
+ * decode step ssm_linear_attn_state_update) keeps a matrix of states per head,
+ * and group norm (ssm_group_norm_fwd, ssm_group_norm_bwd) is the norm behind it.
  *
  * What is computed (for every batch row b and channel d independently):
  *
@@ -75,9 +76,9 @@
  *    release threshold is 0: freed blocks are reused by later calls on the
  *    stream and returned to the device at the next synchronisation.
  *  - The gated recurrence, the norms and linear attention (ssm_gated_*,
- *    ssm_norm_*, ssm_linear_attn_*) allocate nothing; their backwards, and the
- *    linear-attention forward, take a workspace of the caller's, whose size a
- *    query gives.  Two calls that may overlap in time need two workspaces.
+ *    ssm_norm_*, ssm_group_norm_*, ssm_linear_attn_*) allocate nothing; their
+ *    backwards, and the forwards of linear attention and group norm, take a
+ *    workspace of the caller's, whose size a query gives.  Two calls that may overlap in time need two workspaces.
  *  - Calls on different streams are independent; the library is re-entrant.
  */
 #ifndef SSM_SCAN_H
@@ -89,7 +90,7 @@
 extern "C" {
 #endif
 
-#define SSM_ABI_VERSION 15
+#define SSM_ABI_VERSION 16
 
 struct ihipStream_t; /* the same incomplete type as HIP's hipStream_t */
 
@@ -656,6 +657,84 @@ ssm_status_t ssm_norm_bwd(int64_t rows, int64_t dim, ssm_dtype_t io, ssm_dtype_t
 /* Bytes of workspace ssm_norm_bwd takes for these sizes when it sums dweight or dbias; bytes may be NULL. */
 ssm_status_t ssm_norm_bwd_workspace_bytes(int64_t rows, int64_t dim, ssm_dtype_t io, ssm_dtype_t res_io,
                                           int64_t* bytes);
+
+/*
+ * Group norm over channels-last arrays, with an activation and an output gate
+ * behind it: the norm behind linear attention's heads (a group per head, length
+ * 1, a batch row per token) and of a feature map (length positions).  For every
+ * (batch row, group), over its length x channels / groups numbers:
+ *
+ *   mean = sum(x) / count                      (0 for SSM_NORM_RMS)
+ *   rstd = 1 / sqrt(sum((x - mean)^2) / count + eps)
+ *   n    = (x - mean) * rstd
+ *   f    = act(n * weight + bias)
+ *   y    = f * silu(z)                         (f without z)
+ *
+ * All sums, mean and rstd are fp32 or more; the variance is summed about the
+ * mean, or about a number of the same channel and corrected.
+ */
+typedef enum {
+  SSM_ACT_NONE = 0, /* f = p                  */
+  SSM_ACT_SILU = 1  /* f = p / (1 + exp(-p))  */
+} ssm_act_t;
+
+/*
+ * ssm_group_norm_fwd
+ *
+ *   x          [batch, length, channels]  io
+ *   z          [batch, length, channels]  io    may be NULL (no output gate)
+ *   weight     [channels]                 fp32  may be NULL (1)
+ *   bias       [channels]                 fp32  may be NULL (0)
+ *   y          [batch, length, channels]  io    written
+ *   mean, rstd [batch, groups]            fp32  written when not NULL (mean: SSM_NORM_LAYER only)
+ *   workspace                             device memory, 4-byte aligned, of ssm_group_norm_fwd_workspace_bytes
+ *                                         bytes (may be NULL when that is 0: length 1 with groups of up to 2048
+ *                                         channels); overwritten.  Too small is SSM_ERR_WORKSPACE.
+ *
+ * groups must divide channels (SSM_ERR_SHAPE); channels up to 65536 (larger is
+ * SSM_ERR_UNSUPPORTED, as are launches of 2^32 lanes and a kind or act outside
+ * its enum); any element-aligned pointers.  No output may overlap an input or
+ * another output.  Allocates nothing; deterministic.
+ */
+ssm_status_t ssm_group_norm_fwd(int64_t batch, int64_t length, int64_t channels, int64_t groups, ssm_dtype_t io,
+                                ssm_norm_t kind, ssm_act_t act, const void* x, const void* z, const float* weight,
+                                const float* bias, float eps, void* y, float* mean, float* rstd, void* workspace,
+                                int64_t workspace_bytes, struct ihipStream_t* stream);
+
+/* Bytes of workspace ssm_group_norm_fwd takes for these sizes; bytes may be NULL. */
+ssm_status_t ssm_group_norm_fwd_workspace_bytes(int64_t batch, int64_t length, int64_t channels, int64_t groups,
+                                                ssm_dtype_t io, int64_t* bytes);
+
+/*
+ * ssm_group_norm_bwd -- every gradient of sum(dy * y) for ssm_group_norm_fwd:
+ * with p = n * weight + bias,
+ *
+ *   dz = dy * f * silu'(z);   dp = dy * silu(z) * act'(p);   g = dp * weight
+ *   dx = rstd (g - sum(g) / count - n sum(g n) / count)     (sum(g) for SSM_NORM_LAYER only)
+ *   dweight = sum over batch and length of dp * n;   dbias = sum of dp
+ *
+ *   dy, x, z       [batch, length, channels]  io    z as the forward (NULL without it)
+ *   weight, bias   [channels]                 fp32  may be NULL, as the forward
+ *   mean, rstd     [batch, groups]            fp32  as the forward wrote them (mean: SSM_NORM_LAYER only)
+ *   dx             [batch, length, channels]  io    written
+ *   dz             [batch, length, channels]  io    written when z and dz are not NULL
+ *   dweight, dbias [channels]                 fp32  written when not NULL
+ *   workspace                                 device memory, 4-byte aligned, of ssm_group_norm_bwd_workspace_bytes
+ *                                             bytes (may be NULL when length is 1, groups have up to 2048 channels and
+ *                                             neither dweight nor dbias is asked for); overwritten
+ *
+ * Errors as ssm_group_norm_fwd.  Allocates nothing; sums are taken in a fixed
+ * order, so the result is deterministic.
+ */
+ssm_status_t ssm_group_norm_bwd(int64_t batch, int64_t length, int64_t channels, int64_t groups, ssm_dtype_t io,
+                                ssm_norm_t kind, ssm_act_t act, const void* dy, const void* x, const void* z,
+                                const float* weight, const float* bias, const float* mean, const float* rstd, void* dx,
+                                void* dz, float* dweight, float* dbias, void* workspace, int64_t workspace_bytes,
+                                struct ihipStream_t* stream);
+
+/* Bytes of workspace ssm_group_norm_bwd takes for these sizes when it sums dweight or dbias; bytes may be NULL. */
+ssm_status_t ssm_group_norm_bwd_workspace_bytes(int64_t batch, int64_t length, int64_t channels, int64_t groups,
+                                                ssm_dtype_t io, int64_t* bytes);
 
 /*
  * Linear attention with a decay for each head: the selective scan's recurrence

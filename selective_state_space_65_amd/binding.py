@@ -38,6 +38,8 @@ STATUS_NAMES = {
 GATED_MODES = {"plain": 0, "convex": 1, "norm": 2}
 # ssm_norm_t: layer norm, or RMS norm (no mean).
 NORM_KINDS = {"layer": 0, "rms": 1}
+# ssm_act_t: the activation behind a group norm.
+ACTIVATIONS = {"none": 0, "silu": 1}
 # Tokens between the checkpoints of gated_scan_fwd_save.
 GATED_CKPT_STEP = 128
 # Tokens between the states that linear_attn_fwd_save keeps.
@@ -89,6 +91,12 @@ SIGNATURES = {
     "ssm_linear_attn_bwd_workspace_bytes": (_I, [_I64, _I64, _I64, _I64, _I64, _I64, _I, _I, ctypes.POINTER(_I64)]),
     "ssm_linear_attn_state_update": (_I, [_I64, _I64, _I64, _I64, _I64, _I, _P, _P, _P, _P, _P, _P, ctypes.c_float, _P,
                                           _P]),
+    "ssm_group_norm_fwd": (_I, [_I64, _I64, _I64, _I64, _I, _I, _I, _P, _P, _P, _P, ctypes.c_float, _P, _P, _P, _P, _I64,
+                                _P]),
+    "ssm_group_norm_fwd_workspace_bytes": (_I, [_I64, _I64, _I64, _I64, _I, ctypes.POINTER(_I64)]),
+    "ssm_group_norm_bwd": (_I, [_I64, _I64, _I64, _I64, _I, _I, _I, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _I64,
+                                _P]),
+    "ssm_group_norm_bwd_workspace_bytes": (_I, [_I64, _I64, _I64, _I64, _I, ctypes.POINTER(_I64)]),
     "ssm_status_string": (ctypes.c_char_p, [_I]),
     "ssm_last_hip_error": (_I, []),
     "ssm_abi_version": (_I, []),
@@ -1153,3 +1161,104 @@ def linear_attn_state_update(state, q, k, v, rate, step=None, scale=1.0, out=Non
     if st:
         _check("ssm_linear_attn_state_update", st)
     return out
+
+
+def _act_code(activation):
+    if activation not in ACTIVATIONS:
+        raise ValueError("activation must be one of %s" % sorted(ACTIVATIONS))
+    return ACTIVATIONS[activation]
+
+
+def _group_norm_inputs(x, name, groups, weight, bias, z):
+    if x.dim() < 2:
+        raise ValueError("%s must be (batch, ..., channels)" % name)
+    if not x.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+    shape, io, dev = x.shape, x.dtype, x.device
+    if weight is not None:
+        _need(weight, "weight", shape[-1:], torch.float32, dev)
+    if bias is not None:
+        _need(bias, "bias", shape[-1:], torch.float32, dev)
+    if z is not None:
+        _need(z, "z", shape, io, dev)
+    batch, channels = shape[0], shape[-1]
+    length = 1 if len(shape) == 2 else x.numel() // (batch * channels) if batch and channels else 0
+    return shape, batch, length, channels, io, dev
+
+
+def group_norm_fwd(x, groups, weight=None, bias=None, z=None, eps=1e-5, kind="layer", activation="none", out=None,
+                   save_stats=True, stream=None):
+    """Group norm over channels-last x, an activation and an output gate behind it (ssm_group_norm_fwd); returns
+    (y, mean, rstd).
+
+    n = (x - mean) * rstd over the middle dimensions and each group's channels
+    (mean 0 for kind "rms"), f = n * weight + bias, or its silu with activation
+    "silu", y = f, or f * silu(z).  x, z: (batch, ..., channels) in float32 or
+    bfloat16; weight, bias: (channels,) float32.  The norm behind attention's
+    heads takes tokens as the batch: x.view(batch * seqlen, heads * dv) with
+    groups = heads.  mean and rstd are float32 (batch, groups) for
+    group_norm_bwd: None without save_stats, and mean None for "rms".
+    stream: run on that torch.cuda.Stream instead of the current one; new
+    outputs then belong to it, as tensors made under torch.cuda.stream do.
+    """
+    if stream is not None or not x.is_cuda or x.get_device() != _device():
+        return _elsewhere(group_norm_fwd, **locals())
+    shape, batch, length, channels, io, dev = _group_norm_inputs(x, "x", groups, weight, bias, z)
+    code, act = _kind_code(kind), _act_code(activation)
+    if out is None:
+        out = torch.empty_like(x)
+    else:
+        _need(out, "out", shape, io, dev)
+    mean = rstd = None
+    if save_stats:
+        rstd = torch.empty((batch, groups), dtype=torch.float32, device=dev)
+        if kind == "layer":
+            mean = torch.empty_like(rstd)
+    lib = _lib or load_library()
+    io_code = _io_code(io)
+    size = _workspace_bytes("ssm_group_norm_fwd_workspace_bytes", batch, length, channels, groups, io_code)
+    work = torch.empty(size, dtype=torch.uint8, device=dev) if size else None
+    st = lib.ssm_group_norm_fwd(batch, length, channels, groups, io_code, code, act, x.data_ptr(), _ptr(z),
+                                _ptr(weight), _ptr(bias), eps, out.data_ptr(), _ptr(mean), _ptr(rstd), _ptr(work),
+                                size, _raw_stream(dev.index))
+    if st:
+        _check("ssm_group_norm_fwd", st)
+    return out, mean, rstd
+
+
+def group_norm_bwd(dy, x, rstd, groups, mean=None, weight=None, bias=None, z=None, kind="layer", activation="none",
+                   need=("dweight", "dbias", "dz"), stream=None):
+    """Gradients of sum(dy * y) for group_norm_fwd (ssm_group_norm_bwd).
+
+    x, weight, bias, z, kind and activation as in the forward, mean and rstd as
+    it returned them (mean for kind "layer" only).  Returns a dict: dx (io
+    dtype) and, when named in `need`, dweight and dbias (channels,) float32 and dz
+    (io dtype, only with z); None for the others.
+    """
+    if stream is not None or not dy.is_cuda or dy.get_device() != _device():
+        return _elsewhere(group_norm_bwd, **locals())
+    shape, batch, length, channels, io, dev = _group_norm_inputs(dy, "dy", groups, weight, bias, z)
+    code, act = _kind_code(kind), _act_code(activation)
+    f32 = torch.float32
+    _need(x, "x", shape, io, dev)
+    _need(rstd, "rstd", (batch, groups), f32, dev)
+    if kind == "layer":
+        if mean is None:
+            raise ValueError("kind \"layer\" needs the mean")
+        _need(mean, "mean", (batch, groups), f32, dev)
+    else:
+        mean = None
+    g = dict(dx=torch.empty_like(dy), dz=torch.empty_like(dy) if ("dz" in need and z is not None) else None,
+             dweight=_vector(weight, channels, dev) if "dweight" in need else None,
+             dbias=_vector(bias, channels, dev) if "dbias" in need else None)
+    lib = _lib or load_library()
+    io_code = _io_code(io)
+    size = _workspace_bytes("ssm_group_norm_bwd_workspace_bytes", batch, length, channels, groups, io_code)
+    work = torch.empty(size, dtype=torch.uint8, device=dev) if size else None
+    st = lib.ssm_group_norm_bwd(batch, length, channels, groups, io_code, code, act, dy.data_ptr(), x.data_ptr(),
+                                _ptr(z), _ptr(weight), _ptr(bias), _ptr(mean), _ptr(rstd), g["dx"].data_ptr(),
+                                _ptr(g["dz"]), _ptr(g["dweight"]), _ptr(g["dbias"]), _ptr(work), size,
+                                _raw_stream(dev.index))
+    if st:
+        _check("ssm_group_norm_bwd", st)
+    return g

@@ -3,7 +3,7 @@
 The library is the whole product path: C ABI + kernels in one shared object
 (csrc/ssm_scan.hip: the scan's ABI and most of its kernels;
 csrc/scan_chunked.hip: the chunked prefill scan; csrc/gated_scan.hip: the gated
-recurrence; csrc/norm.hip: the norms; csrc/linear_attn*.hip: linear attention; header
+recurrence; csrc/norm.hip and csrc/group_norm.hip: the norms; csrc/linear_attn*.hip: linear attention; header
 include/ssm_scan.h).  The translation units are compiled in parallel and linked.  Packed FP32 instructions are disabled for
 every HIP compile (-packed-fp32-ops).
 """
@@ -14,6 +14,7 @@ import sys
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 SRCS = [os.path.join(HERE, "csrc", name) for name in ("ssm_scan.hip", "scan_chunked.hip", "gated_scan.hip", "norm.hip",
+                                                        "group_norm.hip",
                                                         "linear_attn.hip", "linear_attn_bf16.hip",
                                                         "linear_attn_f32.hip")]
 INCLUDE = os.path.join(ROOT, "include")

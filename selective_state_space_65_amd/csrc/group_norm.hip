@@ -1,0 +1,862 @@
+// group_norm.hip -- group norm over channels-last arrays, with an activation
+// and an output gate behind it: forward and backward.  C ABI:
+// include/ssm_scan.h.
+//
+// Two layouts of a group's numbers.
+//
+// One position (length 1, the norm behind attention's heads): a group is one
+// contiguous run of d = channels / groups numbers, held in registers by G lanes
+// (8 to 64, up to 4 pieces of 8 a lane) from its one read to its write.  The
+// backward gives a group of lanes many batch rows of the same channels, whose
+// sums it keeps in registers.
+//
+// A map (length above 1, or d above what a wave holds): a block takes a run of
+// positions with all their channels, a thread 8 channels and every TY-th of the
+// positions, so that all reads are contiguous; channels are joined into groups
+// at the end of the run, runs by a small second kernel, and a last kernel reads
+// the numbers again and writes.  The variance is summed about a pivot, each
+// channel's first number in the run, and joined from means and sums of squares
+// about them, so that it does not suffer from a large mean.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+
+#include "device_common.h"
+#include "host_common.h"
+#include "lane_rows.h"
+#include "ssm_scan.h"
+
+namespace {
+
+constexpr int kMostRun = 64 * kPiece * 4;  // numbers a wave holds
+constexpr int kThreads = 256;
+
+struct Args {
+  const void* x;
+  const void* z;        // may be null
+  const float* weight;  // may be null
+  const float* bias;    // may be null
+  void* y;              // forward
+  float* mean;          // [batch, groups]; may be null
+  float* rstd;          // [batch, groups]; may be null in the forward
+  const void* dy;       // backward from here
+  void* dx;
+  void* dz;             // may be null
+  float* part;          // partial sums, may be null
+  float* sums;          // [2][batch, groups]
+  int64_t batch, length, channels;
+  int groups, d;        // d channels in a group
+  int rms, silu;
+  float eps;
+  int runs;             // maps: blocks along the positions
+  int64_t run;          // maps: positions of a block
+  int64_t stride;       // one position, backward: batch rows between two of a lane's
+};
+
+__device__ __forceinline__ float sigmoid_f32(float x) { return rcp_hw(1.0f + exp2_hw(-x * kLog2e)); }
+
+// f = p or silu(p), and its slope.
+__device__ __forceinline__ float activate(float p, bool silu, float* slope) {
+  if (!silu) {
+    *slope = 1.0f;
+    return p;
+  }
+  const float s = sigmoid_f32(p);
+  *slope = s * __builtin_fmaf(p, 1.0f - s, 1.0f);
+  return p * s;
+}
+
+// y of one number.
+__device__ __forceinline__ float output(float n, float w, float b, float z, bool silu, bool gated) {
+  float slope;
+  const float f = activate(__builtin_fmaf(n, w, b), silu, &slope);
+  return gated ? f * silu_f32(z) : f;
+}
+
+// dL/dp of one number, p the activation's input, and dL/dz.
+__device__ __forceinline__ float inner(float n, float w, float b, float z, float dy, bool silu, bool gated, float* dz) {
+  float slope;
+  const float f = activate(__builtin_fmaf(n, w, b), silu, &slope);
+  *dz = 0.0f;
+  if (gated) {
+    float gate_slope;
+    const float gate = activate(z, true, &gate_slope);
+    *dz = dy * f * gate_slope;
+    dy *= gate;
+  }
+  return dy * slope;
+}
+
+__device__ __forceinline__ void fill(float v[kPiece], float x) {
+#pragma unroll
+  for (int j = 0; j < kPiece; ++j) v[j] = x;
+}
+
+// ---- one position -------------------------------------------------------------
+
+template <int G, typename T>
+__device__ __forceinline__ void piece(const T* row, int c, int gl, int d, float out[kPiece]) {
+  Raw8<T> r = request_piece<G>(row, c, gl, d);
+  finish_piece<G>(r, c, gl, d);
+  r.get(out);
+}
+
+template <typename T, int G, int K, bool kGated>
+__global__ __launch_bounds__(kThreads) void group_norm_row_fwd_kernel(const Args p) {
+  const int lane = threadIdx.x & 63, gl = lane & (G - 1);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t rows = p.batch * p.groups;
+  const int64_t row = ((int64_t)blockIdx.x * (kThreads / 64) + wave) * (64 / G) + lane / G;
+  const bool live = row < rows;
+  const int64_t at = (live ? row : rows - 1) * p.d;
+  const int d = p.d, first = (int)((live ? row : rows - 1) % p.groups) * d;
+  const T* x = static_cast<const T*>(p.x) + at;
+  const float count = (float)d;
+  Raw8<T> px[K], pz[K];
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    px[k] = request_piece<G>(x, (k * G + gl) * kPiece, gl, d);
+    if constexpr (kGated) pz[k] = request_piece<G>(static_cast<const T*>(p.z) + at, (k * G + gl) * kPiece, gl, d);
+  }
+  float v[K][kPiece], t = 0.0f;
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    const int c = (k * G + gl) * kPiece;
+    finish_piece<G>(px[k], c, gl, d);
+    px[k].get(v[k]);
+#pragma unroll
+    for (int j = 0; j < kPiece; ++j) t += v[k][j];
+  }
+  const float mean = p.rms ? 0.0f : group_sum<G>(t) / count;
+  float q = 0.0f;
+#pragma unroll
+  for (int k = 0; k < K; ++k)
+#pragma unroll
+    for (int j = 0; j < kPiece; ++j) {
+      const float e = (k * G + gl) * kPiece + j < d ? v[k][j] - mean : 0.0f;
+      q = __builtin_fmaf(e, e, q);
+    }
+  const float rstd = 1.0f / __builtin_sqrtf(group_sum<G>(q) / count + p.eps);
+  if (!live) return;
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    const int c = (k * G + gl) * kPiece;
+    float w[kPiece], b[kPiece], z[kPiece], o[kPiece];
+    fill(w, 1.0f);
+    fill(b, 0.0f);
+    fill(z, 0.0f);
+    if (p.weight) piece<G>(p.weight + first, c, gl, d, w);
+    if (p.bias) piece<G>(p.bias + first, c, gl, d, b);
+    if constexpr (kGated) {
+      finish_piece<G>(pz[k], c, gl, d);
+      pz[k].get(z);
+    }
+#pragma unroll
+    for (int j = 0; j < kPiece; ++j) o[j] = output((v[k][j] - mean) * rstd, w[j], b[j], z[j], p.silu, kGated);
+    store_row8(static_cast<T*>(p.y) + at, c, d, whole<G>(c, gl, d), o);
+  }
+  if (gl == 0) {
+    if (!p.rms && p.mean) p.mean[row] = mean;
+    if (p.rstd) p.rstd[row] = rstd;
+  }
+}
+
+// A group of lanes has one group of channels and every stride-th batch row.
+template <typename T, int G, int K, bool kGated>
+__global__ __launch_bounds__(kThreads) void group_norm_row_bwd_kernel(const Args p) {
+  const int lane = threadIdx.x & 63, gl = lane & (G - 1);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t id = ((int64_t)blockIdx.x * (kThreads / 64) + wave) * (64 / G) + lane / G;
+  const int d = p.d, group = (int)(id % p.groups);
+  const int64_t b0 = id / p.groups;
+  const int64_t sweeps = (p.batch + p.stride - 1) / p.stride;
+  float w[K][kPiece], b[K][kPiece], aw[K][kPiece], ab[K][kPiece];
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    const int c = (k * G + gl) * kPiece;
+    fill(w[k], 1.0f);
+    fill(b[k], 0.0f);
+    fill(aw[k], 0.0f);
+    fill(ab[k], 0.0f);
+    if (p.weight) piece<G>(p.weight + (int64_t)group * d, c, gl, d, w[k]);
+    if (p.bias) piece<G>(p.bias + (int64_t)group * d, c, gl, d, b[k]);
+  }
+  const float inv = 1.0f / (float)d;
+  for (int64_t i = 0; i < sweeps; ++i) {
+    const int64_t at_b = b0 + i * p.stride;
+    const bool live = b0 < p.stride && at_b < p.batch;
+    const int64_t row = (live ? at_b : 0) * p.groups + group, at = row * d;
+    const float mean = p.rms ? 0.0f : p.mean[row], rstd = p.rstd[row];
+    float n[K][kPiece], g[K][kPiece], dz[K][kPiece];
+    float c1 = 0.0f, c2 = 0.0f;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int c = (k * G + gl) * kPiece;
+      float z[kPiece];
+      piece<G>(static_cast<const T*>(p.x) + at, c, gl, d, n[k]);
+      piece<G>(static_cast<const T*>(p.dy) + at, c, gl, d, g[k]);  // 0 past the run: so is all that follows
+      fill(z, 0.0f);
+      if constexpr (kGated) piece<G>(static_cast<const T*>(p.z) + at, c, gl, d, z);
+#pragma unroll
+      for (int j = 0; j < kPiece; ++j) {
+        n[k][j] = (n[k][j] - mean) * rstd;
+        const float dp = inner(n[k][j], w[k][j], b[k][j], z[j], g[k][j], p.silu, kGated, &dz[k][j]);
+        if (live) {
+          aw[k][j] = __builtin_fmaf(dp, n[k][j], aw[k][j]);
+          ab[k][j] += dp;
+        }
+        g[k][j] = dp * w[k][j];
+        c1 += g[k][j];
+        c2 = __builtin_fmaf(g[k][j], n[k][j], c2);
+      }
+    }
+    c1 = p.rms ? 0.0f : group_sum<G>(c1) * inv;
+    c2 = group_sum<G>(c2) * inv;
+    if (!live) continue;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int c = (k * G + gl) * kPiece;
+      float o[kPiece];
+#pragma unroll
+      for (int j = 0; j < kPiece; ++j) o[j] = rstd * __builtin_fmaf(-n[k][j], c2, g[k][j] - c1);
+      store_row8(static_cast<T*>(p.dx) + at, c, d, whole<G>(c, gl, d), o);
+      if (kGated && p.dz) store_row8(static_cast<T*>(p.dz) + at, c, d, whole<G>(c, gl, d), dz[k]);
+    }
+  }
+  if (!p.part || b0 >= p.stride) return;
+  float* part = p.part + b0 * 2 * p.channels + (int64_t)group * d;
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    const int c = (k * G + gl) * kPiece;
+    store_row8(part, c, d, whole<G>(c, gl, d), aw[k]);
+    store_row8(part + p.channels, c, d, whole<G>(c, gl, d), ab[k]);
+  }
+}
+
+// dweight and dbias from partial rows of 2 x channels: 32 columns a block, 32
+// slices of the rows, added in order.
+__global__ __launch_bounds__(1024) void group_norm_columns_kernel(const float* part, float* dweight, float* dbias,
+                                                                  int64_t rows, int64_t channels) {
+  __shared__ float sums[32][33];
+  const int col = threadIdx.x & 31, slice = threadIdx.x >> 5;
+  const int64_t c = (int64_t)blockIdx.x * 32 + col;
+  float t = 0.0f;
+  if (c < 2 * channels) {
+    int64_t r = slice;
+    for (; r + 7 * 32 < rows; r += 8 * 32) {
+      float v[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = part[(r + j * 32) * 2 * channels + c];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) t += v[j];
+    }
+    for (; r < rows; r += 32) t += part[r * 2 * channels + c];
+  }
+  sums[slice][col] = t;
+  __syncthreads();
+  if (slice == 0 && c < 2 * channels) {
+#pragma unroll
+    for (int i = 1; i < 32; ++i) t += sums[i][col];
+    float* out = c < channels ? dweight : dbias;
+    if (out) out[c < channels ? c : c - channels] = t;
+  }
+}
+
+// ---- maps ----------------------------------------------------------------------
+
+// A block's threads: TX along the channels (8 each), TY along the positions; wide
+// maps take several columns of TX.
+struct Plane {
+  int tx, ty, x, y;
+};
+
+__device__ __forceinline__ Plane plane(int64_t channels) {
+  const int pieces = (int)((channels + kPiece - 1) / kPiece);
+  Plane t;
+  t.tx = min(pieces, kThreads);
+  t.ty = kThreads / t.tx;
+  t.x = threadIdx.x % t.tx;
+  t.y = threadIdx.x / t.tx;
+  return t;
+}
+
+template <typename T>
+__device__ __forceinline__ Raw8<T> request_at(const T* row, int c, int n) {
+  return request8<true>(row, c, 0, n);
+}
+
+template <typename T>
+__device__ __forceinline__ void finish_at(Raw8<T>& r, int c, int n, float out[kPiece]) {
+  finish8<true>(r, c, 0, n);
+  r.get(out);
+}
+
+__device__ __forceinline__ float wave_sum_f32(float v) { return group_sum<64>(v); }
+
+// part[batch][run][2][groups]: each run's means, and sums of squares about them.
+template <typename T>
+__global__ __launch_bounds__(kThreads) void group_norm_map_stats_kernel(const Args p) {
+  __shared__ float cols[2][kThreads * kPiece];
+  const Plane t = plane(p.channels);
+  const int64_t batch = blockIdx.x / p.runs;
+  const int run = (int)(blockIdx.x % p.runs);
+  const int64_t l0 = run * p.run, l1 = min(l0 + p.run, p.length);
+  const float count = (float)(l1 - l0);
+  const int n = (int)p.channels, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const T* x = static_cast<const T*>(p.x) + batch * p.length * n;
+  float* out = p.part + (batch * p.runs + run) * 2 * p.groups;
+  for (int c0 = 0; c0 < n; c0 += t.tx * kPiece) {
+    const int c = c0 + t.x * kPiece;
+    const bool live = t.y < t.ty && c < n;
+    float s1[kPiece], s2[kPiece], pivot[kPiece];
+    fill(s1, 0.0f);
+    fill(s2, 0.0f);
+    fill(pivot, 0.0f);
+    if (live) {
+      if (!p.rms) {
+        Raw8<T> r = request_at(x + l0 * n, c, n);
+        finish_at(r, c, n, pivot);
+      }
+      constexpr int kAhead = 4;
+      for (int64_t l = l0 + t.y; l < l1; l += kAhead * t.ty) {
+        Raw8<T> r[kAhead];
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) r[u] = request_at(x + min(l + u * t.ty, l1 - 1) * n, c, n);
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+          if (l + u * t.ty >= l1) break;
+          float v[kPiece];
+          finish_at(r[u], c, n, v);
+#pragma unroll
+          for (int j = 0; j < kPiece; ++j) {
+            const float e = v[j] - pivot[j];
+            s1[j] += e;
+            s2[j] = __builtin_fmaf(e, e, s2[j]);
+          }
+        }
+      }
+    }
+    // Over the block's rows of threads, in order, then a channel's mean and squares about it.
+    for (int y = t.ty - 1; y >= 0; --y) {
+      __syncthreads();
+      if (live && t.y == y) {
+#pragma unroll
+        for (int j = 0; j < kPiece; ++j) {
+          float* a = &cols[0][t.x * kPiece + j];
+          float* b = &cols[1][t.x * kPiece + j];
+          if (y < t.ty - 1) s1[j] += *a, s2[j] += *b;
+          if (y == 0) {
+            const float m = p.rms ? 0.0f : s1[j] / count;
+            s2[j] -= m * s1[j];
+            s1[j] = pivot[j] + m;
+            if (p.rms) s1[j] = 0.0f;
+          }
+          *a = s1[j];
+          *b = s2[j];
+        }
+      }
+    }
+    __syncthreads();
+    // Groups, a wave each; one that began in an earlier column is joined with what is there.
+    const int c1 = min(n, c0 + t.tx * kPiece);
+    for (int g = c0 / p.d + wave; g <= (c1 - 1) / p.d; g += kThreads / 64) {
+      const int lo = max(g * p.d, c0) - c0, hi = min((g + 1) * p.d, c1) - c0;
+      const float here = (float)(hi - lo);
+      float m = 0.0f, q = 0.0f;
+      for (int i = lo + lane; i < hi; i += 64) m += cols[0][i];
+      m = wave_sum_f32(m) / here;
+      for (int i = lo + lane; i < hi; i += 64) {
+        const float e = cols[0][i] - m;
+        q += __builtin_fmaf(count * e, e, cols[1][i]);
+      }
+      q = wave_sum_f32(q);
+      if (lane == 0) {
+        if (g * p.d < c0) {
+          const float before = (float)(c0 - g * p.d), m0 = out[g], all = before + here, e = m - m0;
+          m = m0 + e * (here / all);
+          q += out[p.groups + g] + count * e * e * (before * here / all);
+        }
+        out[g] = m;
+        out[p.groups + g] = q;
+      }
+    }
+  }
+}
+
+// Runs joined: mean and rstd of a (batch, group), a wave each.
+__global__ __launch_bounds__(kThreads) void group_norm_map_join_kernel(const Args p) {
+  const int lane = threadIdx.x & 63;
+  const int64_t row = (int64_t)blockIdx.x * (kThreads / 64) + (threadIdx.x >> 6);
+  if (row >= p.batch * p.groups) return;
+  const int64_t batch = row / p.groups;
+  const int g = (int)(row % p.groups);
+  const float* part = p.part + batch * p.runs * 2 * p.groups + g;
+  const double all = (double)p.length;
+  double m = 0.0;
+  const auto count = [&](int r) { return (double)(min(r * p.run + p.run, p.length) - r * p.run); };
+  for (int r = lane; r < p.runs; r += 64) m += count(r) * (double)part[(int64_t)r * 2 * p.groups];
+#pragma unroll
+  for (int s = 1; s < 64; s <<= 1) m += __shfl_xor(m, s);
+  m /= all;
+  double q = 0.0;
+  for (int r = lane; r < p.runs; r += 64) {
+    const double e = (double)part[(int64_t)r * 2 * p.groups] - m;
+    q += (double)part[((int64_t)r * 2 + 1) * p.groups] + count(r) * (double)p.d * e * e;
+  }
+#pragma unroll
+  for (int s = 1; s < 64; s <<= 1) q += __shfl_xor(q, s);
+  if (lane == 0) {
+    if (p.mean) p.mean[row] = (float)m;
+    p.rstd[row] = (float)(1.0 / __builtin_sqrt(q / (all * p.d) + (double)p.eps));
+  }
+}
+
+// What a thread's 8 channels have in common over the positions.
+struct Columns {
+  float w[kPiece], b[kPiece], mean[kPiece], rstd[kPiece];
+};
+
+__device__ __forceinline__ void load_columns(const Args& p, int64_t batch, int c, int n, Columns* k) {
+  fill(k->w, 1.0f);
+  fill(k->b, 0.0f);
+  if (p.weight) {
+    Raw8<float> r = request_at(p.weight, c, n);
+    finish_at(r, c, n, k->w);
+  }
+  if (p.bias) {
+    Raw8<float> r = request_at(p.bias, c, n);
+    finish_at(r, c, n, k->b);
+  }
+#pragma unroll
+  for (int j = 0; j < kPiece; ++j) {
+    const int64_t row = batch * p.groups + min(c + j, n - 1) / p.d;
+    k->mean[j] = p.rms ? 0.0f : p.mean[row];
+    k->rstd[j] = p.rstd[row];
+  }
+}
+
+template <typename T, bool kGated>
+__global__ __launch_bounds__(kThreads) void group_norm_map_fwd_kernel(const Args p) {
+  const Plane t = plane(p.channels);
+  const int64_t batch = blockIdx.x / p.runs;
+  const int run = (int)(blockIdx.x % p.runs);
+  const int64_t l0 = run * p.run, l1 = min(l0 + p.run, p.length);
+  const int n = (int)p.channels;
+  const int64_t base = batch * p.length * n;
+  if (t.y >= t.ty) return;
+  for (int c = t.x * kPiece; c < n; c += t.tx * kPiece) {
+    Columns k;
+    load_columns(p, batch, c, n, &k);
+    constexpr int kAhead = 4;
+    for (int64_t l = l0 + t.y; l < l1; l += kAhead * t.ty) {
+      Raw8<T> rx[kAhead], rz[kAhead];
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        const int64_t at = base + min(l + u * t.ty, l1 - 1) * n;
+        rx[u] = request_at(static_cast<const T*>(p.x) + at, c, n);
+        if constexpr (kGated) rz[u] = request_at(static_cast<const T*>(p.z) + at, c, n);
+      }
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        if (l + u * t.ty >= l1) break;
+        float v[kPiece], z[kPiece];
+        finish_at(rx[u], c, n, v);
+        fill(z, 0.0f);
+        if constexpr (kGated) finish_at(rz[u], c, n, z);
+#pragma unroll
+        for (int j = 0; j < kPiece; ++j)
+          v[j] = output((v[j] - k.mean[j]) * k.rstd[j], k.w[j], k.b[j], z[j], p.silu, kGated);
+        store_row8(static_cast<T*>(p.y) + base + (l + u * t.ty) * n, c, n, c + kPiece <= n, v);
+      }
+    }
+  }
+}
+
+// part[batch][run][2][channels]: sums of dp n and of dp.
+template <typename T, bool kGated>
+__global__ __launch_bounds__(kThreads) void group_norm_map_sums_kernel(const Args p) {
+  __shared__ float cols[2][kThreads * kPiece];
+  const Plane t = plane(p.channels);
+  const int64_t batch = blockIdx.x / p.runs;
+  const int run = (int)(blockIdx.x % p.runs);
+  const int64_t l0 = run * p.run, l1 = min(l0 + p.run, p.length);
+  const int n = (int)p.channels;
+  const int64_t base = batch * p.length * n;
+  float* out = p.part + (batch * p.runs + run) * 2 * n;
+  for (int c0 = 0; c0 < n; c0 += t.tx * kPiece) {
+    const int c = c0 + t.x * kPiece;
+    const bool live = t.y < t.ty && c < n;
+    float aw[kPiece], ab[kPiece];
+    fill(aw, 0.0f);
+    fill(ab, 0.0f);
+    if (live) {
+      Columns k;
+      load_columns(p, batch, c, n, &k);
+      constexpr int kAhead = 4;
+      for (int64_t l = l0 + t.y; l < l1; l += kAhead * t.ty) {
+        Raw8<T> rx[kAhead], rd[kAhead], rz[kAhead];
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+          const int64_t at = base + min(l + u * t.ty, l1 - 1) * n;
+          rx[u] = request_at(static_cast<const T*>(p.x) + at, c, n);
+          rd[u] = request_at(static_cast<const T*>(p.dy) + at, c, n);
+          if constexpr (kGated) rz[u] = request_at(static_cast<const T*>(p.z) + at, c, n);
+        }
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+          if (l + u * t.ty >= l1) break;
+          float v[kPiece], d[kPiece], z[kPiece];
+          finish_at(rx[u], c, n, v);
+          finish_at(rd[u], c, n, d);
+          fill(z, 0.0f);
+          if constexpr (kGated) finish_at(rz[u], c, n, z);
+#pragma unroll
+          for (int j = 0; j < kPiece; ++j) {
+            float dz;
+            const float m = (v[j] - k.mean[j]) * k.rstd[j];
+            const float dp = inner(m, k.w[j], k.b[j], z[j], d[j], p.silu, kGated, &dz);
+            aw[j] = __builtin_fmaf(dp, m, aw[j]);
+            ab[j] += dp;
+          }
+        }
+      }
+    }
+    for (int y = t.ty - 1; y >= 0; --y) {
+      __syncthreads();
+      if (live && t.y == y) {
+#pragma unroll
+        for (int j = 0; j < kPiece; ++j) {
+          float* a = &cols[0][t.x * kPiece + j];
+          float* b = &cols[1][t.x * kPiece + j];
+          if (y < t.ty - 1) aw[j] += *a, ab[j] += *b;
+          *a = aw[j];
+          *b = ab[j];
+        }
+        if (y == 0) {
+          store_row8(out, c, n, c + kPiece <= n, aw);
+          store_row8(out + n, c, n, c + kPiece <= n, ab);
+        }
+      }
+    }
+  }
+}
+
+// sums[0 / 1][batch, group]: mean over the group of g n and of g (g = dp weight);
+// dweight and dbias.  A block has one group; a channel's runs are added in
+// order, channels and batch rows likewise.
+__global__ __launch_bounds__(kThreads) void group_norm_map_reduce_kernel(const Args p, float* dweight, float* dbias) {
+  __shared__ float parts[2][kThreads / 64];
+  const int g = blockIdx.x, n = (int)p.channels, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t rows = p.batch * p.groups;
+  const float inv = 1.0f / ((float)p.length * (float)p.d);
+  for (int64_t b = 0; b < p.batch; ++b) {
+    float c1 = 0.0f, c2 = 0.0f;
+    for (int i = threadIdx.x; i < p.d; i += kThreads) {
+      const int c = g * p.d + i;
+      const float* at = p.part + b * p.runs * 2 * n + c;
+      float aw = 0.0f, ab = 0.0f;
+      for (int r = 0; r < p.runs; ++r) {
+        aw += at[(int64_t)r * 2 * n];
+        ab += at[((int64_t)r * 2 + 1) * n];
+      }
+      const float w = p.weight ? p.weight[c] : 1.0f;
+      c2 = __builtin_fmaf(aw, w, c2);
+      c1 = __builtin_fmaf(ab, w, c1);
+      if (dweight) dweight[c] = b ? dweight[c] + aw : aw;
+      if (dbias) dbias[c] = b ? dbias[c] + ab : ab;
+    }
+    c1 = wave_sum_f32(c1);
+    c2 = wave_sum_f32(c2);
+    __syncthreads();
+    if (lane == 0) parts[0][wave] = c2, parts[1][wave] = c1;
+    __syncthreads();
+    if (threadIdx.x < 2) {
+      const float* s = parts[threadIdx.x];
+      p.sums[threadIdx.x * rows + b * p.groups + g] = ((s[0] + s[1]) + (s[2] + s[3])) * inv;
+    }
+  }
+}
+
+template <typename T, bool kGated>
+__global__ __launch_bounds__(kThreads) void group_norm_map_bwd_kernel(const Args p) {
+  const Plane t = plane(p.channels);
+  const int64_t batch = blockIdx.x / p.runs;
+  const int run = (int)(blockIdx.x % p.runs);
+  const int64_t l0 = run * p.run, l1 = min(l0 + p.run, p.length);
+  const int n = (int)p.channels;
+  const int64_t base = batch * p.length * n, rows = p.batch * p.groups;
+  if (t.y >= t.ty) return;
+  for (int c = t.x * kPiece; c < n; c += t.tx * kPiece) {
+    Columns k;
+    load_columns(p, batch, c, n, &k);
+    float c1[kPiece], c2[kPiece];
+#pragma unroll
+    for (int j = 0; j < kPiece; ++j) {
+      const int64_t row = batch * p.groups + min(c + j, n - 1) / p.d;
+      c2[j] = p.sums[row];
+      c1[j] = p.rms ? 0.0f : p.sums[rows + row];
+    }
+    constexpr int kAhead = 2;
+    for (int64_t l = l0 + t.y; l < l1; l += kAhead * t.ty) {
+      Raw8<T> rx[kAhead], rd[kAhead], rz[kAhead];
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        const int64_t at = base + min(l + u * t.ty, l1 - 1) * n;
+        rx[u] = request_at(static_cast<const T*>(p.x) + at, c, n);
+        rd[u] = request_at(static_cast<const T*>(p.dy) + at, c, n);
+        if constexpr (kGated) rz[u] = request_at(static_cast<const T*>(p.z) + at, c, n);
+      }
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        if (l + u * t.ty >= l1) break;
+        float v[kPiece], d[kPiece], z[kPiece], dz[kPiece];
+        finish_at(rx[u], c, n, v);
+        finish_at(rd[u], c, n, d);
+        fill(z, 0.0f);
+        if constexpr (kGated) finish_at(rz[u], c, n, z);
+#pragma unroll
+        for (int j = 0; j < kPiece; ++j) {
+          const float m = (v[j] - k.mean[j]) * k.rstd[j];
+          const float g = inner(m, k.w[j], k.b[j], z[j], d[j], p.silu, kGated, &dz[j]) * k.w[j];
+          v[j] = k.rstd[j] * __builtin_fmaf(-m, c2[j], g - c1[j]);
+        }
+        const int64_t at = base + (l + u * t.ty) * n;
+        store_row8(static_cast<T*>(p.dx) + at, c, n, c + kPiece <= n, v);
+        if (kGated && p.dz) store_row8(static_cast<T*>(p.dz) + at, c, n, c + kPiece <= n, dz);
+      }
+    }
+  }
+}
+
+// ---- host side ---------------------------------------------------------------
+
+struct Plan {
+  bool map;
+  int lanes, pieces;    // one position: of a run of channels
+  int64_t row_blocks;   // forward
+  int64_t stride, bwd_blocks;
+  int64_t runs, run;    // maps
+};
+
+Plan make_plan(int64_t batch, int64_t length, int64_t channels, int64_t groups) {
+  Plan p = {};
+  const int64_t d = channels / groups;
+  p.map = length > 1 || d > kMostRun;
+  if (!p.map) {
+    p.lanes = 8;
+    while (p.lanes < 64 && p.lanes * kPiece < d) p.lanes *= 2;
+    p.pieces = 1;
+    while ((int64_t)p.lanes * kPiece * p.pieces < d) p.pieces *= 2;
+    const int64_t per_block = kThreads / p.lanes;
+    p.row_blocks = (batch * groups + per_block - 1) / per_block;
+    // Batch rows side by side: enough for the chip's lanes, and no more partial rows than 512.
+    p.stride = std::min<int64_t>(batch, std::max<int64_t>(1, std::min<int64_t>(512, 2048 * per_block / groups)));
+    p.bwd_blocks = (p.stride * groups + per_block - 1) / per_block;
+  } else {
+    const int64_t pieces = (channels + kPiece - 1) / kPiece;
+    const int64_t ty = kThreads / std::min<int64_t>(pieces, kThreads);
+    // Blocks for the whole chip, and at most 128 positions to a thread: no sum gets long.
+    const int64_t wanted = std::max((1024 + batch - 1) / batch, (length + 128 * ty - 1) / (128 * ty));
+    const int64_t least = ty * 4;  // positions that a block's threads have in flight
+    p.runs = std::max<int64_t>(1, std::min(wanted, (length + least - 1) / least));
+    p.run = (length + p.runs - 1) / p.runs;
+    p.runs = (length + p.run - 1) / p.run;
+  }
+  return p;
+}
+
+ssm_status_t check_shape(int64_t batch, int64_t length, int64_t channels, int64_t groups, ssm_dtype_t io, int64_t* n) {
+  if (io != SSM_F32 && io != SSM_BF16) return SSM_ERR_DTYPE;
+  if (batch < 1 || length < 1 || channels < 1 || groups < 1 || channels % groups) return SSM_ERR_SHAPE;
+  int64_t bytes;
+  if (!mul_ok(batch, length, n) || !mul_ok(*n, channels, n) || !mul_ok(*n, 64, &bytes)) return SSM_ERR_SHAPE;
+  if (channels > 65536) return SSM_ERR_UNSUPPORTED;
+  const Plan p = make_plan(batch, length, channels, groups);
+  if (!launch_ok(p.map ? batch * p.runs : p.row_blocks, kThreads)) return SSM_ERR_UNSUPPORTED;
+  return SSM_OK;
+}
+
+// Workspace of the forward: maps' partial sums, and mean and rstd where they are not asked for.
+int64_t fwd_bytes(const Plan& p, int64_t batch, int64_t groups) {
+  return p.map ? (batch * p.runs * 2 * groups + 2 * batch * groups) * 4 : 0;
+}
+
+int64_t bwd_bytes(const Plan& p, int64_t batch, int64_t channels, int64_t groups, bool sums) {
+  if (p.map) return (batch * p.runs * 2 * channels + 2 * batch * groups) * 4;
+  return sums ? p.stride * 2 * channels * 4 : 0;
+}
+
+#define SSM_GROUP_NORM_GEOMETRY(CALL)                \
+  switch (p.lanes) {                                 \
+    case 8: CALL(8, 1); break;                       \
+    case 16: CALL(16, 1); break;                     \
+    case 32: CALL(32, 1); break;                     \
+    default:                                         \
+      if (p.pieces == 1) { CALL(64, 1); }            \
+      else if (p.pieces == 2) { CALL(64, 2); }       \
+      else { CALL(64, 4); }                          \
+  }
+
+template <typename T, bool kGated>
+hipError_t launch_fwd(const Args& a, const Plan& p, hipStream_t st) {
+  const dim3 threads(kThreads);
+  if (!p.map) {
+#define SSM_GROUP_NORM_CALL(G, K)                                                                              \
+  hipLaunchKernelGGL((group_norm_row_fwd_kernel<T, G, K, kGated>), dim3((unsigned)p.row_blocks), threads, 0, st, a)
+    SSM_GROUP_NORM_GEOMETRY(SSM_GROUP_NORM_CALL)
+#undef SSM_GROUP_NORM_CALL
+    return hipGetLastError();
+  }
+  const dim3 grid((unsigned)(a.batch * p.runs));
+  hipLaunchKernelGGL(group_norm_map_stats_kernel<T>, grid, threads, 0, st, a);
+  const int64_t per_block = kThreads / 64;
+  hipLaunchKernelGGL(group_norm_map_join_kernel, dim3((unsigned)((a.batch * a.groups + per_block - 1) / per_block)),
+                     threads, 0, st, a);
+  hipLaunchKernelGGL((group_norm_map_fwd_kernel<T, kGated>), grid, threads, 0, st, a);
+  return hipGetLastError();
+}
+
+template <typename T, bool kGated>
+hipError_t launch_bwd(const Args& a, const Plan& p, float* dweight, float* dbias, hipStream_t st) {
+  const dim3 threads(kThreads);
+  if (!p.map) {
+#define SSM_GROUP_NORM_CALL(G, K)                                                                              \
+  hipLaunchKernelGGL((group_norm_row_bwd_kernel<T, G, K, kGated>), dim3((unsigned)p.bwd_blocks), threads, 0, st, a)
+    SSM_GROUP_NORM_GEOMETRY(SSM_GROUP_NORM_CALL)
+#undef SSM_GROUP_NORM_CALL
+    if (a.part)
+      hipLaunchKernelGGL(group_norm_columns_kernel, dim3((unsigned)((2 * a.channels + 31) / 32)), dim3(1024), 0, st,
+                         a.part, dweight, dbias, p.stride, a.channels);
+    return hipGetLastError();
+  }
+  const dim3 grid((unsigned)(a.batch * p.runs));
+  hipLaunchKernelGGL((group_norm_map_sums_kernel<T, kGated>), grid, threads, 0, st, a);
+  hipLaunchKernelGGL(group_norm_map_reduce_kernel, dim3((unsigned)a.groups), threads, 0, st, a, dweight, dbias);
+  hipLaunchKernelGGL((group_norm_map_bwd_kernel<T, kGated>), grid, threads, 0, st, a);
+  return hipGetLastError();
+}
+
+Args make_args(int64_t batch, int64_t length, int64_t channels, int64_t groups, const Plan& p, ssm_norm_t kind,
+               ssm_act_t act) {
+  Args a = {};
+  a.batch = batch;
+  a.length = length;
+  a.channels = channels;
+  a.groups = (int)groups;
+  a.d = (int)(channels / groups);
+  a.rms = kind == SSM_NORM_RMS;
+  a.silu = act == SSM_ACT_SILU;
+  a.runs = (int)p.runs;
+  a.run = p.run;
+  a.stride = p.stride;
+  return a;
+}
+
+bool options_ok(ssm_norm_t kind, ssm_act_t act) {
+  return (kind == SSM_NORM_LAYER || kind == SSM_NORM_RMS) && (act == SSM_ACT_NONE || act == SSM_ACT_SILU);
+}
+
+}  // namespace
+
+// ----------------------------------------------------------------------------
+// C ABI
+// ----------------------------------------------------------------------------
+
+extern "C" {
+
+ssm_status_t ssm_group_norm_fwd_workspace_bytes(int64_t batch, int64_t length, int64_t channels, int64_t groups,
+                                                ssm_dtype_t io, int64_t* bytes) {
+  int64_t n;
+  const ssm_status_t st = check_shape(batch, length, channels, groups, io, &n);
+  if (st == SSM_OK && bytes) *bytes = fwd_bytes(make_plan(batch, length, channels, groups), batch, groups);
+  return st;
+}
+
+ssm_status_t ssm_group_norm_fwd(int64_t batch, int64_t length, int64_t channels, int64_t groups, ssm_dtype_t io,
+                                ssm_norm_t kind, ssm_act_t act, const void* x, const void* z, const float* weight,
+                                const float* bias, float eps, void* y, float* mean, float* rstd, void* workspace,
+                                int64_t workspace_bytes, struct ihipStream_t* stream) {
+  int64_t n;
+  ssm_status_t st = check_shape(batch, length, channels, groups, io, &n);
+  if (st != SSM_OK) return st;
+  if (!options_ok(kind, act)) return SSM_ERR_UNSUPPORTED;
+  if (!x || !y) return SSM_ERR_NULL;
+  if (kind == SSM_NORM_RMS) mean = nullptr;
+  const Plan p = make_plan(batch, length, channels, groups);
+  const int64_t need = fwd_bytes(p, batch, groups), rows = batch * groups;
+  if (workspace_bytes < need) return SSM_ERR_WORKSPACE;
+  if (need && !workspace) return SSM_ERR_NULL;
+  if (!need) workspace = nullptr;
+  const size_t es = io_size(io);
+  const Buf ins[] = {{x, n * (int64_t)es, es}, {z, n * (int64_t)es, es}, {weight, channels * 4, 4}, {bias, channels * 4, 4}};
+  const Buf outs[] = {{y, n * (int64_t)es, es}, {mean, rows * 4, 4}, {rstd, rows * 4, 4}, {workspace, need, 4}};
+  st = check_buffers(ins, 4, outs, 4);
+  if (st != SSM_OK) return st;
+  Args a = make_args(batch, length, channels, groups, p, kind, act);
+  a.x = x; a.z = z; a.weight = weight; a.bias = bias; a.eps = eps; a.y = y;
+  a.mean = mean; a.rstd = rstd;
+  a.part = static_cast<float*>(workspace);
+  if (p.map) {
+    float* stats = a.part + batch * p.runs * 2 * groups;
+    if (!a.mean) a.mean = stats;
+    if (!a.rstd) a.rstd = stats + rows;
+  }
+  hipStream_t hs = reinterpret_cast<hipStream_t>(stream);
+  hipError_t e;
+  if (io == SSM_F32)
+    e = z ? launch_fwd<float, true>(a, p, hs) : launch_fwd<float, false>(a, p, hs);
+  else
+    e = z ? launch_fwd<bf16_t, true>(a, p, hs) : launch_fwd<bf16_t, false>(a, p, hs);
+  return e == hipSuccess ? SSM_OK : hip_fail(e);
+}
+
+ssm_status_t ssm_group_norm_bwd_workspace_bytes(int64_t batch, int64_t length, int64_t channels, int64_t groups,
+                                                ssm_dtype_t io, int64_t* bytes) {
+  int64_t n;
+  const ssm_status_t st = check_shape(batch, length, channels, groups, io, &n);
+  if (st == SSM_OK && bytes) *bytes = bwd_bytes(make_plan(batch, length, channels, groups), batch, channels, groups, true);
+  return st;
+}
+
+ssm_status_t ssm_group_norm_bwd(int64_t batch, int64_t length, int64_t channels, int64_t groups, ssm_dtype_t io,
+                                ssm_norm_t kind, ssm_act_t act, const void* dy, const void* x, const void* z,
+                                const float* weight, const float* bias, const float* mean, const float* rstd, void* dx,
+                                void* dz, float* dweight, float* dbias, void* workspace, int64_t workspace_bytes,
+                                struct ihipStream_t* stream) {
+  int64_t n;
+  ssm_status_t st = check_shape(batch, length, channels, groups, io, &n);
+  if (st != SSM_OK) return st;
+  if (!options_ok(kind, act)) return SSM_ERR_UNSUPPORTED;
+  if (!dy || !x || !rstd || !dx || (kind == SSM_NORM_LAYER && !mean)) return SSM_ERR_NULL;
+  if (kind == SSM_NORM_RMS) mean = nullptr;
+  if (!z) dz = nullptr;
+  const Plan p = make_plan(batch, length, channels, groups);
+  const int64_t need = bwd_bytes(p, batch, channels, groups, dweight || dbias), rows = batch * groups;
+  if (workspace_bytes < need) return SSM_ERR_WORKSPACE;
+  if (need && !workspace) return SSM_ERR_NULL;
+  if (!need) workspace = nullptr;
+  const size_t es = io_size(io);
+  const int64_t bytes = n * (int64_t)es;
+  const Buf ins[] = {{dy, bytes, es}, {x, bytes, es}, {z, bytes, es}, {weight, channels * 4, 4}, {bias, channels * 4, 4},
+                     {mean, rows * 4, 4}, {rstd, rows * 4, 4}};
+  const Buf outs[] = {{dx, bytes, es}, {dz, bytes, es}, {dweight, channels * 4, 4}, {dbias, channels * 4, 4},
+                      {workspace, need, 4}};
+  st = check_buffers(ins, 7, outs, 5);
+  if (st != SSM_OK) return st;
+  Args a = make_args(batch, length, channels, groups, p, kind, act);
+  a.dy = dy; a.x = x; a.z = z; a.weight = weight; a.bias = bias;
+  a.mean = const_cast<float*>(mean); a.rstd = const_cast<float*>(rstd);
+  a.dx = dx; a.dz = dz;
+  a.part = static_cast<float*>(workspace);
+  a.sums = p.map ? a.part + batch * p.runs * 2 * channels : nullptr;
+  hipStream_t hs = reinterpret_cast<hipStream_t>(stream);
+  hipError_t e;
+  if (io == SSM_F32)
+    e = z ? launch_bwd<float, true>(a, p, dweight, dbias, hs) : launch_bwd<float, false>(a, p, dweight, dbias, hs);
+  else
+    e = z ? launch_bwd<bf16_t, true>(a, p, dweight, dbias, hs) : launch_bwd<bf16_t, false>(a, p, dweight, dbias, hs);
+  return e == hipSuccess ? SSM_OK : hip_fail(e);
+}
+
+}  // extern "C"
