@@ -38,6 +38,7 @@ struct Role {
   float* dots;           // [v.d / 32 rounded up][batch, heads, seqlen]
   float* part;           // state passes: a segment's own state, [batch, heads, segments][k.d][v.d]
   float* total;          // and its decay, [batch, heads, segments]
+  int dma;               // rows are whole 16-byte units at 16-byte addresses
   int tiles;             // blocks side by side along v.d
   int64_t first_block;   // of the launch that is this role's
 };

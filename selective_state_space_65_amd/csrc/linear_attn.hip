@@ -49,7 +49,7 @@ __global__ __launch_bounds__(256) void linear_attn_join_kernel(float* part, cons
     float x[8];
 #pragma unroll
     for (int u = 0; u < 8; ++u) {
-      const int j = min(j0 + u, segments - 1);
+      const int j = min(j0 + u, segments - 2);  // the last segment's own state is not wanted
       x[u] = at[(reverse ? segments - 1 - j : j) * n];
     }
 #pragma unroll
@@ -57,6 +57,7 @@ __global__ __launch_bounds__(256) void linear_attn_join_kernel(float* part, cons
       if (j0 + u >= segments) break;
       const int j = reverse ? segments - 1 - (j0 + u) : j0 + u;
       at[j * n] = s;
+      if (j0 + u == segments - 1) break;
       const float d = decay[j];
       s = (d == 0.0f ? 0.0f : s * d) + x[u];
     }
@@ -268,16 +269,19 @@ struct Split {
   int64_t per, count;  // blocks of kBlock tokens in a segment, segments
 };
 
-Split split_tokens(const Sizes& s, int64_t blocks_each) {
+int64_t waves(int64_t dv) { return tiles(dv) * linattn::tile_width((int)dv) / 32; }
+
+// Segments: as many as give the chip's 1024 SIMDs two waves each.
+Split split_tokens(const Sizes& s, int64_t waves_each) {
   Split p{s.blocks(), 1};
-  const int64_t wanted = blocks_each < 256 ? (512 + blocks_each - 1) / blocks_each : 1;
+  const int64_t wanted = waves_each < 1024 ? (2048 + waves_each - 1) / waves_each : 1;
   p.per = std::max<int64_t>(1, p.per / wanted);
   p.count = (s.blocks() + p.per - 1) / p.per;
   return p;
 }
 
-Split fwd_split(const Sizes& s) { return split_tokens(s, s.rows() * tiles(s.dv)); }
-Split bwd_split(const Sizes& s) { return split_tokens(s, s.rows() * (2 * tiles(s.dk) + tiles(s.dv))); }
+Split fwd_split(const Sizes& s) { return split_tokens(s, s.rows() * waves(s.dv)); }
+Split bwd_split(const Sizes& s) { return split_tokens(s, s.rows() * std::min(2 * waves(s.dk), waves(s.dv))); }
 
 // Segments' states and decays.
 int64_t segment_bytes(const Sizes& s, const Split& p) { return p.count > 1 ? s.rows() * p.count * (s.state() + 1) * 4 : 0; }
@@ -306,7 +310,14 @@ BwdSpace bwd_space(const Sizes& s, bool decays) {
   return w;
 }
 
-hipError_t launch_pass(const Args& a, int64_t blocks, bool state_only, bool exact, ssm_dtype_t io, hipStream_t st) {
+bool whole_units(const Side& s, size_t es) { return s.d * es % 16 == 0 && aligned(s.p, 16); }
+
+hipError_t launch_pass(Args a, int64_t blocks, bool state_only, bool exact, ssm_dtype_t io, hipStream_t st) {
+  const size_t es = io_size(io);
+  for (int i = 0; i < a.roles; ++i) {
+    Role& r = a.role[i];
+    r.dma = whole_units(r.q, es) && whole_units(r.k, es) && whole_units(r.v, es);
+  }
   return io == SSM_BF16 ? linattn::launch_bf16(a, blocks, state_only, exact, st)
                         : linattn::launch_f32(a, blocks, state_only, exact, st);
 }
@@ -333,7 +344,7 @@ hipError_t segment_states(Args a, Role role, const Sizes& s, const float* first,
   role.first_block = 0;
   a.role[0] = role;
   a.roles = 1;
-  const hipError_t e = launch_pass(a, s.rows() * a.segments * role.tiles, true, false, io, st);
+  const hipError_t e = launch_pass(a, s.rows() * (a.segments - 1) * role.tiles, true, false, io, st);
   if (e != hipSuccess) return e;
   const int64_t n = s.state();
   hipLaunchKernelGGL(linear_attn_join_kernel, dim3((unsigned)((n + 255) / 256), (unsigned)s.rows()), dim3(256), 0, st,

@@ -12,13 +12,15 @@
 //
 // A block owns one (batch, head), one segment of the tokens and a tile of v's
 // columns; each of its waves owns 32 columns, with their whole state (k.d rows)
-// in its accumulators.  All four products run on 32 x 32 MFMA tiles:
-//   scores  k q^T, quarters of the chunk by turns; scaled, stored to LDS
-//   q . S   S as it lies in the accumulators: the rows of the update's left
-//           operand are permuted so that a lane's 8 consecutive accumulators
-//           are 8 consecutive rows of S, which is an MFMA operand
-//   scores . v
+// in its accumulators.  All four products run on MFMA tiles:
+//   scores      k q^T, 16 x 16 tiles of the chunk by turns; scaled, stored to LDS
+//   S^T q^T     S as it lies in the accumulators: the rows of the update's left
+//               operand are permuted so that a lane's 8 consecutive accumulators
+//               are 8 consecutive rows of S, which is an MFMA operand
+//   v^T scores^T  on the same accumulators: a lane has one token's outputs
 //   the update, whose v are scaled in registers.
+// The last three are 32 x 32 tiles: an operand read from LDS feeds twice the
+// products of a 16 x 16 one, which the LDS could not keep up with.
 // q, k and v tiles are stored as they come (rows of a token); operands that run
 // along the tokens are read with the transposing LDS loads (bf16) or by
 // single words (fp32).  16-byte units of a tile's rows are permuted by the row so
@@ -49,6 +51,7 @@ using linattn::Side;
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef short i16x4 __attribute__((ext_vector_type(4)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 // 8 values of one row (or column) of an MFMA operand, consecutive along the
@@ -66,9 +69,19 @@ struct Frag<float> {
   float v[8];
 };
 
-// acc[row][col] += sum over 16 values; lanes 0-31 hold values 0-7 of row (col)
-// lane, lanes 32-63 values 8-15.  acc element i of a lane: column lane % 32, row
-// 8 (i / 4) + 4 (lane / 32) + i % 4.
+// acc[row][col] += sum over 32 values; lane has values 8 (lane / 16) .. + 7 of row
+// (col) lane % 16.  acc element i of a lane: column lane % 16, row 4 (lane / 16) + i.
+// 32 x 32 tiles, 16 values: values 8 (lane / 32) .. + 7 of row (col) lane % 32; element i
+// is column lane % 32, row 8 (i / 4) + 4 (lane / 32) + i % 4.
+__device__ __forceinline__ void mma(f32x4& acc, const Frag<bf16_t>& a, const Frag<bf16_t>& b) {
+  acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.v, b.v, acc, 0, 0, 0);
+}
+
+__device__ __forceinline__ void mma(f32x4& acc, const Frag<float>& a, const Frag<float>& b) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) acc = __builtin_amdgcn_mfma_f32_16x16x4f32(a.v[j], b.v[j], acc, 0, 0, 0);
+}
+
 __device__ __forceinline__ void mma(f32x16& acc, const Frag<bf16_t>& a, const Frag<bf16_t>& b) {
   acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a.v, b.v, acc, 0, 0, 0);
 }
@@ -78,18 +91,32 @@ __device__ __forceinline__ void mma(f32x16& acc, const Frag<float>& a, const Fra
   for (int j = 0; j < 8; ++j) acc = __builtin_amdgcn_mfma_f32_32x32x2f32(a.v[j], b.v[j], acc, 0, 0, 0);
 }
 
-// 8 floats as kParts operands that sum to them (fp32: one, exact).
+// The upper halves of two words, side by side.
+__device__ __forceinline__ uint32_t upper_halves(uint32_t lo, uint32_t hi) {
+  return __builtin_amdgcn_perm(hi, lo, 0x07060302);
+}
+
+// 8 floats as kParts bf16 operands: one, rounded to nearest; or several, each
+// the upper half of what the ones before left over, so that three hold every bit.
 template <int kParts>
 __device__ __forceinline__ void split(Frag<bf16_t>* f, const float x[8]) {
-  float r[8];
+  if constexpr (kParts == 1) {
 #pragma unroll
-  for (int j = 0; j < 8; ++j) r[j] = x[j];
+    for (int j = 0; j < 8; ++j) f[0].v[j] = (__bf16)x[j];
+  } else {
+    float r[8];
 #pragma unroll
-  for (int p = 0; p < kParts; ++p) {
+    for (int j = 0; j < 8; ++j) r[j] = x[j];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      f[p].v[j] = (__bf16)r[j];
-      if (p + 1 < kParts) r[j] -= (float)f[p].v[j];
+    for (int p = 0; p < kParts; ++p) {
+      words4 w;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) w[j] = upper_halves(__float_as_uint(r[2 * j]), __float_as_uint(r[2 * j + 1]));
+      f[p].v = __builtin_bit_cast(bf16x8, w);
+      if (p + 1 < kParts) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) r[j] -= __uint_as_float(__float_as_uint(r[j]) & 0xffff0000u);
+      }
     }
   }
 }
@@ -114,22 +141,24 @@ struct Traits<float> {
 };
 
 // A tile of rows of COLS elements in LDS.  Unit u (16 bytes) of row r lies at
-// u ^ key(r): the 16 rows of a row read's pass, and the 4 rows x 4 units of a
-// transposing read's, then fall on different banks.
+// u ^ key(r).  The key puts the 16 rows of one unit, which a row read takes at
+// once, on different banks; and of a column read the 4 rows x 4 units of 32 lanes
+// (bf16), or the two rows 8 apart (fp32).
 template <typename T, int COLS>
 struct Tile {
-  static constexpr int kUnits = COLS * (int)sizeof(T) / 16;
-  static constexpr int kPerUnit = 16 / (int)sizeof(T);
-  static __device__ __forceinline__ int key(int r) {
-    if constexpr (kUnits >= 16) return (r & 3) << 2 | (r >> 2 & 3);
+  static constexpr unsigned kUnits = COLS * sizeof(T) / 16;
+  static constexpr unsigned kPerUnit = 16 / sizeof(T);
+  static __device__ __forceinline__ unsigned key(unsigned r) {
+    if constexpr (kUnits >= 16 && sizeof(T) == 2) return (r & 3) << 2 | (r >> 2 & 3);
+    if constexpr (kUnits >= 16) return r & 15;
     if constexpr (kUnits == 8) return (r >> 1 & 1) << 2 | (r >> 2 & 3);
     return r >> 2 & 3;
   }
-  static __device__ __forceinline__ int at(int r, int c) {  // element offset
+  static __device__ __forceinline__ unsigned at(unsigned r, unsigned c) {  // element offset
     return (r * kUnits + (c / kPerUnit ^ key(r))) * kPerUnit + c % kPerUnit;
   }
   // Values c .. c + 7 of row r; c is a multiple of 8.
-  static __device__ __forceinline__ Frag<T> row(const T* p, int r, int c) {
+  static __device__ __forceinline__ Frag<T> row(const T* p, unsigned r, unsigned c) {
     Frag<T> f;
     if constexpr (sizeof(T) == 2) {
       f.v = *reinterpret_cast<const bf16x8*>(p + at(r, c));
@@ -144,21 +173,21 @@ struct Tile {
   // Rows r .. r + 7 (r differs between the wave's halves) of the lane's column:
   // c + lane % 32, or with kSwap that number with bits 2 and 3 exchanged.
   template <bool kSwap>
-  static __device__ __forceinline__ Frag<T> column(const T* p, int r, int c, int lane) {
+  static __device__ __forceinline__ Frag<T> column(const T* p, unsigned r, unsigned c, unsigned lane) {
     Frag<T> f;
     if constexpr (sizeof(T) == 2) {
       // Lane 4 j + i of 16 gives the address of row j's columns 4 i .. 4 i + 3 and
-      // gets column 4 i + j of the four rows.
-      const int i = lane & 3, q = kSwap ? (i & 1) << 1 | i >> 1 : i;
-      const int col = c + (lane & 16) + 4 * q, row0 = r + (lane >> 2 & 3);
+      // gets column 4 j + i of the four rows (the load transposes).
+      const unsigned i = lane & 3, q = kSwap ? (i & 1) << 1 | i >> 1 : i;
+      const unsigned col = c + (lane & 16) + 4 * q, row0 = r + (lane >> 2 & 3);
       typedef __attribute__((address_space(3))) i16x4* lds_ptr;
       const i16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(p + at(row0, col)));
       const i16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(p + at(row0 + 4, col)));
       f.v = __builtin_bit_cast(bf16x8, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
     } else {
-      const int i = lane & 31, q = kSwap ? (i & 19) | (i & 4) << 1 | (i & 8) >> 1 : i;
+      const unsigned i = lane & 31, q = kSwap ? (i & 19) | (i & 4) << 1 | (i & 8) >> 1 : i;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) f.v[j] = p[at(r + j, c + q)];
+      for (unsigned j = 0; j < 8; ++j) f.v[j] = p[at(r + j, c + q)];
     }
     return f;
   }
@@ -180,7 +209,7 @@ __device__ __forceinline__ void get8(const Frag<float>& f, float out[8]) {
 // What a chunk's decays give.
 template <int C>
 struct Decays {
-  double sum[C];     // G
+  double sum[C];     // G (reverse: -G)
   float in[C];       // factor of q_t . S
   float up[C];       // factor of k_s v_s^T in the update
   float each[C];     // a_t, 0 where the state is dropped
@@ -222,7 +251,7 @@ __device__ __forceinline__ void chunk_decays(Decays<C>* d, float rate, float ste
   const bool slow = __any(bad && lane < len);
   const bool zeros = __any(up == 0.0f && lane < len);
   if (lane < C) {
-    d->sum[lane] = sum;
+    d->sum[lane] = p.reverse ? -sum : sum;
     d->in[lane] = p.s_in * (p.reverse ? to_end : from_start);
     d->up[lane] = up;
     d->each[lane] = exp2_hw((float)g);
@@ -234,64 +263,13 @@ __device__ __forceinline__ void chunk_decays(Decays<C>* d, float rate, float ste
   }
 }
 
-// A wave's LDS writes before it are seen by its own reads after it.
-__device__ __forceinline__ void wave_lds_fence() {
-  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
-  __builtin_amdgcn_wave_barrier();
-  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront", "local");
-}
+// a b, and 0 where a factor is 0 whatever the other is.
+extern "C" __device__ float ssmi_mul_legacy(float a, float b) __asm("llvm.amdgcn.fmul.legacy");
+__device__ __forceinline__ float drop_mul(float a, float b) { return ssmi_mul_legacy(a, b); }
 
-// Rows of one operand of a chunk on their way from memory to LDS: pieces of 8
-// elements, requested a chunk ahead.
-template <typename T, int COLS, int C, int kThreads>
-struct Stage {
-  using Lds = Tile<T, COLS>;
-  static constexpr int kPieces = C * COLS / 8;
-  static constexpr int kEach = (kPieces + kThreads - 1) / kThreads;
-  Raw8<T> r[kEach];
-  // base: the chunk's first row; n elements of each row are there, len rows.
-  // Rows of less than 8 are left to elements().
-  __device__ __forceinline__ void request(const T* base, uint32_t stride, int n, int len, int tid) {
-    if (n < 8) return;
-#pragma unroll
-    for (int i = 0; i < kEach; ++i) {
-      const int p = min(tid + i * kThreads, kPieces - 1);
-      const uint32_t row = min(p / (COLS / 8), len - 1) * stride;
-      r[i].template load<false>(base + (row + (uint32_t)min(p % (COLS / 8) * 8, n - 8)));
-    }
-  }
-  __device__ __forceinline__ void store(T* tile, const T* base, uint32_t stride, int n, int len, int tid) {
-    if (n < 8) {
-      elements(tile, base, stride, n, len);
-      return;
-    }
-#pragma unroll
-    for (int i = 0; i < kEach; ++i) {
-      const int p = tid + i * kThreads;
-      const int row = p / (COLS / 8), c = p % (COLS / 8) * 8;
-      if (kPieces % kThreads == 0 || p < kPieces) {
-        if (row < len)
-          finish8<false>(r[i], c, 0, n);
-        else
-          r[i].clear();
-        if constexpr (sizeof(T) == 2) {
-          *reinterpret_cast<words4*>(tile + Lds::at(row, c)) = r[i].w;
-        } else {
-          *reinterpret_cast<words4*>(tile + Lds::at(row, c)) = r[i].lo;
-          *reinterpret_cast<words4*>(tile + Lds::at(row, c + 4)) = r[i].hi;
-        }
-      }
-    }
-  }
-  // The same, one element at a time and not requested before.
-  static __device__ __forceinline__ void elements(T* tile, const T* base, uint32_t stride, int n, int len) {
-#pragma unroll 1
-    for (int i = threadIdx.x; i < C * COLS; i += kThreads) {
-      const int row = i / COLS, c = i % COLS;
-      tile[Lds::at(row, c)] = row < len && c < n ? base[row * stride + c] : T(0);
-    }
-  }
-};
+// A condition that hardly ever holds: registers are not spilled elsewhere for
+// what it guards.
+__device__ __forceinline__ bool rare(bool c) { return __builtin_expect(c, 0); }
 
 // v, unknown to the compiler: what is computed from it stays where it is used.
 // Else every LDS address of the chunk loop is computed before it and kept, in
@@ -301,19 +279,162 @@ __device__ __forceinline__ int opaque(int v) {
   return v;
 }
 
+constexpr int kWaitVmcnt0 = 0x0F70;  // s_waitcnt vmcnt(0) expcnt(7) lgkmcnt(15): vector memory only
+
+// Rows of one operand of a chunk on their way from memory to LDS: straight there
+// (dma), a chunk ahead, where rows are whole 16-byte units; else in pieces of 8
+// elements through registers.
+template <typename T, int COLS, int C, int kThreads>
+struct Stage {
+  using Lds = Tile<T, COLS>;
+  static constexpr unsigned kPieces = C * COLS / 8;
+  // base: the chunk's first row; n elements of each row are there, len rows.  A
+  // piece that ends behind its row is read as the row's last 8 elements, shifted.
+  static __device__ __forceinline__ void pieces(T* tile, const T* base, uint32_t stride, int n, int len, unsigned tid) {
+    if (n < 8) {
+      elements(tile, base, stride, n, len);
+      return;
+    }
+    constexpr int kAhead = 4;  // in flight at once
+#pragma unroll 1
+    for (unsigned p0 = tid; p0 < kPieces; p0 += kAhead * kThreads) {
+      Raw8<T> r[kAhead];
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        const unsigned p = min(p0 + i * kThreads, kPieces - 1), row = p / (COLS / 8), c = p % (COLS / 8) * 8;
+        r[i].template load<false>(base + (min((int)row, len - 1) * stride + (uint32_t)min((int)c, n - 8)));
+      }
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        const unsigned p = p0 + i * kThreads, row = p / (COLS / 8), c = p % (COLS / 8) * 8;
+        if (p >= kPieces) break;
+        if (n % 8) finish8<false>(r[i], (int)c, 0, n);
+        if ((int)row >= len || (int)c >= n) r[i].clear();
+        if constexpr (sizeof(T) == 2) {
+          *reinterpret_cast<words4*>(tile + Lds::at(row, c)) = r[i].w;
+        } else {
+          *reinterpret_cast<words4*>(tile + Lds::at(row, c)) = r[i].lo;
+          *reinterpret_cast<words4*>(tile + Lds::at(row, c + 4)) = r[i].hi;
+        }
+      }
+    }
+  }
+  // Straight to LDS: an instruction fills 64 units of the tile, lane by lane, so a
+  // lane requests the unit that its place holds.  Units behind the row's end and
+  // rows behind the last are not requested: the caller keeps those 0.
+  static constexpr int kFills = C * (int)Lds::kUnits / 64, kWaves = kThreads / 64;
+  static constexpr int kEach = (kFills + kWaves - 1) / kWaves;
+  static constexpr uint32_t kNone = ~0u;
+  // Bytes from a chunk's first row to what a lane requests, kNone behind the row's end.
+  static __device__ __forceinline__ void offsets(uint32_t from[kEach], uint32_t stride, int n, int wave, unsigned lane) {
+    const unsigned place = wave * 64 + lane;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      const unsigned r = place / Lds::kUnits + i * (kWaves * 64 / Lds::kUnits), u = place % Lds::kUnits ^ Lds::key(r);
+      from[i] = (int)(u * Lds::kPerUnit) < n ? (r * stride + u * Lds::kPerUnit) * (uint32_t)sizeof(T) : kNone;
+    }
+  }
+  static __device__ __forceinline__ void dma(T* tile, const T* base, const uint32_t from[kEach], int n, int len, int wave,
+                                             unsigned lane) {
+    const uint32_t to = __builtin_amdgcn_readfirstlane(
+        (uint32_t)(uintptr_t)(__attribute__((address_space(3))) T*)tile + wave * 1024);
+    if (!rare(len < C || n < COLS)) {
+#pragma unroll
+      for (int i = 0; i < kEach; ++i) {
+        if (kFills % kWaves && wave + i * kWaves >= kFills) break;
+        fill(to + i * kWaves * 1024, base, from[i]);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < kEach; ++i) {
+        if (kFills % kWaves && wave + i * kWaves >= kFills) break;
+        const int r = ((wave + i * kWaves) * 64 + lane) / Lds::kUnits;
+        if (r < len && from[i] != kNone) fill(to + i * kWaves * 1024, base, from[i]);
+      }
+    }
+  }
+  // The compiler does not see this load, so it waits for none of them before LDS
+  // reads of other tiles; the chunk loop waits for all of them itself.
+  static __device__ __forceinline__ void fill(uint32_t to, const T* base, uint32_t from) {
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(from), "s"(base), "s"(to)
+                 : "memory", "m0");
+  }
+  // Zeros in rows from first on.
+  static __device__ __forceinline__ void clear(T* tile, int first, unsigned tid) {
+#pragma unroll 1
+    for (unsigned i = first * Lds::kUnits + tid; i < C * Lds::kUnits; i += kThreads)
+      reinterpret_cast<words4*>(tile)[i] = words4{0, 0, 0, 0};
+  }
+  // The same, one element at a time and not requested before.
+  static __device__ __forceinline__ void elements(T* tile, const T* base, uint32_t stride, int n, int len) {
+#pragma unroll 1
+    for (unsigned i = threadIdx.x; i < C * COLS; i += kThreads) {
+      const unsigned row = i / COLS, c = i % COLS;
+      tile[Lds::at(row, c)] = (int)row < len && (int)c < n ? base[row * stride + c] : T(0);
+    }
+  }
+};
+
 // First row of a side for this batch row and head.
 template <typename T>
 __device__ __forceinline__ const T* side_rows(const Side& s, int64_t batch_tokens, int head) {
   return static_cast<const T*>(s.p) + (batch_tokens * s.heads + head / s.share) * s.d;
 }
 
+// A row's columns c + 8 g .. c + 8 g + 3, g = 0 .. 3: written from, and dotted with,
+// a lane's elements of a 32 x 32 accumulator.  Columns from n on are not there.
+template <bool kWhole, typename T>
+__device__ __forceinline__ void store_columns(T* base, uint32_t row, int c, int n, const f32x16& v) {
+#pragma unroll
+  for (int g = 0; g < 4; ++g) {
+    const int at = c + 8 * g;
+    if (kWhole || at + 4 <= n) {
+      const float x[4] = {v[4 * g], v[4 * g + 1], v[4 * g + 2], v[4 * g + 3]};
+      store_n<4>(base + (row + at), x);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 3; ++j)
+        if (at + j < n) Io<T>::store1(base + (row + at + j), v[4 * g + j]);
+    }
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ float dot_columns(const T* row, int c, int n, const f32x16& v) {
+  float t = 0.0f;
+#pragma unroll
+  for (int g = 0; g < 4; ++g) {
+    const int at = c + 8 * g;
+    if (!rare(at + 4 > n)) {
+      float x[4];
+      load_n<4>(row + at, x);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) t = __builtin_fmaf(x[j], v[4 * g + j], t);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 3; ++j)
+        if (at + j < n) t = __builtin_fmaf(Io<T>::load1(row + at + j), v[4 * g + j], t);
+    }
+  }
+  return t;
+}
+
 template <typename T, int NK, int NW, int kParts, bool kOut>
 struct Layout {
   static constexpr int C = Traits<T>::chunk, DK = 32 * NK, TV = 32 * NW;
-  static constexpr int q_bytes = !kOut ? 0 : C * DK * (int)sizeof(T) > NW * 4096 ? C * DK * (int)sizeof(T) : NW * 4096;
+  static constexpr int q_bytes = kOut ? C * DK * (int)sizeof(T) : 0;
   static constexpr int k_bytes = C * DK * (int)sizeof(T), v_bytes = C * TV * (int)sizeof(T);
   static constexpr int s_bytes = kOut ? kParts * C * C * (int)sizeof(T) : 0;
-  static constexpr int bytes = q_bytes + k_bytes + v_bytes + s_bytes + 3 * (int)sizeof(Decays<C>) + 8;
+  // q's and v's tiles are free for the next chunk's once every wave has its scores and
+  // its operands of v; k's is read to the chunk's end and needs a second one for
+  // that (so does v's where there are no scores), if the LDS still holds two
+  // blocks, or if it would not hold two without.
+  static constexpr int v_tiles = kOut ? 1 : 2;
+  static constexpr int rest = q_bytes + v_tiles * v_bytes + s_bytes + 3 * (int)sizeof(Decays<C>) + 16;
+  static constexpr int kHalf = 80 * 1024;
+  static constexpr int k_tiles =
+      rest + 2 * k_bytes <= kHalf || (rest + k_bytes > kHalf && rest + 2 * k_bytes <= 2 * kHalf) ? 2 : 1;
+  static constexpr int bytes = rest + k_tiles * k_bytes;
 };
 
 // kOut: false computes the states alone (a segment's own, and its decay).
@@ -325,18 +446,16 @@ __global__ __launch_bounds__(64 * NW, NK <= 4 ? 2 : 1) void linear_attn_kernel(c
   using TileK = Tile<T, DK>;
   using TileV = Tile<T, TV>;
   using TileS = Tile<T, C>;
-  using TileO = Tile<float, 32>;
   __shared__ __align__(16) unsigned char lds[L::bytes];
   T* const qs = reinterpret_cast<T*>(lds);
-  T* const ks = reinterpret_cast<T*>(lds + L::q_bytes);
-  T* const vs = reinterpret_cast<T*>(lds + L::q_bytes + L::k_bytes);
-  T* const ss = reinterpret_cast<T*>(lds + L::q_bytes + L::k_bytes + L::v_bytes);
+  T* const k_base = reinterpret_cast<T*>(lds + L::q_bytes);
+  T* const v_base = reinterpret_cast<T*>(lds + L::q_bytes + L::k_tiles * L::k_bytes);
+  T* const ss = reinterpret_cast<T*>(lds + L::q_bytes + L::k_tiles * L::k_bytes + L::v_tiles * L::v_bytes);
   Decays<C>* const decays =
-      reinterpret_cast<Decays<C>*>(lds + L::q_bytes + L::k_bytes + L::v_bytes + L::s_bytes);
-  int* const again = reinterpret_cast<int*>(decays + 3);  // of chunk c in [c & 1]: some wave's outputs are not finite
-  const int thread = threadIdx.x, tid = thread, lane = tid & 63, col = lane & 31, half = lane >> 5;
+      reinterpret_cast<Decays<C>*>(lds + L::q_bytes + L::k_tiles * L::k_bytes + L::v_tiles * L::v_bytes + L::s_bytes);
+  int* const again = reinterpret_cast<int*>(decays + 3);  // of chunk c in [c & 3]: some wave's outputs are not finite
+  const int thread = threadIdx.x, tid = thread, lane = tid & 63, lane0 = lane, col = lane & 31, half = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  float* const out_tile = reinterpret_cast<float*>(lds) + wave * 1024;  // q's space, when q is no longer read
 
   // ---- which rows, segment and columns this block has
   int r = 0;
@@ -345,8 +464,10 @@ __global__ __launch_bounds__(64 * NW, NK <= 4 ? 2 : 1) void linear_attn_kernel(c
   const int64_t index = (int64_t)blockIdx.x - p.first_block;
   const int tile = (int)(index % p.tiles);
   const int64_t rest = index / p.tiles;
-  const int segment = (int)(rest % a.segments);
-  const int64_t row = rest / a.segments;  // (batch, head)
+  // State passes leave out the segment that no other starts behind.
+  const int parts = kOut ? a.segments : a.segments - 1;
+  const int segment = (int)(rest % parts) + (!kOut && p.reverse ? 1 : 0);
+  const int64_t row = rest / parts;  // (batch, head)
   const int head = (int)(row % a.heads);
   const int64_t batch_tokens = row / a.heads * a.seqlen;
   const bool reverse = p.reverse;
@@ -361,22 +482,20 @@ __global__ __launch_bounds__(64 * NW, NK <= 4 ? 2 : 1) void linear_attn_kernel(c
   const T* const k_rows = side_rows<T>(p.k, batch_tokens, head);
   const T* const v_rows = side_rows<T>(p.v, batch_tokens, head) + v0;
   // A chunk's rows are addressed by 32-bit offsets from its first (heads are limited so).
-  const uint32_t q_stride = kOut ? p.q.heads * dk : 0, k_stride = p.k.heads * dk, v_stride = p.v.heads * dv;
+  const uint32_t k_stride = p.k.heads * dk, v_stride = p.v.heads * dv;  // q's rows lie as k's do
 
   // ---- the state: acc[b][i] is row 32 b + 16 (i / 8) + 8 half + i % 8, column vc
   f32x16 acc[NK];
   const int64_t state_size = (int64_t)dk * dv;
-  const auto state_row = [&](int b, int i) { return 32 * b + 16 * (i >> 3) + 8 * half + (i & 7); };
   {
     const float* from = kOut && p.start ? p.start + (row * p.start_slots + segment * p.start_step) * state_size : nullptr;
+    const int64_t k_step = p.transposed ? 1 : dv, at = p.transposed ? (int64_t)vc * dk : vc;
 #pragma unroll
     for (int b = 0; b < NK; ++b)
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
-        const int k = state_row(b, i);
-        float x = 0.0f;
-        if (from && k < dk && vc < dv) x = from[p.transposed ? (int64_t)vc * dk + k : (int64_t)k * dv + vc];
-        acc[b][i] = x;
+        const int k = 32 * b + 16 * (i >> 3) + (i & 7) + 8 * half;
+        acc[b][i] = from && k < dk && vc < dv ? from[at + k * k_step] : 0.0f;
       }
   }
   const auto store_state = [&](float* to) {  // states that are written are never transposed
@@ -391,17 +510,32 @@ __global__ __launch_bounds__(64 * NW, NK <= 4 ? 2 : 1) void linear_attn_kernel(c
       }
   };
 
-  // ---- requests, a chunk ahead; decays, computed a chunk ahead of their use
-  Stage<T, DK, C, kThreads> q_in, k_in;
-  Stage<T, TV, C, kThreads> v_in;
+  // ---- tiles, requested a chunk ahead; decays, computed a chunk ahead
+  using StageK = Stage<T, DK, C, kThreads>;
+  using StageV = Stage<T, TV, C, kThreads>;
+  const auto k_tile = [&](int i) { return k_base + (i & (L::k_tiles - 1)) * (L::k_bytes / (int)sizeof(T)); };
+  const auto v_tile = [&](int i) { return v_base + (i & (L::v_tiles - 1)) * (L::v_bytes / (int)sizeof(T)); };
   const auto chunk_at = [&](int i) { return t_lo + (int64_t)(reverse ? chunks - 1 - i : i) * C; };
   const auto chunk_len = [&](int64_t t0) { return (int)(t_hi - t0 < C ? t_hi - t0 : C); };
-  const auto request = [&](int i) {
+  const bool dma = p.dma;
+  uint32_t k_from[StageK::kEach], v_from[StageV::kEach];  // q's rows lie as k's do
+  StageK::offsets(k_from, k_stride, dk, wave, lane);
+  StageV::offsets(v_from, v_stride, dv - v0, wave, lane);
+  const auto request_k = [&](int i) {
     const int64_t t0 = chunk_at(i);
     const int len = chunk_len(t0), id = opaque(tid);
-    if constexpr (kOut) q_in.request(q_rows + t0 * (int64_t)q_stride, q_stride, dk, len, id);
-    k_in.request(k_rows + t0 * (int64_t)k_stride, k_stride, dk, len, id);
-    v_in.request(v_rows + t0 * (int64_t)v_stride, v_stride, dv - v0, len, id);
+    StageK::dma(k_tile(i), k_rows + t0 * (int64_t)k_stride, k_from, dk, len, wave, id & 63);
+    if (rare(len < C)) StageK::clear(k_tile(i), len, id);
+  };
+  const auto request_qv = [&](int i) {
+    const int64_t t0 = chunk_at(i);
+    const int len = chunk_len(t0), id = opaque(tid);
+    if constexpr (kOut) StageK::dma(qs, q_rows + t0 * (int64_t)k_stride, k_from, dk, len, wave, id & 63);
+    StageV::dma(v_tile(i), v_rows + t0 * (int64_t)v_stride, v_from, dv - v0, len, wave, id & 63);
+    if (rare(len < C)) {
+      if constexpr (kOut) StageK::clear(qs, len, id);
+      StageV::clear(v_tile(i), len, id);
+    }
   };
   float next_step = 1.0f;
   int next_reset = 0;
@@ -413,71 +547,97 @@ __global__ __launch_bounds__(64 * NW, NK <= 4 ? 2 : 1) void linear_attn_kernel(c
   };
   const bool decay_wave = wave == NW - 1;
   float carried = 1.0f;  // decay of the whole segment
-  request(0);
+  if (dma) {
+    if (dk < DK || dv - v0 < TV) {  // units behind the rows' ends stay 0
+      if constexpr (kOut) StageK::clear(qs, 0, tid);
+#pragma unroll 1
+      for (int i = 0; i < 2; ++i) {
+        StageK::clear(k_tile(i), 0, tid);
+        StageV::clear(v_tile(i), 0, tid);
+      }
+      lds_barrier();
+    }
+    if (L::k_tiles == 2) request_k(0);
+    request_qv(0);
+  }
   if (decay_wave) {
     request_step(0);
     chunk_decays<C>(&decays[0], rate, next_step, next_reset, constant, chunk_len(chunk_at(0)), lane, p);
     if (chunks > 1) request_step(1);
   }
-  if (tid == 0) again[0] = again[1] = 0;
+  if (tid < 4) again[tid] = 0;
+  if constexpr (kOut) {  // scores that no token sees: half of the tiles beside the diagonal's are read
+    for (int i = tid; i < kParts * C * C; i += kThreads) ss[i] = 0;
+  }
 
   int c = 0;
   int single = -1;       // chunks of one token: which of chunk c's is in turn
   bool pending = false;  // this wave's state still lacks them
-  for (;; ) {
-    lds_barrier();  // the last tiles are no longer read; decays and marks are there
-    if (single >= 0) {
-      if (++single == chunk_len(chunk_at(c))) {
-        single = -1;
-        pending = false;
-        ++c;
-      }
-    } else if (c > 0 && again[(c - 1) & 1]) {
-      --c;
-      single = 0;
-    }
-    if (c == chunks) break;
+  const auto land = [&] {
+    __builtin_amdgcn_s_waitcnt(kWaitVmcnt0);
+    lds_barrier();  // the next chunk's tiles have landed, the last one's are no longer read; decays and marks are there
+  };
+  land();
+  // The loop has one exit, at its end: with one at its head the state is copied
+  // from registers to registers in every turn.
+  do {
     const int tid = opaque(thread), lane = tid & 63, col = lane & 31, half = lane >> 5;
     const bool whole = single < 0;
     const int64_t t0 = chunk_at(c) + (whole ? 0 : reverse ? chunk_len(chunk_at(c)) - 1 - single : single);
     const int len = whole ? chunk_len(t0) : 1;
     const Decays<C>& d = whole ? decays[c & 1] : decays[2];
-    const T* const q_at = kOut ? q_rows + t0 * (int64_t)q_stride : nullptr;
+    T* const ks = k_tile(c);
+    T* const vs = v_tile(c);
+    const T* const q_at = kOut ? q_rows + t0 * (int64_t)k_stride : nullptr;
     const T* const k_at = k_rows + t0 * (int64_t)k_stride;
     const T* const v_at = v_rows + t0 * (int64_t)v_stride;
-    if (whole) {
+    if (!rare(!whole)) {
       if (kOut && p.save) {
         // Forward: the state before a block; reverse: the state behind it.
         const bool border = reverse ? (t0 + C) % linattn::kBlock == 0 || t0 + C >= a.seqlen : t0 % linattn::kBlock == 0;
-        if (border) store_state(p.save + (row * p.save_slots + t0 / linattn::kBlock) * state_size);
+        if (rare(border)) store_state(p.save + (row * p.save_slots + t0 / linattn::kBlock) * state_size);
       }
-      if constexpr (kOut) q_in.store(qs, q_at, q_stride, dk, len, tid);
-      k_in.store(ks, k_at, k_stride, dk, len, tid);
-      v_in.store(vs, v_at, v_stride, dv - v0, len, tid);
+      if (L::k_tiles == 1 && dma) {
+        request_k(c);
+        land();
+      }
+      if (rare(!dma)) {
+        if constexpr (kOut) StageK::pieces(qs, q_at, k_stride, dk, len, tid);
+        StageK::pieces(ks, k_at, k_stride, dk, len, tid);
+        StageV::pieces(vs, v_at, v_stride, dv - v0, len, tid);
+        lds_barrier();
+      }
     } else {
       // The token in row 0, zeros in the others.
-      if constexpr (kOut) Stage<T, DK, C, kThreads>::elements(qs, q_at, q_stride, dk, 1);
-      Stage<T, DK, C, kThreads>::elements(ks, k_at, k_stride, dk, 1);
-      Stage<T, TV, C, kThreads>::elements(vs, v_at, v_stride, dv - v0, 1);
+      if constexpr (kOut) StageK::elements(qs, q_at, k_stride, dk, 1);
+      StageK::elements(ks, k_at, k_stride, dk, 1);
+      StageV::elements(vs, v_at, v_stride, dv - v0, 1);
       if (tid < C) {
         const float each = decays[c & 1].each[t0 - chunk_at(c)];
         Decays<C>& one = decays[2];
-        one.sum[tid] = 0.0;
+        // A decay that is NaN makes the state NaN, what is 0 of it too: here what is
+        // read of it, below what is kept.
+        one.sum[tid] = tid == 0 && !reverse && each != each ? (double)each : 0.0;
         one.in[tid] = tid ? 0.0f : p.s_in * (reverse ? 1.0f : each);
-        one.up[tid] = tid ? 0.0f : p.s_up * (reverse ? each : 1.0f);
+        one.up[tid] = tid ? 0.0f : p.s_up * (reverse || each != each ? each : 1.0f);
         if (tid == 0) {
           one.total = each;
           one.zeros = one.up[0] == 0.0f;
         }
       }
+      lds_barrier();
     }
-    lds_barrier();
-    if (whole && c + 1 < chunks) request(c + 1);
-    if (whole && tid == 0) again[(c + 1) & 1] = 0;
+    if (whole) {
+      if (tid == 0) again[(c + 1) & 3] = 0;  // last read before this chunk's barrier
+      if (dma && c + 1 < chunks) {
+        if (L::k_tiles == 2) request_k(c + 1);
+        if (!kOut) request_qv(c + 1);
+      }
+    }
 
     if constexpr (!kOut) {
       // A row whose factor is 0 is dropped: its k are made 0 (its v below).
-      if (whole && d.zeros) {
+      if (whole && rare(d.zeros)) {
 #pragma unroll 1
         for (int i = tid; i < C * DK; i += kThreads)
           if (d.up[i / DK] == 0.0f) ks[TileK::at(i / DK, i % DK)] = 0;
@@ -487,47 +647,43 @@ __global__ __launch_bounds__(64 * NW, NK <= 4 ? 2 : 1) void linear_attn_kernel(c
 
     f32x16 out[RT];
     if constexpr (kOut) {
-      // ---- scores, a 32 x 32 quarter at a time: rows s, columns t
-      constexpr int kQuarters = RT == 2 ? 3 : 1;
-      for (int n = wave; n < kQuarters; n += NW) {
-        const int ti = reverse ? n >> 1 : (n + 1) >> 1;
-        const int si = reverse ? (n + 1) >> 1 : n >> 1;
-        f32x16 x = {};
+      // ---- scores, a 16 x 16 tile at a time: rows s, columns t
+      constexpr int kTiles = C / 16;
+      const int quad = lane >> 4, c16 = lane & 15;
+      for (int n = wave; n < kTiles * (kTiles + 1) / 2; n += NW) {
+        const int hi = n < 1 ? 0 : n < 3 ? 1 : n < 6 ? 2 : 3, lo = n - hi * (hi + 1) / 2;
+        const int ti = reverse ? lo : hi, si = reverse ? hi : lo;
+        f32x4 x = {};
 #pragma unroll
-        for (int f = 0; f < DK / 16; ++f)
-          mma(x, TileK::row(ks, 32 * si + col, 16 * f + 8 * half), TileK::row(qs, 32 * ti + col, 16 * f + 8 * half));
-        const int t = 32 * ti + col;
+        for (int m = 0; m < NK; ++m)
+          mma(x, TileK::row(ks, 16 * si + c16, 32 * m + 8 * quad), TileK::row(qs, 16 * ti + c16, 32 * m + 8 * quad));
+        const int t = 16 * ti + c16, s0 = 16 * si + 4 * quad;
         const double gt = d.sum[t];
         const float s_both = p.s_in * p.s_up;
+        const int late = reverse ? t - s0 : s0 - t;  // seen: not after t
+        float y[4];
 #pragma unroll
-        for (int i = 0; i < 16; i += 4) {
-          const int s0 = 32 * si + 2 * i + 4 * half;
-          float y[4];
+        for (int j = 0; j < 4; ++j) {
+          const float e = exp2_hw((float)(gt - d.sum[s0 + j]));
+          y[j] = late <= (reverse ? j : -j) ? x[j] * (e * s_both) : 0.0f;
+        }
+        if constexpr (sizeof(T) == 2) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const double diff = reverse ? d.sum[s0 + j] - gt : gt - d.sum[s0 + j];
-            const float e = exp2_hw((float)diff);
-            const bool seen = reverse ? s0 + j >= t : s0 + j <= t;
-            y[j] = seen && e != 0.0f ? x[i + j] * (e * s_both) : 0.0f;
+          for (int part = 0; part < kParts; ++part) {
+            words2 w;
+            w.x = Io<bf16_t>::pack2(y[0], y[1]);
+            w.y = Io<bf16_t>::pack2(y[2], y[3]);
+            *reinterpret_cast<words2*>(ss + part * C * C + TileS::at(t, s0)) = w;
+            y[0] -= bf16_lo(w.x);
+            y[1] -= bf16_hi(w.x);
+            y[2] -= bf16_lo(w.y);
+            y[3] -= bf16_hi(w.y);
           }
-          if constexpr (sizeof(T) == 2) {
-#pragma unroll
-            for (int part = 0; part < kParts; ++part) {
-              words2 w;
-              w.x = Io<bf16_t>::pack2(y[0], y[1]);
-              w.y = Io<bf16_t>::pack2(y[2], y[3]);
-              *reinterpret_cast<words2*>(ss + part * C * C + TileS::at(t, s0)) = w;
-              y[0] -= bf16_lo(w.x);
-              y[1] -= bf16_hi(w.x);
-              y[2] -= bf16_lo(w.y);
-              y[3] -= bf16_hi(w.y);
-            }
-          } else {
-            *reinterpret_cast<float4*>(ss + TileS::at(t, s0)) = make_float4(y[0], y[1], y[2], y[3]);
-          }
+        } else {
+          *reinterpret_cast<float4*>(ss + TileS::at(t, s0)) = make_float4(y[0], y[1], y[2], y[3]);
         }
       }
-      // ---- q . S
+      // ---- S^T q^T
 #pragma unroll
       for (int ti = 0; ti < RT; ++ti) out[ti] = f32x16{};
 #pragma unroll
@@ -537,20 +693,20 @@ __global__ __launch_bounds__(64 * NW, NK <= 4 ? 2 : 1) void linear_attn_kernel(c
         for (int j = 0; j < 8; ++j) x[j] = acc[f >> 1][8 * (f & 1) + j];
         Frag<T> s[kParts];
         split<kParts>(s, x);
+        Frag<T> q[RT];
 #pragma unroll
-        for (int ti = 0; ti < RT; ++ti) {
-          const Frag<T> q = TileK::row(qs, 32 * ti + col, 16 * f + 8 * half);
+        for (int ti = 0; ti < RT; ++ti) q[ti] = TileK::row(qs, 32 * ti + (lane0 & 31), 16 * f + 8 * (lane0 >> 5));
 #pragma unroll
-          for (int part = 0; part < kParts; ++part) mma(out[ti], q, s[part]);
-        }
+        for (int part = 0; part < kParts; ++part)
+#pragma unroll
+          for (int ti = 0; ti < RT; ++ti) mma(out[ti], s[part], q[ti]);
       }
 #pragma unroll
-      for (int ti = 0; ti < RT; ++ti)
+      for (int ti = 0; ti < RT; ++ti) {
+        const float in = d.in[32 * ti + col];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const float f = d.in[32 * ti + 8 * (i >> 2) + 4 * half + (i & 3)];
-          out[ti][i] = f == 0.0f ? 0.0f : out[ti][i] * f;
-        }
+        for (int i = 0; i < 16; ++i) out[ti][i] = drop_mul(in, out[ti][i]);
+      }
     }
     if (whole && decay_wave && c + 1 < chunks) {
       chunk_decays<C>(&decays[(c + 1) & 1], rate, next_step, next_reset, constant, chunk_len(chunk_at(c + 1)), lane, p);
@@ -559,20 +715,29 @@ __global__ __launch_bounds__(64 * NW, NK <= 4 ? 2 : 1) void linear_attn_kernel(c
     Frag<T> v[C / 16];
 #pragma unroll
     for (int f = 0; f < C / 16; ++f)
-      v[f] = TileV::template column<false>(vs, 16 * f + 8 * half, wave * 32, lane);
+      v[f] = TileV::template column<false>(vs, 16 * f + 8 * (lane0 >> 5), wave * 32, lane0);
     bool skip = !whole && !pending;
     if (whole) pending = d.slow;
     if constexpr (kOut) {
       lds_barrier();
-      // ---- scores . v
+      if (whole && dma && c + 1 < chunks) request_qv(c + 1);
+      // ---- v^T scores^T
+      const auto seen = [&](int ti, int f) {
 #pragma unroll
-      for (int ti = 0; ti < RT; ++ti) {
+        for (int part = 0; part < kParts; ++part)
+          mma(out[ti], v[f], TileS::row(ss + part * C * C, 32 * ti + col, 16 * f + 8 * half));
+      };
 #pragma unroll
-        for (int f = 0; f < C / 16; ++f) {
-          if (RT == 2 && (ti == 0 ? f >= 2 && !reverse : f < 2 && reverse)) continue;
+      for (int f = 0; f < 2; ++f)
 #pragma unroll
-          for (int part = 0; part < kParts; ++part)
-            mma(out[ti], TileS::row(ss + part * C * C, 32 * ti + col, 16 * f + 8 * half), v[f]);
+        for (int ti = 0; ti < RT; ++ti) seen(ti, 2 * ti + f);
+      if constexpr (RT == 2) {
+        if (reverse) {
+          seen(0, 2);
+          seen(0, 3);
+        } else {
+          seen(1, 0);
+          seen(1, 1);
         }
       }
       float nan = 0.0f;  // stays 0 while every output is finite
@@ -583,85 +748,94 @@ __global__ __launch_bounds__(64 * NW, NK <= 4 ? 2 : 1) void linear_attn_kernel(c
       if (whole && __any(!(nan == 0.0f))) pending = true;
     }
     if (whole) {
-      if (pending) {
-        if (lane == 0) again[c & 1] = 1;
+      if (rare(pending)) {
+        if (lane == 0) again[c & 3] = 1;
         skip = true;
       }
       carried *= d.total;
     }
 
-    if (!skip) {
+    if (!rare(skip)) {
+      if constexpr (kOut) {
+        // ---- outputs: a lane has columns 8 i + 4 half .. + 3 (i < 4) of token 32 ti + col
+        const int first = v0 + wave * 32 + 4 * half;
+        const uint32_t out_stride = a.heads * dv;
+        const int64_t out_first = ((batch_tokens + t0) * a.heads + head) * dv;
+        if (!rare(p.out_f32 || len < C || v0 + TV > dv)) {
+#pragma unroll
+          for (int ti = 0; ti < RT; ++ti)
+            store_columns<true>(static_cast<T*>(p.out) + out_first, (32 * ti + col) * out_stride, first, dv, out[ti]);
+        } else {
+#pragma unroll
+          for (int ti = 0; ti < RT; ++ti) {
+            if (32 * ti + col >= len) continue;
+            if (p.out_f32)
+              store_columns<false>(static_cast<float*>(p.out) + out_first, (32 * ti + col) * out_stride, first, dv, out[ti]);
+            else
+              store_columns<false>(static_cast<T*>(p.out) + out_first, (32 * ti + col) * out_stride, first, dv, out[ti]);
+          }
+        }
+        if (p.with.p) {
+#pragma unroll
+          for (int ti = 0; ti < RT; ++ti) {
+            const int t = 32 * ti + col;
+            const bool live = t < len;
+            float dot = 0.0f;
+            if (live) {
+              const T* with = side_rows<T>(p.with, batch_tokens, head) + (t0 + t) * p.with.heads * dv;
+              dot = dot_columns(with, first, dv, out[ti]);
+            }
+            dot += __shfl_xor(dot, 32);
+            const int part = tile * NW + wave;
+            if (half == 0 && live && part * 32 < dv)
+              p.dots[((int64_t)part * a.batch * a.heads + row) * a.seqlen + t0 + t] = dot;
+          }
+        }
+      }
       // ---- the update
       const float total = d.total;
 #pragma unroll
       for (int b = 0; b < NK; ++b)
 #pragma unroll
-        for (int i = 0; i < 16; ++i) acc[b][i] = total == 0.0f ? 0.0f : acc[b][i] * total;
-      if (whole || !d.zeros) {
+        for (int i = 0; i < 16; ++i) acc[b][i] = drop_mul(total, acc[b][i]);
+      if (!rare(!whole && d.zeros)) {
 #pragma unroll
         for (int f = 0; f < C / 16; ++f) {
           float x[8];
           get8(v[f], x);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const float up = d.up[16 * f + 8 * half + j];
-            x[j] = up == 0.0f ? 0.0f : x[j] * up;
-          }
+          for (int j = 0; j < 8; ++j) x[j] = drop_mul(d.up[16 * f + 8 * half + j], x[j]);
           Frag<T> w[kUp];
           split<kUp>(w, x);
+          constexpr int kPair = NK < 2 ? 1 : 2;
 #pragma unroll
-          for (int b = 0; b < NK; ++b) {
-            const Frag<T> k = TileK::template column<true>(ks, 16 * f + 8 * half, 32 * b, lane);
+          for (int b = 0; b < NK; b += kPair) {
+            Frag<T> k[kPair];
 #pragma unroll
-            for (int part = kUp - 1; part >= 0; --part) mma(acc[b], k, w[part]);
-          }
-        }
-      }
-      if constexpr (kOut) {
-        // ---- outputs: through the wave's own LDS tile, so that a lane has 8 of a row
+            for (int u = 0; u < kPair; ++u) k[u] = TileK::template column<true>(ks, 16 * f + 8 * half, 32 * (b + u), lane);
 #pragma unroll
-        for (int ti = 0; ti < RT; ++ti) {
-          wave_lds_fence();
+            for (int part = kUp - 1; part >= 0; --part)
 #pragma unroll
-          for (int i = 0; i < 16; ++i) out_tile[TileO::at(8 * (i >> 2) + 4 * half + (i & 3), col)] = out[ti][i];
-          wave_lds_fence();
-#pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            const int piece = lane + 64 * u, rr = piece >> 2, c8 = (piece & 3) * 8;
-            const int t = 32 * ti + rr, vcol = v0 + wave * 32 + c8;
-            const bool live = t < len && vcol < dv;
-            const Frag<float> y = TileO::row(out_tile, rr, c8);
-            const int64_t token = batch_tokens + t0 + t;
-            if (live) {
-              const int64_t at = (token * a.heads + head) * dv;
-              if (p.out_f32)
-                store_row8(static_cast<float*>(p.out) + at, vcol, dv, false, y.v);
-              else
-                store_row8(static_cast<T*>(p.out) + at, vcol, dv, false, y.v);
-            }
-            if (p.with.p) {
-              float dot = 0.0f;
-              if (live) {
-                const T* with = static_cast<const T*>(p.with.p) + (token * p.with.heads + head / p.with.share) * dv;
-                Raw8<T> raw = request8<true>(with, vcol, 0, dv);
-                finish8<true>(raw, vcol, 0, dv);
-                float x[8];
-                raw.get(x);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) dot = __builtin_fmaf(x[j], vcol + j < dv ? y.v[j] : 0.0f, dot);
-              }
-              dot += __shfl_xor(dot, 1);
-              dot += __shfl_xor(dot, 2);
-              const int part = tile * NW + wave;
-              if ((lane & 3) == 0 && t < len && part * 32 < dv)
-                p.dots[((int64_t)part * a.batch * a.heads + row) * a.seqlen + t0 + t] = dot;
-            }
+              for (int u = 0; u < kPair; ++u) mma(acc[b + u], k[u], w[part]);
           }
         }
       }
     }
-    if (whole) ++c;
-  }
+    land();
+    if (whole) {
+      if (rare(again[c & 3]))
+        single = 0;
+      else
+        ++c;
+    } else if (++single == chunk_len(chunk_at(c))) {
+      single = -1;
+      pending = false;
+      if (++c < chunks && dma && kOut) {  // the next chunk's, which the single tokens wrote over
+        request_qv(c);
+        land();
+      }
+    }
+  } while (c < chunks);
 
   // ---- the segment's end
   if constexpr (kOut) {
