@@ -4,7 +4,9 @@
 //
 // With few (batch, head) pairs the tokens are cut into segments: a state pass
 // gives every segment's own state, a join turns them into the states the
-// segments start from, and the main pass runs all segments at once.
+// segments start from, and the main pass runs all segments at once.  The
+// backward takes the forward's states from its checkpoints where its segments are
+// whole blocks of them, and else from a state pass of its own.
 //
 // The backward is the same pass three times over,
 //   dq = pass(dy, v, k), state S^T;   dv = reverse pass(k, q, dy), state R;
@@ -13,7 +15,8 @@
 //   dL/dg_t = <a_t S_{t-1}, R_t>
 //           = sum over u >= t in the block of (q_u . dq_u - k_u . dk_u) + <S, R> behind the block
 // since all that is written and read behind t cancels in the sum; blocks are
-// kBlock tokens, so that no longer sum loses what it cancels to.
+// kBlock tokens, so that no longer sum loses what it cancels to, and <S, R> in front of
+// the block says how far the sums' roundings have come.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -37,14 +40,26 @@ using linattn::Side;
 // States of the segments' own tokens become the states the segments start from.
 // A thread has one element of the state and walks the segments, 8 requested at
 // once (in slots that it alone reads and writes).
-__global__ __launch_bounds__(256) void linear_attn_join_kernel(float* part, const float* total, const float* first,
-                                                               int64_t n, int segments, int reverse) {
+struct Join {
+  float* part;
+  const float* total;
+  const float* first;  // may be null (0)
+  int64_t first_step;  // from row to row of first
+  int reverse;
+};
+
+__global__ __launch_bounds__(256) void linear_attn_join_kernel(const Join one, const Join other, int64_t n, int segments) {
+  const Join& p = blockIdx.z ? other : one;
+  float* const part = p.part;
+  const float* const total = p.total;
+  const float* const first = p.first;
+  const int reverse = p.reverse;
   const int64_t row = blockIdx.y;
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (i >= n) return;
   float* at = part + row * segments * n + i;
   const float* decay = total + row * segments;
-  float s = first ? first[row * n + i] : 0.0f;
+  float s = first ? first[row * p.first_step + i] : 0.0f;
   for (int j0 = 0; j0 < segments; j0 += 8) {
     float x[8];
 #pragma unroll
@@ -82,6 +97,7 @@ struct DecayArgs {
   const float* dstates;  // [rows][blocks][n], behind each block
   const float* dots_q;   // [parts_q][rows][seqlen]
   const float* dots_k;   // [parts_k][rows][seqlen]
+  const float* dh0;      // [rows][n], in front of the first block
   const float* rate;
   const void* step;      // may be null
   const uint8_t* reset;  // may be null
@@ -100,15 +116,20 @@ __device__ __forceinline__ double wave_sum(double v) {
 // One block of kBlock tokens of one (batch, head); a thread has two tokens.
 template <typename T>
 __global__ __launch_bounds__(256) void linear_attn_decay_kernel(const DecayArgs p) {
-  __shared__ double slots[3][4];
+  __shared__ double slots[4][4];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int block = (int)(blockIdx.x % p.blocks);
   const int64_t row = blockIdx.x / p.blocks;
   const int head = (int)(row % p.heads);
   const float* s = p.states + (row * (p.blocks + 1) + block + 1) * p.n;
   const float* r = p.dstates + (row * p.blocks + block) * p.n;
-  double cross = 0.0;
-  for (int64_t i = tid; i < p.n; i += 256) cross += (double)s[i] * (double)r[i];
+  const float* s0 = s - p.n;  // in front of the block
+  const float* r0 = block ? r - p.n : p.dh0 + row * p.n;
+  double cross = 0.0, front = 0.0;
+  for (int64_t i = tid; i < p.n; i += 256) {
+    cross += (double)s[i] * (double)r[i];
+    front += (double)s0[i] * (double)r0[i];
+  }
   const int64_t t0 = (int64_t)block * kBlock;
   double w[2] = {0.0, 0.0};
 #pragma unroll
@@ -119,21 +140,31 @@ __global__ __launch_bounds__(256) void linear_attn_decay_kernel(const DecayArgs 
     for (int i = 0; i < p.parts_k; ++i) w[j] -= (double)p.dots_k[(i * p.rows + row) * p.seqlen + t];
   }
   cross = wave_sum(cross);
+  front = wave_sum(front);
   double behind = w[0] + w[1];  // of this lane and those behind it
 #pragma unroll
   for (int m = 1; m < 64; m <<= 1) {
     const double o = __shfl_down(behind, m);
     if (lane + m < 64) behind += o;
   }
-  if (lane == 0) slots[0][wave] = cross, slots[1][wave] = behind;
+  if (lane == 0) slots[0][wave] = cross, slots[1][wave] = behind, slots[3][wave] = front;
   __syncthreads();
   cross = slots[0][0] + slots[0][1] + slots[0][2] + slots[0][3];
+  const double all = slots[1][0] + slots[1][1] + slots[1][2] + slots[1][3];
   for (int v = 3; v > wave; --v) behind += slots[1][v];
+  // What the sums say is carried into the block is known on its own, <S, R> in
+  // front of it.  The sums' roundings between the two ends are spread over the
+  // tokens as a walk between two fixed ends would be.
+  front = slots[3][0] + slots[3][1] + slots[3][2] + slots[3][3];
+  double off = front - (cross + all);
+  if (!(__builtin_fabs(off) < 1e300)) off = 0.0;
+  const int64_t count = min((int64_t)kBlock, p.seqlen - (int64_t)block * kBlock);
   double sum = 0.0;
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
     const int64_t t = t0 + 2 * tid + j;
     double g = cross + behind - (j ? w[0] : 0.0);
+    g += off * (double)(t0 + count - t) / (double)count;
     if (t >= p.seqlen) continue;
     const int64_t at = row / p.heads * p.seqlen + t;
     const double rate = (double)p.rate[head];
@@ -265,29 +296,49 @@ ssm_status_t check_sizes(const Sizes& s, ssm_dtype_t io) {
 
 int64_t tiles(int64_t dv) { return (dv + linattn::tile_width((int)dv) - 1) / linattn::tile_width((int)dv); }
 
+constexpr int64_t kUnit = 64;  // tokens; a segment is so many of them, a multiple of either chunk
+
 struct Split {
-  int64_t per, count;  // blocks of kBlock tokens in a segment, segments
+  int64_t per, count;  // units of a segment, segments
+  bool blocks() const { return per * kUnit % kBlock == 0 || count == 1; }
 };
 
-int64_t waves(int64_t dv) { return tiles(dv) * linattn::tile_width((int)dv) / 32; }
+// Blocks of a pass that the chip holds at once: as the LDS and registers of its
+// kernel allow.
+int64_t resident(int64_t dk) {
+  return 256 * (dk > 128 ? 1 : dk > 64 ? 2 : 3);
+}
 
-// Segments: as many as give the chip's 1024 SIMDs two waves each.
-Split split_tokens(const Sizes& s, int64_t waves_each) {
-  Split p{s.blocks(), 1};
-  const int64_t wanted = waves_each < 1024 ? (2048 + waves_each - 1) / waves_each : 1;
-  p.per = std::max<int64_t>(1, p.per / wanted);
-  p.count = (s.blocks() + p.per - 1) / p.per;
+// Segments: as many as are resident at once, of two units or more.
+Split split_tokens(const Sizes& s, int64_t most) {
+  const int64_t units = (s.seqlen + kUnit - 1) / kUnit;
+  Split p{units, 1};
+  const int64_t wanted = std::max<int64_t>(1, most);
+  p.per = std::max<int64_t>(std::min<int64_t>(2, units), (units + wanted - 1) / wanted);
+  p.count = (units + p.per - 1) / p.per;
   return p;
 }
 
-Split fwd_split(const Sizes& s) { return split_tokens(s, s.rows() * waves(s.dv)); }
-Split bwd_split(const Sizes& s) { return split_tokens(s, s.rows() * std::min(2 * waves(s.dk), waves(s.dv))); }
+Split fwd_split(const Sizes& s) { return split_tokens(s, resident(s.dk) / (s.rows() * tiles(s.dv))); }
+
+// The three passes have one split: what the pass with the fewest blocks asks for.
+Split bwd_split(const Sizes& s) {
+  const int64_t to_v = resident(s.dk) / (s.rows() * tiles(s.dv));
+  const int64_t to_qk = resident(s.dv) / (s.rows() * 2 * tiles(s.dk));
+  Split p = split_tokens(s, std::max(to_v, to_qk));
+  const int64_t block = kBlock / kUnit;
+  if (p.per >= block) {  // whole blocks: the forward's states are checkpoints
+    p.per = p.per / block * block;
+    p.count = ((s.seqlen + kUnit - 1) / kUnit + p.per - 1) / p.per;
+  }
+  return p;
+}
 
 // Segments' states and decays.
 int64_t segment_bytes(const Sizes& s, const Split& p) { return p.count > 1 ? s.rows() * p.count * (s.state() + 1) * 4 : 0; }
 
 struct BwdSpace {
-  int64_t segments, dstates, dots_q, dots_k, drate, dq, dk, bytes;  // offsets
+  int64_t states, segments, dstates, dh0, dots_q, dots_k, drate, dq, dk, bytes;  // offsets
 };
 
 BwdSpace bwd_space(const Sizes& s, bool decays) {
@@ -299,8 +350,11 @@ BwdSpace bwd_space(const Sizes& s, bool decays) {
     return here;
   };
   w.drate = take(decays ? s.rows() * s.blocks() * 8 : 0);
-  w.segments = take(segment_bytes(s, bwd_split(s)));
+  const Split p = bwd_split(s);
+  w.segments = take(segment_bytes(s, p));
+  w.states = take(p.blocks() ? 0 : segment_bytes(s, p));
   w.dstates = take(decays ? s.rows() * s.blocks() * s.state() * 4 : 0);
+  w.dh0 = take(decays ? s.rows() * s.state() * 4 : 0);
   w.dots_q = take(decays ? (s.dk + 31) / 32 * s.rows() * s.seqlen * 4 : 0);
   w.dots_k = take(decays ? (s.dk + 31) / 32 * s.rows() * s.seqlen * 4 : 0);
   const bool shared = s.groups != s.heads;
@@ -331,24 +385,35 @@ Args pass_args(const Sizes& s, const Split& p, const float* rate, const void* st
   a.step = step;
   a.reset = reset;
   a.segments = (int)p.count;
-  a.segment_len = p.per * kBlock;
+  a.segment_len = p.per * kUnit;
   return a;
 }
 
-// The states that the segments start from, into `space` (segment_bytes).
-hipError_t segment_states(Args a, Role role, const Sizes& s, const float* first, void* space, ssm_dtype_t io,
-                          hipStream_t st) {
-  role.part = static_cast<float*>(space);
-  role.total = role.part + s.rows() * a.segments * s.state();
-  role.tiles = (int)tiles(s.dv);
-  role.first_block = 0;
-  a.role[0] = role;
-  a.roles = 1;
-  const hipError_t e = launch_pass(a, s.rows() * (a.segments - 1) * role.tiles, true, false, io, st);
+// The states that the segments start from: of one or two roles, `first` in front of
+// all tokens (behind them, reverse), into their spaces (segment_bytes each).
+struct Front {
+  const float* state;  // may be null
+  int64_t step;        // from (batch, head) to (batch, head)
+};
+
+hipError_t segment_states(Args a, const Role* roles, const Front* first, void* const* space, int count, const Sizes& s,
+                          ssm_dtype_t io, hipStream_t st) {
+  Join join[2] = {};
+  a.roles = count;
+  const int64_t blocks = s.rows() * (a.segments - 1) * tiles(s.dv);
+  for (int i = 0; i < count; ++i) {
+    Role& r = a.role[i] = roles[i];
+    r.part = static_cast<float*>(space[i]);
+    r.total = r.part + s.rows() * a.segments * s.state();
+    r.tiles = (int)tiles(s.dv);
+    r.first_block = i * blocks;
+    join[i] = Join{r.part, r.total, first[i].state, first[i].step, r.reverse};
+  }
+  const hipError_t e = launch_pass(a, blocks * count, true, false, io, st);
   if (e != hipSuccess) return e;
   const int64_t n = s.state();
-  hipLaunchKernelGGL(linear_attn_join_kernel, dim3((unsigned)((n + 255) / 256), (unsigned)s.rows()), dim3(256), 0, st,
-                     role.part, role.total, first, n, a.segments, role.reverse);
+  hipLaunchKernelGGL(linear_attn_join_kernel, dim3((unsigned)((n + 255) / 256), (unsigned)s.rows(), (unsigned)count),
+                     dim3(256), 0, st, join[0], join[1], n, a.segments);
   return hipGetLastError();
 }
 
@@ -411,7 +476,8 @@ ssm_status_t ssm_linear_attn_fwd(int64_t batch, int64_t seqlen, int64_t heads, i
   r.start_slots = 1;
   hipError_t e = hipSuccess;
   if (p.count > 1) {
-    e = segment_states(a, r, s, h0, workspace, io, hs);
+    const Front first{h0, s.state()};
+    e = segment_states(a, &r, &first, &workspace, 1, s, io, hs);
     r.start = static_cast<const float*>(workspace);
     r.start_slots = p.count;
     r.start_step = 1;
@@ -478,21 +544,35 @@ ssm_status_t ssm_linear_attn_bwd(int64_t batch, int64_t seqlen, int64_t heads, i
   to_v.reverse = 1;
   to_v.s_in = 1.0f;
   to_v.s_up = scale;
+  to_v.start = dlast;
+  to_v.start_slots = 1;
+  to_q.start = ckpt;
+  to_q.start_slots = s.blocks() + 1;
+  to_q.start_step = p.per * kUnit / kBlock;
   hipError_t e = hipSuccess;
   if (p.count > 1) {
-    e = segment_states(a, to_v, s, dlast, at(w.segments), io, hs);
+    Role forward = {};  // S again, from the states in front of all tokens
+    forward.q = qs; forward.k = ks; forward.v = vs;
+    forward.s_in = forward.s_up = 1.0f;
+    const Role roles[2] = {to_v, forward};
+    const Front first[2] = {{dlast, s.state()}, {ckpt, (s.blocks() + 1) * s.state()}};
+    void* const spaces[2] = {at(w.segments), at(w.states)};
+    e = segment_states(a, roles, first, spaces, p.blocks() ? 1 : 2, s, io, hs);
     if (e != hipSuccess) return hip_fail(e);
     to_v.start = at(w.segments);
     to_v.start_slots = p.count;
     to_v.start_step = 1;
-  } else {
-    to_v.start = dlast;
-    to_v.start_slots = 1;
+    if (!p.blocks()) {
+      to_q.start = at(w.states);
+      to_q.start_slots = p.count;
+      to_q.start_step = 1;
+    }
   }
   to_v.out = dv_out;
   to_v.last = dh0;
   to_v.tiles = (int)tiles(dv);
   if (decays) {
+    if (!dh0) to_v.last = at(w.dh0);
     to_v.save = at(w.dstates);
     to_v.save_slots = s.blocks();
   }
@@ -505,9 +585,6 @@ ssm_status_t ssm_linear_attn_bwd(int64_t batch, int64_t seqlen, int64_t heads, i
   to_q.transposed = 1;
   to_q.s_in = scale;
   to_q.s_up = 1.0f;
-  to_q.start = ckpt;
-  to_q.start_slots = s.blocks() + 1;
-  to_q.start_step = p.per;
   to_q.tiles = to_k.tiles;
   const bool shared = groups != heads;
   to_q.out = shared ? at(w.dq) : dq;
@@ -552,6 +629,7 @@ ssm_status_t ssm_linear_attn_bwd(int64_t batch, int64_t seqlen, int64_t heads, i
     d.dstates = at(w.dstates);
     d.dots_q = at(w.dots_q);
     d.dots_k = at(w.dots_k);
+    d.dh0 = to_v.last;
     d.rate = rate;
     d.step = step;
     d.reset = reset;

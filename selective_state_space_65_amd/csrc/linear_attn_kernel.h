@@ -747,12 +747,12 @@ __global__ __launch_bounds__(64 * NW, NK <= 4 ? 2 : 1) void linear_attn_kernel(c
         for (int i = 0; i < 16; ++i) nan = __builtin_fmaf(out[ti][i], 0.0f, nan);
       if (whole && __any(!(nan == 0.0f))) pending = true;
     }
+    if (!(whole && d.slow)) carried = drop_mul(d.total, carried);
     if (whole) {
       if (rare(pending)) {
         if (lane == 0) again[c & 3] = 1;
         skip = true;
       }
-      carried *= d.total;
     }
 
     if (!rare(skip)) {

@@ -341,7 +341,7 @@ def test_graphs():
 
 
 def test_offsets_past_32_bits():
-    """v and y of more than 2^31 elements: the last tokens, behind a reset, equal a short call's."""
+    """v and y of more than 2^31 elements: the last tokens, behind a reset, against the float64 form of those alone."""
     heads, dv, seqlen, tail = 16, 256, 540_000, 300
     say("linear attention, %d elements" % (heads * dv * seqlen))
     g = torch.Generator(device=DEV).manual_seed(5)
@@ -353,9 +353,9 @@ def test_offsets_past_32_bits():
     cut -= cut % 512
     reset[0, cut] = 1
     y, last = ssm.linear_attn_fwd(q, k, v, rate, reset=reset)
-    ys, lasts = ssm.linear_attn_fwd(q[:, cut:].contiguous(), k[:, cut:].contiguous(), v[:, cut:].contiguous(), rate)
     torch.cuda.synchronize()
-    assert torch.equal(y[:, cut:], ys) and torch.equal(last, lasts)
+    tail = {n: t[:, cut:].cpu() for n, t in dict(q=q, k=k, v=v).items()}
+    check(dict(y=y[:, cut:].cpu(), last_state=last.cpu()), ref.everything(dict(tail, rate=rate.cpu()), io=BF16), "tail")
 
 
 def test_refusals():
