@@ -102,63 +102,74 @@ __device__ __forceinline__ void piece(const T* row, int c, int gl, int d, float 
   r.get(out);
 }
 
+// Groups that G lanes have in flight: more bytes, and half the blocks.
+constexpr int rows_ahead(int K) { return K == 1 ? 2 : 1; }
+
 template <typename T, int G, int K, bool kGated>
 __global__ __launch_bounds__(kThreads) void group_norm_row_fwd_kernel(const Args p) {
+  constexpr int U = rows_ahead(K);
   const int lane = threadIdx.x & 63, gl = lane & (G - 1);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t rows = p.batch * p.groups;
-  const int64_t row = ((int64_t)blockIdx.x * (kThreads / 64) + wave) * (64 / G) + lane / G;
-  const bool live = row < rows;
-  const int64_t at = (live ? row : rows - 1) * p.d;
-  const int d = p.d, first = (int)((live ? row : rows - 1) % p.groups) * d;
-  const T* x = static_cast<const T*>(p.x) + at;
+  const int64_t row0 = ((int64_t)blockIdx.x * (kThreads / 64) + wave) * (64 / G) * U + lane / G;
+  const int d = p.d;
   const float count = (float)d;
-  Raw8<T> px[K], pz[K];
+  int64_t at[U];
+  Raw8<T> px[U][K], pz[U][K];
 #pragma unroll
-  for (int k = 0; k < K; ++k) {
-    px[k] = request_piece<G>(x, (k * G + gl) * kPiece, gl, d);
-    if constexpr (kGated) pz[k] = request_piece<G>(static_cast<const T*>(p.z) + at, (k * G + gl) * kPiece, gl, d);
-  }
-  float v[K][kPiece], t = 0.0f;
+  for (int u = 0; u < U; ++u) {
+    at[u] = min(row0 + u * (64 / G), rows - 1) * d;
 #pragma unroll
-  for (int k = 0; k < K; ++k) {
-    const int c = (k * G + gl) * kPiece;
-    finish_piece<G>(px[k], c, gl, d);
-    px[k].get(v[k]);
-#pragma unroll
-    for (int j = 0; j < kPiece; ++j) t += v[k][j];
-  }
-  const float mean = p.rms ? 0.0f : group_sum<G>(t) / count;
-  float q = 0.0f;
-#pragma unroll
-  for (int k = 0; k < K; ++k)
-#pragma unroll
-    for (int j = 0; j < kPiece; ++j) {
-      const float e = (k * G + gl) * kPiece + j < d ? v[k][j] - mean : 0.0f;
-      q = __builtin_fmaf(e, e, q);
+    for (int k = 0; k < K; ++k) {
+      px[u][k] = request_piece<G>(static_cast<const T*>(p.x) + at[u], (k * G + gl) * kPiece, gl, d);
+      if constexpr (kGated)
+        pz[u][k] = request_piece<G>(static_cast<const T*>(p.z) + at[u], (k * G + gl) * kPiece, gl, d);
     }
-  const float rstd = 1.0f / __builtin_sqrtf(group_sum<G>(q) / count + p.eps);
-  if (!live) return;
-#pragma unroll
-  for (int k = 0; k < K; ++k) {
-    const int c = (k * G + gl) * kPiece;
-    float w[kPiece], b[kPiece], z[kPiece], o[kPiece];
-    fill(w, 1.0f);
-    fill(b, 0.0f);
-    fill(z, 0.0f);
-    if (p.weight) piece<G>(p.weight + first, c, gl, d, w);
-    if (p.bias) piece<G>(p.bias + first, c, gl, d, b);
-    if constexpr (kGated) {
-      finish_piece<G>(pz[k], c, gl, d);
-      pz[k].get(z);
-    }
-#pragma unroll
-    for (int j = 0; j < kPiece; ++j) o[j] = output((v[k][j] - mean) * rstd, w[j], b[j], z[j], p.silu, kGated);
-    store_row8(static_cast<T*>(p.y) + at, c, d, whole<G>(c, gl, d), o);
   }
-  if (gl == 0) {
-    if (!p.rms && p.mean) p.mean[row] = mean;
-    if (p.rstd) p.rstd[row] = rstd;
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int64_t row = row0 + u * (64 / G);
+    const int first = (int)(min(row, rows - 1) % p.groups) * d;
+    float v[K][kPiece], t = 0.0f;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      finish_piece<G>(px[u][k], (k * G + gl) * kPiece, gl, d);
+      px[u][k].get(v[k]);
+#pragma unroll
+      for (int j = 0; j < kPiece; ++j) t += v[k][j];
+    }
+    const float mean = p.rms ? 0.0f : group_sum<G>(t) / count;
+    float q = 0.0f;
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+      for (int j = 0; j < kPiece; ++j) {
+        const float e = (k * G + gl) * kPiece + j < d ? v[k][j] - mean : 0.0f;
+        q = __builtin_fmaf(e, e, q);
+      }
+    const float rstd = 1.0f / __builtin_sqrtf(group_sum<G>(q) / count + p.eps);
+    if (row >= rows) return;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int c = (k * G + gl) * kPiece;
+      float w[kPiece], b[kPiece], z[kPiece], o[kPiece];
+      fill(w, 1.0f);
+      fill(b, 0.0f);
+      fill(z, 0.0f);
+      if (p.weight) piece<G>(p.weight + first, c, gl, d, w);
+      if (p.bias) piece<G>(p.bias + first, c, gl, d, b);
+      if constexpr (kGated) {
+        finish_piece<G>(pz[u][k], c, gl, d);
+        pz[u][k].get(z);
+      }
+#pragma unroll
+      for (int j = 0; j < kPiece; ++j) o[j] = output((v[k][j] - mean) * rstd, w[j], b[j], z[j], p.silu, kGated);
+      store_row8(static_cast<T*>(p.y) + at[u], c, d, whole<G>(c, gl, d), o);
+    }
+    if (gl == 0) {
+      if (!p.rms && p.mean) p.mean[row] = mean;
+      if (p.rstd) p.rstd[row] = rstd;
+    }
   }
 }
 
@@ -281,21 +292,54 @@ __device__ __forceinline__ Plane plane(int64_t channels) {
   return t;
 }
 
-template <typename T>
+// kShort: fewer than 8 channels.  A kernel of its own: the branch it takes to a
+// load would have each load waited for.
+template <bool kShort, typename T>
 __device__ __forceinline__ Raw8<T> request_at(const T* row, int c, int n) {
-  return request8<true>(row, c, 0, n);
+  return request8<kShort>(row, c, 0, n);
 }
 
-template <typename T>
+template <bool kShort, typename T>
 __device__ __forceinline__ void finish_at(Raw8<T>& r, int c, int n, float out[kPiece]) {
-  finish8<true>(r, c, 0, n);
+  finish8<kShort>(r, c, 0, n);
   r.get(out);
 }
 
-__device__ __forceinline__ float wave_sum_f32(float v) { return group_sum<64>(v); }
+// Positions that a thread has in flight: 128 bytes of one to three arrays.
+template <typename T, int kArrays>
+constexpr int kAhead = kArrays == 1 ? 16 / sizeof(T) : kArrays == 2 ? 8 / sizeof(T) : 2;
+
+// Mean and squares about it of the groups that columns [c0, c1) have, from their
+// columns' means and squares; G lanes a group.  A group that began in an earlier
+// column is joined with what is there.
+template <int G>
+__device__ __forceinline__ void join_columns(const Args& p, const float* means, const float* squares, int c0, int c1,
+                                             float count, float* out) {
+  const int gl = threadIdx.x & (G - 1);
+  for (int g = c0 / p.d + threadIdx.x / G; g <= (c1 - 1) / p.d; g += kThreads / G) {
+    const int lo = max(g * p.d, c0) - c0, hi = min((g + 1) * p.d, c1) - c0;
+    const float here = (float)(hi - lo);
+    float m = 0.0f, q = 0.0f;
+    for (int i = lo + gl; i < hi; i += G) m += means[i];
+    m = group_sum<G>(m) / here;
+    for (int i = lo + gl; i < hi; i += G) {
+      const float e = means[i] - m;
+      q += __builtin_fmaf(count * e, e, squares[i]);
+    }
+    q = group_sum<G>(q);
+    if (gl) continue;
+    if (g * p.d < c0) {
+      const float before = (float)(c0 - g * p.d), m0 = out[g], all = before + here, e = m - m0;
+      m = m0 + e * (here / all);
+      q += out[p.groups + g] + count * e * e * (before * here / all);
+    }
+    out[g] = m;
+    out[p.groups + g] = q;
+  }
+}
 
 // part[batch][run][2][groups]: each run's means, and sums of squares about them.
-template <typename T>
+template <typename T, bool kShort>
 __global__ __launch_bounds__(kThreads) void group_norm_map_stats_kernel(const Args p) {
   __shared__ float cols[2][kThreads * kPiece];
   const Plane t = plane(p.channels);
@@ -303,7 +347,7 @@ __global__ __launch_bounds__(kThreads) void group_norm_map_stats_kernel(const Ar
   const int run = (int)(blockIdx.x % p.runs);
   const int64_t l0 = run * p.run, l1 = min(l0 + p.run, p.length);
   const float count = (float)(l1 - l0);
-  const int n = (int)p.channels, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int n = (int)p.channels;
   const T* x = static_cast<const T*>(p.x) + batch * p.length * n;
   float* out = p.part + (batch * p.runs + run) * 2 * p.groups;
   for (int c0 = 0; c0 < n; c0 += t.tx * kPiece) {
@@ -312,25 +356,24 @@ __global__ __launch_bounds__(kThreads) void group_norm_map_stats_kernel(const Ar
     float s1[kPiece], s2[kPiece], pivot[kPiece];
     fill(s1, 0.0f);
     fill(s2, 0.0f);
-    fill(pivot, 0.0f);
     if (live) {
-      if (!p.rms) {
-        Raw8<T> r = request_at(x + l0 * n, c, n);
-        finish_at(r, c, n, pivot);
-      }
-      constexpr int kAhead = 4;
-      for (int64_t l = l0 + t.y; l < l1; l += kAhead * t.ty) {
-        Raw8<T> r[kAhead];
+      Raw8<T> first = request_at<kShort>(x + l0 * n, c, n);
+      for (int64_t l = l0 + t.y; l < l1; l += kAhead<T, 1> * t.ty) {
+        Raw8<T> r[kAhead<T, 1>];
 #pragma unroll
-        for (int u = 0; u < kAhead; ++u) r[u] = request_at(x + min(l + u * t.ty, l1 - 1) * n, c, n);
+        for (int u = 0; u < kAhead<T, 1>; ++u) r[u] = request_at<kShort>(x + min(l + u * t.ty, l1 - 1) * n, c, n);
+        if (l == l0 + t.y) {
+          finish_at<kShort>(first, c, n, pivot);
+          if (p.rms) fill(pivot, 0.0f);
+        }
 #pragma unroll
-        for (int u = 0; u < kAhead; ++u) {
-          if (l + u * t.ty >= l1) break;
+        for (int u = 0; u < kAhead<T, 1>; ++u) {
+          const bool in = l + u * t.ty < l1;
           float v[kPiece];
-          finish_at(r[u], c, n, v);
+          finish_at<kShort>(r[u], c, n, v);
 #pragma unroll
           for (int j = 0; j < kPiece; ++j) {
-            const float e = v[j] - pivot[j];
+            const float e = in ? v[j] - pivot[j] : 0.0f;
             s1[j] += e;
             s2[j] = __builtin_fmaf(e, e, s2[j]);
           }
@@ -349,8 +392,7 @@ __global__ __launch_bounds__(kThreads) void group_norm_map_stats_kernel(const Ar
           if (y == 0) {
             const float m = p.rms ? 0.0f : s1[j] / count;
             s2[j] -= m * s1[j];
-            s1[j] = pivot[j] + m;
-            if (p.rms) s1[j] = 0.0f;
+            s1[j] = p.rms ? 0.0f : pivot[j] + m;
           }
           *a = s1[j];
           *b = s2[j];
@@ -358,29 +400,13 @@ __global__ __launch_bounds__(kThreads) void group_norm_map_stats_kernel(const Ar
       }
     }
     __syncthreads();
-    // Groups, a wave each; one that began in an earlier column is joined with what is there.
     const int c1 = min(n, c0 + t.tx * kPiece);
-    for (int g = c0 / p.d + wave; g <= (c1 - 1) / p.d; g += kThreads / 64) {
-      const int lo = max(g * p.d, c0) - c0, hi = min((g + 1) * p.d, c1) - c0;
-      const float here = (float)(hi - lo);
-      float m = 0.0f, q = 0.0f;
-      for (int i = lo + lane; i < hi; i += 64) m += cols[0][i];
-      m = wave_sum_f32(m) / here;
-      for (int i = lo + lane; i < hi; i += 64) {
-        const float e = cols[0][i] - m;
-        q += __builtin_fmaf(count * e, e, cols[1][i]);
-      }
-      q = wave_sum_f32(q);
-      if (lane == 0) {
-        if (g * p.d < c0) {
-          const float before = (float)(c0 - g * p.d), m0 = out[g], all = before + here, e = m - m0;
-          m = m0 + e * (here / all);
-          q += out[p.groups + g] + count * e * e * (before * here / all);
-        }
-        out[g] = m;
-        out[p.groups + g] = q;
-      }
-    }
+    if (p.d <= 8)
+      join_columns<8>(p, cols[0], cols[1], c0, c1, count, out);
+    else if (p.d <= 32)
+      join_columns<16>(p, cols[0], cols[1], c0, c1, count, out);
+    else
+      join_columns<64>(p, cols[0], cols[1], c0, c1, count, out);
   }
 }
 
@@ -392,22 +418,23 @@ __global__ __launch_bounds__(kThreads) void group_norm_map_join_kernel(const Arg
   const int64_t batch = row / p.groups;
   const int g = (int)(row % p.groups);
   const float* part = p.part + batch * p.runs * 2 * p.groups + g;
-  const double all = (double)p.length;
-  double m = 0.0;
-  const auto count = [&](int r) { return (double)(min(r * p.run + p.run, p.length) - r * p.run); };
-  for (int r = lane; r < p.runs; r += 64) m += count(r) * (double)part[(int64_t)r * 2 * p.groups];
-#pragma unroll
-  for (int s = 1; s < 64; s <<= 1) m += __shfl_xor(m, s);
-  m /= all;
-  double q = 0.0;
+  // Means and squares about the first run's mean.
+  const double all = (double)p.length, m0 = (double)part[0];
+  double m = 0.0, q = 0.0;
   for (int r = lane; r < p.runs; r += 64) {
-    const double e = (double)part[(int64_t)r * 2 * p.groups] - m;
-    q += (double)part[((int64_t)r * 2 + 1) * p.groups] + count(r) * (double)p.d * e * e;
+    const double count = (double)(min(r * p.run + p.run, p.length) - r * p.run);
+    const double e = (double)part[(int64_t)r * 2 * p.groups] - m0;
+    m += count * e;
+    q += (double)part[((int64_t)r * 2 + 1) * p.groups] + count * (double)p.d * e * e;
   }
 #pragma unroll
-  for (int s = 1; s < 64; s <<= 1) q += __shfl_xor(q, s);
+  for (int s = 1; s < 64; s <<= 1) {
+    m += __shfl_xor(m, s);
+    q += __shfl_xor(q, s);
+  }
   if (lane == 0) {
-    if (p.mean) p.mean[row] = (float)m;
+    q -= m * m / all * (double)p.d;
+    if (p.mean) p.mean[row] = (float)(m0 + m / all);
     p.rstd[row] = (float)(1.0 / __builtin_sqrt(q / (all * p.d) + (double)p.eps));
   }
 }
@@ -417,26 +444,37 @@ struct Columns {
   float w[kPiece], b[kPiece], mean[kPiece], rstd[kPiece];
 };
 
+// f(j, group of channel c + j), with one division.
+template <typename F>
+__device__ __forceinline__ void each_group(const Args& p, int c, int n, F f) {
+  int g = c / p.d, left = p.d - (c - g * p.d);
+#pragma unroll
+  for (int j = 0; j < kPiece; ++j) {
+    f(j, g);
+    if (--left == 0 && c + j + 1 < n) ++g, left = p.d;
+  }
+}
+
+template <bool kShort>
 __device__ __forceinline__ void load_columns(const Args& p, int64_t batch, int c, int n, Columns* k) {
   fill(k->w, 1.0f);
   fill(k->b, 0.0f);
   if (p.weight) {
-    Raw8<float> r = request_at(p.weight, c, n);
-    finish_at(r, c, n, k->w);
+    Raw8<float> r = request_at<kShort>(p.weight, c, n);
+    finish_at<kShort>(r, c, n, k->w);
   }
   if (p.bias) {
-    Raw8<float> r = request_at(p.bias, c, n);
-    finish_at(r, c, n, k->b);
+    Raw8<float> r = request_at<kShort>(p.bias, c, n);
+    finish_at<kShort>(r, c, n, k->b);
   }
-#pragma unroll
-  for (int j = 0; j < kPiece; ++j) {
-    const int64_t row = batch * p.groups + min(c + j, n - 1) / p.d;
+  each_group(p, c, n, [&](int j, int g) {
+    const int64_t row = batch * p.groups + g;
     k->mean[j] = p.rms ? 0.0f : p.mean[row];
     k->rstd[j] = p.rstd[row];
-  }
+  });
 }
 
-template <typename T, bool kGated>
+template <typename T, bool kGated, bool kShort>
 __global__ __launch_bounds__(kThreads) void group_norm_map_fwd_kernel(const Args p) {
   const Plane t = plane(p.channels);
   const int64_t batch = blockIdx.x / p.runs;
@@ -447,23 +485,22 @@ __global__ __launch_bounds__(kThreads) void group_norm_map_fwd_kernel(const Args
   if (t.y >= t.ty) return;
   for (int c = t.x * kPiece; c < n; c += t.tx * kPiece) {
     Columns k;
-    load_columns(p, batch, c, n, &k);
-    constexpr int kAhead = 4;
-    for (int64_t l = l0 + t.y; l < l1; l += kAhead * t.ty) {
-      Raw8<T> rx[kAhead], rz[kAhead];
+    load_columns<kShort>(p, batch, c, n, &k);
+    for (int64_t l = l0 + t.y; l < l1; l += kAhead<T, kGated ? 2 : 1> * t.ty) {
+      Raw8<T> rx[kAhead<T, kGated ? 2 : 1>], rz[kAhead<T, kGated ? 2 : 1>];
 #pragma unroll
-      for (int u = 0; u < kAhead; ++u) {
+      for (int u = 0; u < kAhead<T, kGated ? 2 : 1>; ++u) {
         const int64_t at = base + min(l + u * t.ty, l1 - 1) * n;
-        rx[u] = request_at(static_cast<const T*>(p.x) + at, c, n);
-        if constexpr (kGated) rz[u] = request_at(static_cast<const T*>(p.z) + at, c, n);
+        rx[u] = request_at<kShort>(static_cast<const T*>(p.x) + at, c, n);
+        if constexpr (kGated) rz[u] = request_at<kShort>(static_cast<const T*>(p.z) + at, c, n);
       }
 #pragma unroll
-      for (int u = 0; u < kAhead; ++u) {
+      for (int u = 0; u < kAhead<T, kGated ? 2 : 1>; ++u) {
         if (l + u * t.ty >= l1) break;
         float v[kPiece], z[kPiece];
-        finish_at(rx[u], c, n, v);
+        finish_at<kShort>(rx[u], c, n, v);
         fill(z, 0.0f);
-        if constexpr (kGated) finish_at(rz[u], c, n, z);
+        if constexpr (kGated) finish_at<kShort>(rz[u], c, n, z);
 #pragma unroll
         for (int j = 0; j < kPiece; ++j)
           v[j] = output((v[j] - k.mean[j]) * k.rstd[j], k.w[j], k.b[j], z[j], p.silu, kGated);
@@ -474,7 +511,7 @@ __global__ __launch_bounds__(kThreads) void group_norm_map_fwd_kernel(const Args
 }
 
 // part[batch][run][2][channels]: sums of dp n and of dp.
-template <typename T, bool kGated>
+template <typename T, bool kGated, bool kShort>
 __global__ __launch_bounds__(kThreads) void group_norm_map_sums_kernel(const Args p) {
   __shared__ float cols[2][kThreads * kPiece];
   const Plane t = plane(p.channels);
@@ -492,25 +529,24 @@ __global__ __launch_bounds__(kThreads) void group_norm_map_sums_kernel(const Arg
     fill(ab, 0.0f);
     if (live) {
       Columns k;
-      load_columns(p, batch, c, n, &k);
-      constexpr int kAhead = 4;
-      for (int64_t l = l0 + t.y; l < l1; l += kAhead * t.ty) {
-        Raw8<T> rx[kAhead], rd[kAhead], rz[kAhead];
+      load_columns<kShort>(p, batch, c, n, &k);
+      for (int64_t l = l0 + t.y; l < l1; l += kAhead<T, kGated ? 3 : 2> * t.ty) {
+        Raw8<T> rx[kAhead<T, kGated ? 3 : 2>], rd[kAhead<T, kGated ? 3 : 2>], rz[kAhead<T, kGated ? 3 : 2>];
 #pragma unroll
-        for (int u = 0; u < kAhead; ++u) {
+        for (int u = 0; u < kAhead<T, kGated ? 3 : 2>; ++u) {
           const int64_t at = base + min(l + u * t.ty, l1 - 1) * n;
-          rx[u] = request_at(static_cast<const T*>(p.x) + at, c, n);
-          rd[u] = request_at(static_cast<const T*>(p.dy) + at, c, n);
-          if constexpr (kGated) rz[u] = request_at(static_cast<const T*>(p.z) + at, c, n);
+          rx[u] = request_at<kShort>(static_cast<const T*>(p.x) + at, c, n);
+          rd[u] = request_at<kShort>(static_cast<const T*>(p.dy) + at, c, n);
+          if constexpr (kGated) rz[u] = request_at<kShort>(static_cast<const T*>(p.z) + at, c, n);
         }
 #pragma unroll
-        for (int u = 0; u < kAhead; ++u) {
+        for (int u = 0; u < kAhead<T, kGated ? 3 : 2>; ++u) {
           if (l + u * t.ty >= l1) break;
           float v[kPiece], d[kPiece], z[kPiece];
-          finish_at(rx[u], c, n, v);
-          finish_at(rd[u], c, n, d);
+          finish_at<kShort>(rx[u], c, n, v);
+          finish_at<kShort>(rd[u], c, n, d);
           fill(z, 0.0f);
-          if constexpr (kGated) finish_at(rz[u], c, n, z);
+          if constexpr (kGated) finish_at<kShort>(rz[u], c, n, z);
 #pragma unroll
           for (int j = 0; j < kPiece; ++j) {
             float dz;
@@ -542,43 +578,69 @@ __global__ __launch_bounds__(kThreads) void group_norm_map_sums_kernel(const Arg
   }
 }
 
-// sums[0 / 1][batch, group]: mean over the group of g n and of g (g = dp weight);
-// dweight and dbias.  A block has one group; a channel's runs are added in
-// order, channels and batch rows likewise.
-__global__ __launch_bounds__(kThreads) void group_norm_map_reduce_kernel(const Args p, float* dweight, float* dbias) {
-  __shared__ float parts[2][kThreads / 64];
-  const int g = blockIdx.x, n = (int)p.channels, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t rows = p.batch * p.groups;
-  const float inv = 1.0f / ((float)p.length * (float)p.d);
-  for (int64_t b = 0; b < p.batch; ++b) {
-    float c1 = 0.0f, c2 = 0.0f;
-    for (int i = threadIdx.x; i < p.d; i += kThreads) {
-      const int c = g * p.d + i;
-      const float* at = p.part + b * p.runs * 2 * n + c;
-      float aw = 0.0f, ab = 0.0f;
-      for (int r = 0; r < p.runs; ++r) {
-        aw += at[(int64_t)r * 2 * n];
-        ab += at[((int64_t)r * 2 + 1) * n];
-      }
-      const float w = p.weight ? p.weight[c] : 1.0f;
-      c2 = __builtin_fmaf(aw, w, c2);
-      c1 = __builtin_fmaf(ab, w, c1);
-      if (dweight) dweight[c] = b ? dweight[c] + aw : aw;
-      if (dbias) dbias[c] = b ? dbias[c] + ab : ab;
+// A batch row's runs of sums added into its first run's place: 32 columns of the
+// 2 x channels a block, 16 slices of the runs, each added in order.
+__global__ __launch_bounds__(512) void group_norm_map_columns_kernel(const Args p, int64_t tiles) {
+  __shared__ float sums[16][33];
+  const int col = threadIdx.x & 31, slice = threadIdx.x >> 5;
+  const int64_t batch = blockIdx.x / tiles, n = 2 * p.channels, c = blockIdx.x % tiles * 32 + col;
+  float* part = p.part + batch * p.runs * n;
+  float t = 0.0f;
+  if (c < n) {
+    constexpr int kRows = 8;
+    for (int r = slice; r < p.runs; r += kRows * 16) {
+      float v[kRows];
+#pragma unroll
+      for (int j = 0; j < kRows; ++j) v[j] = part[min(r + j * 16, p.runs - 1) * n + c];
+#pragma unroll
+      for (int j = 0; j < kRows; ++j) t += r + j * 16 < p.runs ? v[j] : 0.0f;
     }
-    c1 = wave_sum_f32(c1);
-    c2 = wave_sum_f32(c2);
-    __syncthreads();
-    if (lane == 0) parts[0][wave] = c2, parts[1][wave] = c1;
-    __syncthreads();
-    if (threadIdx.x < 2) {
-      const float* s = parts[threadIdx.x];
-      p.sums[threadIdx.x * rows + b * p.groups + g] = ((s[0] + s[1]) + (s[2] + s[3])) * inv;
-    }
+  }
+  sums[slice][col] = t;
+  __syncthreads();
+  if (slice == 0 && c < n) {
+#pragma unroll
+    for (int i = 1; i < 16; ++i) t += sums[i][col];
+    part[c] = t;
   }
 }
 
-template <typename T, bool kGated>
+// sums[0 / 1][batch, group]: mean over the group of g n and of g (g = dp weight),
+// a wave each; in the blocks behind those, dweight and dbias, a thread a column,
+// batch rows added in order.
+__global__ __launch_bounds__(kThreads) void group_norm_map_reduce_kernel(const Args p, int64_t group_blocks,
+                                                                         float* dweight, float* dbias) {
+  const int64_t n = p.channels, rows = p.batch * p.groups, pitch = p.runs * 2 * n;
+  if (blockIdx.x >= group_blocks) {
+    const int64_t c = (blockIdx.x - group_blocks) * kThreads + threadIdx.x;
+    float* out = c < n ? dweight : dbias;
+    if (c >= 2 * n || !out) return;
+    float t = 0.0f;
+    for (int64_t b = 0; b < p.batch; ++b) t += p.part[b * pitch + c];
+    out[c < n ? c : c - n] = t;
+    return;
+  }
+  const int lane = threadIdx.x & 63;
+  const int64_t row = (int64_t)blockIdx.x * (kThreads / 64) + (threadIdx.x >> 6);
+  if (row >= rows) return;
+  const int64_t first = row % p.groups * p.d;
+  const float* at = p.part + row / p.groups * pitch + first;
+  float c1 = 0.0f, c2 = 0.0f;
+  for (int i = lane; i < p.d; i += 64) {
+    const float w = p.weight ? p.weight[first + i] : 1.0f;
+    c2 = __builtin_fmaf(at[i], w, c2);
+    c1 = __builtin_fmaf(at[n + i], w, c1);
+  }
+  const float inv = 1.0f / ((float)p.length * (float)p.d);
+  c1 = group_sum<64>(c1);
+  c2 = group_sum<64>(c2);
+  if (lane == 0) {
+    p.sums[row] = c2 * inv;
+    p.sums[rows + row] = c1 * inv;
+  }
+}
+
+template <typename T, bool kGated, bool kShort>
 __global__ __launch_bounds__(kThreads) void group_norm_map_bwd_kernel(const Args p) {
   const Plane t = plane(p.channels);
   const int64_t batch = blockIdx.x / p.runs;
@@ -589,32 +651,30 @@ __global__ __launch_bounds__(kThreads) void group_norm_map_bwd_kernel(const Args
   if (t.y >= t.ty) return;
   for (int c = t.x * kPiece; c < n; c += t.tx * kPiece) {
     Columns k;
-    load_columns(p, batch, c, n, &k);
+    load_columns<kShort>(p, batch, c, n, &k);
     float c1[kPiece], c2[kPiece];
-#pragma unroll
-    for (int j = 0; j < kPiece; ++j) {
-      const int64_t row = batch * p.groups + min(c + j, n - 1) / p.d;
+    each_group(p, c, n, [&](int j, int g) {
+      const int64_t row = batch * p.groups + g;
       c2[j] = p.sums[row];
       c1[j] = p.rms ? 0.0f : p.sums[rows + row];
-    }
-    constexpr int kAhead = 2;
-    for (int64_t l = l0 + t.y; l < l1; l += kAhead * t.ty) {
-      Raw8<T> rx[kAhead], rd[kAhead], rz[kAhead];
+    });
+    for (int64_t l = l0 + t.y; l < l1; l += kAhead<T, kGated ? 3 : 2> * t.ty) {
+      Raw8<T> rx[kAhead<T, kGated ? 3 : 2>], rd[kAhead<T, kGated ? 3 : 2>], rz[kAhead<T, kGated ? 3 : 2>];
 #pragma unroll
-      for (int u = 0; u < kAhead; ++u) {
+      for (int u = 0; u < kAhead<T, kGated ? 3 : 2>; ++u) {
         const int64_t at = base + min(l + u * t.ty, l1 - 1) * n;
-        rx[u] = request_at(static_cast<const T*>(p.x) + at, c, n);
-        rd[u] = request_at(static_cast<const T*>(p.dy) + at, c, n);
-        if constexpr (kGated) rz[u] = request_at(static_cast<const T*>(p.z) + at, c, n);
+        rx[u] = request_at<kShort>(static_cast<const T*>(p.x) + at, c, n);
+        rd[u] = request_at<kShort>(static_cast<const T*>(p.dy) + at, c, n);
+        if constexpr (kGated) rz[u] = request_at<kShort>(static_cast<const T*>(p.z) + at, c, n);
       }
 #pragma unroll
-      for (int u = 0; u < kAhead; ++u) {
+      for (int u = 0; u < kAhead<T, kGated ? 3 : 2>; ++u) {
         if (l + u * t.ty >= l1) break;
         float v[kPiece], d[kPiece], z[kPiece], dz[kPiece];
-        finish_at(rx[u], c, n, v);
-        finish_at(rd[u], c, n, d);
+        finish_at<kShort>(rx[u], c, n, v);
+        finish_at<kShort>(rd[u], c, n, d);
         fill(z, 0.0f);
-        if constexpr (kGated) finish_at(rz[u], c, n, z);
+        if constexpr (kGated) finish_at<kShort>(rz[u], c, n, z);
 #pragma unroll
         for (int j = 0; j < kPiece; ++j) {
           const float m = (v[j] - k.mean[j]) * k.rstd[j];
@@ -649,7 +709,8 @@ Plan make_plan(int64_t batch, int64_t length, int64_t channels, int64_t groups) 
     p.pieces = 1;
     while ((int64_t)p.lanes * kPiece * p.pieces < d) p.pieces *= 2;
     const int64_t per_block = kThreads / p.lanes;
-    p.row_blocks = (batch * groups + per_block - 1) / per_block;
+    const int64_t fwd_rows = per_block * rows_ahead(p.pieces);
+    p.row_blocks = (batch * groups + fwd_rows - 1) / fwd_rows;
     // Batch rows side by side: enough for the chip's lanes, and no more partial rows than 512.
     p.stride = std::min<int64_t>(batch, std::max<int64_t>(1, std::min<int64_t>(512, 2048 * per_block / groups)));
     p.bwd_blocks = (p.stride * groups + per_block - 1) / per_block;
@@ -709,11 +770,17 @@ hipError_t launch_fwd(const Args& a, const Plan& p, hipStream_t st) {
     return hipGetLastError();
   }
   const dim3 grid((unsigned)(a.batch * p.runs));
-  hipLaunchKernelGGL(group_norm_map_stats_kernel<T>, grid, threads, 0, st, a);
+  if (a.channels < kPiece)
+    hipLaunchKernelGGL((group_norm_map_stats_kernel<T, true>), grid, threads, 0, st, a);
+  else
+    hipLaunchKernelGGL((group_norm_map_stats_kernel<T, false>), grid, threads, 0, st, a);
   const int64_t per_block = kThreads / 64;
   hipLaunchKernelGGL(group_norm_map_join_kernel, dim3((unsigned)((a.batch * a.groups + per_block - 1) / per_block)),
                      threads, 0, st, a);
-  hipLaunchKernelGGL((group_norm_map_fwd_kernel<T, kGated>), grid, threads, 0, st, a);
+  if (a.channels < kPiece)
+    hipLaunchKernelGGL((group_norm_map_fwd_kernel<T, kGated, true>), grid, threads, 0, st, a);
+  else
+    hipLaunchKernelGGL((group_norm_map_fwd_kernel<T, kGated, false>), grid, threads, 0, st, a);
   return hipGetLastError();
 }
 
@@ -731,9 +798,22 @@ hipError_t launch_bwd(const Args& a, const Plan& p, float* dweight, float* dbias
     return hipGetLastError();
   }
   const dim3 grid((unsigned)(a.batch * p.runs));
-  hipLaunchKernelGGL((group_norm_map_sums_kernel<T, kGated>), grid, threads, 0, st, a);
-  hipLaunchKernelGGL(group_norm_map_reduce_kernel, dim3((unsigned)a.groups), threads, 0, st, a, dweight, dbias);
-  hipLaunchKernelGGL((group_norm_map_bwd_kernel<T, kGated>), grid, threads, 0, st, a);
+  const bool narrow = a.channels < kPiece;
+  if (narrow)
+    hipLaunchKernelGGL((group_norm_map_sums_kernel<T, kGated, true>), grid, threads, 0, st, a);
+  else
+    hipLaunchKernelGGL((group_norm_map_sums_kernel<T, kGated, false>), grid, threads, 0, st, a);
+  const int64_t tiles = (2 * a.channels + 31) / 32, per_block = kThreads / 64;
+  const int64_t group_blocks = (a.batch * a.groups + per_block - 1) / per_block;
+  const int64_t column_blocks = dweight || dbias ? (2 * a.channels + kThreads - 1) / kThreads : 0;
+  if (p.runs > 1)
+    hipLaunchKernelGGL(group_norm_map_columns_kernel, dim3((unsigned)(a.batch * tiles)), dim3(512), 0, st, a, tiles);
+  hipLaunchKernelGGL(group_norm_map_reduce_kernel, dim3((unsigned)(group_blocks + column_blocks)), threads, 0, st, a,
+                     group_blocks, dweight, dbias);
+  if (narrow)
+    hipLaunchKernelGGL((group_norm_map_bwd_kernel<T, kGated, true>), grid, threads, 0, st, a);
+  else
+    hipLaunchKernelGGL((group_norm_map_bwd_kernel<T, kGated, false>), grid, threads, 0, st, a);
   return hipGetLastError();
 }
 
