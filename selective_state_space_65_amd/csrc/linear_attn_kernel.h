@@ -143,51 +143,67 @@ struct Traits<float> {
 // A tile of rows of COLS elements in LDS.  Unit u (16 bytes) of row r lies at
 // u ^ key(r).  The key puts the 16 rows of one unit, which a row read takes at
 // once, on different banks; and of a column read the 4 rows x 4 units of 32 lanes
-// (bf16), or the two rows 8 apart (fp32).
+// (bf16), or the two rows 8 apart (fp32).  It is linear in the bits of r % 16, so a
+// lane needs one place (a byte offset) for all its reads of a kind: columns x further
+// on are place ^ x sizeof(T), rows 16 further on place + 16 kPitch, and rows j < 8
+// of 8 further on (place ^ 16 key(j)) + j kPitch, x and j constants.
 template <typename T, int COLS>
 struct Tile {
   static constexpr unsigned kUnits = COLS * sizeof(T) / 16;
   static constexpr unsigned kPerUnit = 16 / sizeof(T);
-  static __device__ __forceinline__ unsigned key(unsigned r) {
-    if constexpr (kUnits >= 16 && sizeof(T) == 2) return (r & 3) << 2 | (r >> 2 & 3);
-    if constexpr (kUnits >= 16) return r & 15;
-    if constexpr (kUnits == 8) return (r >> 1 & 1) << 2 | (r >> 2 & 3);
+  static constexpr unsigned kPitch = COLS * sizeof(T);
+  static constexpr __host__ __device__ unsigned key(unsigned r) {
+    if (kUnits >= 16 && sizeof(T) == 2) return (r & 3) << 2 | (r >> 2 & 3);
+    if (kUnits >= 16) return r & 15;
+    if (kUnits == 8) return (r >> 1 & 1) << 2 | (r >> 2 & 3);
     return r >> 2 & 3;
   }
   static __device__ __forceinline__ unsigned at(unsigned r, unsigned c) {  // element offset
     return (r * kUnits + (c / kPerUnit ^ key(r))) * kPerUnit + c % kPerUnit;
   }
-  // Values c .. c + 7 of row r; c is a multiple of 8.
-  static __device__ __forceinline__ Frag<T> row(const T* p, unsigned r, unsigned c) {
+  static __device__ __forceinline__ unsigned place(unsigned r, unsigned c) { return at(r, c) * sizeof(T); }
+  template <typename V>
+  static __device__ __forceinline__ V get(const T* p, unsigned place) {
+    return *reinterpret_cast<const V*>(reinterpret_cast<const char*>(p) + place);
+  }
+  // The 8 values of a row from place(row, column) on; the column is a multiple of 8.
+  static __device__ __forceinline__ Frag<T> row(const T* p, unsigned place, unsigned x, unsigned rows) {
     Frag<T> f;
+    const unsigned at = (place ^ (unsigned)(x * sizeof(T))) + rows * kPitch;
     if constexpr (sizeof(T) == 2) {
-      f.v = *reinterpret_cast<const bf16x8*>(p + at(r, c));
+      f.v = get<bf16x8>(p, at);
     } else {
-      const float4 lo = *reinterpret_cast<const float4*>(p + at(r, c));
-      const float4 hi = *reinterpret_cast<const float4*>(p + at(r, c + 4));
+      const float4 lo = get<float4>(p, at);
+      const float4 hi = get<float4>(p, (place ^ (unsigned)(x * sizeof(T) + 16)) + rows * kPitch);
       f.v[0] = lo.x; f.v[1] = lo.y; f.v[2] = lo.z; f.v[3] = lo.w;
       f.v[4] = hi.x; f.v[5] = hi.y; f.v[6] = hi.z; f.v[7] = hi.w;
     }
     return f;
   }
-  // Rows r .. r + 7 (r differs between the wave's halves) of the lane's column:
-  // c + lane % 32, or with kSwap that number with bits 2 and 3 exchanged.
-  template <bool kSwap>
-  static __device__ __forceinline__ Frag<T> column(const T* p, unsigned r, unsigned c, unsigned lane) {
-    Frag<T> f;
+  // Place of a column read: rows 8 (lane / 32) .. + 7 of the lane's column, c + lane % 32,
+  // or with swap that number with bits 2 and 3 exchanged; c is a multiple of 32.
+  static __device__ __forceinline__ unsigned column_place(bool swap, unsigned c, unsigned lane) {
     if constexpr (sizeof(T) == 2) {
       // Lane 4 j + i of 16 gives the address of row j's columns 4 i .. 4 i + 3 and
       // gets column 4 j + i of the four rows (the load transposes).
-      const unsigned i = lane & 3, q = kSwap ? (i & 1) << 1 | i >> 1 : i;
-      const unsigned col = c + (lane & 16) + 4 * q, row0 = r + (lane >> 2 & 3);
+      const unsigned i = lane & 3, q = swap ? (i & 1) << 1 | i >> 1 : i;
+      return place(8 * (lane >> 5) + (lane >> 2 & 3), c + (lane & 16) + 4 * q);
+    } else {
+      const unsigned i = lane & 31, q = swap ? (i & 19) | (i & 4) << 1 | (i & 8) >> 1 : i;
+      return place(8 * (lane >> 5), c + q);
+    }
+  }
+  static __device__ __forceinline__ Frag<T> column(const T* p, unsigned place, unsigned x, unsigned rows) {
+    Frag<T> f;
+    const auto at = [&](unsigned j) { return (place ^ (unsigned)(x * sizeof(T) ^ key(j) << 4)) + (rows + j) * kPitch; };
+    if constexpr (sizeof(T) == 2) {
       typedef __attribute__((address_space(3))) i16x4* lds_ptr;
-      const i16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(p + at(row0, col)));
-      const i16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(p + at(row0 + 4, col)));
+      const i16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(reinterpret_cast<const char*>(p) + at(0)));
+      const i16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(reinterpret_cast<const char*>(p) + at(4)));
       f.v = __builtin_bit_cast(bf16x8, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
     } else {
-      const unsigned i = lane & 31, q = kSwap ? (i & 19) | (i & 4) << 1 | (i & 8) >> 1 : i;
 #pragma unroll
-      for (unsigned j = 0; j < 8; ++j) f.v[j] = p[at(r + j, c + q)];
+      for (unsigned j = 0; j < 8; ++j) f.v[j] = get<float>(p, at(j));
     }
     return f;
   }
@@ -274,7 +290,8 @@ __device__ __forceinline__ bool rare(bool c) { return __builtin_expect(c, 0); }
 // v, unknown to the compiler: what is computed from it stays where it is used.
 // Else every LDS address of the chunk loop is computed before it and kept, in
 // registers that the products need.
-__device__ __forceinline__ int opaque(int v) {
+template <typename N>
+__device__ __forceinline__ N opaque(N v) {
   asm volatile("" : "+v"(v));
   return v;
 }
@@ -381,20 +398,36 @@ __device__ __forceinline__ const T* side_rows(const Side& s, int64_t batch_token
   return static_cast<const T*>(s.p) + (batch_tokens * s.heads + head / s.share) * s.d;
 }
 
+__device__ __forceinline__ void store4(float* p, float a, float b, float c, float d) {
+  const float v[4] = {a, b, c, d};
+  store_n<4>(p, v);
+}
+
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+
+__device__ __forceinline__ uint32_t round2(float a, float b) {
+  return __builtin_bit_cast(uint32_t, bf16x2{(__bf16)a, (__bf16)b});
+}
+
+__device__ __forceinline__ void store4(bf16_t* p, float a, float b, float c, float d) {
+  const words2 w = {round2(a, b), round2(c, d)};
+  __builtin_memcpy(p, &w, 8);
+}
+
 // A row's columns c + 8 g .. c + 8 g + 3, g = 0 .. 3: written from, and dotted with,
 // a lane's elements of a 32 x 32 accumulator.  Columns from n on are not there.
+// (heads of a row are limited so that byte offsets of a chunk's rows have 32 bits.)
 template <bool kWhole, typename T>
 __device__ __forceinline__ void store_columns(T* base, uint32_t row, int c, int n, const f32x16& v) {
+  T* const at = reinterpret_cast<T*>(reinterpret_cast<char*>(base) + (row + c) * (uint32_t)sizeof(T));
 #pragma unroll
   for (int g = 0; g < 4; ++g) {
-    const int at = c + 8 * g;
-    if (kWhole || at + 4 <= n) {
-      const float x[4] = {v[4 * g], v[4 * g + 1], v[4 * g + 2], v[4 * g + 3]};
-      store_n<4>(base + (row + at), x);
+    if (kWhole || c + 8 * g + 4 <= n) {
+      store4(at + 8 * g, v[4 * g], v[4 * g + 1], v[4 * g + 2], v[4 * g + 3]);
     } else {
 #pragma unroll
       for (int j = 0; j < 3; ++j)
-        if (at + j < n) Io<T>::store1(base + (row + at + j), v[4 * g + j]);
+        if (c + 8 * g + j < n) Io<T>::store1(at + 8 * g + j, v[4 * g + j]);
     }
   }
 }
@@ -454,7 +487,7 @@ __global__ __launch_bounds__(64 * NW, NK <= 4 ? 2 : 1) void linear_attn_kernel(c
   Decays<C>* const decays =
       reinterpret_cast<Decays<C>*>(lds + L::q_bytes + L::k_tiles * L::k_bytes + L::v_tiles * L::v_bytes + L::s_bytes);
   int* const again = reinterpret_cast<int*>(decays + 3);  // of chunk c in [c & 3]: some wave's outputs are not finite
-  const int thread = threadIdx.x, tid = thread, lane = tid & 63, lane0 = lane, col = lane & 31, half = lane >> 5;
+  const int thread = threadIdx.x, tid = thread, lane = tid & 63, col = lane & 31, half = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
 
   // ---- which rows, segment and columns this block has
@@ -546,6 +579,10 @@ __global__ __launch_bounds__(64 * NW, NK <= 4 ? 2 : 1) void linear_attn_kernel(c
     if (a.reset) next_reset = a.reset[at];
   };
   const bool decay_wave = wave == NW - 1;
+  // Places of this lane's reads and writes in the tiles.
+  const unsigned row16 = TileK::place(lane & 15, 8 * (lane >> 4)), row32 = TileK::place(col, 8 * half);
+  const unsigned scores_at = TileS::place(lane & 15, 4 * (lane >> 4)), scores_row = TileS::place(col, 8 * half);
+  const unsigned k_column = TileK::column_place(true, 0, lane), v_column = TileV::column_place(false, wave * 32, lane);
   float carried = 1.0f;  // decay of the whole segment
   if (dma) {
     if (dk < DK || dv - v0 < TV) {  // units behind the rows' ends stay 0
@@ -582,6 +619,7 @@ __global__ __launch_bounds__(64 * NW, NK <= 4 ? 2 : 1) void linear_attn_kernel(c
   // from registers to registers in every turn.
   do {
     const int tid = opaque(thread), lane = tid & 63, col = lane & 31, half = lane >> 5;
+    const unsigned k_other = (c & (L::k_tiles - 1)) * L::k_bytes;
     const bool whole = single < 0;
     const int64_t t0 = chunk_at(c) + (whole ? 0 : reverse ? chunk_len(chunk_at(c)) - 1 - single : single);
     const int len = whole ? chunk_len(t0) : 1;
@@ -650,13 +688,15 @@ __global__ __launch_bounds__(64 * NW, NK <= 4 ? 2 : 1) void linear_attn_kernel(c
       // ---- scores, a 16 x 16 tile at a time: rows s, columns t
       constexpr int kTiles = C / 16;
       const int quad = lane >> 4, c16 = lane & 15;
+      const unsigned k_place = opaque(row16) + k_other, q_place = opaque(row16), s_place = opaque(scores_at);
       for (int n = wave; n < kTiles * (kTiles + 1) / 2; n += NW) {
         const int hi = n < 1 ? 0 : n < 3 ? 1 : n < 6 ? 2 : 3, lo = n - hi * (hi + 1) / 2;
         const int ti = reverse ? lo : hi, si = reverse ? hi : lo;
         f32x4 x = {};
 #pragma unroll
         for (int m = 0; m < NK; ++m)
-          mma(x, TileK::row(ks, 16 * si + c16, 32 * m + 8 * quad), TileK::row(qs, 16 * ti + c16, 32 * m + 8 * quad));
+          mma(x, TileK::row(k_base, k_place + 16 * si * TileK::kPitch, 32 * m, 0),
+              TileK::row(qs, q_place + 16 * ti * TileK::kPitch, 32 * m, 0));
         const int t = 16 * ti + c16, s0 = 16 * si + 4 * quad;
         const double gt = d.sum[t];
         const float s_both = p.s_in * p.s_up;
@@ -667,20 +707,20 @@ __global__ __launch_bounds__(64 * NW, NK <= 4 ? 2 : 1) void linear_attn_kernel(c
           const float e = exp2_hw((float)(gt - d.sum[s0 + j]));
           y[j] = late <= (reverse ? j : -j) ? x[j] * (e * s_both) : 0.0f;
         }
+        const unsigned s_at = (s_place ^ 16 * si * (unsigned)sizeof(T)) + 16 * ti * TileS::kPitch;
+        unsigned char* const to = reinterpret_cast<unsigned char*>(ss) + s_at;
         if constexpr (sizeof(T) == 2) {
 #pragma unroll
           for (int part = 0; part < kParts; ++part) {
-            words2 w;
-            w.x = Io<bf16_t>::pack2(y[0], y[1]);
-            w.y = Io<bf16_t>::pack2(y[2], y[3]);
-            *reinterpret_cast<words2*>(ss + part * C * C + TileS::at(t, s0)) = w;
+            const words2 w = {round2(y[0], y[1]), round2(y[2], y[3])};
+            *reinterpret_cast<words2*>(to + part * C * C * sizeof(T)) = w;
             y[0] -= bf16_lo(w.x);
             y[1] -= bf16_hi(w.x);
             y[2] -= bf16_lo(w.y);
             y[3] -= bf16_hi(w.y);
           }
         } else {
-          *reinterpret_cast<float4*>(ss + TileS::at(t, s0)) = make_float4(y[0], y[1], y[2], y[3]);
+          *reinterpret_cast<float4*>(to) = make_float4(y[0], y[1], y[2], y[3]);
         }
       }
       // ---- S^T q^T
@@ -695,7 +735,7 @@ __global__ __launch_bounds__(64 * NW, NK <= 4 ? 2 : 1) void linear_attn_kernel(c
         split<kParts>(s, x);
         Frag<T> q[RT];
 #pragma unroll
-        for (int ti = 0; ti < RT; ++ti) q[ti] = TileK::row(qs, 32 * ti + (lane0 & 31), 16 * f + 8 * (lane0 >> 5));
+        for (int ti = 0; ti < RT; ++ti) q[ti] = TileK::row(qs, row32, 16 * f, 32 * ti);
 #pragma unroll
         for (int part = 0; part < kParts; ++part)
 #pragma unroll
@@ -714,18 +754,18 @@ __global__ __launch_bounds__(64 * NW, NK <= 4 ? 2 : 1) void linear_attn_kernel(c
     }
     Frag<T> v[C / 16];
 #pragma unroll
-    for (int f = 0; f < C / 16; ++f)
-      v[f] = TileV::template column<false>(vs, 16 * f + 8 * (lane0 >> 5), wave * 32, lane0);
+    for (int f = 0; f < C / 16; ++f) v[f] = TileV::column(vs, v_column, 0, 16 * f);
     bool skip = !whole && !pending;
     if (whole) pending = d.slow;
     if constexpr (kOut) {
       lds_barrier();
       if (whole && dma && c + 1 < chunks) request_qv(c + 1);
       // ---- v^T scores^T
+      const unsigned s_row = opaque(scores_row);
       const auto seen = [&](int ti, int f) {
 #pragma unroll
         for (int part = 0; part < kParts; ++part)
-          mma(out[ti], v[f], TileS::row(ss + part * C * C, 32 * ti + col, 16 * f + 8 * half));
+          mma(out[ti], v[f], TileS::row(ss + part * C * C, s_row, 16 * f, 32 * ti));
       };
 #pragma unroll
       for (int f = 0; f < 2; ++f)
@@ -799,6 +839,7 @@ __global__ __launch_bounds__(64 * NW, NK <= 4 ? 2 : 1) void linear_attn_kernel(c
 #pragma unroll
         for (int i = 0; i < 16; ++i) acc[b][i] = drop_mul(total, acc[b][i]);
       if (!rare(!whole && d.zeros)) {
+        const unsigned k_col = opaque(k_column) + k_other;
 #pragma unroll
         for (int f = 0; f < C / 16; ++f) {
           float x[8];
@@ -812,7 +853,7 @@ __global__ __launch_bounds__(64 * NW, NK <= 4 ? 2 : 1) void linear_attn_kernel(c
           for (int b = 0; b < NK; b += kPair) {
             Frag<T> k[kPair];
 #pragma unroll
-            for (int u = 0; u < kPair; ++u) k[u] = TileK::template column<true>(ks, 16 * f + 8 * half, 32 * (b + u), lane);
+            for (int u = 0; u < kPair; ++u) k[u] = TileK::column(k_base, k_col, 32 * (b + u), 16 * f);
 #pragma unroll
             for (int part = kUp - 1; part >= 0; --part)
 #pragma unroll
