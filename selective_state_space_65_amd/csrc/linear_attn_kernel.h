@@ -296,6 +296,11 @@ __device__ __forceinline__ N opaque(N v) {
   return v;
 }
 
+__device__ __forceinline__ int opaque_scalar(int v) {
+  asm volatile("" : "+s"(v));
+  return v;
+}
+
 constexpr int kWaitVmcnt0 = 0x0F70;  // s_waitcnt vmcnt(0) expcnt(7) lgkmcnt(15): vector memory only
 
 // Rows of one operand of a chunk on their way from memory to LDS: straight there
@@ -511,9 +516,6 @@ __global__ __launch_bounds__(64 * NW, NK <= 4 ? 2 : 1) void linear_attn_kernel(c
   const int chunks = (int)((t_hi - t_lo + C - 1) / C);
   const float rate = a.rate[head];
   const bool constant = !a.step && !a.reset;
-  const T* const q_rows = kOut ? side_rows<T>(p.q, batch_tokens, head) : nullptr;
-  const T* const k_rows = side_rows<T>(p.k, batch_tokens, head);
-  const T* const v_rows = side_rows<T>(p.v, batch_tokens, head) + v0;
   // A chunk's rows are addressed by 32-bit offsets from its first (heads are limited so).
   const uint32_t k_stride = p.k.heads * dk, v_stride = p.v.heads * dv;  // q's rows lie as k's do
 
@@ -554,17 +556,29 @@ __global__ __launch_bounds__(64 * NW, NK <= 4 ? 2 : 1) void linear_attn_kernel(c
   uint32_t k_from[StageK::kEach], v_from[StageV::kEach];  // q's rows lie as k's do
   StageK::offsets(k_from, k_stride, dk, wave, lane);
   StageV::offsets(v_from, v_stride, dv - v0, wave, lane);
+  // First row of what is requested next; chunks are requested in their order.
+  const int64_t t_first = chunk_at(0);
+  const T* q_next = kOut ? side_rows<T>(p.q, batch_tokens, head) + t_first * (int64_t)k_stride : nullptr;
+  const T* k_next = side_rows<T>(p.k, batch_tokens, head) + t_first * (int64_t)k_stride;
+  const T* v_next = side_rows<T>(p.v, batch_tokens, head) + t_first * (int64_t)v_stride + v0;
+  const int k_move = reverse ? -C * (int)k_stride : C * (int)k_stride;
+  const int v_move = reverse ? -C * (int)v_stride : C * (int)v_stride;
+  const int last_len = (int)(t_hi - t_lo) - (chunks - 1) * C;  // tokens of the chunk at the segment's end
+  const auto len_of = [&](int i) { return i == (reverse ? 0 : chunks - 1) ? last_len : C; };
   const auto request_k = [&](int i) {
-    const int64_t t0 = chunk_at(i);
-    const int len = chunk_len(t0), id = opaque(tid);
-    StageK::dma(k_tile(i), k_rows + t0 * (int64_t)k_stride, k_from, dk, len, wave, id & 63);
+    const int len = len_of(i), id = opaque(tid);
+    StageK::dma(k_tile(i), k_next, k_from, dk, len, wave, id & 63);
+    k_next += k_move;
     if (rare(len < C)) StageK::clear(k_tile(i), len, id);
   };
   const auto request_qv = [&](int i) {
-    const int64_t t0 = chunk_at(i);
-    const int len = chunk_len(t0), id = opaque(tid);
-    if constexpr (kOut) StageK::dma(qs, q_rows + t0 * (int64_t)k_stride, k_from, dk, len, wave, id & 63);
-    StageV::dma(v_tile(i), v_rows + t0 * (int64_t)v_stride, v_from, dv - v0, len, wave, id & 63);
+    const int len = len_of(i), id = opaque(tid);
+    if constexpr (kOut) {
+      StageK::dma(qs, q_next, k_from, dk, len, wave, id & 63);
+      q_next += k_move;
+    }
+    StageV::dma(v_tile(i), v_next, v_from, dv - v0, len, wave, id & 63);
+    v_next += v_move;
     if (rare(len < C)) {
       if constexpr (kOut) StageK::clear(qs, len, id);
       StageV::clear(v_tile(i), len, id);
@@ -626,9 +640,11 @@ __global__ __launch_bounds__(64 * NW, NK <= 4 ? 2 : 1) void linear_attn_kernel(c
     const Decays<C>& d = whole ? decays[c & 1] : decays[2];
     T* const ks = k_tile(c);
     T* const vs = v_tile(c);
-    const T* const q_at = kOut ? q_rows + t0 * (int64_t)k_stride : nullptr;
-    const T* const k_at = k_rows + t0 * (int64_t)k_stride;
-    const T* const v_at = v_rows + t0 * (int64_t)v_stride;
+    // This chunk's first rows, found anew where they are wanted: kept, they take
+    // scalar registers that the chunks in their common course lack.
+    const auto q_at = [&] { const Role& o = a.role[opaque_scalar(r)]; return side_rows<T>(o.q, batch_tokens + t0, head); };
+    const auto k_at = [&] { const Role& o = a.role[opaque_scalar(r)]; return side_rows<T>(o.k, batch_tokens + t0, head); };
+    const auto v_at = [&] { const Role& o = a.role[opaque_scalar(r)]; return side_rows<T>(o.v, batch_tokens + t0, head) + v0; };
     if (!rare(!whole)) {
       if (kOut && p.save) {
         // Forward: the state before a block; reverse: the state behind it.
@@ -640,16 +656,16 @@ __global__ __launch_bounds__(64 * NW, NK <= 4 ? 2 : 1) void linear_attn_kernel(c
         land();
       }
       if (rare(!dma)) {
-        if constexpr (kOut) StageK::pieces(qs, q_at, k_stride, dk, len, tid);
-        StageK::pieces(ks, k_at, k_stride, dk, len, tid);
-        StageV::pieces(vs, v_at, v_stride, dv - v0, len, tid);
+        if constexpr (kOut) StageK::pieces(qs, q_at(), k_stride, dk, len, tid);
+        StageK::pieces(ks, k_at(), k_stride, dk, len, tid);
+        StageV::pieces(vs, v_at(), v_stride, dv - v0, len, tid);
         lds_barrier();
       }
     } else {
       // The token in row 0, zeros in the others.
-      if constexpr (kOut) StageK::elements(qs, q_at, k_stride, dk, 1);
-      StageK::elements(ks, k_at, k_stride, dk, 1);
-      StageV::elements(vs, v_at, v_stride, dv - v0, 1);
+      if constexpr (kOut) StageK::elements(qs, q_at(), k_stride, dk, 1);
+      StageK::elements(ks, k_at(), k_stride, dk, 1);
+      StageV::elements(vs, v_at(), v_stride, dv - v0, 1);
       if (tid < C) {
         const float each = decays[c & 1].each[t0 - chunk_at(c)];
         Decays<C>& one = decays[2];
@@ -872,6 +888,8 @@ __global__ __launch_bounds__(64 * NW, NK <= 4 ? 2 : 1) void linear_attn_kernel(c
       single = -1;
       pending = false;
       if (++c < chunks && dma && kOut) {  // the next chunk's, which the single tokens wrote over
+        q_next -= k_move;
+        v_next -= v_move;
         request_qv(c);
         land();
       }
