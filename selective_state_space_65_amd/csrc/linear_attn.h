@@ -31,8 +31,10 @@ struct Role {
   const float* start;    // state a segment starts from (null: zero): slot segment * start_step
   int64_t start_slots;   // of start_slots slots for each (batch, head)
   int64_t start_step;
-  float* save;           // state at the border of every block of kBlock tokens, may be null
-  int64_t save_slots;    // (forward: before block c, and behind the last; reverse: behind block c)
+  float* save;           // forward: state in front of every block of kBlock tokens, and behind the last; may be null
+  const float* meet;     // reverse: states as save has them, that this pass's are multiplied with
+  double* cross;         // there: <meet, state> in parts, [batch, heads, border][v.d / 32 rounded up]
+  int64_t slots;         // of save, meet and cross for each (batch, head)
   float* last;           // state after the last (reverse: before the first) token, may be null
   Side with;             // rows that the outputs are dotted with (p may be null)
   float* dots;           // [v.d / 32 rounded up][batch, heads, seqlen]
@@ -52,7 +54,7 @@ struct Args {
   const void* step;      // may be null
   const uint8_t* reset;  // may be null
   int segments;
-  int64_t segment_len;   // a multiple of kBlock
+  int64_t segment_len;   // a multiple of 64
 };
 
 // Columns of one block: 64, or 128 where v.d is above 64.

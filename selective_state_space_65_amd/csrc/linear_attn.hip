@@ -83,28 +83,26 @@ __global__ __launch_bounds__(256) void linear_attn_join_kernel(const Join one, c
 template <typename T>
 __global__ __launch_bounds__(256) void linear_attn_group_kernel(const float* part, T* out, int64_t n, int groups,
                                                                 int share, int d) {
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;  // [token][group][d]
-  if (i >= n) return;
-  const int64_t tg = i / d;
-  const float* at = part + tg * share * d + i % d;
-  float t = at[0];
-  for (int h = 1; h < share; ++h) t += at[(int64_t)h * d];
-  Io<T>::store1(out + i, t);
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {  // [token][group][d]
+    const int64_t tg = i / d;
+    const float* at = part + tg * share * d + i % d;
+    float t = at[0];
+    for (int h = 1; h < share; ++h) t += at[(int64_t)h * d];
+    Io<T>::store1(out + i, t);
+  }
 }
 
 struct DecayArgs {
-  const float* states;   // ckpt: [rows][blocks + 1][n]
-  const float* dstates;  // [rows][blocks][n], behind each block
-  const float* dots_q;   // [parts_q][rows][seqlen]
-  const float* dots_k;   // [parts_k][rows][seqlen]
-  const float* dh0;      // [rows][n], in front of the first block
+  const double* cross;   // <S, R> in parts, [rows][blocks + 1][parts_v], in front of each block and behind the last
+  const float* dots_q;   // [parts_qk][rows][seqlen]
+  const float* dots_k;   // the same
   const float* rate;
   const void* step;      // may be null
   const uint8_t* reset;  // may be null
   void* dstep;           // may be null
   double* drate;         // [rows][blocks]
-  int64_t n, rows, seqlen;
-  int heads, blocks, parts_q, parts_k;
+  int64_t rows, seqlen;
+  int heads, blocks, parts_qk, parts_v;
 };
 
 __device__ __forceinline__ double wave_sum(double v) {
@@ -116,19 +114,16 @@ __device__ __forceinline__ double wave_sum(double v) {
 // One block of kBlock tokens of one (batch, head); a thread has two tokens.
 template <typename T>
 __global__ __launch_bounds__(256) void linear_attn_decay_kernel(const DecayArgs p) {
-  __shared__ double slots[4][4];
+  __shared__ double slots[1][4];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int block = (int)(blockIdx.x % p.blocks);
   const int64_t row = blockIdx.x / p.blocks;
   const int head = (int)(row % p.heads);
-  const float* s = p.states + (row * (p.blocks + 1) + block + 1) * p.n;
-  const float* r = p.dstates + (row * p.blocks + block) * p.n;
-  const float* s0 = s - p.n;  // in front of the block
-  const float* r0 = block ? r - p.n : p.dh0 + row * p.n;
-  double cross = 0.0, front = 0.0;
-  for (int64_t i = tid; i < p.n; i += 256) {
-    cross += (double)s[i] * (double)r[i];
-    front += (double)s0[i] * (double)r0[i];
+  const double* at_front = p.cross + (row * (p.blocks + 1) + block) * p.parts_v;
+  double cross = 0.0, front = 0.0;  // <S, R> behind and in front of the block
+  for (int i = 0; i < p.parts_v; ++i) {
+    front += at_front[i];
+    cross += at_front[p.parts_v + i];
   }
   const int64_t t0 = (int64_t)block * kBlock;
   double w[2] = {0.0, 0.0};
@@ -136,26 +131,24 @@ __global__ __launch_bounds__(256) void linear_attn_decay_kernel(const DecayArgs 
   for (int j = 0; j < 2; ++j) {
     const int64_t t = t0 + 2 * tid + j;
     if (t >= p.seqlen) continue;
-    for (int i = 0; i < p.parts_q; ++i) w[j] += (double)p.dots_q[(i * p.rows + row) * p.seqlen + t];
-    for (int i = 0; i < p.parts_k; ++i) w[j] -= (double)p.dots_k[(i * p.rows + row) * p.seqlen + t];
+    for (int i = 0; i < p.parts_qk; ++i) {
+      const int64_t at = (i * p.rows + row) * p.seqlen + t;
+      w[j] += (double)p.dots_q[at] - (double)p.dots_k[at];
+    }
   }
-  cross = wave_sum(cross);
-  front = wave_sum(front);
   double behind = w[0] + w[1];  // of this lane and those behind it
 #pragma unroll
   for (int m = 1; m < 64; m <<= 1) {
     const double o = __shfl_down(behind, m);
     if (lane + m < 64) behind += o;
   }
-  if (lane == 0) slots[0][wave] = cross, slots[1][wave] = behind, slots[3][wave] = front;
+  if (lane == 0) slots[0][wave] = behind;
   __syncthreads();
-  cross = slots[0][0] + slots[0][1] + slots[0][2] + slots[0][3];
-  const double all = slots[1][0] + slots[1][1] + slots[1][2] + slots[1][3];
-  for (int v = 3; v > wave; --v) behind += slots[1][v];
+  const double all = slots[0][0] + slots[0][1] + slots[0][2] + slots[0][3];
+  for (int v = 3; v > wave; --v) behind += slots[0][v];
   // What the sums say is carried into the block is known on its own, <S, R> in
   // front of it.  The sums' roundings between the two ends are spread over the
   // tokens as a walk between two fixed ends would be.
-  front = slots[3][0] + slots[3][1] + slots[3][2] + slots[3][3];
   double off = front - (cross + all);
   if (!(__builtin_fabs(off) < 1e300)) off = 0.0;
   const int64_t count = min((int64_t)kBlock, p.seqlen - (int64_t)block * kBlock);
@@ -177,9 +170,9 @@ __global__ __launch_bounds__(256) void linear_attn_decay_kernel(const DecayArgs 
     if (p.dstep) Io<T>::store1(static_cast<T*>(p.dstep) + at * p.heads + head, dropped ? 0.0f : (float)(-g * rate));
   }
   sum = wave_sum(sum);
-  if (lane == 0) slots[2][wave] = sum;
+  if (lane == 0) slots[1][wave] = sum;
   __syncthreads();
-  if (tid == 0) p.drate[row * p.blocks + block] = (slots[2][0] + slots[2][1]) + (slots[2][2] + slots[2][3]);
+  if (tid == 0) p.drate[row * p.blocks + block] = (slots[1][0] + slots[1][1]) + (slots[1][2] + slots[1][3]);
 }
 
 // drate[h] = -sum over the batch rows and blocks, in a fixed order.
@@ -193,7 +186,7 @@ __global__ __launch_bounds__(256) void linear_attn_drate_kernel(const double* pa
   t = wave_sum(t);
   if ((tid & 63) == 0) slots[tid >> 6] = t;
   __syncthreads();
-  if (tid == 0) drate[head] = -(float)((slots[0] + slots[1]) + (slots[2] + slots[3]));
+  if (tid == 0) drate[head] = -(float)((slots[0] + slots[1]) + (slots[1] + slots[3]));
 }
 
 // ---- the decode step ---------------------------------------------------------
@@ -338,7 +331,7 @@ Split bwd_split(const Sizes& s) {
 int64_t segment_bytes(const Sizes& s, const Split& p) { return p.count > 1 ? s.rows() * p.count * (s.state() + 1) * 4 : 0; }
 
 struct BwdSpace {
-  int64_t states, segments, dstates, dh0, dots_q, dots_k, drate, dq, dk, bytes;  // offsets
+  int64_t states, segments, cross, dots_q, dots_k, drate, dq, dk, bytes;  // offsets
 };
 
 BwdSpace bwd_space(const Sizes& s, bool decays) {
@@ -353,8 +346,7 @@ BwdSpace bwd_space(const Sizes& s, bool decays) {
   const Split p = bwd_split(s);
   w.segments = take(segment_bytes(s, p));
   w.states = take(p.blocks() ? 0 : segment_bytes(s, p));
-  w.dstates = take(decays ? s.rows() * s.blocks() * s.state() * 4 : 0);
-  w.dh0 = take(decays ? s.rows() * s.state() * 4 : 0);
+  w.cross = take(decays ? s.rows() * (s.blocks() + 1) * ((s.dv + 31) / 32) * 8 : 0);
   w.dots_q = take(decays ? (s.dk + 31) / 32 * s.rows() * s.seqlen * 4 : 0);
   w.dots_k = take(decays ? (s.dk + 31) / 32 * s.rows() * s.seqlen * 4 : 0);
   const bool shared = s.groups != s.heads;
@@ -485,7 +477,7 @@ ssm_status_t ssm_linear_attn_fwd(int64_t batch, int64_t seqlen, int64_t heads, i
   if (e == hipSuccess) {
     r.out = y;
     r.save = ckpt;
-    r.save_slots = s.blocks() + 1;
+    r.slots = s.blocks() + 1;
     r.last = last_state;
     r.tiles = (int)tiles(dv);
     a.role[0] = r;
@@ -513,7 +505,7 @@ ssm_status_t ssm_linear_attn_bwd(int64_t batch, int64_t seqlen, int64_t heads, i
   ssm_status_t st = check_sizes(s, io);
   if (st != SSM_OK) return st;
   const Split p = bwd_split(s);
-  if (!passes_ok(s, p, 2 * tiles(dk) + tiles(dv))) return SSM_ERR_UNSUPPORTED;
+  if (!passes_ok(s, p, 2 * tiles(dk) + tiles(dv)) || !launch_ok(s.rows() * s.blocks(), 256)) return SSM_ERR_UNSUPPORTED;
   if (!q || !k || !v || !rate || !ckpt || !dy || !dq || !dk_out || !dv_out) return SSM_ERR_NULL;
   if (!step) dstep = nullptr;
   const bool decays = drate || dstep;
@@ -572,14 +564,15 @@ ssm_status_t ssm_linear_attn_bwd(int64_t batch, int64_t seqlen, int64_t heads, i
   to_v.last = dh0;
   to_v.tiles = (int)tiles(dv);
   if (decays) {
-    if (!dh0) to_v.last = at(w.dh0);
-    to_v.save = at(w.dstates);
-    to_v.save_slots = s.blocks();
+    to_v.meet = ckpt;
+    to_v.cross = reinterpret_cast<double*>(space + w.cross);
+    to_v.slots = s.blocks() + 1;
   }
   to_k = to_v;
   to_k.q = vs; to_k.k = ys; to_k.v = qs;
   to_k.transposed = 1;
-  to_k.last = to_k.save = nullptr;
+  to_k.last = nullptr;
+  to_k.meet = nullptr;
   to_k.tiles = (int)tiles(dk);
   to_q.q = ys; to_q.k = vs; to_q.v = ks;
   to_q.transposed = 1;
@@ -610,7 +603,7 @@ ssm_status_t ssm_linear_attn_bwd(int64_t batch, int64_t seqlen, int64_t heads, i
   if (e != hipSuccess) return hip_fail(e);
   if (shared) {
     const int64_t n = tokens * groups * dk;
-    const unsigned blocks = (unsigned)((n + 255) / 256);
+    const unsigned blocks = (unsigned)std::min<int64_t>((n + 255) / 256, 65536);
     for (int i = 0; i < 2; ++i) {
       const float* part = at(i ? w.dk : w.dq);
       if (io == SSM_BF16)
@@ -625,22 +618,20 @@ ssm_status_t ssm_linear_attn_bwd(int64_t batch, int64_t seqlen, int64_t heads, i
   }
   if (decays) {
     DecayArgs d = {};
-    d.states = ckpt;
-    d.dstates = at(w.dstates);
+    d.cross = to_v.cross;
     d.dots_q = at(w.dots_q);
     d.dots_k = at(w.dots_k);
-    d.dh0 = to_v.last;
     d.rate = rate;
     d.step = step;
     d.reset = reset;
     d.dstep = dstep;
     d.drate = reinterpret_cast<double*>(space + w.drate);
-    d.n = s.state();
     d.rows = s.rows();
     d.seqlen = seqlen;
     d.heads = (int)heads;
     d.blocks = (int)s.blocks();
-    d.parts_q = d.parts_k = (int)((dk + 31) / 32);
+    d.parts_qk = (int)((dk + 31) / 32);
+    d.parts_v = (int)((dv + 31) / 32);
     const unsigned blocks = (unsigned)(s.rows() * s.blocks());
     if (io == SSM_BF16)
       hipLaunchKernelGGL(linear_attn_decay_kernel<bf16_t>, dim3(blocks), dim3(256), 0, hs, d);

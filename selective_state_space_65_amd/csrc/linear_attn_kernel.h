@@ -545,6 +545,35 @@ __global__ __launch_bounds__(64 * NW, NK <= 4 ? 2 : 1) void linear_attn_kernel(c
       }
   };
 
+  // <meet, state> at a border, this wave's columns of it.
+  const auto meet_state = [&](int64_t border) {
+    const int first = opaque(8 * half);
+    const float* from = p.meet + (row * p.slots + border) * state_size;
+    double sum = 0.0;
+    uint32_t at = first * dv + vc;
+    if (vc < dv) {
+#pragma unroll
+      for (int b = 0; b < NK; ++b)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          __builtin_amdgcn_sched_barrier(0);  // 8 loads at a time: no registers for more
+          float x[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) x[i] = from[min(at + (uint32_t)(i * dv), (uint32_t)(dk * dv - 1))];
+          at = opaque(at + 16 * dv);
+          float some = 0.0f;
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            some = 32 * b + 16 * h + i + first < dk ? __builtin_fmaf(x[i], acc[b][8 * h + i], some) : some;
+          sum += (double)some;
+        }
+    }
+#pragma unroll
+    for (int m = 1; m < 64; m <<= 1) sum += __shfl_xor(sum, m);
+    const int part = tile * NW + wave, parts = (dv + 31) / 32;
+    if (lane == 0 && part < parts) p.cross[(row * p.slots + border) * parts + part] = sum;
+  };
+
   // ---- tiles, requested a chunk ahead; decays, computed a chunk ahead
   using StageK = Stage<T, DK, C, kThreads>;
   using StageV = Stage<T, TV, C, kThreads>;
@@ -646,10 +675,12 @@ __global__ __launch_bounds__(64 * NW, NK <= 4 ? 2 : 1) void linear_attn_kernel(c
     const auto k_at = [&] { const Role& o = a.role[opaque_scalar(r)]; return side_rows<T>(o.k, batch_tokens + t0, head); };
     const auto v_at = [&] { const Role& o = a.role[opaque_scalar(r)]; return side_rows<T>(o.v, batch_tokens + t0, head) + v0; };
     if (!rare(!whole)) {
-      if (kOut && p.save) {
-        // Forward: the state before a block; reverse: the state behind it.
+      if constexpr (kOut) {  // a border of blocks lies in front of this chunk
         const bool border = reverse ? (t0 + C) % linattn::kBlock == 0 || t0 + C >= a.seqlen : t0 % linattn::kBlock == 0;
-        if (rare(border)) store_state(p.save + (row * p.save_slots + t0 / linattn::kBlock) * state_size);
+        if (rare(border)) {
+          if (p.save) store_state(p.save + (row * p.slots + t0 / linattn::kBlock) * state_size);
+          if (p.meet) meet_state(t0 / linattn::kBlock + 1);
+        }
       }
       if (L::k_tiles == 1 && dma) {
         request_k(c);
@@ -901,7 +932,8 @@ __global__ __launch_bounds__(64 * NW, NK <= 4 ? 2 : 1) void linear_attn_kernel(c
     const bool final_segment = reverse ? segment == 0 : segment == a.segments - 1;
     if (final_segment) {
       if (p.last) store_state(p.last + row * state_size);
-      if (p.save && !reverse) store_state(p.save + (row * p.save_slots + p.save_slots - 1) * state_size);
+      if (p.save) store_state(p.save + (row * p.slots + p.slots - 1) * state_size);
+      if (p.meet) meet_state(0);
     }
   } else {
     store_state(p.part + (row * a.segments + segment) * state_size);
