@@ -79,10 +79,12 @@ __global__ __launch_bounds__(256) void linear_attn_join_kernel(const Join one, c
   }
 }
 
-// dq or dk of a group: its heads' parts, added in order.
+// dq and dk of a group (blockIdx.y): its heads' parts, added in order.
 template <typename T>
-__global__ __launch_bounds__(256) void linear_attn_group_kernel(const float* part, T* out, int64_t n, int groups,
-                                                                int share, int d) {
+__global__ __launch_bounds__(256) void linear_attn_group_kernel(const float* part_q, const float* part_k, T* dq, T* dk,
+                                                                int64_t n, int share, int d) {
+  const float* const part = blockIdx.y ? part_k : part_q;
+  T* const out = blockIdx.y ? dk : dq;
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {  // [token][group][d]
     const int64_t tg = i / d;
     const float* at = part + tg * share * d + i % d;
@@ -606,15 +608,12 @@ ssm_status_t ssm_linear_attn_bwd(int64_t batch, int64_t seqlen, int64_t heads, i
   if (shared) {
     const int64_t n = tokens * groups * dk;
     const unsigned blocks = (unsigned)std::min<int64_t>((n + 255) / 256, 65536);
-    for (int i = 0; i < 2; ++i) {
-      const float* part = at(i ? w.dk : w.dq);
-      if (io == SSM_BF16)
-        hipLaunchKernelGGL(linear_attn_group_kernel<bf16_t>, dim3(blocks), dim3(256), 0, hs, part,
-                           static_cast<bf16_t*>(i ? dk_out : dq), n, (int)groups, share, (int)dk);
-      else
-        hipLaunchKernelGGL(linear_attn_group_kernel<float>, dim3(blocks), dim3(256), 0, hs, part,
-                           static_cast<float*>(i ? dk_out : dq), n, (int)groups, share, (int)dk);
-    }
+    if (io == SSM_BF16)
+      hipLaunchKernelGGL(linear_attn_group_kernel<bf16_t>, dim3(blocks, 2), dim3(256), 0, hs, at(w.dq), at(w.dk),
+                         static_cast<bf16_t*>(dq), static_cast<bf16_t*>(dk_out), n, share, (int)dk);
+    else
+      hipLaunchKernelGGL(linear_attn_group_kernel<float>, dim3(blocks, 2), dim3(256), 0, hs, at(w.dq), at(w.dk),
+                         static_cast<float*>(dq), static_cast<float*>(dk_out), n, share, (int)dk);
     e = hipGetLastError();
     if (e != hipSuccess) return hip_fail(e);
   }
