@@ -14,9 +14,11 @@
 // positions with all their channels, a thread 8 channels and every TY-th of the
 // positions, so that all reads are contiguous; channels are joined into groups
 // at the end of the run, runs by a small second kernel, and a last kernel reads
-// the numbers again and writes.  The variance is summed about a pivot, each
-// channel's first number in the run, and joined from means and sums of squares
-// about them, so that it does not suffer from a large mean.
+// the numbers again and writes.  The variance is joined, from a thread's few numbers
+// in flight up to the whole group, from means and sums of squares about them,
+//   M = m1 + (m2 - m1) c2 / (c1 + c2),   Q = q1 + q2 + (m2 - m1)^2 c1 c2 / (c1 + c2),
+// so that a number far off the others does not blur them; and each run of a channel
+// is taken less its first number, so that a large mean does not.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -353,51 +355,70 @@ __global__ __launch_bounds__(kThreads) void group_norm_map_stats_kernel(const Ar
   for (int c0 = 0; c0 < n; c0 += t.tx * kPiece) {
     const int c = c0 + t.x * kPiece;
     const bool live = t.y < t.ty && c < n;
-    float s1[kPiece], s2[kPiece], pivot[kPiece];
-    fill(s1, 0.0f);
-    fill(s2, 0.0f);
+    // Of the thread's own positions, less the run's first number.
+    float pivot[kPiece], mean[kPiece], squares[kPiece], seen = 0.0f;
+    fill(mean, 0.0f);
+    fill(squares, 0.0f);
     if (live) {
       Raw8<T> first = request_at<kShort>(x + l0 * n, c, n);
       for (int64_t l = l0 + t.y; l < l1; l += kAhead<T, 1> * t.ty) {
         Raw8<T> r[kAhead<T, 1>];
+        float v[kAhead<T, 1>][kPiece];
 #pragma unroll
         for (int u = 0; u < kAhead<T, 1>; ++u) r[u] = request_at<kShort>(x + min(l + u * t.ty, l1 - 1) * n, c, n);
         if (l == l0 + t.y) {
           finish_at<kShort>(first, c, n, pivot);
           if (p.rms) fill(pivot, 0.0f);
         }
+        float more = 0.0f;
 #pragma unroll
         for (int u = 0; u < kAhead<T, 1>; ++u) {
-          const bool in = l + u * t.ty < l1;
-          float v[kPiece];
-          finish_at<kShort>(r[u], c, n, v);
-#pragma unroll
-          for (int j = 0; j < kPiece; ++j) {
-            const float e = in ? v[j] - pivot[j] : 0.0f;
-            s1[j] += e;
-            s2[j] = __builtin_fmaf(e, e, s2[j]);
-          }
+          finish_at<kShort>(r[u], c, n, v[u]);
+          more += l + u * t.ty < l1 ? 1.0f : 0.0f;
         }
+        const float one = 1.0f / more, share = more / (seen + more), both = seen * share;
+#pragma unroll
+        for (int j = 0; j < kPiece; ++j) {
+          float m = 0.0f, q = 0.0f;
+#pragma unroll
+          for (int u = 0; u < kAhead<T, 1>; ++u) {
+            v[u][j] -= pivot[j];
+            m += l + u * t.ty < l1 ? v[u][j] : 0.0f;
+          }
+          m = p.rms ? 0.0f : m * one;
+#pragma unroll
+          for (int u = 0; u < kAhead<T, 1>; ++u) {
+            const float e = l + u * t.ty < l1 ? v[u][j] - m : 0.0f;
+            q = __builtin_fmaf(e, e, q);
+          }
+          const float e = m - mean[j];
+          mean[j] = __builtin_fmaf(e, share, mean[j]);
+          squares[j] += __builtin_fmaf(e * both, e, q);
+        }
+        seen += more;
       }
     }
-    // Over the block's rows of threads, in order, then a channel's mean and squares about it.
+    // Over the block's rows of threads, in order; rows y and on have seen `behind` positions.
+    float behind = 0.0f;
     for (int y = t.ty - 1; y >= 0; --y) {
+      const float here = l0 + y < l1 ? (float)((l1 - l0 - y + t.ty - 1) / t.ty) : 0.0f;
       __syncthreads();
       if (live && t.y == y) {
+        const float share = behind > 0.0f ? behind / (here + behind) : 0.0f, both = here * share;
 #pragma unroll
         for (int j = 0; j < kPiece; ++j) {
           float* a = &cols[0][t.x * kPiece + j];
           float* b = &cols[1][t.x * kPiece + j];
-          if (y < t.ty - 1) s1[j] += *a, s2[j] += *b;
-          if (y == 0) {
-            const float m = p.rms ? 0.0f : s1[j] / count;
-            s2[j] -= m * s1[j];
-            s1[j] = p.rms ? 0.0f : pivot[j] + m;
+          if (behind > 0.0f) {
+            const float e = *a - mean[j];
+            mean[j] = __builtin_fmaf(e, share, mean[j]);
+            squares[j] += __builtin_fmaf(e * both, e, *b);
           }
-          *a = s1[j];
-          *b = s2[j];
+          *a = y == 0 && !p.rms ? pivot[j] + mean[j] : mean[j];
+          *b = squares[j];
         }
       }
+      behind += here;
     }
     __syncthreads();
     const int c1 = min(n, c0 + t.tx * kPiece);
@@ -734,6 +755,9 @@ ssm_status_t check_shape(int64_t batch, int64_t length, int64_t channels, int64_
   if (!mul_ok(batch, length, n) || !mul_ok(*n, channels, n) || !mul_ok(*n, 64, &bytes)) return SSM_ERR_SHAPE;
   if (channels > 65536) return SSM_ERR_UNSUPPORTED;
   const Plan p = make_plan(batch, length, channels, groups);
+  // A wave a (batch, group) and 512 threads for 32 sums of a batch row, between a map's passes.
+  if (p.map && (!launch_ok(batch * groups, 64) || !launch_ok(batch * ((2 * channels + 31) / 32) + channels, 512)))
+    return SSM_ERR_UNSUPPORTED;
   if (!launch_ok(p.map ? batch * p.runs : p.row_blocks, kThreads)) return SSM_ERR_UNSUPPORTED;
   return SSM_OK;
 }

@@ -3,9 +3,10 @@ on each output's fp32 error.
 
 u = 2^-24.  No sum in the tests is more than 256 additions deep (positions of a
 thread, threads, channels of a lane, lanes, runs), so it is off by at most
-256 u times the sum of magnitudes.  Over a map (length above 1) a channel is
-summed about its first number of a run of positions, which is at most that channel's
-largest deviation away from its mean.  The sigmoid is off by 8 u of itself and, through its
+256 u times the sum of magnitudes.  Over a map (length above 1) a channel's numbers
+of a run of positions are taken less the run's first, which is at most that channel's
+largest deviation away from its mean (their means and squares are then joined, which
+is no worse than the plain sums that the bound is for).  The sigmoid is off by 8 u of itself and, through its
 argument, by |p| u s (1 - s) <= u / 4; |silu'| <= 1.1 and |silu''| <= 0.5.
 """
 import numpy as np

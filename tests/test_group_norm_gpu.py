@@ -108,6 +108,31 @@ def test_large_mean(case, offset):
     run_all(*case, F32, 200, "offset", gated=False, offset=offset)
 
 
+@pytest.mark.parametrize("io", [F32, BF16])
+@pytest.mark.parametrize("channels", [8, 6, 64])
+def test_one_number_far_off(io, channels):
+    """A run's first position of 1024 times the others' size does not blur them.
+
+    The kernel's means are of numbers less that first one, of size 1024 = M, and are
+    joined in at most 300 steps, each off by u M at most: by e = 300 u M in all.  A
+    sum of squares Q over N numbers is then off by 2048 u Q in its own additions and by
+    2 e times the square root of N Q at most through the means' differences: rstd by
+    1024 u + e / sigma of itself, sigma^2 = Q / N.  Sums of squares about the first
+    number would be off by up to 256 u N / 2 = 0.25 of rstd here.
+    """
+    length = 32768
+    x = torch.randn((2, length, channels), generator=torch.Generator().manual_seed(7)).to(io)
+    x[:, 0] = 1024.0
+    want = x.double().var((1, 2), unbiased=False)
+    y, mean, rstd = ssm.group_norm_fwd(x.to(DEV), 1, eps=0.0)
+    u = 2.0 ** -24
+    off = 1024 * u + 300 * u * 1024 / want.sqrt()
+    err = (rstd.cpu().double()[:, 0] * want.sqrt() - 1).abs()
+    assert (err <= off).all(), (err, off)
+    err = (mean.cpu().double()[:, 0] - x.double().mean((1, 2))).abs()
+    assert (err <= 300 * u * 1024).all(), err
+
+
 @pytest.mark.parametrize("shape", [(3, 300), (3, 17, 60)])
 @pytest.mark.parametrize("kind", ["layer", "rms"])
 def test_constant_and_zero_groups(shape, kind):
