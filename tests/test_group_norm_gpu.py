@@ -177,6 +177,32 @@ def test_needless_outputs_are_left_out():
                     assert torch.equal(v, full[k]), k
 
 
+@pytest.mark.parametrize("io", [F32, BF16])
+@pytest.mark.parametrize("shape", [(5, 96), (3, 33), (2, 70, 64), (2, 40, 30), (3, 9, 6)])
+def test_addresses_that_are_only_element_aligned(io, shape):
+    """The same loads at other addresses: the results are the same bits, and nothing else is written."""
+    gen = torch.Generator().manual_seed(71)
+    x, z, dy = (torch.randn(shape, generator=gen).to(io).to(DEV) for _ in range(3))
+    weight, bias = (torch.randn(shape[-1:], generator=gen).to(DEV) for _ in range(2))
+
+    def shifted(t, by):
+        whole = torch.full((t.numel() + by + 64,), 0.5, dtype=t.dtype, device=DEV)
+        view = whole[by:by + t.numel()].view(t.shape)
+        view.copy_(t)
+        return view, whole
+
+    kw = dict(groups=4 if shape[-1] == 64 else 3, activation="silu")
+    y, mean, rstd = ssm.group_norm_fwd(x, weight=weight, bias=bias, z=z, **kw)
+    g = ssm.group_norm_bwd(dy, x, rstd, mean=mean, weight=weight, bias=bias, z=z, **kw)
+    out, around = shifted(torch.zeros_like(y), 3)
+    sx, sz, sdy, sw, sb, sm, sr = (shifted(t, i + 1)[0] for i, t in enumerate((x, z, dy, weight, bias, mean, rstd)))
+    y2, mean2, rstd2 = ssm.group_norm_fwd(sx, weight=sw, bias=sb, z=sz, out=out, **kw)
+    assert y2 is out and torch.equal(y2, y) and torch.equal(mean2, mean) and torch.equal(rstd2, rstd)
+    assert (around[:3] == 0.5).all() and (around[3 + y.numel():] == 0.5).all()
+    h = ssm.group_norm_bwd(sdy, sx, sr, mean=sm, weight=sw, bias=sb, z=sz, **kw)
+    assert all(torch.equal(g[k], h[k]) for k in g)
+
+
 def test_streams_and_graphs():
     jobs = [draw((3, 700, 48), BF16, 11 + i) for i in range(2)] + [draw((500, 256), BF16, 13)]
 

@@ -282,6 +282,54 @@ def test_repeats_are_equal():
         assert all(torch.equal(first[k], again[k]) for k in first)
 
 
+def shifted(t, by):
+    """t at an address `by` elements behind a 256-byte boundary, and the buffer around it, 0.5 elsewhere."""
+    whole = torch.full((t.numel() + by + 64,), 0.5, dtype=t.dtype, device=DEV)
+    view = whole[by:by + t.numel()].view(t.shape)
+    view.copy_(t)
+    return view, whole
+
+
+@pytest.mark.parametrize("io", [F32, BF16])
+@pytest.mark.parametrize("shape", [(2, 150, 2, 1, 64, 128), (1, 700, 3, 3, 40, 72)])
+def test_addresses_that_are_only_element_aligned(io, shape):
+    """Other loads than those of 16-byte rows, the same sums: the results are the same bits, and nothing else is written."""
+    d, dy, dlast = draw(*shape, io, 61, reset=0.02)
+    say("linear attention misaligned %s %s" % (shape, io))
+    want, ckpt = run(d, dy, dlast)
+    t = {k: shifted(v, i + 1)[0] if v.dtype == io else v.to(DEV) for i, (k, v) in enumerate(d.items())}
+    assert any(t[k].data_ptr() % 16 for k in ("q", "k", "v"))
+    out, around = shifted(torch.zeros(dy.shape, dtype=io), 3)
+    state, beside = shifted(torch.zeros(dlast.shape), 5)
+    y, last = ssm.linear_attn_fwd(out=out, last_state=state, **t)
+    assert y is out and last is state
+    assert torch.equal(y.cpu(), want["y"]) and torch.equal(last.cpu(), want["last_state"])
+    for whole, by, n in ((around, 3, y.numel()), (beside, 5, last.numel())):
+        assert (whole[:by] == 0.5).all() and (whole[by + n:] == 0.5).all()
+    t.pop("h0")
+    g = ssm.linear_attn_bwd(dy=shifted(dy, 1)[0], ckpt=shifted(ckpt, 1)[0], dlast=shifted(dlast, 1)[0], **t)
+    for k, v in g.items():
+        assert torch.equal(v.cpu(), want[k]), k
+
+
+@pytest.mark.parametrize("io", [F32, BF16])
+@pytest.mark.parametrize("shape", [(3, 4, 2, 8, 12), (2, 3, 1, 33, 130)])
+def test_state_update_at_element_aligned_addresses(io, shape):
+    batch, heads, groups, dk, dv = shape
+    d, _, _ = draw(batch, 1, heads, groups, dk, dv, io, 67)
+    t = on_gpu(d)
+    rows = [t[k][:, 0].contiguous() for k in ("q", "k", "v", "step")]
+    want = t["h0"].clone()
+    y = ssm.linear_attn_state_update(want, *rows[:3], t["rate"], step=rows[3])
+    state, beside = shifted(t["h0"], 1)
+    out, around = shifted(torch.zeros_like(y), 5)
+    odd = [shifted(r, i + 1)[0] for i, r in enumerate(rows)]
+    ssm.linear_attn_state_update(state, *odd[:3], t["rate"], step=odd[3], out=out)
+    assert torch.equal(out, y) and torch.equal(state, want)
+    for whole, by, n in ((around, 5, y.numel()), (beside, 1, state.numel())):
+        assert (whole[:by] == 0.5).all() and (whole[by + n:] == 0.5).all()
+
+
 def test_streams():
     """On a side stream, and on two at once: each has a workspace of its own."""
     jobs = [draw(1, 2100, 2, 2, 40, 72, BF16, 37 + i) for i in range(2)]
