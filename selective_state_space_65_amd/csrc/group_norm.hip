@@ -282,6 +282,7 @@ __global__ __launch_bounds__(1024) void group_norm_columns_kernel(const float* p
 // maps take several columns of TX.
 struct Plane {
   int tx, ty, x, y;
+  int half;  // the largest power of 2 below ty, 0 for one row: where sums over the rows start to be joined
 };
 
 __device__ __forceinline__ Plane plane(int64_t channels) {
@@ -291,6 +292,7 @@ __device__ __forceinline__ Plane plane(int64_t channels) {
   t.ty = kThreads / t.tx;
   t.x = threadIdx.x % t.tx;
   t.y = threadIdx.x / t.tx;
+  t.half = t.ty > 1 ? 1 << (31 - __builtin_clz(t.ty - 1)) : 0;
   return t;
 }
 
@@ -343,7 +345,7 @@ __device__ __forceinline__ void join_columns(const Args& p, const float* means, 
 // part[batch][run][2][groups]: each run's means, and sums of squares about them.
 template <typename T, bool kShort>
 __global__ __launch_bounds__(kThreads) void group_norm_map_stats_kernel(const Args p) {
-  __shared__ float cols[2][kThreads * kPiece];
+  __shared__ float cols[2][kThreads * kPiece], counts[kThreads];
   const Plane t = plane(p.channels);
   const int64_t batch = blockIdx.x / p.runs;
   const int run = (int)(blockIdx.x % p.runs);
@@ -398,27 +400,36 @@ __global__ __launch_bounds__(kThreads) void group_norm_map_stats_kernel(const Ar
         seen += more;
       }
     }
-    // Over the block's rows of threads, in order; rows y and on have seen `behind` positions.
-    float behind = 0.0f;
-    for (int y = t.ty - 1; y >= 0; --y) {
-      const float here = l0 + y < l1 ? (float)((l1 - l0 - y + t.ty - 1) / t.ty) : 0.0f;
+    // Over the block's rows of threads, by halves; a thread's place in cols is, in row 0,
+    // that of its channels.
+    float* const means = &cols[0][threadIdx.x * kPiece];
+    float* const sums = &cols[1][threadIdx.x * kPiece];
+    const auto keep = [&](bool whole) {
+#pragma unroll
+      for (int j = 0; j < kPiece; ++j) {
+        means[j] = whole && !p.rms ? pivot[j] + mean[j] : mean[j];
+        sums[j] = squares[j];
+      }
+      counts[threadIdx.x] = seen;
+    };
+    __syncthreads();
+    if (live) keep(t.half == 0);
+    for (int step = t.half; step > 0; step /= 2) {
       __syncthreads();
-      if (live && t.y == y) {
-        const float share = behind > 0.0f ? behind / (here + behind) : 0.0f, both = here * share;
+      if (!live || t.y >= step || t.y + step >= t.ty) continue;
+      const int other = step * t.tx;
+      const float more = counts[threadIdx.x + other];
+      if (more > 0.0f) {
+        const float share = more / (seen + more), both = seen * share;
 #pragma unroll
         for (int j = 0; j < kPiece; ++j) {
-          float* a = &cols[0][t.x * kPiece + j];
-          float* b = &cols[1][t.x * kPiece + j];
-          if (behind > 0.0f) {
-            const float e = *a - mean[j];
-            mean[j] = __builtin_fmaf(e, share, mean[j]);
-            squares[j] += __builtin_fmaf(e * both, e, *b);
-          }
-          *a = y == 0 && !p.rms ? pivot[j] + mean[j] : mean[j];
-          *b = squares[j];
+          const float e = means[other * kPiece + j] - mean[j];
+          mean[j] = __builtin_fmaf(e, share, mean[j]);
+          squares[j] += __builtin_fmaf(e * both, e, sums[other * kPiece + j]);
         }
+        seen += more;
       }
-      behind += here;
+      keep(step == 1);
     }
     __syncthreads();
     const int c1 = min(n, c0 + t.tx * kPiece);
@@ -579,22 +590,25 @@ __global__ __launch_bounds__(kThreads) void group_norm_map_sums_kernel(const Arg
         }
       }
     }
-    for (int y = t.ty - 1; y >= 0; --y) {
-      __syncthreads();
-      if (live && t.y == y) {
+    float* const own_w = &cols[0][threadIdx.x * kPiece];
+    float* const own_b = &cols[1][threadIdx.x * kPiece];
+    const auto keep = [&] {
 #pragma unroll
-        for (int j = 0; j < kPiece; ++j) {
-          float* a = &cols[0][t.x * kPiece + j];
-          float* b = &cols[1][t.x * kPiece + j];
-          if (y < t.ty - 1) aw[j] += *a, ab[j] += *b;
-          *a = aw[j];
-          *b = ab[j];
-        }
-        if (y == 0) {
-          store_row8(out, c, n, c + kPiece <= n, aw);
-          store_row8(out + n, c, n, c + kPiece <= n, ab);
-        }
-      }
+      for (int j = 0; j < kPiece; ++j) own_w[j] = aw[j], own_b[j] = ab[j];
+    };
+    __syncthreads();
+    if (live) keep();
+    for (int step = t.half; step > 0; step /= 2) {
+      __syncthreads();
+      if (!live || t.y >= step || t.y + step >= t.ty) continue;
+      const int other = step * t.tx * kPiece;
+#pragma unroll
+      for (int j = 0; j < kPiece; ++j) aw[j] += own_w[other + j], ab[j] += own_b[other + j];
+      keep();
+    }
+    if (live && t.y == 0) {
+      store_row8(out, c, n, c + kPiece <= n, aw);
+      store_row8(out + n, c, n, c + kPiece <= n, ab);
     }
   }
 }
@@ -732,15 +746,18 @@ Plan make_plan(int64_t batch, int64_t length, int64_t channels, int64_t groups) 
     const int64_t per_block = kThreads / p.lanes;
     const int64_t fwd_rows = per_block * rows_ahead(p.pieces);
     p.row_blocks = (batch * groups + fwd_rows - 1) / fwd_rows;
-    // Batch rows side by side: enough for the chip's lanes, and no more partial rows than 512.
-    p.stride = std::min<int64_t>(batch, std::max<int64_t>(1, std::min<int64_t>(512, 2048 * per_block / groups)));
+    // Batch rows side by side: 2048 blocks, but no more partial rows than 512, or than 2048
+    // where those are not yet 512 blocks.
+    const int64_t most = std::max<int64_t>(512, std::min<int64_t>(2048, 512 * per_block / groups));
+    p.stride = std::min<int64_t>(batch, std::max<int64_t>(1, std::min<int64_t>(most, 2048 * per_block / groups)));
     p.bwd_blocks = (p.stride * groups + per_block - 1) / per_block;
   } else {
     const int64_t pieces = (channels + kPiece - 1) / kPiece;
     const int64_t ty = kThreads / std::min<int64_t>(pieces, kThreads);
     // Blocks for the whole chip, and at most 128 positions to a thread: no sum gets long.
     const int64_t wanted = std::max((1024 + batch - 1) / batch, (length + 128 * ty - 1) / (128 * ty));
-    const int64_t least = ty * 4;  // positions that a block's threads have in flight
+    // Positions that a block's threads have in flight; but one where they go over several columns.
+    const int64_t least = pieces > kThreads ? 1 : ty * 4;
     p.runs = std::max<int64_t>(1, std::min(wanted, (length + least - 1) / least));
     p.run = (length + p.runs - 1) / p.runs;
     p.runs = (length + p.run - 1) / p.run;

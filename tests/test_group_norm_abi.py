@@ -95,7 +95,7 @@ def test_common_refusals(lib, call):
     assert call(lib, groups=128) == SHAPE
     assert call(lib, batch=1 << 50, length=1 << 12) == SHAPE
     assert call(lib, channels=65537, groups=1) == UNSUPPORTED
-    assert call(lib, batch=1 << 26, length=1, channels=512, groups=1) == UNSUPPORTED   # 2^32 lanes
+    assert call(lib, batch=1 << 27, length=1, channels=512, groups=1) == UNSUPPORTED   # 2^32 lanes, two rows each
     assert call(lib, kind=2) == UNSUPPORTED
     assert call(lib, act=2) == UNSUPPORTED
     assert call(lib, x=None) == NULL
