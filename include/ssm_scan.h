@@ -753,8 +753,8 @@ ssm_status_t ssm_group_norm_bwd_workspace_bytes(int64_t batch, int64_t length, i
  * not be negative.
  *
  * A reset drops the state before it, whatever its value (infinities and NaN
- * too).  So does a decay that is 0, and a product of the decays of tokens of one
- * chunk (64 in bf16, 32 in fp32, counted from a multiple of 512) that is below the
+ * too).  So does a decay that is 0, and a product of the decays of consecutive
+ * tokens of a chunk (64 tokens in bf16, 32 in fp32) or of more that is below the
  * smallest normal float.  A token's infinities and NaN reach no earlier token
  * and none behind a reset.
  *

@@ -32,6 +32,7 @@ namespace {
 
 using linattn::Args;
 using linattn::kBlock;
+using linattn::role_blocks;
 using linattn::Role;
 using linattn::Side;
 
@@ -376,6 +377,7 @@ Args pass_args(const Sizes& s, const Split& p, const float* rate, const void* st
   Args a = {};
   a.batch = (int)s.batch;
   a.heads = (int)s.heads;
+  a.groups = (int)s.groups;
   a.seqlen = s.seqlen;
   a.rate = rate;
   a.step = step;
@@ -396,16 +398,17 @@ hipError_t segment_states(Args a, const Role* roles, const Front* first, void* c
                           ssm_dtype_t io, hipStream_t st) {
   Join join[2] = {};
   a.roles = count;
-  const int64_t blocks = s.rows() * (a.segments - 1) * tiles(s.dv);
+  int64_t blocks = 0;
   for (int i = 0; i < count; ++i) {
     Role& r = a.role[i] = roles[i];
     r.part = static_cast<float*>(space[i]);
     r.total = r.part + s.rows() * a.segments * s.state();
     r.tiles = (int)tiles(s.dv);
-    r.first_block = i * blocks;
+    r.first_block = (int)blocks;
+    blocks += role_blocks(&r, s.batch, s.heads, s.groups, a.segments - 1);
     join[i] = Join{r.part, r.total, first[i].state, first[i].step, r.reverse};
   }
-  const hipError_t e = launch_pass(a, blocks * count, true, false, io, st);
+  const hipError_t e = launch_pass(a, blocks, true, false, io, st);
   if (e != hipSuccess) return e;
   const int64_t n = s.state();
   hipLaunchKernelGGL(linear_attn_join_kernel, dim3((unsigned)((n + 255) / 256), (unsigned)s.rows(), (unsigned)count),
@@ -414,7 +417,8 @@ hipError_t segment_states(Args a, const Role* roles, const Front* first, void* c
 }
 
 bool passes_ok(const Sizes& s, const Split& p, int64_t blocks_each) {
-  return s.rows() < 65536 * (int64_t)16 && launch_ok(s.rows() * p.count * blocks_each, 256);
+  // Up to 1/16 more are launched than have work.
+  return s.rows() < 65536 * (int64_t)16 && launch_ok(s.rows() * p.count * blocks_each / 16 * 17 + 16, 256);
 }
 
 }  // namespace
@@ -484,9 +488,10 @@ ssm_status_t ssm_linear_attn_fwd(int64_t batch, int64_t seqlen, int64_t heads, i
     r.slots = s.blocks() + 1;
     r.last = last_state;
     r.tiles = (int)tiles(dv);
+    const int64_t blocks = role_blocks(&r, batch, heads, groups, p.count);
     a.role[0] = r;
     a.roles = 1;
-    e = launch_pass(a, s.rows() * p.count * r.tiles, false, false, io, hs);
+    e = launch_pass(a, blocks, false, false, io, hs);
   }
   return e == hipSuccess ? SSM_OK : hip_fail(e);
 }
@@ -594,16 +599,17 @@ ssm_status_t ssm_linear_attn_bwd(int64_t batch, int64_t seqlen, int64_t heads, i
     to_k.dots = at(w.dots_k);
   }
   // dq's and dk's passes contract v's columns, dv's contracts q's.
-  const int64_t each = s.rows() * p.count;
+  const auto blocks_of = [&](Role* r) { return role_blocks(r, batch, heads, groups, p.count); };
+  const int64_t q_blocks = blocks_of(&to_q), k_blocks = blocks_of(&to_k), v_blocks = blocks_of(&to_v);
+  to_k.first_block = (int)q_blocks;
   a.role[0] = to_q;
   a.role[1] = to_k;
-  a.role[1].first_block = each * to_q.tiles;
   a.roles = 2;
-  e = launch_pass(a, each * (to_q.tiles + to_k.tiles), false, decays, io, hs);
+  e = launch_pass(a, q_blocks + k_blocks, false, decays, io, hs);
   if (e != hipSuccess) return hip_fail(e);
   a.role[0] = to_v;
   a.roles = 1;
-  e = launch_pass(a, each * to_v.tiles, false, false, io, hs);
+  e = launch_pass(a, v_blocks, false, false, io, hs);
   if (e != hipSuccess) return hip_fail(e);
   if (shared) {
     const int64_t n = tokens * groups * dk;

@@ -26,6 +26,17 @@
 // single words (fp32).  16-byte units of a tile's rows are permuted by the row so
 // that neither kind of read has bank conflicts.
 //
+// What bounds it (4 x 4096 tokens x 32 heads of 128 x 128, bf16; 164 us for the pass
+// with outputs, 77 for the states of 3 of 4 segments, 18 for their join).  The two waves
+// a SIMD has, which the state's registers and the tiles' LDS allow, do not hide each
+// other: of a wave's time 19% is issue of vector instructions (864 per wave and chunk, 80 of
+// them products, which keep the matrix units busy for 21%), 30% is waiting to issue and
+// 40% waiting for LDS, barriers and memory; bytes move at 60% of a copy's rate.  Chunks
+// of 64 (32 in fp32): the scores' work per token grows with the chunk, scaling
+// the state and the barriers shrink with it, and one of 128 would leave one block a CU.
+// 32 columns a wave: with 16 the LDS was the bound (344 us, all passes together, where
+// these take 243).
+//
 // Roundings (bf16 io).  The scaled v of the update are split in three bf16 parts
 // (24 bits): states are sums in 32 bits of products exact to 2^-24.  Scores and
 // the state as an operand are rounded to bf16 once, half a step each like the
@@ -500,16 +511,26 @@ __global__ __launch_bounds__(64 * NW, NK <= 4 ? 2 : 1) void linear_attn_kernel(c
 
   // ---- which rows, segment and columns this block has
   int r = 0;
-  while (r + 1 < a.roles && (int64_t)blockIdx.x >= a.role[r + 1].first_block) ++r;
+  while (r + 1 < a.roles && (int)blockIdx.x >= a.role[r + 1].first_block) ++r;
   const Role& p = a.role[r];
-  const int64_t index = (int64_t)blockIdx.x - p.first_block;
-  const int tile = (int)(index % p.tiles);
-  const int64_t rest = index / p.tiles;
   // State passes leave out the segment that no other starts behind.
   const int parts = kOut ? a.segments : a.segments - 1;
-  const int segment = (int)(rest % parts) + (!kOut && p.reverse ? 1 : 0);
-  const int64_t row = rest / parts;  // (batch, head)
-  const int head = (int)(row % a.heads);
+  const int index = (int)blockIdx.x - p.first_block;
+  const int tile = p.units ? index / linattn::kDies % p.tiles : index % p.tiles;
+  int part, row;  // segment, (batch, head)
+  if (p.units) {
+    const int share = a.heads / a.groups, each = share * p.tiles;
+    const int slot = index / linattn::kDies;
+    const int unit = slot / each * linattn::kDies + index % linattn::kDies;
+    if (unit >= p.units) return;
+    part = unit % parts;
+    row = unit / parts * share + slot / p.tiles % share;
+  } else {
+    part = index / p.tiles % parts;
+    row = index / p.tiles / parts;
+  }
+  const int segment = part + (!kOut && p.reverse ? 1 : 0);
+  const int head = row % a.heads;
   const int64_t batch_tokens = row / a.heads * a.seqlen;
   const bool reverse = p.reverse;
   const int dk = p.k.d, dv = p.v.d;
@@ -526,7 +547,7 @@ __global__ __launch_bounds__(64 * NW, NK <= 4 ? 2 : 1) void linear_attn_kernel(c
   f32x16 acc[NK];
   const int64_t state_size = (int64_t)dk * dv;
   {
-    const float* from = kOut && p.start ? p.start + (row * p.start_slots + segment * p.start_step) * state_size : nullptr;
+    const float* from = kOut && p.start ? p.start + ((int64_t)row * p.start_slots + segment * p.start_step) * state_size : nullptr;
     const int64_t k_step = p.transposed ? 1 : dv, at = p.transposed ? (int64_t)vc * dk : vc;
 #pragma unroll
     for (int b = 0; b < NK; ++b)
@@ -551,7 +572,7 @@ __global__ __launch_bounds__(64 * NW, NK <= 4 ? 2 : 1) void linear_attn_kernel(c
   // <meet, state> at a border, this wave's columns of it.
   const auto meet_state = [&](int64_t border) {
     const int first = opaque(8 * half);
-    const float* from = p.meet + (row * p.slots + border) * state_size;
+    const float* from = p.meet + ((int64_t)row * p.slots + border) * state_size;
     double sum = 0.0;
     uint32_t at = first * dv + vc;
     if (vc < dv) {
@@ -574,7 +595,7 @@ __global__ __launch_bounds__(64 * NW, NK <= 4 ? 2 : 1) void linear_attn_kernel(c
 #pragma unroll
     for (int m = 1; m < 64; m <<= 1) sum += __shfl_xor(sum, m);
     const int part = tile * NW + wave, parts = (dv + 31) / 32;
-    if (lane == 0 && part < parts) p.cross[(row * p.slots + border) * parts + part] = sum;
+    if (lane == 0 && part < parts) p.cross[((int64_t)row * p.slots + border) * parts + part] = sum;
   };
 
   // ---- tiles, requested a chunk ahead; decays, computed a chunk ahead
@@ -681,7 +702,7 @@ __global__ __launch_bounds__(64 * NW, NK <= 4 ? 2 : 1) void linear_attn_kernel(c
       if constexpr (kOut) {  // a border of blocks lies in front of this chunk
         const bool border = reverse ? (t0 + C) % linattn::kBlock == 0 || t0 + C >= a.seqlen : t0 % linattn::kBlock == 0;
         if (rare(border)) {
-          if (p.save) store_state(p.save + (row * p.slots + t0 / linattn::kBlock) * state_size);
+          if (p.save) store_state(p.save + ((int64_t)row * p.slots + t0 / linattn::kBlock) * state_size);
           if (p.meet) meet_state(t0 / linattn::kBlock + 1);
         }
       }
@@ -935,11 +956,11 @@ __global__ __launch_bounds__(64 * NW, NK <= 4 ? 2 : 1) void linear_attn_kernel(c
     const bool final_segment = reverse ? segment == 0 : segment == a.segments - 1;
     if (final_segment) {
       if (p.last) store_state(p.last + row * state_size);
-      if (p.save) store_state(p.save + (row * p.slots + p.slots - 1) * state_size);
+      if (p.save) store_state(p.save + ((int64_t)row * p.slots + p.slots - 1) * state_size);
       if (p.meet) meet_state(0);
     }
   } else {
-    store_state(p.part + (row * a.segments + segment) * state_size);
+    store_state(p.part + ((int64_t)row * a.segments + segment) * state_size);
     if (tile == 0 && tid == 0) p.total[row * a.segments + segment] = carried;
   }
 }
