@@ -31,7 +31,7 @@
 // a SIMD has, which the state's registers and the tiles' LDS allow, do not hide each
 // other: of a wave's time 19% is issue of vector instructions (864 per wave and chunk, 80 of
 // them products, which keep the matrix units busy for 21%), 30% is waiting to issue and
-// 40% waiting for LDS, barriers and memory; bytes move at 60% of a copy's rate.  Chunks
+// 40% waiting for LDS, barriers and memory; bytes move at 70% of a copy's rate.  Chunks
 // of 64 (32 in fp32): the scores' work per token grows with the chunk, scaling
 // the state and the barriers shrink with it, and one of 128 would leave one block a CU.
 // 32 columns a wave: with 16 the LDS was the bound (344 us, all passes together, where
