@@ -128,6 +128,25 @@ def test_values(shape, io):
     check(got, ref.everything(d, dy, dlast, scale=0.25, io=io), str(shape))
 
 
+# Groups whose heads' blocks are laid on one die: two tiles and a grid with blocks that have no work in the
+# main pass, the states' pass alone, the main pass alone.
+SHARED = [(7, 300, 6, 3, 40, 136), (2, 1100, 4, 2, 130, 24), (2, 1000, 6, 2, 24, 72)]
+
+
+@pytest.mark.parametrize("io", [F32, BF16])
+@pytest.mark.parametrize("shape", SHARED)
+def test_shared_heads(shape, io):
+    i = SHARED.index(shape)
+    say("linear attention shared heads %s %s" % (shape, io))
+    d, dy, dlast = draw(*shape, io, 150 + i, reset=0.004)
+    got, _ = run(d, dy, dlast, scale=0.25)
+    check(got, ref.everything(d, dy, dlast, scale=0.25, io=io), str(shape))
+    if io == F32:
+        d, dy, dlast = draw(*shape, io, 160 + i, reset=0.004, whole=True)
+        got, _ = run(d, dy, dlast)
+        check_equal(got, ref.everything(d, dy, dlast), str(shape))
+
+
 @pytest.mark.parametrize("io", [F32, BF16])
 def test_checkpoints(io):
     d, _, _ = draw(2, 1100, 2, 2, 24, 40, io, 7)
