@@ -28,9 +28,9 @@ struct Role {
   int reverse;
   int transposed;        // states in memory are [v.d][k.d]
   float s_in, s_up;      // sI, sU
-  const float* start;    // state a segment starts from (null: zero): slot segment * start_step
-  int64_t start_slots;   // of start_slots slots for each (batch, head)
-  int64_t start_step;
+  const float* start;    // state a segment starts from (null: zero): slot segment * start_step + start_first,
+  int64_t start_slots;   // or the last one, of start_slots slots for each (batch, head)
+  int64_t start_step, start_first;
   float* save;           // forward: state in front of every block of kBlock tokens, and behind the last; may be null
   const float* meet;     // reverse: states as save has them, that this pass's are multiplied with
   double* cross;         // there: <meet, state> in parts, [batch, heads, border][v.d / 32 rounded up]

@@ -5,7 +5,7 @@
 // With few (batch, head) pairs the tokens are cut into segments: a state pass
 // gives every segment's own state, a join turns them into the states the
 // segments start from, and the main pass runs all segments at once.  The
-// backward takes the forward's states from its checkpoints where its segments are
+// backward takes the forward's states from its checkpoints where dq's segments are
 // whole blocks of them, and else from a state pass of its own.
 //
 // The backward is the same pass three times over,
@@ -321,7 +321,7 @@ Split split_tokens(const Sizes& s, int64_t most) {
 
 Split fwd_split(const Sizes& s) { return split_tokens(s, resident(s.dk, s.dv) / (s.rows() * tiles(s.dv))); }
 
-// The three passes have one split: what the pass with the fewest blocks asks for.
+// What the pass with the fewest blocks asks for; dq's and dk's may be coarser.
 Split bwd_split(const Sizes& s) {
   const int64_t to_v = resident(s.dk, s.dv) / (s.rows() * tiles(s.dv));
   const int64_t to_qk = resident(s.dv, s.dk) / (s.rows() * 2 * tiles(s.dk));
@@ -332,6 +332,16 @@ Split bwd_split(const Sizes& s) {
     p.count = ((s.seqlen + kUnit - 1) / kUnit + p.per - 1) / p.per;
   }
   return p;
+}
+
+// dq's and dk's passes: where the segments are parts of a block, whole blocks, which
+// start from checkpoints and from every so many-th of dv's states, if their blocks
+// still fill the chip: 8 x 2048 x 12 heads of 64 x 128 fp32 train in 604 us so, in 667
+// with one split and a pass for the forward's states.
+Split qk_split(const Sizes& s, const Split& p) {
+  const int64_t block = kBlock / kUnit;
+  if (p.blocks() || block % p.per || 2 * s.rows() * tiles(s.dk) * s.blocks() < resident(s.dv, s.dk)) return p;
+  return Split{block, s.blocks()};
 }
 
 // Segments' states and decays.
@@ -352,7 +362,7 @@ BwdSpace bwd_space(const Sizes& s, bool decays) {
   w.drate = take(decays ? s.rows() * s.blocks() * 8 : 0);
   const Split p = bwd_split(s);
   w.segments = take(segment_bytes(s, p));
-  w.states = take(p.blocks() ? 0 : segment_bytes(s, p));
+  w.states = take(qk_split(s, p).blocks() ? 0 : segment_bytes(s, p));
   w.cross = take(decays ? s.rows() * (s.blocks() + 1) * ((s.dv + 31) / 32) * 8 : 0);
   w.dots_q = take(decays ? (s.dk + 31) / 32 * s.rows() * s.seqlen * 4 : 0);
   w.dots_k = take(decays ? (s.dk + 31) / 32 * s.rows() * s.seqlen * 4 : 0);
@@ -515,7 +525,7 @@ ssm_status_t ssm_linear_attn_bwd(int64_t batch, int64_t seqlen, int64_t heads, i
   const Sizes s{batch, seqlen, heads, groups, dk, dv};
   ssm_status_t st = check_sizes(s, io);
   if (st != SSM_OK) return st;
-  const Split p = bwd_split(s);
+  const Split p = bwd_split(s), qk = qk_split(s, p);
   if (!passes_ok(s, p, 2 * tiles(dk) + tiles(dv)) || !launch_ok(s.rows() * s.blocks(), 256)) return SSM_ERR_UNSUPPORTED;
   if (!q || !k || !v || !rate || !ckpt || !dy || !dq || !dk_out || !dv_out) return SSM_ERR_NULL;
   if (!step) dstep = nullptr;
@@ -551,7 +561,7 @@ ssm_status_t ssm_linear_attn_bwd(int64_t batch, int64_t seqlen, int64_t heads, i
   to_v.start_slots = 1;
   to_q.start = ckpt;
   to_q.start_slots = s.blocks() + 1;
-  to_q.start_step = p.per * kUnit / kBlock;
+  to_q.start_step = qk.per * kUnit / kBlock;
   hipError_t e = hipSuccess;
   if (p.count > 1) {
     Role forward = {};  // S again, from the states in front of all tokens
@@ -560,12 +570,12 @@ ssm_status_t ssm_linear_attn_bwd(int64_t batch, int64_t seqlen, int64_t heads, i
     const Role roles[2] = {to_v, forward};
     const Front first[2] = {{dlast, s.state()}, {ckpt, (s.blocks() + 1) * s.state()}};
     void* const spaces[2] = {at(w.segments), at(w.states)};
-    e = segment_states(a, roles, first, spaces, p.blocks() ? 1 : 2, s, io, hs);
+    e = segment_states(a, roles, first, spaces, qk.blocks() ? 1 : 2, s, io, hs);
     if (e != hipSuccess) return hip_fail(e);
     to_v.start = at(w.segments);
     to_v.start_slots = p.count;
     to_v.start_step = 1;
-    if (!p.blocks()) {
+    if (!qk.blocks()) {
       to_q.start = at(w.states);
       to_q.start_slots = p.count;
       to_q.start_step = 1;
@@ -585,6 +595,10 @@ ssm_status_t ssm_linear_attn_bwd(int64_t batch, int64_t seqlen, int64_t heads, i
   to_k.last = nullptr;
   to_k.meet = nullptr;
   to_k.tiles = (int)tiles(dk);
+  if (p.count > 1) {  // the state behind each segment of qk is that behind its last one of p
+    to_k.start_step = qk.per / p.per;
+    to_k.start_first = to_k.start_step - 1;
+  }
   to_q.q = ys; to_q.k = vs; to_q.v = ks;
   to_q.transposed = 1;
   to_q.s_in = scale;
@@ -601,16 +615,21 @@ ssm_status_t ssm_linear_attn_bwd(int64_t batch, int64_t seqlen, int64_t heads, i
     to_k.dots = at(w.dots_k);
   }
   // dq's and dk's passes contract v's columns, dv's contracts q's.
-  const auto blocks_of = [&](Role* r) { return role_blocks(r, batch, heads, groups, p.count); };
-  const int64_t q_blocks = blocks_of(&to_q), k_blocks = blocks_of(&to_k), v_blocks = blocks_of(&to_v);
+  const int64_t q_blocks = role_blocks(&to_q, batch, heads, groups, qk.count);
+  const int64_t k_blocks = role_blocks(&to_k, batch, heads, groups, qk.count);
+  const int64_t v_blocks = role_blocks(&to_v, batch, heads, groups, p.count);
   to_k.first_block = (int)q_blocks;
   a.role[0] = to_q;
   a.role[1] = to_k;
   a.roles = 2;
+  a.segments = (int)qk.count;
+  a.segment_len = qk.per * kUnit;
   e = launch_pass(a, q_blocks + k_blocks, false, decays, io, hs);
   if (e != hipSuccess) return hip_fail(e);
   a.role[0] = to_v;
   a.roles = 1;
+  a.segments = (int)p.count;
+  a.segment_len = p.per * kUnit;
   e = launch_pass(a, v_blocks, false, false, io, hs);
   if (e != hipSuccess) return hip_fail(e);
   if (shared) {

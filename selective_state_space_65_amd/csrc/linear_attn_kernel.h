@@ -547,7 +547,8 @@ __global__ __launch_bounds__(64 * NW, NK <= 4 ? 2 : 1) void linear_attn_kernel(c
   f32x16 acc[NK];
   const int64_t state_size = (int64_t)dk * dv;
   {
-    const float* from = kOut && p.start ? p.start + ((int64_t)row * p.start_slots + segment * p.start_step) * state_size : nullptr;
+    const int64_t slot = min(segment * p.start_step + p.start_first, p.start_slots - 1);
+    const float* from = kOut && p.start ? p.start + ((int64_t)row * p.start_slots + slot) * state_size : nullptr;
     const int64_t k_step = p.transposed ? 1 : dv, at = p.transposed ? (int64_t)vc * dk : vc;
 #pragma unroll
     for (int b = 0; b < NK; ++b)

@@ -129,8 +129,9 @@ def test_values(shape, io):
 
 
 # Groups whose heads' blocks are laid on one die: two tiles and a grid with blocks that have no work in the
-# main pass, the states' pass alone, the main pass alone.
-SHARED = [(7, 300, 6, 3, 40, 136), (2, 1100, 4, 2, 130, 24), (2, 1000, 6, 2, 24, 72)]
+# main pass, the states' pass alone, the main pass alone; and a backward whose passes for q and k have segments of
+# 512 tokens, the last one cut short, where that for v has 128.
+SHARED = [(7, 300, 6, 3, 40, 136), (2, 1100, 4, 2, 130, 24), (2, 1000, 6, 2, 24, 72), (8, 700, 8, 4, 8, 136)]
 
 
 @pytest.mark.parametrize("io", [F32, BF16])
