@@ -373,6 +373,13 @@ BwdSpace bwd_space(const Sizes& s, bool decays) {
   return w;
 }
 
+// bf16: whether scores and states keep their 24 bits as operands though no decay's
+// gradient needs it.  Over many tokens the outputs' error from their rounding is that of the
+// output's own rounding; with few, one score's rounding may be all of it (up to 2^-8
+// of a token's whole output), and the three-part products cost such calls, which are a launch's
+// latency, next to nothing.
+bool few_tokens(const Sizes& s) { return s.rows() * s.seqlen <= 4096; }
+
 bool whole_units(const Side& s, size_t es) { return s.d * es % 16 == 0 && aligned(s.p, 16); }
 
 hipError_t launch_pass(Args a, int64_t blocks, bool state_only, bool exact, ssm_dtype_t io, hipStream_t st) {
@@ -503,7 +510,7 @@ ssm_status_t ssm_linear_attn_fwd(int64_t batch, int64_t seqlen, int64_t heads, i
     const int64_t blocks = role_blocks(&r, batch, heads, groups, p.count);
     a.role[0] = r;
     a.roles = 1;
-    e = launch_pass(a, blocks, false, false, io, hs);
+    e = launch_pass(a, blocks, false, few_tokens(s), io, hs);
   }
   return e == hipSuccess ? SSM_OK : hip_fail(e);
 }
@@ -624,13 +631,13 @@ ssm_status_t ssm_linear_attn_bwd(int64_t batch, int64_t seqlen, int64_t heads, i
   a.roles = 2;
   a.segments = (int)qk.count;
   a.segment_len = qk.per * kUnit;
-  e = launch_pass(a, q_blocks + k_blocks, false, decays, io, hs);
+  e = launch_pass(a, q_blocks + k_blocks, false, decays || few_tokens(s), io, hs);
   if (e != hipSuccess) return hip_fail(e);
   a.role[0] = to_v;
   a.roles = 1;
   a.segments = (int)p.count;
   a.segment_len = p.per * kUnit;
-  e = launch_pass(a, v_blocks, false, false, io, hs);
+  e = launch_pass(a, v_blocks, false, few_tokens(s), io, hs);
   if (e != hipSuccess) return hip_fail(e);
   if (shared) {
     const int64_t n = tokens * groups * dk;

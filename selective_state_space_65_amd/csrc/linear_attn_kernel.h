@@ -41,7 +41,8 @@
 // (24 bits): states are sums in 32 bits of products exact to 2^-24.  Scores and
 // the state as an operand are rounded to bf16 once, half a step each like the
 // output itself; kParts = 3 splits them in three (2^-24), for gradients whose dot
-// products with the inputs are summed up over the tokens (the decays').
+// products with the inputs are summed up over the tokens (the decays'), and for
+// calls of few tokens, whose roundings do not average out.
 //
 // What a zero factor multiplies is dropped, whatever its value, and a NaN or an
 // infinity of a token reaches no token that it should not: products on the
