@@ -148,6 +148,17 @@ def test_shared_heads(shape, io):
         check_equal(got, ref.everything(d, dy, dlast), str(shape))
 
 
+@pytest.mark.parametrize("shape", [(1, 1, 1, 1, 8, 8), (2, 3, 2, 1, 40, 24), (1, 70, 3, 3, 64, 128), (4, 512, 2, 2, 16, 16)])
+def test_few_tokens_round_once(shape):
+    """Up to 4096 tokens x heads, bf16 outputs are the fp32 sums (whose parts are exact to 2^-24, within fp32's bound) rounded
+    once, half a step: 2^-8 of the value."""
+    say("linear attention few tokens %s" % (shape,))
+    d, dy, dlast = draw(*shape, BF16, 170, reset=0.01)
+    got, _ = run(d, dy, dlast, scale=0.25)
+    want = ref.everything(d, dy, dlast, scale=0.25, io=F32)
+    check(got, {k: (v, b + 2.0 ** -8 * (v.abs() + b)) for k, (v, b) in want.items()}, str(shape))
+
+
 @pytest.mark.parametrize("io", [F32, BF16])
 def test_checkpoints(io):
     d, _, _ = draw(2, 1100, 2, 2, 24, 40, io, 7)
