@@ -117,7 +117,7 @@ __device__ __forceinline__ double wave_sum(double v) {
 // One block of kBlock tokens of one (batch, head); a thread has two tokens.
 template <typename T>
 __global__ __launch_bounds__(256) void linear_attn_decay_kernel(const DecayArgs p) {
-  __shared__ double slots[1][4];
+  __shared__ double slots[2][4];  // a row for each use, with one barrier between its writes and its reads
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int block = (int)(blockIdx.x % p.blocks);
   const int64_t row = blockIdx.x / p.blocks;
