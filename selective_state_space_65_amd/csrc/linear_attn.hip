@@ -189,7 +189,7 @@ __global__ __launch_bounds__(256) void linear_attn_drate_kernel(const double* pa
   t = wave_sum(t);
   if ((tid & 63) == 0) slots[tid >> 6] = t;
   __syncthreads();
-  if (tid == 0) drate[head] = -(float)((slots[0] + slots[1]) + (slots[1] + slots[3]));
+  if (tid == 0) drate[head] = -(float)((slots[0] + slots[1]) + (slots[2] + slots[3]));
 }
 
 // ---- the decode step ---------------------------------------------------------

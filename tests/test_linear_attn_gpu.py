@@ -148,6 +148,21 @@ def test_shared_heads(shape, io):
         check_equal(got, ref.everything(d, dy, dlast), str(shape))
 
 
+# The rates' gradient is a sum over batch rows and blocks of 512 tokens, by four waves of 64 lanes in strides of 256: two
+# waves, three, four, all of them twice, and many blocks of one row.
+MANY = [(65, 3, 2, 1, 8, 8), (130, 3, 2, 2, 8, 8), (200, 3, 2, 1, 8, 8), (270, 5, 3, 3, 8, 12), (1, 512 * 70 + 9, 1, 1, 2, 3)]
+
+
+@pytest.mark.parametrize("io,shape", [(F32, s) for s in MANY] + [(BF16, s) for s in MANY[:4]])
+def test_rates_gradient_over_many_blocks(io, shape):
+    """Whole numbers: the sum of the double's parts is exact, whatever their order."""
+    i = MANY.index(shape)
+    say("linear attention many blocks %s %s" % (shape, io))
+    d, dy, dlast = draw(*shape, io, 180 + i, reset=0.002, whole=True)
+    got, _ = run(d, dy, dlast)
+    check_equal(got, ref.everything(d, dy, dlast, io=io), str(shape))
+
+
 @pytest.mark.parametrize("shape", [(1, 1, 1, 1, 8, 8), (2, 3, 2, 1, 40, 24), (1, 70, 3, 3, 64, 128), (4, 512, 2, 2, 16, 16)])
 def test_few_tokens_round_once(shape):
     """Up to 4096 tokens x heads, bf16 outputs are the fp32 sums (whose parts are exact to 2^-24, within fp32's bound) rounded
