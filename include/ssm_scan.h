@@ -758,10 +758,9 @@ ssm_status_t ssm_group_norm_bwd_workspace_bytes(int64_t batch, int64_t length, i
  * smallest normal float.  A token's infinities and NaN reach no earlier token
  * and none behind a reset.
  *
- * Decays and sums are fp32 or more.  In bf16, scores (q . k with their decay) and
- * the state as q reads it are rounded to bf16 once for the product that follows;
- * in the gradients of q and k, when those of rate or step are asked for, and
- * where batch heads seqlen is at most 4096, they keep 24 bits, as states do always.
+ * Decays and sums are fp32 or more, and what is computed and multiplied again
+ * (scores, states) keeps 24 bits: in bf16 only the outputs are rounded to it.  Where
+ * the formula gives an infinity, NaN may come out in bf16.
  *
  * dk and dv up to 256, heads up to 16384 (larger is SSM_ERR_UNSUPPORTED, as are
  * launches of 2^32 lanes); any seqlen >= 1, any element-aligned pointers;

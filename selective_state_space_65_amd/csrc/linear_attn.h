@@ -76,8 +76,8 @@ inline int tile_width(int dv) { return dv > 64 ? 128 : 64; }
 
 // Launches the roles, whose contracted dimensions (k.d) have the same number
 // of 32-wide parts (rounded up to 1, 2, 4 or 8) and whose tile widths are the
-// same; exact: bf16 intermediates in three parts.
-hipError_t launch_bf16(const Args& a, int64_t blocks, bool state_only, bool exact, hipStream_t st);
-hipError_t launch_f32(const Args& a, int64_t blocks, bool state_only, bool exact, hipStream_t st);
+// same.
+hipError_t launch_bf16(const Args& a, int64_t blocks, bool state_only, hipStream_t st);
+hipError_t launch_f32(const Args& a, int64_t blocks, bool state_only, hipStream_t st);
 
 }  // namespace linattn

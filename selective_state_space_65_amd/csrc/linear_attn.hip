@@ -272,13 +272,14 @@ __global__ __launch_bounds__(256) void linear_attn_step_kernel(const StepArgs p)
 
 struct Sizes {
   int64_t batch, seqlen, heads, groups, dk, dv;
+  ssm_dtype_t io;
   int64_t rows() const { return batch * heads; }
   int64_t state() const { return dk * dv; }
   int64_t blocks() const { return (seqlen + kBlock - 1) / kBlock; }
 };
 
-ssm_status_t check_sizes(const Sizes& s, ssm_dtype_t io) {
-  if (io != SSM_F32 && io != SSM_BF16) return SSM_ERR_DTYPE;
+ssm_status_t check_sizes(const Sizes& s) {
+  if (s.io != SSM_F32 && s.io != SSM_BF16) return SSM_ERR_DTYPE;
   if (s.batch < 1 || s.seqlen < 1 || s.heads < 1 || s.groups < 1 || s.dk < 1 || s.dv < 1) return SSM_ERR_SHAPE;
   if (s.heads % s.groups) return SSM_ERR_SHAPE;
   int64_t n, m;
@@ -302,11 +303,12 @@ struct Split {
 };
 
 // Blocks of a pass that the chip holds at once: as the LDS and registers of its
-// kernel allow.  4 x 4096 x 32 heads of 128 x 128 in bf16 take 280 us so, 312 with 3/4
-// as many blocks, 324 with 3/2; 131072 tokens x 20 heads of 64 x 128 755, 843 with
-// 2/3 and 863 with 4/3.
-int64_t resident(int64_t dk, int64_t dv) {
-  return 256 * (dk > 128 ? 1 : dk > 64 && dv > 64 ? 2 : 3);
+// kernel allow (in bf16 three parts of the scores take more LDS: 8 x 2048 x 20 heads of
+// 64 x 128 trained in 663 us so, 685 counting three blocks a compute unit; 4 x 4096 x 32
+// of 128 x 64 in 962, and 1038).
+int64_t resident(int64_t dk, int64_t dv, ssm_dtype_t io) {
+  const bool two = io == SSM_BF16 ? dk > 64 || dv > 64 : dk > 64 && dv > 64;
+  return 256 * (dk > 128 ? 1 : two ? 2 : 3);
 }
 
 // Segments: as many as are resident at once, of two units or more.
@@ -319,12 +321,22 @@ Split split_tokens(const Sizes& s, int64_t most) {
   return p;
 }
 
-Split fwd_split(const Sizes& s) { return split_tokens(s, resident(s.dk, s.dv) / (s.rows() * tiles(s.dv))); }
+// Fewer where a die would get more blocks than it holds, which are a second round: 131072
+// tokens x 20 heads (4 of q and k) of 64 x 128 bf16 take 1267 us in 25 segments, 65 blocks on
+// some dies for 64 places, and 922 in 24.
+Split fwd_split(const Sizes& s) {
+  const int64_t most = resident(s.dk, s.dv, s.io);
+  Role r = {};
+  r.tiles = (int)tiles(s.dv);
+  Split p = split_tokens(s, most / (s.rows() * r.tiles));
+  while (p.count > 1 && role_blocks(&r, s.batch, s.heads, s.groups, p.count) > most) p = split_tokens(s, p.count - 1);
+  return p;
+}
 
 // What the pass with the fewest blocks asks for; dq's and dk's may be coarser.
 Split bwd_split(const Sizes& s) {
-  const int64_t to_v = resident(s.dk, s.dv) / (s.rows() * tiles(s.dv));
-  const int64_t to_qk = resident(s.dv, s.dk) / (s.rows() * 2 * tiles(s.dk));
+  const int64_t to_v = resident(s.dk, s.dv, s.io) / (s.rows() * tiles(s.dv));
+  const int64_t to_qk = resident(s.dv, s.dk, s.io) / (s.rows() * 2 * tiles(s.dk));
   Split p = split_tokens(s, std::max(to_v, to_qk));
   const int64_t block = kBlock / kUnit;
   if (p.per >= block) {  // whole blocks: the forward's states are checkpoints
@@ -340,7 +352,7 @@ Split bwd_split(const Sizes& s) {
 // with one split and a pass for the forward's states.
 Split qk_split(const Sizes& s, const Split& p) {
   const int64_t block = kBlock / kUnit;
-  if (p.blocks() || block % p.per || 2 * s.rows() * tiles(s.dk) * s.blocks() < resident(s.dv, s.dk)) return p;
+  if (p.blocks() || block % p.per || 2 * s.rows() * tiles(s.dk) * s.blocks() < resident(s.dv, s.dk, s.io)) return p;
   return Split{block, s.blocks()};
 }
 
@@ -373,23 +385,16 @@ BwdSpace bwd_space(const Sizes& s, bool decays) {
   return w;
 }
 
-// bf16: whether scores and states keep their 24 bits as operands though no decay's
-// gradient needs it.  Over many tokens the outputs' error from their rounding is that of the
-// output's own rounding; with few, one score's rounding may be all of it (up to 2^-8
-// of a token's whole output), and the three-part products cost such calls, which are a launch's
-// latency, next to nothing.
-bool few_tokens(const Sizes& s) { return s.rows() * s.seqlen <= 4096; }
-
 bool whole_units(const Side& s, size_t es) { return s.d * es % 16 == 0 && aligned(s.p, 16); }
 
-hipError_t launch_pass(Args a, int64_t blocks, bool state_only, bool exact, ssm_dtype_t io, hipStream_t st) {
+hipError_t launch_pass(Args a, int64_t blocks, bool state_only, ssm_dtype_t io, hipStream_t st) {
   const size_t es = io_size(io);
   for (int i = 0; i < a.roles; ++i) {
     Role& r = a.role[i];
     r.dma = whole_units(r.q, es) && whole_units(r.k, es) && whole_units(r.v, es);
   }
-  return io == SSM_BF16 ? linattn::launch_bf16(a, blocks, state_only, exact, st)
-                        : linattn::launch_f32(a, blocks, state_only, exact, st);
+  return io == SSM_BF16 ? linattn::launch_bf16(a, blocks, state_only, st)
+                        : linattn::launch_f32(a, blocks, state_only, st);
 }
 
 Args pass_args(const Sizes& s, const Split& p, const float* rate, const void* step, const uint8_t* reset) {
@@ -414,7 +419,7 @@ struct Front {
 };
 
 hipError_t segment_states(Args a, const Role* roles, const Front* first, void* const* space, int count, const Sizes& s,
-                          ssm_dtype_t io, hipStream_t st) {
+                          hipStream_t st) {
   Join join[2] = {};
   a.roles = count;
   int64_t blocks = 0;
@@ -427,7 +432,7 @@ hipError_t segment_states(Args a, const Role* roles, const Front* first, void* c
     blocks += role_blocks(&r, s.batch, s.heads, s.groups, a.segments - 1);
     join[i] = Join{r.part, r.total, first[i].state, first[i].step, r.reverse};
   }
-  const hipError_t e = launch_pass(a, blocks, true, false, io, st);
+  const hipError_t e = launch_pass(a, blocks, true, s.io, st);
   if (e != hipSuccess) return e;
   const int64_t n = s.state();
   hipLaunchKernelGGL(linear_attn_join_kernel, dim3((unsigned)((n + 255) / 256), (unsigned)s.rows(), (unsigned)count),
@@ -450,8 +455,8 @@ extern "C" {
 
 ssm_status_t ssm_linear_attn_fwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t heads, int64_t groups,
                                                  int64_t dk, int64_t dv, ssm_dtype_t io, int64_t* bytes) {
-  const Sizes s{batch, seqlen, heads, groups, dk, dv};
-  const ssm_status_t st = check_sizes(s, io);
+  const Sizes s{batch, seqlen, heads, groups, dk, dv, io};
+  const ssm_status_t st = check_sizes(s);
   if (st == SSM_OK && bytes) *bytes = segment_bytes(s, fwd_split(s));
   return st;
 }
@@ -461,8 +466,8 @@ ssm_status_t ssm_linear_attn_fwd(int64_t batch, int64_t seqlen, int64_t heads, i
                                  const void* step, const uint8_t* reset, const float* h0, float scale, void* y,
                                  float* last_state, float* ckpt, void* workspace, int64_t workspace_bytes,
                                  struct ihipStream_t* stream) {
-  const Sizes s{batch, seqlen, heads, groups, dk, dv};
-  ssm_status_t st = check_sizes(s, io);
+  const Sizes s{batch, seqlen, heads, groups, dk, dv, io};
+  ssm_status_t st = check_sizes(s);
   if (st != SSM_OK) return st;
   const Split p = fwd_split(s);
   if (!passes_ok(s, p, tiles(dv))) return SSM_ERR_UNSUPPORTED;
@@ -496,7 +501,7 @@ ssm_status_t ssm_linear_attn_fwd(int64_t batch, int64_t seqlen, int64_t heads, i
   hipError_t e = hipSuccess;
   if (p.count > 1) {
     const Front first{h0, s.state()};
-    e = segment_states(a, &r, &first, &workspace, 1, s, io, hs);
+    e = segment_states(a, &r, &first, &workspace, 1, s, hs);
     r.start = static_cast<const float*>(workspace);
     r.start_slots = p.count;
     r.start_step = 1;
@@ -510,15 +515,15 @@ ssm_status_t ssm_linear_attn_fwd(int64_t batch, int64_t seqlen, int64_t heads, i
     const int64_t blocks = role_blocks(&r, batch, heads, groups, p.count);
     a.role[0] = r;
     a.roles = 1;
-    e = launch_pass(a, blocks, false, few_tokens(s), io, hs);
+    e = launch_pass(a, blocks, false, io, hs);
   }
   return e == hipSuccess ? SSM_OK : hip_fail(e);
 }
 
 ssm_status_t ssm_linear_attn_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t heads, int64_t groups,
                                                  int64_t dk, int64_t dv, ssm_dtype_t io, int decays, int64_t* bytes) {
-  const Sizes s{batch, seqlen, heads, groups, dk, dv};
-  const ssm_status_t st = check_sizes(s, io);
+  const Sizes s{batch, seqlen, heads, groups, dk, dv, io};
+  const ssm_status_t st = check_sizes(s);
   if (st == SSM_OK && bytes) *bytes = bwd_space(s, decays != 0).bytes;
   return st;
 }
@@ -529,8 +534,8 @@ ssm_status_t ssm_linear_attn_bwd(int64_t batch, int64_t seqlen, int64_t heads, i
                                  const void* dy, const float* dlast, void* dq, void* dk_out, void* dv_out,
                                  float* drate, void* dstep, float* dh0, void* workspace, int64_t workspace_bytes,
                                  struct ihipStream_t* stream) {
-  const Sizes s{batch, seqlen, heads, groups, dk, dv};
-  ssm_status_t st = check_sizes(s, io);
+  const Sizes s{batch, seqlen, heads, groups, dk, dv, io};
+  ssm_status_t st = check_sizes(s);
   if (st != SSM_OK) return st;
   const Split p = bwd_split(s), qk = qk_split(s, p);
   if (!passes_ok(s, p, 2 * tiles(dk) + tiles(dv)) || !launch_ok(s.rows() * s.blocks(), 256)) return SSM_ERR_UNSUPPORTED;
@@ -577,7 +582,7 @@ ssm_status_t ssm_linear_attn_bwd(int64_t batch, int64_t seqlen, int64_t heads, i
     const Role roles[2] = {to_v, forward};
     const Front first[2] = {{dlast, s.state()}, {ckpt, (s.blocks() + 1) * s.state()}};
     void* const spaces[2] = {at(w.segments), at(w.states)};
-    e = segment_states(a, roles, first, spaces, qk.blocks() ? 1 : 2, s, io, hs);
+    e = segment_states(a, roles, first, spaces, qk.blocks() ? 1 : 2, s, hs);
     if (e != hipSuccess) return hip_fail(e);
     to_v.start = at(w.segments);
     to_v.start_slots = p.count;
@@ -631,13 +636,13 @@ ssm_status_t ssm_linear_attn_bwd(int64_t batch, int64_t seqlen, int64_t heads, i
   a.roles = 2;
   a.segments = (int)qk.count;
   a.segment_len = qk.per * kUnit;
-  e = launch_pass(a, q_blocks + k_blocks, false, decays || few_tokens(s), io, hs);
+  e = launch_pass(a, q_blocks + k_blocks, false, io, hs);
   if (e != hipSuccess) return hip_fail(e);
   a.role[0] = to_v;
   a.roles = 1;
   a.segments = (int)p.count;
   a.segment_len = p.per * kUnit;
-  e = launch_pass(a, v_blocks, false, few_tokens(s), io, hs);
+  e = launch_pass(a, v_blocks, false, io, hs);
   if (e != hipSuccess) return hip_fail(e);
   if (shared) {
     const int64_t n = tokens * groups * dk;
@@ -684,8 +689,8 @@ ssm_status_t ssm_linear_attn_state_update(int64_t batch, int64_t heads, int64_t 
                                           ssm_dtype_t io, float* state, const void* q, const void* k, const void* v,
                                           const float* rate, const void* step, float scale, void* y,
                                           struct ihipStream_t* stream) {
-  const Sizes s{batch, 1, heads, groups, dk, dv};
-  ssm_status_t st = check_sizes(s, io);
+  const Sizes s{batch, 1, heads, groups, dk, dv, io};
+  ssm_status_t st = check_sizes(s);
   if (st != SSM_OK) return st;
   if (!launch_ok(s.rows(), 256)) return SSM_ERR_UNSUPPORTED;
   if (!state || !q || !k || !v || !rate || !y) return SSM_ERR_NULL;

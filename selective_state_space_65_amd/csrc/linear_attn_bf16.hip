@@ -3,8 +3,8 @@
 
 namespace linattn {
 
-hipError_t launch_bf16(const Args& a, int64_t blocks, bool state_only, bool exact, hipStream_t st) {
-  return launch<bf16_t>(a, blocks, state_only, exact, st);
+hipError_t launch_bf16(const Args& a, int64_t blocks, bool state_only, hipStream_t st) {
+  return launch<bf16_t>(a, blocks, state_only, st);
 }
 
 }  // namespace linattn

@@ -37,12 +37,12 @@
 // 32 columns a wave: with 16 the LDS was the bound (344 us, all passes together, where
 // these take 243).
 //
-// Roundings (bf16 io).  The scaled v of the update are split in three bf16 parts
-// (24 bits): states are sums in 32 bits of products exact to 2^-24.  Scores and
-// the state as an operand are rounded to bf16 once, half a step each like the
-// output itself; kParts = 3 splits them in three (2^-24), for gradients whose dot
-// products with the inputs are summed up over the tokens (the decays'), and for
-// calls of few tokens, whose roundings do not average out.
+// Roundings (bf16 io).  What is computed and multiplied again -- the scaled v of the
+// update, the scores, and the state as an operand -- is split in three bf16 parts (24
+// bits), so states and outputs are sums in 32 bits of products exact to 2^-24, and
+// only what is written in bf16 is rounded to it.  One part each for the scores and the state
+// would leave outputs off by 2.6e-3 of their size, more than the 1.7e-3 of their own rounding,
+// and two by 2e-4; the layer above takes 244, 254 and 269 us with one, two and three.
 //
 // What a zero factor multiplies is dropped, whatever its value, and a NaN or an
 // infinity of a token reaches no token that it should not: products on the
@@ -108,33 +108,26 @@ __device__ __forceinline__ uint32_t upper_halves(uint32_t lo, uint32_t hi) {
   return __builtin_amdgcn_perm(hi, lo, 0x07060302);
 }
 
-// 8 floats as kParts bf16 operands: one, rounded to nearest; or several, each
-// the upper half of what the ones before left over, so that three hold every bit.
-template <int kParts>
-__device__ __forceinline__ void split(Frag<bf16_t>* f, const float x[8]) {
-  if constexpr (kParts == 1) {
+// 8 floats as operands: three in bf16, each the upper half of what the ones before left
+// over, so that they hold every bit (an infinity's later ones are NaN).
+__device__ __forceinline__ void split(Frag<bf16_t> f[3], const float x[8]) {
+  float r[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) f[0].v[j] = (__bf16)x[j];
-  } else {
-    float r[8];
+  for (int j = 0; j < 8; ++j) r[j] = x[j];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) r[j] = x[j];
+  for (int p = 0; p < 3; ++p) {
+    words4 w;
 #pragma unroll
-    for (int p = 0; p < kParts; ++p) {
-      words4 w;
+    for (int j = 0; j < 4; ++j) w[j] = upper_halves(__float_as_uint(r[2 * j]), __float_as_uint(r[2 * j + 1]));
+    f[p].v = __builtin_bit_cast(bf16x8, w);
+    if (p < 2) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) w[j] = upper_halves(__float_as_uint(r[2 * j]), __float_as_uint(r[2 * j + 1]));
-      f[p].v = __builtin_bit_cast(bf16x8, w);
-      if (p + 1 < kParts) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) r[j] -= __uint_as_float(__float_as_uint(r[j]) & 0xffff0000u);
-      }
+      for (int j = 0; j < 8; ++j) r[j] -= __uint_as_float(__float_as_uint(r[j]) & 0xffff0000u);
     }
   }
 }
 
-template <int kParts>
-__device__ __forceinline__ void split(Frag<float>* f, const float x[8]) {
+__device__ __forceinline__ void split(Frag<float> f[1], const float x[8]) {
 #pragma unroll
   for (int j = 0; j < 8; ++j) f[0].v[j] = x[j];
 }
@@ -144,12 +137,12 @@ struct Traits;
 
 template <>
 struct Traits<bf16_t> {
-  static constexpr int chunk = 64, update_parts = 3;
+  static constexpr int chunk = 64, parts = 3;  // parts: bf16 operands that hold 24 bits
 };
 
 template <>
 struct Traits<float> {
-  static constexpr int chunk = 32, update_parts = 1;
+  static constexpr int chunk = 32, parts = 1;
 };
 
 // A tile of rows of COLS elements in LDS.  Unit u (16 bytes) of row r lies at
@@ -469,18 +462,18 @@ __device__ __forceinline__ float dot_columns(const T* row, int c, int n, const f
   return t;
 }
 
-template <typename T, int NK, int NW, int kParts, bool kOut>
+template <typename T, int NK, int NW, bool kOut>
 struct Layout {
   static constexpr int C = Traits<T>::chunk, DK = 32 * NK, TV = 32 * NW;
   static constexpr int q_bytes = kOut ? C * DK * (int)sizeof(T) : 0;
   static constexpr int k_bytes = C * DK * (int)sizeof(T), v_bytes = C * TV * (int)sizeof(T);
-  static constexpr int s_bytes = kOut ? kParts * C * C * (int)sizeof(T) : 0;
+  static constexpr int s_bytes = kOut ? Traits<T>::parts * C * C * (int)sizeof(T) : 0;
   // q's and v's tiles are free for the next chunk's once every wave has its scores and
   // its operands of v; k's is read to the chunk's end and needs a second one for
   // that (so does v's where there are no scores), if the LDS holds two blocks with it
   // or would not without; but three blocks of two waves rather than two of them: 4 x
-  // 4096 x 32 heads of 128 x 64 in bf16 197 us with two and 165 with one, 8 x 2048 x 12
-  // heads of 128 x 64 in fp32 trained in 831 and 730.
+  // 4096 x 32 heads of 64 x 64 in bf16 214 us with two and 153 with one, 8 x 2048 x 12
+  // heads of 64 x 128 in fp32 trained in 694 and 607.
   static constexpr int v_tiles = kOut ? 1 : 2;
   static constexpr int rest = q_bytes + v_tiles * v_bytes + s_bytes + 3 * (int)sizeof(Decays<C>) + 16;
   static constexpr int blocks(int tiles) { return 160 * 1024 / (rest + tiles * k_bytes); }
@@ -491,11 +484,11 @@ struct Layout {
 };
 
 // kOut: false computes the states alone (a segment's own, and its decay).
-template <typename T, int NK, int NW, int kParts, bool kOut>
+template <typename T, int NK, int NW, bool kOut>
 __global__ __launch_bounds__(64 * NW, NK <= 4 ? 2 : 1) void linear_attn_kernel(const Args a) {
-  using L = Layout<T, NK, NW, kParts, kOut>;
+  using L = Layout<T, NK, NW, kOut>;
   constexpr int C = L::C, DK = L::DK, TV = L::TV, RT = C / 32, kThreads = 64 * NW;
-  constexpr int kUp = Traits<T>::update_parts;
+  constexpr int kParts = Traits<T>::parts;
   using TileK = Tile<T, DK>;
   using TileV = Tile<T, TV>;
   using TileS = Tile<T, C>;
@@ -805,7 +798,7 @@ __global__ __launch_bounds__(64 * NW, NK <= 4 ? 2 : 1) void linear_attn_kernel(c
 #pragma unroll
         for (int j = 0; j < 8; ++j) x[j] = acc[f >> 1][8 * (f & 1) + j];
         Frag<T> s[kParts];
-        split<kParts>(s, x);
+        split(s, x);
         Frag<T> q[RT];
 #pragma unroll
         for (int ti = 0; ti < RT; ++ti) q[ti] = TileK::row(qs, row32, 16 * f, 32 * ti);
@@ -919,8 +912,8 @@ __global__ __launch_bounds__(64 * NW, NK <= 4 ? 2 : 1) void linear_attn_kernel(c
           get8(v[f], x);
 #pragma unroll
           for (int j = 0; j < 8; ++j) x[j] = drop_mul(d.up[16 * f + 8 * half + j], x[j]);
-          Frag<T> w[kUp];
-          split<kUp>(w, x);
+          Frag<T> w[kParts];
+          split(w, x);
           constexpr int kPair = NK < 2 ? 1 : 2;
 #pragma unroll
           for (int b = 0; b < NK; b += kPair) {
@@ -928,7 +921,7 @@ __global__ __launch_bounds__(64 * NW, NK <= 4 ? 2 : 1) void linear_attn_kernel(c
 #pragma unroll
             for (int u = 0; u < kPair; ++u) k[u] = TileK::column(k_base, k_col, 32 * (b + u), 16 * f);
 #pragma unroll
-            for (int part = kUp - 1; part >= 0; --part)
+            for (int part = kParts - 1; part >= 0; --part)
 #pragma unroll
               for (int u = 0; u < kPair; ++u) mma(acc[b + u], k[u], w[part]);
           }
@@ -967,34 +960,29 @@ __global__ __launch_bounds__(64 * NW, NK <= 4 ? 2 : 1) void linear_attn_kernel(c
   }
 }
 
-template <typename T, int NK, int NW, int kParts, bool kOut>
-hipError_t launch_one(const Args& a, int64_t blocks, hipStream_t st) {
-  hipLaunchKernelGGL((linear_attn_kernel<T, NK, NW, kParts, kOut>), dim3((unsigned)blocks), dim3(64 * NW), 0, st, a);
+template <typename T, int NK, int NW>
+hipError_t launch_one(const Args& a, int64_t blocks, bool state_only, hipStream_t st) {
+  const dim3 grid((unsigned)blocks), threads(64 * NW);
+  if (state_only)
+    hipLaunchKernelGGL((linear_attn_kernel<T, NK, NW, false>), grid, threads, 0, st, a);
+  else
+    hipLaunchKernelGGL((linear_attn_kernel<T, NK, NW, true>), grid, threads, 0, st, a);
   return hipGetLastError();
 }
 
-template <typename T, int NK, int NW>
-hipError_t launch_kind(const Args& a, int64_t blocks, bool state_only, bool exact, hipStream_t st) {
-  if (state_only) return launch_one<T, NK, NW, 1, false>(a, blocks, st);
-  if constexpr (sizeof(T) == 2) {
-    if (exact) return launch_one<T, NK, NW, 3, true>(a, blocks, st);
-  }
-  return launch_one<T, NK, NW, 1, true>(a, blocks, st);
-}
-
 template <typename T, int NW>
-hipError_t launch_width(const Args& a, int64_t blocks, bool state_only, bool exact, hipStream_t st) {
+hipError_t launch_width(const Args& a, int64_t blocks, bool state_only, hipStream_t st) {
   const int parts = (a.role[0].k.d + 31) / 32;
-  if (parts <= 1) return launch_kind<T, 1, NW>(a, blocks, state_only, exact, st);
-  if (parts <= 2) return launch_kind<T, 2, NW>(a, blocks, state_only, exact, st);
-  if (parts <= 4) return launch_kind<T, 4, NW>(a, blocks, state_only, exact, st);
-  return launch_kind<T, 8, NW>(a, blocks, state_only, exact, st);
+  if (parts <= 1) return launch_one<T, 1, NW>(a, blocks, state_only, st);
+  if (parts <= 2) return launch_one<T, 2, NW>(a, blocks, state_only, st);
+  if (parts <= 4) return launch_one<T, 4, NW>(a, blocks, state_only, st);
+  return launch_one<T, 8, NW>(a, blocks, state_only, st);
 }
 
 template <typename T>
-hipError_t launch(const Args& a, int64_t blocks, bool state_only, bool exact, hipStream_t st) {
-  return linattn::tile_width(a.role[0].v.d) == 64 ? launch_width<T, 2>(a, blocks, state_only, exact, st)
-                                                  : launch_width<T, 4>(a, blocks, state_only, exact, st);
+hipError_t launch(const Args& a, int64_t blocks, bool state_only, hipStream_t st) {
+  return linattn::tile_width(a.role[0].v.d) == 64 ? launch_width<T, 2>(a, blocks, state_only, st)
+                                                  : launch_width<T, 4>(a, blocks, state_only, st);
 }
 
 }  // namespace

@@ -174,6 +174,22 @@ def test_few_tokens_round_once(shape):
     check(got, {k: (v, b + 2.0 ** -8 * (v.abs() + b)) for k, (v, b) in want.items()}, str(shape))
 
 
+@pytest.mark.parametrize("shape", [(2, 700, 8, 4, 64, 128), (4, 2100, 2, 2, 16, 24), (3, 1500, 4, 1, 130, 72)])
+@pytest.mark.parametrize("need", [("drate", "dstep", "dh0"), ("dh0",)])
+def test_long_calls_round_once(shape, need):
+    """However many tokens, and whichever gradients are asked for: bf16 outputs are the fp32 sums rounded once."""
+    say("linear attention rounds once %s %s" % (shape, need))
+    d, dy, dlast = draw(*shape, BF16, 171, reset=0.01)
+    t = on_gpu(d)
+    y, last, ckpt = ssm.linear_attn_fwd_save(scale=0.25, **t)
+    t.pop("h0")
+    g = ssm.linear_attn_bwd(dy=dy.to(DEV), ckpt=ckpt, dlast=dlast.to(DEV), scale=0.25, need=need, **t)
+    got = dict(y=y.cpu(), last_state=last.cpu(), **{k: v.cpu() for k, v in g.items() if v is not None})
+    want = ref.everything(d, dy, dlast, scale=0.25, io=F32)
+    check(got, {k: (v, b + 2.0 ** -8 * (v.abs() + b) if k in got and got[k].dtype == BF16 else b) for k, (v, b) in want.items()},
+          str(shape))
+
+
 @pytest.mark.parametrize("io", [F32, BF16])
 def test_checkpoints(io):
     d, _, _ = draw(2, 1100, 2, 2, 24, 40, io, 7)
