@@ -166,8 +166,8 @@ __global__ __launch_bounds__(256) void linear_attn_decay_kernel(const DecayArgs 
     const double rate = (double)p.rate[head];
     double step = 1.0;
     if (p.step) step = (double)Io<T>::load1(static_cast<const T*>(p.step) + at * p.heads + head);
-    // Nothing is carried over a reset or a decay of 0 (e^-104 < 2^-149), whatever the sums' roundings say.
-    const bool dropped = (p.reset && p.reset[at]) || rate * step > 104.0;
+    // Nothing is carried over a reset or what is a decay of 0 to the passes, whatever the sums' roundings say.
+    const bool dropped = (p.reset && p.reset[at]) || exp2_hw((float)(-rate * step * 1.4426950408889634)) == 0.0f;
     if (dropped) g = 0.0;
     if (!dropped) sum += g * step;
     if (p.dstep) Io<T>::store1(static_cast<T*>(p.dstep) + at * p.heads + head, dropped ? 0.0f : (float)(-g * rate));

@@ -221,6 +221,21 @@ def test_decays_of_every_size(io):
 
 
 @pytest.mark.parametrize("io", [F32, BF16])
+def test_no_gradient_where_the_decay_is_0(io):
+    """Decays below the smallest normal float, 2^-126 = e^-87.34, drop the state: their gradient is 0, not what the sums
+    that cancel leave over."""
+    d, dy, dlast = draw(2, 700, 3, 3, 40, 24, io, 12)
+    d["rate"] = torch.ones(3)
+    d["step"] = (d["step"].float() * 0.05).to(io)
+    for i, s in enumerate((88.0, 92.0, 100.0, 103.5, 104.0)):
+        d["step"][:, 100 + 100 * i] = s
+    got, _ = run(d, dy, dlast)
+    for i in range(5):
+        assert (got["dstep"][:, 100 + 100 * i] == 0).all(), i
+    check(got, ref.everything(d, dy, dlast, io=io), "dropped")
+
+
+@pytest.mark.parametrize("io", [F32, BF16])
 @pytest.mark.parametrize("field", ["q", "k", "v", "step"])
 @pytest.mark.parametrize("value", [float("nan"), float("inf")])
 def test_not_a_number_stays_behind(io, field, value):
