@@ -14,9 +14,10 @@
 // S from the forward's checkpoints.  The decays' gradient is
 //   dL/dg_t = <a_t S_{t-1}, R_t>
 //           = sum over u >= t in the block of (q_u . dq_u - k_u . dk_u) + <S, R> behind the block
+//           = <S, R> in front of the block - sum over u < t in it of the same
 // since all that is written and read behind t cancels in the sum; blocks are
-// kBlock tokens, so that no longer sum loses what it cancels to, and <S, R> in front of
-// the block says how far the sums' roundings have come.
+// kBlock tokens, so that no longer sum loses what it cancels to, and the two say how far
+// the sums' roundings have come.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -114,68 +115,92 @@ __device__ __forceinline__ double wave_sum(double v) {
   return v;
 }
 
-// One block of kBlock tokens of one (batch, head); a thread has two tokens.
+// One block of kBlock tokens of one (batch, head), a token to a thread.  Nothing is
+// carried over a reset or what is a decay of 0 to the passes, so the sums run
+// between such tokens (or the block's ends) and from either side: what is carried
+// into a run, 0 or <S, R> in front of the block, is known as well as what is carried
+// out of it.  The roundings between the two ends are spread over the run's tokens
+// as a walk between two fixed ends would be; and where a token of the run is not
+// finite, the side that it does not lie on holds.
 template <typename T>
-__global__ __launch_bounds__(256) void linear_attn_decay_kernel(const DecayArgs p) {
-  __shared__ double slots[2][4];  // a row for each use, with one barrier between its writes and its reads
+__global__ __launch_bounds__(kBlock) void linear_attn_decay_kernel(const DecayArgs p) {
+  constexpr int kWaves = kBlock / 64;
+  __shared__ uint64_t cuts[kWaves];
+  __shared__ double heads[kWaves], tails[kWaves], sums[kWaves];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int block = (int)(blockIdx.x % p.blocks);
   const int64_t row = blockIdx.x / p.blocks;
   const int head = (int)(row % p.heads);
-  const double* at_front = p.cross + (row * (p.blocks + 1) + block) * p.parts_v;
-  double cross = 0.0, front = 0.0;  // <S, R> behind and in front of the block
-  for (int i = 0; i < p.parts_v; ++i) {
-    front += at_front[i];
-    cross += at_front[p.parts_v + i];
-  }
-  const int64_t t0 = (int64_t)block * kBlock;
-  double w[2] = {0.0, 0.0};
-#pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    const int64_t t = t0 + 2 * tid + j;
-    if (t >= p.seqlen) continue;
+  const int64_t t = (int64_t)block * kBlock + tid;
+  const int count = (int)min((int64_t)kBlock, p.seqlen - (int64_t)block * kBlock);
+  const int64_t at = row / p.heads * p.seqlen + t;
+  const double rate = (double)p.rate[head];
+  double w = 0.0, step = 1.0;
+  bool dropped = false;
+  if (tid < count) {
     for (int i = 0; i < p.parts_qk; ++i) {
-      const int64_t at = (i * p.rows + row) * p.seqlen + t;
-      w[j] += (double)p.dots_q[at] - (double)p.dots_k[at];
+      const int64_t dot = (i * p.rows + row) * p.seqlen + t;
+      w += (double)p.dots_q[dot] - (double)p.dots_k[dot];
     }
+    if (p.step) step = (double)Io<T>::load1(static_cast<const T*>(p.step) + at * p.heads + head);
+    dropped = (p.reset && p.reset[at]) || exp2_hw((float)(-rate * step * 1.4426950408889634)) == 0.0f;
   }
-  double behind = w[0] + w[1];  // of this lane and those behind it
+  const uint64_t here = __ballot(dropped);
+  if (lane == 0) cuts[wave] = here;
+  __syncthreads();
+  // The token's run, [first, next).
+  double carried_in = 0.0, carried_out = 0.0;
+  int first = -1, next = -1;
+  for (int v = wave; v >= 0 && first < 0; --v) {
+    const uint64_t m = v == wave ? here & (~0ull >> (63 - lane)) : cuts[v];
+    if (m) first = v * 64 + 63 - __builtin_clzll(m);
+  }
+  for (int v = wave; v < kWaves && next < 0; ++v) {
+    const uint64_t m = v == wave ? here & ~(~0ull >> (63 - lane)) : cuts[v];
+    if (m) next = v * 64 + __builtin_ctzll(m);
+  }
+  const double* borders = p.cross + (row * (p.blocks + 1) + block) * p.parts_v;
+  if (first < 0) {
+    first = 0;
+    for (int i = 0; i < p.parts_v; ++i) carried_in += borders[i];
+  }
+  if (next < 0) {
+    next = count;
+    for (int i = 0; i < p.parts_v; ++i) carried_out += borders[p.parts_v + i];
+  }
+  double behind = w, before = w;  // over the run's tokens of this wave from this one on, and up to it
 #pragma unroll
   for (int m = 1; m < 64; m <<= 1) {
-    const double o = __shfl_down(behind, m);
-    if (lane + m < 64) behind += o;
+    const double b = __shfl_down(behind, m), f = __shfl_up(before, m);
+    if (lane + m < 64 && tid + m < next) behind += b;
+    if (lane >= m && tid - m >= first) before += f;
   }
-  if (lane == 0) slots[0][wave] = behind;
+  if (lane == 0) heads[wave] = behind;
+  if (lane == 63) tails[wave] = before;
+  before = __shfl_up(before, 1);  // up to the one in front of it
+  if (lane == 0 || tid == first) before = 0.0;
   __syncthreads();
-  const double all = slots[0][0] + slots[0][1] + slots[0][2] + slots[0][3];
-  for (int v = 3; v > wave; --v) behind += slots[0][v];
-  // What the sums say is carried into the block is known on its own, <S, R> in
-  // front of it.  The sums' roundings between the two ends are spread over the
-  // tokens as a walk between two fixed ends would be.
-  double off = front - (cross + all);
-  if (!(__builtin_fabs(off) < 1e300)) off = 0.0;
-  const int64_t count = min((int64_t)kBlock, p.seqlen - (int64_t)block * kBlock);
+  for (int v = wave + 1; v < kWaves && v * 64 < next; ++v) behind += heads[v];
+  for (int v = wave - 1; v >= 0 && v * 64 + 63 >= first; --v) before += tails[v];
+  const double from_end = carried_out + behind, from_start = carried_in - before;
+  const bool end_ok = __builtin_fabs(from_end) < 1e300, start_ok = __builtin_fabs(from_start) < 1e300;
+  double g = end_ok ? from_end : from_start;
+  if (end_ok && start_ok) g += (from_start - from_end) * (double)(next - tid) / (double)(next - first);
+  if (dropped) g = 0.0;
   double sum = 0.0;
-#pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    const int64_t t = t0 + 2 * tid + j;
-    double g = cross + behind - (j ? w[0] : 0.0);
-    g += off * (double)(t0 + count - t) / (double)count;
-    if (t >= p.seqlen) continue;
-    const int64_t at = row / p.heads * p.seqlen + t;
-    const double rate = (double)p.rate[head];
-    double step = 1.0;
-    if (p.step) step = (double)Io<T>::load1(static_cast<const T*>(p.step) + at * p.heads + head);
-    // Nothing is carried over a reset or what is a decay of 0 to the passes, whatever the sums' roundings say.
-    const bool dropped = (p.reset && p.reset[at]) || exp2_hw((float)(-rate * step * 1.4426950408889634)) == 0.0f;
-    if (dropped) g = 0.0;
-    if (!dropped) sum += g * step;
+  if (tid < count) {
+    if (!dropped) sum = g * step;
     if (p.dstep) Io<T>::store1(static_cast<T*>(p.dstep) + at * p.heads + head, dropped ? 0.0f : (float)(-g * rate));
   }
   sum = wave_sum(sum);
-  if (lane == 0) slots[1][wave] = sum;
+  if (lane == 0) sums[wave] = sum;
   __syncthreads();
-  if (tid == 0) p.drate[row * p.blocks + block] = (slots[1][0] + slots[1][1]) + (slots[1][2] + slots[1][3]);
+  if (tid == 0) {
+    double all = sums[0];
+#pragma unroll
+    for (int v = 1; v < kWaves; ++v) all += sums[v];
+    p.drate[row * p.blocks + block] = all;
+  }
 }
 
 // drate[h] = -sum over the batch rows and blocks, in a fixed order.
@@ -538,7 +563,7 @@ ssm_status_t ssm_linear_attn_bwd(int64_t batch, int64_t seqlen, int64_t heads, i
   ssm_status_t st = check_sizes(s);
   if (st != SSM_OK) return st;
   const Split p = bwd_split(s), qk = qk_split(s, p);
-  if (!passes_ok(s, p, 2 * tiles(dk) + tiles(dv)) || !launch_ok(s.rows() * s.blocks(), 256)) return SSM_ERR_UNSUPPORTED;
+  if (!passes_ok(s, p, 2 * tiles(dk) + tiles(dv)) || !launch_ok(s.rows() * s.blocks(), kBlock)) return SSM_ERR_UNSUPPORTED;
   if (!q || !k || !v || !rate || !ckpt || !dy || !dq || !dk_out || !dv_out) return SSM_ERR_NULL;
   if (!step) dstep = nullptr;
   const bool decays = drate || dstep;
@@ -674,9 +699,9 @@ ssm_status_t ssm_linear_attn_bwd(int64_t batch, int64_t seqlen, int64_t heads, i
     d.parts_v = (int)((dv + 31) / 32);
     const unsigned blocks = (unsigned)(s.rows() * s.blocks());
     if (io == SSM_BF16)
-      hipLaunchKernelGGL(linear_attn_decay_kernel<bf16_t>, dim3(blocks), dim3(256), 0, hs, d);
+      hipLaunchKernelGGL(linear_attn_decay_kernel<bf16_t>, dim3(blocks), dim3(kBlock), 0, hs, d);
     else
-      hipLaunchKernelGGL(linear_attn_decay_kernel<float>, dim3(blocks), dim3(256), 0, hs, d);
+      hipLaunchKernelGGL(linear_attn_decay_kernel<float>, dim3(blocks), dim3(kBlock), 0, hs, d);
     if (drate)
       hipLaunchKernelGGL(linear_attn_drate_kernel, dim3((unsigned)heads), dim3(256), 0, hs, d.drate, drate, batch,
                          (int)heads, d.blocks);

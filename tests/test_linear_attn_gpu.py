@@ -265,6 +265,32 @@ def test_not_a_number_stays_behind(io, field, value):
     assert ((got["last_state"].double() - want["last_state"][0]).abs() <= want["last_state"][1] + 1e-37).all()
 
 
+@pytest.mark.parametrize("io", [F32, BF16])
+@pytest.mark.parametrize("field,value", [(f, v) for f in ("q", "k", "v", "step", "dy") for v in (float("nan"), float("inf"))
+                                         if (f, v) != ("step", float("inf"))])  # a decay of 0: as above
+def test_not_a_number_in_the_steps_gradient(io, field, value):
+    """dstep is not finite where the recurrence makes it so: in the same packed sequence and head, on the side of the token
+    that its state (k, v), its reads (q, dy) or both (step) reach.  The others keep their value, and resets 0."""
+    d, dy, _ = draw(2, 600, 2, 2, 40, 70, io, 14, rates=(0.01, 0.05))
+    d["reset"] = torch.zeros(2, 600, dtype=torch.uint8)
+    d["reset"][0, [30, 90, 512]] = 1
+    clean, clean_dy = {k: v.clone() for k, v in d.items()}, dy.clone()
+    where = (0, 77, 1) if field == "step" else (0, 77, 1, 3)
+    (dy if field == "dy" else d[field])[where] = value
+    got, _ = run(d, dy)
+    want, bound = ref.everything(clean, clean_dy, io=io)["dstep"]
+    bad = ref.everything(d, dy, io=io)["dstep"][0]
+    bad[0, [30, 90, 512]] = want[0, [30, 90, 512]] = 0
+    assert not bad.isfinite().all() and (bad == want)[0, 90:].all()
+    x = got["dstep"].double()
+    assert (x.isfinite() == bad.isfinite()).all()
+    # The sums may come from either side: held to what the bound is over a whole block.
+    bound = torch.cat([bound[:, :512].amax(1, keepdim=True).expand(-1, 512, -1),
+                       bound[:, 512:].amax(1, keepdim=True).expand(-1, 88, -1)], 1)
+    assert ((x - want).abs() <= bound)[bad == want].all(), ((x - want).abs() / bound)[bad == want].max()
+    assert (x[0, [30, 90, 512]] == 0).all()
+
+
 def test_state_that_is_not_finite_is_dropped():
     d, dy, _ = draw(1, 150, 2, 1, 20, 30, BF16, 17)
     d["h0"][0, 0, 3] = float("inf")
