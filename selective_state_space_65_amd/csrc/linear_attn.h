@@ -7,6 +7,8 @@
 
 #include <cstdint>
 
+#include "device_common.h"
+
 namespace linattn {
 
 constexpr int kBlock = 512;  // tokens between saved states
@@ -79,5 +81,36 @@ inline int tile_width(int dv) { return dv > 64 ? 128 : 64; }
 // same.
 hipError_t launch_bf16(const Args& a, int64_t blocks, bool state_only, hipStream_t st);
 hipError_t launch_f32(const Args& a, int64_t blocks, bool state_only, hipStream_t st);
+
+// ---- decays, in device code ----------------------------------------------------
+
+constexpr double kDrop = -4096.0;  // a log2 decay at which every factor is 0 (2^-4096)
+
+// log2 of a token's decay; a NaN stays.
+__device__ __forceinline__ double log2_decay(float rate, float step) {
+  const double g = -(double)rate * (double)step * 1.4426950408889634;
+  return g < kDrop ? kDrop : g;
+}
+
+// An exponent as a whole number and what is left, within 1/2: rounded to 32 bits, that
+// is off by 2^-26 at most whatever the exponent's size, where the exponent in one
+// float would be by 2^-18 at 2^-100.
+struct Exponent {
+  int n;
+  float f;
+};
+
+__device__ __forceinline__ Exponent exponent(double x) {
+  const double n = __builtin_rint(x);
+  return Exponent{(int)n, (float)(x - n)};
+}
+
+// 2^(a - b); 0 below the smallest normal float.
+__device__ __forceinline__ float pow2(Exponent a, Exponent b) {
+  const float e = __builtin_ldexpf(exp2_hw(a.f - b.f), a.n - b.n);
+  return e < 0x1p-126f ? 0.0f : e;
+}
+
+__device__ __forceinline__ float pow2(double x) { return pow2(exponent(x), Exponent{0, 0.0f}); }
 
 }  // namespace linattn

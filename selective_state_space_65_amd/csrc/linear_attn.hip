@@ -134,22 +134,28 @@ __global__ __launch_bounds__(kBlock) void linear_attn_decay_kernel(const DecayAr
   const int64_t t = (int64_t)block * kBlock + tid;
   const int count = (int)min((int64_t)kBlock, p.seqlen - (int64_t)block * kBlock);
   const int64_t at = row / p.heads * p.seqlen + t;
-  const double rate = (double)p.rate[head];
-  double w = 0.0, step = 1.0;
+  const float rate = p.rate[head];
+  float step = 1.0f;
+  const double* borders = p.cross + (row * (p.blocks + 1) + block) * p.parts_v;
+  double carried_in = 0.0, carried_out = 0.0;
+  for (int i = 0; i < p.parts_v; ++i) {
+    carried_in += borders[i];
+    carried_out += borders[p.parts_v + i];
+  }
+  double w = 0.0;
   bool dropped = false;
   if (tid < count) {
     for (int i = 0; i < p.parts_qk; ++i) {
       const int64_t dot = (i * p.rows + row) * p.seqlen + t;
       w += (double)p.dots_q[dot] - (double)p.dots_k[dot];
     }
-    if (p.step) step = (double)Io<T>::load1(static_cast<const T*>(p.step) + at * p.heads + head);
-    dropped = (p.reset && p.reset[at]) || exp2_hw((float)(-rate * step * 1.4426950408889634)) == 0.0f;
+    if (p.step) step = Io<T>::load1(static_cast<const T*>(p.step) + at * p.heads + head);
+    dropped = (p.reset && p.reset[at]) || linattn::pow2(linattn::log2_decay(rate, step)) == 0.0f;
   }
   const uint64_t here = __ballot(dropped);
   if (lane == 0) cuts[wave] = here;
   __syncthreads();
   // The token's run, [first, next).
-  double carried_in = 0.0, carried_out = 0.0;
   int first = -1, next = -1;
   for (int v = wave; v >= 0 && first < 0; --v) {
     const uint64_t m = v == wave ? here & (~0ull >> (63 - lane)) : cuts[v];
@@ -159,15 +165,10 @@ __global__ __launch_bounds__(kBlock) void linear_attn_decay_kernel(const DecayAr
     const uint64_t m = v == wave ? here & ~(~0ull >> (63 - lane)) : cuts[v];
     if (m) next = v * 64 + __builtin_ctzll(m);
   }
-  const double* borders = p.cross + (row * (p.blocks + 1) + block) * p.parts_v;
-  if (first < 0) {
-    first = 0;
-    for (int i = 0; i < p.parts_v; ++i) carried_in += borders[i];
-  }
-  if (next < 0) {
-    next = count;
-    for (int i = 0; i < p.parts_v; ++i) carried_out += borders[p.parts_v + i];
-  }
+  if (first >= 0) carried_in = 0.0;
+  if (next >= 0) carried_out = 0.0;
+  first = max(first, 0);
+  if (next < 0) next = count;
   double behind = w, before = w;  // over the run's tokens of this wave from this one on, and up to it
 #pragma unroll
   for (int m = 1; m < 64; m <<= 1) {
@@ -189,8 +190,8 @@ __global__ __launch_bounds__(kBlock) void linear_attn_decay_kernel(const DecayAr
   if (dropped) g = 0.0;
   double sum = 0.0;
   if (tid < count) {
-    if (!dropped) sum = g * step;
-    if (p.dstep) Io<T>::store1(static_cast<T*>(p.dstep) + at * p.heads + head, dropped ? 0.0f : (float)(-g * rate));
+    if (!dropped) sum = g * (double)step;
+    if (p.dstep) Io<T>::store1(static_cast<T*>(p.dstep) + at * p.heads + head, dropped ? 0.0f : (float)(-g * (double)rate));
   }
   sum = wave_sum(sum);
   if (lane == 0) sums[wave] = sum;
@@ -261,9 +262,8 @@ __global__ __launch_bounds__(256) void linear_attn_step_kernel(const StepArgs p)
   }
   float v[kVec], out[kVec];
   load_n<kVec>(static_cast<const T*>(p.v) + row * p.dv + cc, v);
-  float rate = p.rate[head];
-  if (p.step) rate *= Io<T>::load1(static_cast<const T*>(p.step) + row);
-  const float a = exp2_hw(-rate * kLog2e);
+  const float step = p.step ? Io<T>::load1(static_cast<const T*>(p.step) + row) : 1.0f;
+  const float a = linattn::pow2(linattn::log2_decay(p.rate[head], step));
 #pragma unroll
   for (int j = 0; j < kVec; ++j) out[j] = 0.0f;
   lds_barrier();

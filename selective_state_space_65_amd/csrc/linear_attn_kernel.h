@@ -8,7 +8,9 @@
 //   out_t   = sI e(G_C - G_t) q_t . S + sU sI sum_{s >= t} e(G_s - G_t) (q_t . k_s) v_s
 //   S      <- e(G_C) S + sU sum_s e(G_s) k_s v_s^T.
 // Every exponent is a difference that is <= 0, taken from sums in 64 bits, so no
-// factor overflows and a large step does not blur the small ones behind it.
+// factor overflows and a large step does not blur the small ones behind it; and the
+// whole part of an exponent is never rounded with the rest, so no factor is off by more
+// than a few 2^-24 of itself.
 //
 // A block owns one (batch, head), one segment of the tokens and a tile of v's
 // columns; each of its waves owns 32 columns, with their whole state (k.d rows)
@@ -58,6 +60,8 @@
 namespace {
 
 using linattn::Args;
+using linattn::Exponent;
+using linattn::pow2;
 using linattn::Role;
 using linattn::Side;
 
@@ -230,7 +234,7 @@ __device__ __forceinline__ void get8(const Frag<float>& f, float out[8]) {
 // What a chunk's decays give.
 template <int C>
 struct Decays {
-  double sum[C];     // G (reverse: -G)
+  Exponent sum[C];   // G (reverse: -G)
   float in[C];       // factor of q_t . S
   float up[C];       // factor of k_s v_s^T in the update
   float each[C];     // a_t, 0 where the state is dropped
@@ -239,8 +243,6 @@ struct Decays {
   int zeros;         // some up is 0
   int pad;
 };
-
-constexpr double kDrop = -4096.0;  // a log2 decay at which every factor is 0 (2^-4096)
 
 __device__ __forceinline__ double scan64(double v, int lane) {
 #pragma unroll
@@ -255,9 +257,7 @@ __device__ __forceinline__ double scan64(double v, int lane) {
 template <int C>
 __device__ __forceinline__ void chunk_decays(Decays<C>* d, float rate, float step, int reset, bool constant, int len,
                                              int lane, const Role& p) {
-  double g = -(double)rate * (double)step * 1.4426950408889634;
-  if (g < kDrop) g = kDrop;  // a NaN stays
-  if (reset) g = kDrop;
+  double g = reset ? linattn::kDrop : linattn::log2_decay(rate, step);
   const bool bad = !(__builtin_fabs(g) < 1e300);
   double sum;
   if (constant) {
@@ -267,18 +267,18 @@ __device__ __forceinline__ void chunk_decays(Decays<C>* d, float rate, float ste
     sum = scan64(g, lane);
   }
   const double end = __shfl(sum, 63);
-  const float from_start = exp2_hw((float)sum), to_end = exp2_hw((float)(end - sum));
+  const float from_start = pow2(sum), to_end = pow2(end - sum);
   const float up = p.s_up * (p.reverse ? from_start : to_end);
   const bool slow = __any(bad && lane < len);
   const bool zeros = __any(up == 0.0f && lane < len);
   if (lane < C) {
-    d->sum[lane] = p.reverse ? -sum : sum;
+    d->sum[lane] = linattn::exponent(p.reverse ? -sum : sum);
     d->in[lane] = p.s_in * (p.reverse ? to_end : from_start);
     d->up[lane] = up;
-    d->each[lane] = exp2_hw((float)g);
+    d->each[lane] = pow2(g);
   }
   if (lane == 0) {
-    d->total = exp2_hw((float)end);
+    d->total = pow2(end);
     d->slow = slow;
     d->zeros = zeros;
   }
@@ -721,7 +721,7 @@ __global__ __launch_bounds__(64 * NW, NK <= 4 ? 2 : 1) void linear_attn_kernel(c
         Decays<C>& one = decays[2];
         // A decay that is NaN makes the state NaN, what is 0 of it too: here what is
         // read of it, below what is kept.
-        one.sum[tid] = tid == 0 && !reverse && each != each ? (double)each : 0.0;
+        one.sum[tid] = Exponent{0, tid == 0 && !reverse && each != each ? each : 0.0f};
         one.in[tid] = tid ? 0.0f : p.s_in * (reverse ? 1.0f : each);
         one.up[tid] = tid ? 0.0f : p.s_up * (reverse || each != each ? each : 1.0f);
         if (tid == 0) {
@@ -764,13 +764,13 @@ __global__ __launch_bounds__(64 * NW, NK <= 4 ? 2 : 1) void linear_attn_kernel(c
           mma(x, TileK::row(k_base, k_place + 16 * si * TileK::kPitch, 32 * m, 0),
               TileK::row(qs, q_place + 16 * ti * TileK::kPitch, 32 * m, 0));
         const int t = 16 * ti + c16, s0 = 16 * si + 4 * quad;
-        const double gt = d.sum[t];
+        const Exponent gt = d.sum[t];
         const float s_both = p.s_in * p.s_up;
         const int late = reverse ? t - s0 : s0 - t;  // seen: not after t
         float y[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const float e = exp2_hw((float)(gt - d.sum[s0 + j]));
+          const float e = pow2(gt, d.sum[s0 + j]);
           y[j] = late <= (reverse ? j : -j) ? x[j] * (e * s_both) : 0.0f;
         }
         const unsigned s_at = (s_place ^ 16 * si * (unsigned)sizeof(T)) + 16 * ti * TileS::kPitch;

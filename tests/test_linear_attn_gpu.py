@@ -220,6 +220,34 @@ def test_decays_of_every_size(io):
     check(got, want, "decays")
 
 
+@pytest.mark.parametrize("seqlen", [30, 200])
+@pytest.mark.parametrize("total", [5.0, 40.0, 80.0])
+@pytest.mark.parametrize("constant", [False, True])
+def test_decays_keep_their_bits(seqlen, total, constant):
+    """One token's value read by all later ones, a decay of e^-total in all: every factor is within a few u = 2^-24 of
+    itself, however large its exponent.  A factor's exponent, in whole and rest, is off by u / 2 (1.4 of which 2^x takes over as
+    0.35 u), the exponential by 2 u, and a product takes u / 2: below 8 u for the two factors and the products of an output,
+    and 4 u more for each chunk of 32 tokens that the state was carried over."""
+    k = torch.zeros(1, seqlen, 1, 1)
+    k[0, 0] = 1
+    one = torch.ones(1, seqlen, 1, 1)
+    rate = torch.tensor([total / seqlen])
+    step = torch.rand((1, seqlen, 1), generator=torch.Generator().manual_seed(3)) * 2
+    step[0, 0] = 0
+    steps = torch.ones(seqlen).double().cumsum(0) - 1 if constant else step.double().cumsum(1).flatten()
+    want = torch.exp(-rate.double() * steps)
+    given = {} if constant else dict(step=step.to(DEV))
+    y, last = ssm.linear_attn_fwd(one.to(DEV), k.to(DEV), one.to(DEV), rate.to(DEV), **given)
+    bound = (8 + 4 * (torch.arange(seqlen) // 32)) * ref.U
+    off = (y.cpu().double().flatten() / want - 1).abs()
+    assert (off <= bound).all(), (off / bound).max()
+    assert (last.cpu().double().flatten() / want[-1] - 1).abs() <= bound[-1]
+    state = torch.ones(1, 1, 1, 1, device=DEV)
+    zero = torch.zeros(1, 1, 1, device=DEV)
+    ssm.linear_attn_state_update(state, zero, zero, zero, torch.tensor([total], device=DEV))
+    assert abs(state.item() / torch.exp(torch.tensor(-total).double()).item() - 1) <= 4 * ref.U
+
+
 @pytest.mark.parametrize("io", [F32, BF16])
 def test_no_gradient_where_the_decay_is_0(io):
     """Decays below the smallest normal float, 2^-126 = e^-87.34, drop the state: their gradient is 0, not what the sums
