@@ -381,9 +381,11 @@ struct Stage {
     }
   }
   // The compiler does not see this load, so it waits for none of them before LDS
-  // reads of other tiles; the chunk loop waits for all of them itself.
+  // reads of other tiles; the chunk loop waits for all of them itself.  Nor does it see
+  // its scalar registers read: m0 may be one wait state old, base, which the vector unit may
+  // have read back from a lane, five.
   static __device__ __forceinline__ void fill(uint32_t to, const T* base, uint32_t from) {
-    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(from), "s"(base), "s"(to)
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(from), "s"(base), "s"(to)
                  : "memory", "m0");
   }
   // Zeros in rows from first on.

@@ -16,3 +16,29 @@ def test_no_index_is_past_its_array(source):
     r = subprocess.run([build.hipcc()] + build.HIPCC_FLAGS + ["-Werror=array-bounds", "-I", build.INCLUDE, "--cuda-device-only",
                                                               "-fsyntax-only", source], capture_output=True, text=True)
     assert r.returncode == 0, r.stderr
+
+
+@pytest.mark.parametrize("io", ["float", "bf16_t"])
+def test_loads_to_lds_wait_for_their_base(io, tmp_path):
+    """The compiler counts no wait states inside inline assembly.  A scalar register that a vector instruction wrote (a spilled
+    one that is read back from a lane, say) may be a vector load's base only five wait states later, so the assembly of a
+    load straight to LDS has to hold five of its own in front of the load."""
+    source = tmp_path / "one.hip"
+    source.write_text('#include "linear_attn_kernel.h"\n'
+                      "hipError_t one(const Args& a, hipStream_t st) { return launch_one<%s, 1, 2>(a, 1, false, st); }\n" % io)
+    listing = tmp_path / "one.s"
+    r = subprocess.run([build.hipcc()] + build.HIPCC_FLAGS + ["-I", build.INCLUDE, "-I", os.path.join(build.HERE, "csrc"),
+                                                              "--cuda-device-only", "-S", "-o", str(listing), str(source)],
+                       capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
+    states, loads = 0, 0
+    for line in listing.read_text().splitlines():
+        op = line.split()
+        if ";;#ASMSTART" in line:
+            states = 0
+        elif op and op[0].startswith("global_load_lds"):
+            loads += 1
+            assert states >= 5, "%d wait states before %s" % (states, line.strip())
+        elif op and not op[0].startswith((";", ".")):
+            states += int(op[1]) + 1 if op[0] == "s_nop" else 1
+    assert loads > 0
