@@ -382,11 +382,10 @@ struct Stage {
   }
   // The compiler does not see this load, so it waits for none of them before LDS
   // reads of other tiles; the chunk loop waits for all of them itself.  Nor does it see
-  // its scalar registers read: m0 may be one wait state old, base, which the vector unit may
-  // have read back from a lane, five.
+  // its scalar registers read: m0, the place in LDS, may be one wait state old, and base, which
+  // the vector unit may have read back from a lane, five.
   static __device__ __forceinline__ void fill(uint32_t to, const T* base, uint32_t from) {
-    asm volatile("s_mov_b32 m0, %2\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(from), "s"(base), "s"(to)
-                 : "memory", "m0");
+    asm volatile("s_nop 4\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(from), "s"(base), "{m0}"(to) : "memory");
   }
   // Zeros in rows from first on.
   static __device__ __forceinline__ void clear(T* tile, int first, unsigned tid) {
@@ -483,11 +482,13 @@ struct Layout {
                                  : blocks(2) >= 2 || blocks(1) < 2                    ? 2
                                                                                       : 1;
   static constexpr int bytes = rest + k_tiles * k_bytes;
+  // Waves that a SIMD has at once, for the registers' sake.
+  static constexpr int waves = NK <= 4 && blocks(k_tiles) * NW > 4 ? 2 : 1;
 };
 
 // kOut: false computes the states alone (a segment's own, and its decay).
 template <typename T, int NK, int NW, bool kOut>
-__global__ __launch_bounds__(64 * NW, NK <= 4 ? 2 : 1) void linear_attn_kernel(const Args a) {
+__global__ __launch_bounds__(64 * NW, (Layout<T, NK, NW, kOut>::waves)) void linear_attn_kernel(const Args a) {
   using L = Layout<T, NK, NW, kOut>;
   constexpr int C = L::C, DK = L::DK, TV = L::TV, RT = C / 32, kThreads = 64 * NW;
   constexpr int kParts = Traits<T>::parts;
