@@ -18,6 +18,23 @@ def test_no_index_is_past_its_array(source):
     assert r.returncode == 0, r.stderr
 
 
+def test_warnings_are_seen(capfd, tmp_path):
+    """The build passes on what the compiler says of a file that it compiles, and refuses an index past its array."""
+    def compile(text):
+        source = tmp_path / "one.hip"
+        source.write_text("#include <hip/hip_runtime.h>\n" + text)
+        build._run([[build.hipcc()] + build.HIPCC_FLAGS + ["-c", "-o", str(tmp_path / "one.o"), str(source)]], False)
+
+    kernel = "__global__ void one(float* p) { __shared__ float a[1][4]; a[%d][threadIdx.x] = 1; p[0] = a[0][0]; %s}\n"
+    compile(kernel % (0, ""))
+    assert capfd.readouterr().err == ""
+    compile(kernel % (0, "int left; "))
+    assert "unused variable 'left'" in capfd.readouterr().err
+    with pytest.raises(RuntimeError, match="one.hip"):
+        compile(kernel % (1, ""))
+    assert "past the end of the array" in capfd.readouterr().err
+
+
 @pytest.mark.parametrize("io", ["float", "bf16_t"])
 def test_loads_to_lds_wait_for_their_base(io, tmp_path):
     """The compiler counts no wait states inside inline assembly.  A scalar register that a vector instruction wrote (a spilled
