@@ -619,14 +619,14 @@ __global__ __launch_bounds__(kThreads) void group_norm_map_sums_kernel(const Arg
   }
 }
 
-// A batch row's runs of sums added into its first run's place: 32 columns of the
-// 2 x channels a block, 16 slices of the runs, each added in order.
+// A batch row's runs of sums added into its first run's place, in 64 bits (there may
+// be many): 32 columns of the 2 x channels a block, 16 slices of the runs, each added in order.
 __global__ __launch_bounds__(512) void group_norm_map_columns_kernel(const Args p, int64_t tiles) {
-  __shared__ float sums[16][33];
+  __shared__ double sums[16][33];
   const int col = threadIdx.x & 31, slice = threadIdx.x >> 5;
   const int64_t batch = blockIdx.x / tiles, n = 2 * p.channels, c = blockIdx.x % tiles * 32 + col;
   float* part = p.part + batch * p.runs * n;
-  float t = 0.0f;
+  double t = 0.0;
   if (c < n) {
     constexpr int kRows = 8;
     for (int r = slice; r < p.runs; r += kRows * 16) {
@@ -634,7 +634,7 @@ __global__ __launch_bounds__(512) void group_norm_map_columns_kernel(const Args 
 #pragma unroll
       for (int j = 0; j < kRows; ++j) v[j] = part[min(r + j * 16, p.runs - 1) * n + c];
 #pragma unroll
-      for (int j = 0; j < kRows; ++j) t += r + j * 16 < p.runs ? v[j] : 0.0f;
+      for (int j = 0; j < kRows; ++j) t += r + j * 16 < p.runs ? (double)v[j] : 0.0;
     }
   }
   sums[slice][col] = t;
@@ -642,23 +642,40 @@ __global__ __launch_bounds__(512) void group_norm_map_columns_kernel(const Args 
   if (slice == 0 && c < n) {
 #pragma unroll
     for (int i = 1; i < 16; ++i) t += sums[i][col];
-    part[c] = t;
+    part[c] = (float)t;
   }
 }
 
 // sums[0 / 1][batch, group]: mean over the group of g n and of g (g = dp weight),
-// a wave each; in the blocks behind those, dweight and dbias, a thread a column,
-// batch rows added in order.
+// a wave each; in the blocks behind those, dweight and dbias: 32 columns a block, 8
+// slices of the batch rows, each added in order.  All in 64 bits: a group may have as many
+// channels, and a call as many batch rows, as a sum in 32 bits loses its last bits over.
 __global__ __launch_bounds__(kThreads) void group_norm_map_reduce_kernel(const Args p, int64_t group_blocks,
                                                                          float* dweight, float* dbias) {
   const int64_t n = p.channels, rows = p.batch * p.groups, pitch = p.runs * 2 * n;
   if (blockIdx.x >= group_blocks) {
-    const int64_t c = (blockIdx.x - group_blocks) * kThreads + threadIdx.x;
+    constexpr int kSlices = kThreads / 32, kRows = 8;  // rows in flight
+    __shared__ double sums[kSlices][33];
+    const int col = threadIdx.x & 31, slice = threadIdx.x >> 5;
+    const int64_t c = (blockIdx.x - group_blocks) * 32 + col;
+    double t = 0.0;
+    if (c < 2 * n) {
+      for (int64_t b = slice; b < p.batch; b += kRows * kSlices) {
+        float v[kRows];
+#pragma unroll
+        for (int j = 0; j < kRows; ++j) v[j] = p.part[min(b + j * kSlices, p.batch - 1) * pitch + c];
+#pragma unroll
+        for (int j = 0; j < kRows; ++j) t += b + j * kSlices < p.batch ? (double)v[j] : 0.0;
+      }
+    }
+    sums[slice][col] = t;
+    __syncthreads();
     float* out = c < n ? dweight : dbias;
-    if (c >= 2 * n || !out) return;
-    float t = 0.0f;
-    for (int64_t b = 0; b < p.batch; ++b) t += p.part[b * pitch + c];
-    out[c < n ? c : c - n] = t;
+    if (slice == 0 && c < 2 * n && out) {
+#pragma unroll
+      for (int i = 1; i < kSlices; ++i) t += sums[i][col];
+      out[c < n ? c : c - n] = (float)t;
+    }
     return;
   }
   const int lane = threadIdx.x & 63;
@@ -666,18 +683,21 @@ __global__ __launch_bounds__(kThreads) void group_norm_map_reduce_kernel(const A
   if (row >= rows) return;
   const int64_t first = row % p.groups * p.d;
   const float* at = p.part + row / p.groups * pitch + first;
-  float c1 = 0.0f, c2 = 0.0f;
+  double c1 = 0.0, c2 = 0.0;
   for (int i = lane; i < p.d; i += 64) {
-    const float w = p.weight ? p.weight[first + i] : 1.0f;
-    c2 = __builtin_fmaf(at[i], w, c2);
-    c1 = __builtin_fmaf(at[n + i], w, c1);
+    const double w = p.weight ? (double)p.weight[first + i] : 1.0;
+    c2 = __builtin_fma((double)at[i], w, c2);
+    c1 = __builtin_fma((double)at[n + i], w, c1);
   }
-  const float inv = 1.0f / ((float)p.length * (float)p.d);
-  c1 = group_sum<64>(c1);
-  c2 = group_sum<64>(c2);
+#pragma unroll
+  for (int m = 1; m < 64; m <<= 1) {
+    c1 += __shfl_xor(c1, m);
+    c2 += __shfl_xor(c2, m);
+  }
   if (lane == 0) {
-    p.sums[row] = c2 * inv;
-    p.sums[rows + row] = c1 * inv;
+    const double count = (double)p.length * (double)p.d;
+    p.sums[row] = (float)(c2 / count);
+    p.sums[rows + row] = (float)(c1 / count);
   }
 }
 
@@ -852,7 +872,7 @@ hipError_t launch_bwd(const Args& a, const Plan& p, float* dweight, float* dbias
     hipLaunchKernelGGL((group_norm_map_sums_kernel<T, kGated, false>), grid, threads, 0, st, a);
   const int64_t tiles = (2 * a.channels + 31) / 32, per_block = kThreads / 64;
   const int64_t group_blocks = (a.batch * a.groups + per_block - 1) / per_block;
-  const int64_t column_blocks = dweight || dbias ? (2 * a.channels + kThreads - 1) / kThreads : 0;
+  const int64_t column_blocks = dweight || dbias ? (2 * a.channels + 31) / 32 : 0;
   if (p.runs > 1)
     hipLaunchKernelGGL(group_norm_map_columns_kernel, dim3((unsigned)(a.batch * tiles)), dim3(512), 0, st, a, tiles);
   hipLaunchKernelGGL(group_norm_map_reduce_kernel, dim3((unsigned)(group_blocks + column_blocks)), threads, 0, st, a,

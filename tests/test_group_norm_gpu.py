@@ -133,6 +133,26 @@ def test_one_number_far_off(io, channels):
     assert (err <= 300 * u * 1024).all(), err
 
 
+@pytest.mark.parametrize("shape,groups", [((30000, 2, 8), 1), ((3, 400000, 520), 1), ((5000, 9, 72), 9)])
+def test_sums_over_many_rows_and_runs(shape, groups):
+    """Columns of one number: a sum that grows beside it rounds it the same way each time, so an error shows as it would in
+    a sum of any numbers at worst.  Within the bound that all sums here are held to, 256 additions deep, however many
+    positions and batch rows."""
+    u, deep = 2.0 ** -24, ref.DEEP
+    x = torch.ones(shape, device=DEV)
+    x[..., ::2] = -1
+    x[:, ::2] *= -1
+    dy = torch.full(shape, 1.0 / 3.0, device=DEV)
+    say("group norm, long sums %s" % (shape,))
+    y, _, rstd = ssm.group_norm_fwd(x, groups, kind="rms", eps=0.0)
+    assert torch.equal(y, x)
+    g = ssm.group_norm_bwd(dy, x, rstd, groups, kind="rms")
+    third, count = dy[0, 0, 0].double().item(), shape[0] * shape[1]
+    assert ((g["dbias"].double() / (third * count) - 1).abs() <= deep * u).all()
+    even = x[0, 0].double() * (shape[1] % 2) * shape[0]  # positions of one sign left over
+    assert ((g["dweight"].double() - third * even).abs() <= deep * u * third * count).all()
+
+
 @pytest.mark.parametrize("shape", [(3, 300), (3, 17, 60)])
 @pytest.mark.parametrize("kind", ["layer", "rms"])
 def test_constant_and_zero_groups(shape, kind):
