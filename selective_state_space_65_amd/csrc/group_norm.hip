@@ -254,13 +254,13 @@ __global__ __launch_bounds__(kThreads) void group_norm_row_bwd_kernel(const Args
 }
 
 // dweight and dbias from partial rows of 2 x channels: 32 columns a block, 32
-// slices of the rows, added in order.
+// slices of the rows, added in order and in 64 bits.
 __global__ __launch_bounds__(1024) void group_norm_columns_kernel(const float* part, float* dweight, float* dbias,
                                                                   int64_t rows, int64_t channels) {
-  __shared__ float sums[32][33];
+  __shared__ double sums[32][33];
   const int col = threadIdx.x & 31, slice = threadIdx.x >> 5;
   const int64_t c = (int64_t)blockIdx.x * 32 + col;
-  float t = 0.0f;
+  double t = 0.0;
   if (c < 2 * channels) {
     int64_t r = slice;
     for (; r + 7 * 32 < rows; r += 8 * 32) {
@@ -268,9 +268,9 @@ __global__ __launch_bounds__(1024) void group_norm_columns_kernel(const float* p
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[j] = part[(r + j * 32) * 2 * channels + c];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) t += v[j];
+      for (int j = 0; j < 8; ++j) t += (double)v[j];
     }
-    for (; r < rows; r += 32) t += part[r * 2 * channels + c];
+    for (; r < rows; r += 32) t += (double)part[r * 2 * channels + c];
   }
   sums[slice][col] = t;
   __syncthreads();
@@ -278,7 +278,7 @@ __global__ __launch_bounds__(1024) void group_norm_columns_kernel(const float* p
 #pragma unroll
     for (int i = 1; i < 32; ++i) t += sums[i][col];
     float* out = c < channels ? dweight : dbias;
-    if (out) out[c < channels ? c : c - channels] = t;
+    if (out) out[c < channels ? c : c - channels] = (float)t;
   }
 }
 
@@ -773,9 +773,10 @@ Plan make_plan(int64_t batch, int64_t length, int64_t channels, int64_t groups) 
     const int64_t fwd_rows = per_block * rows_ahead(p.pieces);
     p.row_blocks = (batch * groups + fwd_rows - 1) / fwd_rows;
     // Batch rows side by side: 2048 blocks, but no more partial rows than 512, or than 2048
-    // where those are not yet 512 blocks.
+    // where those are not yet 512 blocks; and at most 256 batch rows to a lane: no sum gets long.
     const int64_t most = std::max<int64_t>(512, std::min<int64_t>(2048, 512 * per_block / groups));
-    p.stride = std::min<int64_t>(batch, std::max<int64_t>(1, std::min<int64_t>(most, 2048 * per_block / groups)));
+    const int64_t least = (batch + 255) / 256;
+    p.stride = std::min<int64_t>(batch, std::max<int64_t>(least, std::min<int64_t>(most, 2048 * per_block / groups)));
     p.bwd_blocks = (p.stride * groups + per_block - 1) / per_block;
   } else {
     const int64_t pieces = (channels + kPiece - 1) / kPiece;

@@ -153,6 +153,21 @@ def test_sums_over_many_rows_and_runs(shape, groups):
     assert ((g["dweight"].double() - third * even).abs() <= deep * u * third * count).all()
 
 
+@pytest.mark.parametrize("shape,groups", [((24576, 8192), 8192), ((200000, 64), 4), ((700000, 8), 1)])
+def test_sums_over_many_rows_of_one_position(shape, groups):
+    """As above, where a lane adds the batch rows of its channels."""
+    say("group norm, long sums %s" % (shape,))
+    x = torch.ones(shape, device=DEV)
+    x[:, ::2] = -1
+    dy = torch.full(shape, 1.0 / 3.0, device=DEV)
+    y, _, rstd = ssm.group_norm_fwd(x, groups, kind="rms", eps=0.0)
+    assert torch.equal(y, x)
+    g = ssm.group_norm_bwd(dy, x, rstd, groups, kind="rms")
+    whole = dy[0, 0].double() * shape[0]
+    assert ((g["dbias"].double() / whole - 1).abs() <= ref.DEEP * ref.U).all()
+    assert ((g["dweight"].double() / (x[0].double() * whole) - 1).abs() <= ref.DEEP * ref.U).all()
+
+
 @pytest.mark.parametrize("shape", [(3, 300), (3, 17, 60)])
 @pytest.mark.parametrize("kind", ["layer", "rms"])
 def test_constant_and_zero_groups(shape, kind):
