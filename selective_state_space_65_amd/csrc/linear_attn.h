@@ -45,26 +45,12 @@ struct Role {
   int dma;               // rows are whole 16-byte units at 16-byte addresses
   int tiles;             // blocks side by side along v.d
   int first_block;       // of the launch that is this role's
-  int units;             // 0, or (batch, group, segment)s whose blocks are put on one die each (role_blocks)
 };
-
-constexpr int kDies = 8;  // consecutive blocks go to the dies (each with an L2) by turns
-
-// Blocks of a role.  The heads of a group and the tiles of a head read the same
-// rows; put on one die they read them from memory once: 131072 tokens x 20 heads
-// that share 4 of q and k (64 x 128, bf16) take 688 us so, 728 with the blocks in
-// the heads' order.  Not done where it would leave dies idle.
-inline int64_t role_blocks(Role* r, int64_t batch, int64_t heads, int64_t groups, int64_t segments) {
-  const int64_t units = batch * groups * segments, each = heads / groups * r->tiles;
-  const int64_t whole = (units + kDies - 1) / kDies * kDies;
-  r->units = each > 1 && whole - units <= units / 16 ? (int)units : 0;
-  return (r->units ? whole : units) * each;
-}
 
 struct Args {
   Role role[3];
   int roles;
-  int batch, heads, groups;
+  int batch, heads;
   int64_t seqlen;
   const float* rate;
   const void* step;      // may be null

@@ -33,7 +33,6 @@ namespace {
 
 using linattn::Args;
 using linattn::kBlock;
-using linattn::role_blocks;
 using linattn::Role;
 using linattn::Side;
 
@@ -346,17 +345,7 @@ Split split_tokens(const Sizes& s, int64_t most) {
   return p;
 }
 
-// Fewer where a die would get more blocks than it holds, which are a second round: 131072
-// tokens x 20 heads (4 of q and k) of 64 x 128 bf16 take 1267 us in 25 segments, 65 blocks on
-// some dies for 64 places, and 922 in 24.
-Split fwd_split(const Sizes& s) {
-  const int64_t most = resident(s.dk, s.dv, s.io);
-  Role r = {};
-  r.tiles = (int)tiles(s.dv);
-  Split p = split_tokens(s, most / (s.rows() * r.tiles));
-  while (p.count > 1 && role_blocks(&r, s.batch, s.heads, s.groups, p.count) > most) p = split_tokens(s, p.count - 1);
-  return p;
-}
+Split fwd_split(const Sizes& s) { return split_tokens(s, resident(s.dk, s.dv, s.io) / (s.rows() * tiles(s.dv))); }
 
 // What the pass with the fewest blocks asks for; dq's and dk's may be coarser.
 Split bwd_split(const Sizes& s) {
@@ -426,7 +415,6 @@ Args pass_args(const Sizes& s, const Split& p, const float* rate, const void* st
   Args a = {};
   a.batch = (int)s.batch;
   a.heads = (int)s.heads;
-  a.groups = (int)s.groups;
   a.seqlen = s.seqlen;
   a.rate = rate;
   a.step = step;
@@ -454,7 +442,7 @@ hipError_t segment_states(Args a, const Role* roles, const Front* first, void* c
     r.total = r.part + s.rows() * a.segments * s.state();
     r.tiles = (int)tiles(s.dv);
     r.first_block = (int)blocks;
-    blocks += role_blocks(&r, s.batch, s.heads, s.groups, a.segments - 1);
+    blocks += s.rows() * r.tiles * (a.segments - 1);
     join[i] = Join{r.part, r.total, first[i].state, first[i].step, r.reverse};
   }
   const hipError_t e = launch_pass(a, blocks, true, s.io, st);
@@ -466,8 +454,7 @@ hipError_t segment_states(Args a, const Role* roles, const Front* first, void* c
 }
 
 bool passes_ok(const Sizes& s, const Split& p, int64_t blocks_each) {
-  // Up to 1/16 more are launched than have work.
-  return s.rows() < 65536 * (int64_t)16 && launch_ok(s.rows() * p.count * blocks_each / 16 * 17 + 16, 256);
+  return s.rows() < 65536 * (int64_t)16 && launch_ok(s.rows() * p.count * blocks_each, 256);
 }
 
 }  // namespace
@@ -537,10 +524,9 @@ ssm_status_t ssm_linear_attn_fwd(int64_t batch, int64_t seqlen, int64_t heads, i
     r.slots = s.blocks() + 1;
     r.last = last_state;
     r.tiles = (int)tiles(dv);
-    const int64_t blocks = role_blocks(&r, batch, heads, groups, p.count);
     a.role[0] = r;
     a.roles = 1;
-    e = launch_pass(a, blocks, false, io, hs);
+    e = launch_pass(a, s.rows() * r.tiles * p.count, false, io, hs);
   }
   return e == hipSuccess ? SSM_OK : hip_fail(e);
 }
@@ -652,16 +638,14 @@ ssm_status_t ssm_linear_attn_bwd(int64_t batch, int64_t seqlen, int64_t heads, i
     to_k.dots = at(w.dots_k);
   }
   // dq's and dk's passes contract v's columns, dv's contracts q's.
-  const int64_t q_blocks = role_blocks(&to_q, batch, heads, groups, qk.count);
-  const int64_t k_blocks = role_blocks(&to_k, batch, heads, groups, qk.count);
-  const int64_t v_blocks = role_blocks(&to_v, batch, heads, groups, p.count);
+  const int64_t q_blocks = s.rows() * to_q.tiles * qk.count, v_blocks = s.rows() * to_v.tiles * p.count;
   to_k.first_block = (int)q_blocks;
   a.role[0] = to_q;
   a.role[1] = to_k;
   a.roles = 2;
   a.segments = (int)qk.count;
   a.segment_len = qk.per * kUnit;
-  e = launch_pass(a, q_blocks + k_blocks, false, io, hs);
+  e = launch_pass(a, 2 * q_blocks, false, io, hs);
   if (e != hipSuccess) return hip_fail(e);
   a.role[0] = to_v;
   a.roles = 1;

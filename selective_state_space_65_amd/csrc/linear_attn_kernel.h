@@ -513,19 +513,7 @@ __global__ __launch_bounds__(64 * NW, (Layout<T, NK, NW, kOut>::waves)) void lin
   // State passes leave out the segment that no other starts behind.
   const int parts = kOut ? a.segments : a.segments - 1;
   const int index = (int)blockIdx.x - p.first_block;
-  const int tile = p.units ? index / linattn::kDies % p.tiles : index % p.tiles;
-  int part, row;  // segment, (batch, head)
-  if (p.units) {
-    const int share = a.heads / a.groups, each = share * p.tiles;
-    const int slot = index / linattn::kDies;
-    const int unit = slot / each * linattn::kDies + index % linattn::kDies;
-    if (unit >= p.units) return;
-    part = unit % parts;
-    row = unit / parts * share + slot / p.tiles % share;
-  } else {
-    part = index / p.tiles % parts;
-    row = index / p.tiles / parts;
-  }
+  const int tile = index % p.tiles, part = index / p.tiles % parts, row = index / p.tiles / parts;
   const int segment = part + (!kOut && p.reverse ? 1 : 0);
   const int head = row % a.heads;
   const int64_t batch_tokens = row / a.heads * a.seqlen;

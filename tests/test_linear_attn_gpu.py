@@ -128,9 +128,9 @@ def test_values(shape, io):
     check(got, ref.everything(d, dy, dlast, scale=0.25, io=io), str(shape))
 
 
-# Groups whose heads' blocks are laid on one die: two tiles and a grid with blocks that have no work in the
-# main pass, the states' pass alone, the main pass alone; and a backward whose passes for q and k have segments of
-# 512 tokens, the last one cut short, where that for v has 128.
+# Heads that share q and k, in launches of two roles: two tiles of columns in the main pass, the states' pass alone, the
+# main pass alone; and a backward whose passes for q and k have segments of 512 tokens, the last one cut short, where
+# that for v has 128.
 SHARED = [(7, 300, 6, 3, 40, 136), (2, 1100, 4, 2, 130, 24), (2, 1000, 6, 2, 24, 72), (8, 700, 8, 4, 8, 136)]
 
 
