@@ -78,7 +78,8 @@
  *  - The gated recurrence, the norms and linear attention (ssm_gated_*,
  *    ssm_norm_*, ssm_group_norm_*, ssm_linear_attn_*) allocate nothing; their
  *    backwards, and the forwards of linear attention and group norm, take a
- *    workspace of the caller's, whose size a query gives.  Two calls that may overlap in time need two workspaces.
+ *    workspace of the caller's, whose size a query gives.  Two calls that may
+ *    overlap in time need two workspaces.
  *  - Calls on different streams are independent; the library is re-entrant.
  */
 #ifndef SSM_SCAN_H
@@ -763,7 +764,7 @@ ssm_status_t ssm_group_norm_bwd_workspace_bytes(int64_t batch, int64_t length, i
  * the formula gives an infinity, NaN may come out in bf16.
  *
  * dk and dv up to 256, heads up to 16384 (larger is SSM_ERR_UNSUPPORTED, as are
- * launches of 2^32 lanes); any seqlen >= 1, any element-aligned pointers;
+ * launches of 2^32 lanes, and batch heads of 2^20 or more but for the decode step); any seqlen >= 1, any element-aligned pointers;
  * groups must divide heads (SSM_ERR_SHAPE).  No output may overlap an input or
  * another output, except last_state == h0.  Allocates nothing; deterministic.
  *
@@ -799,7 +800,7 @@ ssm_status_t ssm_linear_attn_fwd_workspace_bytes(int64_t batch, int64_t seqlen, 
  *
  *   R_t = scale q_t dy_t^T + a_{t+1} R_{t+1}     (no second part before a reset; + dlast at the end)
  *   dq_t = scale S_t dy_t;   dk_t = R_t v_t;   dv_t = R_t^T k_t        (dq, dk summed over a group's heads)
- *   dL/dg_t = a_t <S_{t-1}, R_t>                 (0 at a reset)
+ *   dL/dg_t = a_t <S_{t-1}, R_t>                 (0 at a reset and where a_t is 0)
  *   dstep = -rate dL/dg;  drate[h] = -sum_{b,t} step dL/dg;  dh0 = a_0 R_0
  *
  *   q .. reset, scale, rate              as ssm_linear_attn_fwd

@@ -362,7 +362,7 @@ Split bwd_split(const Sizes& s) {
 
 // dq's and dk's passes: where the segments are parts of a block, whole blocks, which
 // start from checkpoints and from every so many-th of dv's states, if their blocks
-// still fill the chip: 8 x 2048 x 12 heads of 64 x 128 fp32 train in 604 us so, in 667
+// still fill the chip: 8 x 2048 x 12 heads of 64 x 128 fp32 train in 614 us so, in 672
 // with one split and a pass for the forward's states.
 Split qk_split(const Sizes& s, const Split& p) {
   const int64_t block = kBlock / kUnit;

@@ -28,23 +28,23 @@
 // single words (fp32).  16-byte units of a tile's rows are permuted by the row so
 // that neither kind of read has bank conflicts.
 //
-// What bounds it (4 x 4096 tokens x 32 heads of 128 x 128, bf16; 164 us for the pass
+// What bounds it (4 x 4096 tokens x 32 heads of 128 x 128, bf16; 182 us for the pass
 // with outputs, 77 for the states of 3 of 4 segments, 18 for their join).  The two waves
 // a SIMD has, which the state's registers and the tiles' LDS allow, do not hide each
-// other: of a wave's time 19% is issue of vector instructions (864 per wave and chunk, 80 of
-// them products, which keep the matrix units busy for 21%), 30% is waiting to issue and
-// 40% waiting for LDS, barriers and memory; bytes move at 70% of a copy's rate.  Chunks
+// other: of a wave's time 24% is issue of vector instructions (1306 per wave and chunk, 124 of
+// them products, which keep the matrix units busy for 29%), 23% is waiting to issue and
+// 42% waiting for LDS, barriers and memory; bytes move at 62% of a copy's rate.  Chunks
 // of 64 (32 in fp32): the scores' work per token grows with the chunk, scaling
 // the state and the barriers shrink with it, and one of 128 would leave one block a CU.
 // 32 columns a wave: with 16 the LDS was the bound (344 us, all passes together, where
-// these take 243).
+// 32 took 243, the scores and the state in one part each).
 //
 // Roundings (bf16 io).  What is computed and multiplied again -- the scaled v of the
 // update, the scores, and the state as an operand -- is split in three bf16 parts (24
 // bits), so states and outputs are sums in 32 bits of products exact to 2^-24, and
 // only what is written in bf16 is rounded to it.  One part each for the scores and the state
 // would leave outputs off by 2.6e-3 of their size, more than the 1.7e-3 of their own rounding,
-// and two by 2e-4; the layer above takes 244, 254 and 269 us with one, two and three.
+// and two by 2e-4; the layer above takes 244, 254 and 265 us with one, two and three.
 //
 // What a zero factor multiplies is dropped, whatever its value, and a NaN or an
 // infinity of a token reaches no token that it should not: products on the

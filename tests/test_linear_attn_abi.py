@@ -137,6 +137,15 @@ def test_common_refusals(lib, call):
     assert call(lib, io=1, step=addr(30) + 1) == ALIGN
 
 
+def test_batch_rows_times_heads(lib):
+    """2^20 and more are refused but for the decode step; one below is only refused for what else is wrong with it."""
+    for call in (fwd, bwd):
+        few = dict(seqlen=1, heads=4, groups=4, dk=8, dv=8)
+        assert call(lib, batch=1 << 18, **few) == UNSUPPORTED
+        assert call(lib, batch=(1 << 18) - 1, q=None, **few) == NULL
+    assert upd(lib, batch=1 << 18, heads=4, groups=4, dk=8, dv=8, q=None) == NULL
+
+
 def test_forward_refusals(lib):
     assert fwd(lib, seqlen=0) == SHAPE
     assert fwd(lib, y=None) == NULL
