@@ -163,6 +163,23 @@ def test_rates_gradient_over_many_blocks(io, shape):
     check_equal(got, ref.everything(d, dy, dlast, io=io), str(shape))
 
 
+@pytest.mark.parametrize("io", [F32, BF16])
+def test_resets_at_every_border(io):
+    """Resets on and beside the borders of chunks (32, 64), waves of the decays' kernel (64), blocks (512) and segments, side by
+    side, and none: whole numbers (few, so that bf16's sums are exact too), all gradients."""
+    d, dy, dlast = draw(3, 1100, 2, 1, 8, 12, io, 21, whole=True)
+    d["q"][:, :, :, 2:] = 0
+    keep = (torch.arange(1100) % 8 == 0)[None, :, None, None]
+    d["v"] = d["v"] * keep
+    dy = dy * keep
+    d["reset"] = torch.zeros(3, 1100, dtype=torch.uint8)
+    d["reset"][0, [0, 1, 31, 32, 33, 63, 64, 65, 127, 128, 129, 511, 512, 513, 1023, 1024, 1099]] = 1
+    d["reset"][1, 448:576] = 1
+    got, _ = run(d, dy, dlast)
+    want = ref.everything(d, dy, dlast, io=io)
+    check_equal(got, want, "borders")
+
+
 @pytest.mark.parametrize("shape", [(1, 1, 1, 1, 8, 8), (2, 3, 2, 1, 40, 24), (1, 70, 3, 3, 64, 128), (4, 512, 2, 2, 16, 16)])
 def test_few_tokens_round_once(shape):
     """Up to 4096 tokens x heads, bf16 outputs are the fp32 sums (whose parts are exact to 2^-24, within fp32's bound) rounded
@@ -317,6 +334,27 @@ def test_not_a_number_in_the_steps_gradient(io, field, value):
                        bound[:, 512:].amax(1, keepdim=True).expand(-1, 88, -1)], 1)
     assert ((x - want).abs() <= bound)[bad == want].all(), ((x - want).abs() / bound)[bad == want].max()
     assert (x[0, [30, 90, 512]] == 0).all()
+
+
+@pytest.mark.parametrize("io", [F32, BF16])
+@pytest.mark.parametrize("dk,dv", [(32, 64), (64, 64), (64, 128), (128, 64), (128, 128), (256, 64)])
+@pytest.mark.parametrize("field", ["q", "k", "v", "dy"])
+def test_not_a_number_where_tiles_are_fetched_ahead(io, dk, dv, field):
+    """Rows of whole 16-byte units, which go straight to LDS a chunk ahead: a chunk that is done again token by token writes over
+    what was fetched for the next one.  Values, and what is finite, in front of the token, behind it and behind the reset."""
+    d, dy, dlast = draw(1, 330, 2, 2, dk, dv, io, 15, rates=(0.01, 0.05))
+    say("linear attention NaN %s %d x %d %s" % (field, dk, dv, io))
+    d["reset"] = torch.zeros(1, 330, dtype=torch.uint8)
+    d["reset"][0, 201] = 1
+    clean, clean_dy = {k: v.clone() for k, v in d.items()}, dy.clone()
+    (dy if field == "dy" else d[field])[0, 140, 1, 3] = float("nan")
+    got, _ = run(d, dy, dlast)
+    want, bad = ref.everything(clean, clean_dy, dlast, io=io), ref.everything(d, dy, dlast, io=io)
+    for name in ("y", "last_state", "dq", "dk", "dv", "dh0"):
+        x, (value, bound), poisoned = got[name].double(), want[name], bad[name][0]
+        assert (x.isfinite() == poisoned.isfinite()).all(), name
+        same_ = poisoned == value
+        assert ((x - value).abs() <= bound * (1 + 2.0 ** -7) + 1e-37)[same_].all(), name
 
 
 def test_state_that_is_not_finite_is_dropped():
