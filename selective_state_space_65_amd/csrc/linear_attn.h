@@ -80,7 +80,9 @@ __device__ __forceinline__ double log2_decay(float rate, float step) {
 
 // An exponent as a whole number and what is left, within 1/2: rounded to 32 bits, that
 // is off by 2^-26 at most whatever the exponent's size, where the exponent in one
-// float would be by 2^-18 at 2^-100.
+// float would be by 2^-18 at 2^-100.  Factors down to e^-80 are off by at most 1.3 x
+// 2^-24 of themselves so (47 x 2^-24 with the exponent in one float), states that seven
+// chunks were carried over by 5 x 2^-24.
 struct Exponent {
   int n;
   float f;
